@@ -190,6 +190,82 @@ KVC_API int kvc_append(const kvc_desc* d, void* cache, int32_t layer,
                        const int32_t* pos, const int32_t* block_table,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rotary positions of kvc_append_qk (host memory): pairs of the first `dim`
+ * values of a head, pair i rotated by position * f_i.
+ *  pairs      HALF: (i, i + dim / 2); INTERLEAVED: (2 i, 2 i + 1).
+ *  dim        rotated values of a head: even, 0 .. head_dim (0: no rotation).
+ *  scaling    NONE    f_i = base^(-2 i / dim);
+ *             LINEAR  f_i / factor;
+ *             YARN    f_i / factor * r_i + f_i (1 - r_i): r_i rises from 0 to 1
+ *                     over the pairs between floor(pair_of(fast)) and
+ *                     ceil(pair_of(slow)), clamped to 0 .. dim - 1, where
+ *                     pair_of(n) = dim ln(original_len / (2 pi n)) / (2 ln base)
+ *                     makes n turns within original_len positions;
+ *             BANDS   f_i / factor * (1 - r_i) + f_i r_i: r_i rises from 0 to 1
+ *                     as the turns original_len f_i / (2 pi) go from slow to fast.
+ *  magnitude  factor on the rotated values; 0: 1, and for YARN with factor > 1
+ *             0.1 ln(factor) + 1.
+ * kvc_rotary_init checks the fields (KVC_ERR_ARG), and fills in magnitude,
+ * turns (the frequencies as 2^64ths of a turn, so that position * f_i is
+ * reduced exactly) and ready.  Call it again after a change of any field. */
+typedef enum { KVC_PAIRS_HALF = 0, KVC_PAIRS_INTERLEAVED = 1 } kvc_pairs;
+typedef enum { KVC_SCALING_NONE = 0, KVC_SCALING_LINEAR = 1, KVC_SCALING_YARN = 2, KVC_SCALING_BANDS = 3 }
+    kvc_scaling;
+typedef struct kvc_rotary {
+    int32_t pairs;              /* kvc_pairs */
+    int32_t dim;
+    int32_t scaling;            /* kvc_scaling */
+    int32_t original_len;       /* YARN, BANDS: positions the frequencies were made for */
+    float base;                 /* > 1, e.g. 10000 */
+    float factor;               /* > 0 (not NONE) */
+    float fast;                 /* YARN, BANDS: turns, fast > slow > 0 */
+    float slow;
+    float magnitude;
+    int32_t ready;              /* set by kvc_rotary_init */
+    uint64_t turns[128];
+} kvc_rotary;
+KVC_API int kvc_rotary_init(kvc_rotary* rotary);
+
+/* Norms and rotation of kvc_append_qk (host memory).  A weight pointer is
+ * device memory, [head_dim] in the element type of q, 16-byte aligned; NULL:
+ * that side is not normed. */
+typedef struct kvc_qk {
+    const kvc_rotary* rotary;   /* NULL: no rotation */
+    const void* q_weight;
+    const void* k_weight;
+    float eps;                  /* >= 0; with 0 a zero row becomes NaN */
+    float weight_offset;        /* added to every weight (1 for weights stored as w - 1) */
+} kvc_qk;
+
+/* The step between a layer's projection and its attention, in one pass: for
+ * each token, every q and k head is normed, x / sqrt(mean(x^2) + eps) *
+ * (weight + weight_offset), and rotated; q goes to q_out, k and v are
+ * appended to layer `layer` of the cache as kvc_append appends them.  The
+ * attention that follows uses the same descriptor, whose rope is NONE: the
+ * rotation is done here.  (READ_INCACHE caches take the norms alone, no
+ * rotation, else KVC_ERR_UNSUPPORTED; BAKED caches are refused the same way,
+ * their decode would rotate q again.)
+ *   q             [batch, n_new, q_heads, head_dim], k_new and v_new
+ *                 [batch, n_new, kv_heads, head_dim]: token i of sequence b
+ *                 starts at (b n_new + i) * stride elements, its heads dense.
+ *                 A stride of 0 means dense; others are at least a token's
+ *                 elements and multiples of 16 bytes, so that the three may
+ *                 lie side by side in one projection's output.
+ *   pos           [batch] int32: position of token 0 of each sequence.
+ *   n_tok         [batch] int32 or NULL: tokens 0 .. n_tok[b] - 1 of sequence
+ *                 b are real, those behind them padding (NULL: all n_new).
+ *   q_out         [batch, n_new, q_heads, head_dim] dense; may be q itself
+ *                 when q is dense, otherwise it overlaps no input.
+ * Padding tokens and tokens at negative positions are not read; their q_out
+ * rows stay as they were.  Device errors as in kvc_append (the token's q_out
+ * is written all the same).  All arithmetic is fp32 and every stored value is
+ * rounded once.  All pointers are 16-byte aligned but pos, n_tok and
+ * block_table. */
+KVC_API int kvc_append_qk(const kvc_desc* d, void* cache, int32_t layer, const void* q, const void* k_new,
+                          const void* v_new, int32_t q_stride, int32_t k_stride, int32_t v_stride, int32_t n_new,
+                          const int32_t* pos, const int32_t* n_tok, const int32_t* block_table,
+                          const kvc_qk* qk, void* q_out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Decode attention for one layer ([primer] 2.2 and 4.2, [sink] softmax
  * equations): out = softmax(q . K^T * scale) . V over the attended set of
  * each sequence, fp32 online softmax, split over the KV length into partial

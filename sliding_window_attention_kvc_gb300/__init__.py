@@ -39,6 +39,7 @@ ABI_FUNCTIONS = (
     "kvc_block_prepare", "kvc_block_share", "kvc_block_release",
     "kvc_pager_create", "kvc_pager_destroy", "kvc_pager_plan", "kvc_pager_evict", "kvc_pagein_issue",
     "kvc_pagein_commit", "kvc_prefill_workspace_bytes", "kvc_prefill",
+    "kvc_rotary_init", "kvc_append_qk",
 )
 
 
@@ -51,6 +52,24 @@ class KvcDesc(ctypes.Structure):
         ("sinks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
         ("max_blocks_per_seq", ctypes.c_int32), ("num_splits", ctypes.c_int32),
         ("rope_base", ctypes.c_float), ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class KvcRotary(ctypes.Structure):
+    """Mirror of `kvc_rotary` in include/kvc.h (make one with `make_rotary`)."""
+    _fields_ = [
+        ("pairs", ctypes.c_int32), ("dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("original_len", ctypes.c_int32), ("base", ctypes.c_float), ("factor", ctypes.c_float),
+        ("fast", ctypes.c_float), ("slow", ctypes.c_float), ("magnitude", ctypes.c_float),
+        ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128),
+    ]
+
+
+class KvcQk(ctypes.Structure):
+    """Mirror of `kvc_qk` in include/kvc.h (make one with `make_qk`)."""
+    _fields_ = [
+        ("rotary", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
     ]
 
 
@@ -99,6 +118,8 @@ def lib() -> ctypes.CDLL:
         L.kvc_pager_evict.argtypes = [dp, i32, i32, vp, vp, vp, vp, vp]
         L.kvc_pagein_issue.argtypes = [vp, dp, vp, vp, i32, vp, vp, vp, vp]
         L.kvc_pagein_commit.argtypes = [vp, dp, i32, i32, vp, vp, vp, vp, vp]
+        L.kvc_rotary_init.argtypes = [vp]
+        L.kvc_append_qk.argtypes = [dp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_strerror.argtypes = [ctypes.c_int]
         L.kvc_strerror.restype = ctypes.c_char_p
         for name in ABI_FUNCTIONS:
@@ -258,6 +279,96 @@ def append(d: KvcDesc, cache: torch.Tensor, layer: int, k_new: torch.Tensor, v_n
     _check(lib().kvc_append(ctypes.byref(d), _ptr(cache), int(layer), _ptr(k_new), _ptr(v_new), int(n_new),
                             _ptr(pos), _ptr(block_table), _ptr(workspace), workspace.numel(), _stream(stream)),
            "kvc_append")
+
+
+PAIRS = {"half": 0, "interleaved": 1}
+SCALINGS = {"none": 0, "linear": 1, "yarn": 2, "bands": 3}
+
+
+def make_rotary(pairs: str = "half", dim: int = 0, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                original_len: int = 0, fast: float = 32.0, slow: float = 1.0, magnitude: float = 0.0) -> KvcRotary:
+    """kvc_rotary_init: rotary positions of the first `dim` values of a head (include/kvc.h has the formulas)."""
+    r = KvcRotary(PAIRS[pairs], int(dim), SCALINGS[scaling], int(original_len), float(base), float(factor),
+                  float(fast), float(slow), float(magnitude))
+    _check(lib().kvc_rotary_init(ctypes.byref(r)), "kvc_rotary_init")
+    return r
+
+
+def make_qk(d: KvcDesc, rotary: KvcRotary | None = None, q_weight: torch.Tensor | None = None,
+            k_weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0) -> KvcQk:
+    """Norms and rotation for `append_qk`, made once per layer; keeps the rotary and the weights alive."""
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, name, desc_dtype(d), d.head_dim)
+    qk = KvcQk(ctypes.addressof(rotary) if rotary is not None else None, _ptr(q_weight), _ptr(k_weight), float(eps),
+               float(weight_offset))
+    qk.keep = (rotary, q_weight, k_weight)
+    return qk
+
+
+def _need_tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: int) -> int:
+    """[B, n, heads, D] with dense heads and one stride between tokens (n = 1: [B, heads, D] too);
+    returns that stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3 and n == 1:
+        shape, st = (shape[0], 1) + tuple(shape[1:]), (st[0], st[0]) + tuple(st[1:])
+    if tuple(shape) != (B, n, heads, D):
+        raise ValueError(f"{name} must be [{B}, {n}, {heads}, {D}], got {tuple(t.shape)}")
+    if (D > 1 and st[3] != 1) or (heads > 1 and st[2] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    stride = st[1] if n > 1 else (st[0] if B > 1 else heads * D)
+    if (B > 1 and n > 1 and st[0] != n * stride) or not heads * D <= stride < 2 ** 31:
+        raise ValueError(f"{name}: tokens must lie at one stride of at least {heads * D} elements")
+    return stride
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: every tensor of a call lies there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+              pos: torch.Tensor, workspace: torch.Tensor, qk: KvcQk, n_tok: torch.Tensor | None = None,
+              block_table: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """kvc_append_qk: norm and rotate q and k for each head, append k and v, return q.
+
+    q [batch, n_new, q_heads, D], k_new / v_new [batch, n_new, kv_heads, D] (or without n_new for one
+    token); they may be views of one packed projection.  q_out: dense, like q (None: a new tensor)."""
+    dt = desc_dtype(d)
+    n_new = 1 if q.dim() == 3 else q.shape[1] if q.dim() == 4 else -1
+    if n_new < 1:
+        raise ValueError("q must be [batch, n_new, q_heads, head_dim]")
+    qs = _need_tokens(q, "q", dt, d.batch, n_new, d.q_heads, d.head_dim)
+    ks = _need_tokens(k_new, "k_new", dt, d.batch, n_new, d.kv_heads, d.head_dim)
+    vs = _need_tokens(v_new, "v_new", dt, d.batch, n_new, d.kv_heads, d.head_dim)
+    _need_cache(d, cache)
+    _need(pos, "pos", torch.int32, d.batch)
+    _need(workspace, "workspace", torch.uint8)
+    if n_tok is not None:
+        _need(n_tok, "n_tok", torch.int32, d.batch)
+    if block_table is not None:
+        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    _need(q_out, "q_out", dt, q.numel())
+    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        raise ValueError("q_out may be q itself only when q is contiguous")
+    _on_current_device(cache, q, k_new, v_new, pos, workspace, n_tok, block_table, q_out)
+    _check(lib().kvc_append_qk(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new), qs, ks,
+                               vs, n_new, _ptr(pos), _ptr(n_tok), _ptr(block_table), ctypes.byref(qk), _ptr(q_out),
+                               _ptr(workspace), workspace.numel(), _stream(stream)),
+           "kvc_append_qk")
+    return q_out
 
 
 def decode_attention(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
