@@ -290,6 +290,31 @@ KVC_API int kvc_decode_attention(const kvc_desc* d, const void* cache, int32_t l
                                  const int32_t* block_table, const uint32_t* valid_bits,
                                  void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Score modifiers (host memory; slopes and start are device memory).  With
+ * x = q . k * scale for a query of head h at position t and a key at p,
+ *     s = x                                   softcap = 0
+ *     s = softcap * tanh(x / softcap)         softcap > 0
+ *     s = s - slopes[h] * (t - p)             slopes not NULL
+ * and keys below the query's start are not attended (sinks among them): the
+ * document it belongs to begins there.  A value below 0 counts as 0.
+ * Cached rows below every start of their sequence may hold anything; all other
+ * rows up to the query's position hold finite values, as for kvc_prefill. */
+typedef struct kvc_score {
+    const float* slopes;        /* [q_heads] or NULL */
+    const int32_t* start;       /* decode [batch], prefill [batch, T]; or NULL */
+    float softcap;              /* 0: none */
+} kvc_score;
+
+/* kvc_decode_attention with modified scores.  RING, SINK_RING and PAGED
+ * caches, every element type; rope NONE or BAKED (READ_INCACHE is refused with
+ * KVC_ERR_UNSUPPORTED).  A token whose start lies above its position attends
+ * nothing and gets zeros.  PAGED blocks wholly below the start are not read,
+ * nor are most bf16 and INT8 window rows below it. */
+KVC_API int kvc_decode_attention_scored(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                        const int32_t* pos, const int32_t* block_table, const uint32_t* valid_bits,
+                                        const kvc_score* score, void* out, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
 /* One decode step: kvc_append of the token at pos[b] (n_new = 1), then
  * kvc_decode_attention at pos[b], with the same arguments and results as
  * that pair of calls.  For bf16 and INT8 caches, RING / SINK_RING and PAGED
@@ -343,6 +368,17 @@ KVC_API int kvc_prefill(const kvc_desc* d, void* cache, int32_t layer, const voi
                         const void* k_new, const void* v_new, int32_t T, const int32_t* pos0,
                         const int32_t* block_table, const uint32_t* valid_bits,
                         void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* kvc_prefill with modified scores: start is [batch, T], one for each token
+ * of the chunk, so that documents packed into a sequence attend only
+ * themselves.  bf16 and INT8 caches, any GQA group of up to 128 heads, rope
+ * NONE or BAKED; window layouts take chunks no longer than the window, paged
+ * ones blocks whose size is a multiple of 8 dividing 64 (else
+ * KVC_ERR_UNSUPPORTED).  Workspace as for kvc_prefill. */
+KVC_API int kvc_prefill_scored(const kvc_desc* d, void* cache, int32_t layer, const void* q,
+                               const void* k_new, const void* v_new, int32_t T, const int32_t* pos0,
+                               const int32_t* block_table, const uint32_t* valid_bits, const kvc_score* score,
+                               void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Batched block-table update ([share] 3.1 block table, 5.1 block manager):
  * for each i < n, block_table[seq[i]][logical_block[i]] = physical_block[i];

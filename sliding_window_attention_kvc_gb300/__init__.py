@@ -39,7 +39,7 @@ ABI_FUNCTIONS = (
     "kvc_block_prepare", "kvc_block_share", "kvc_block_release",
     "kvc_pager_create", "kvc_pager_destroy", "kvc_pager_plan", "kvc_pager_evict", "kvc_pagein_issue",
     "kvc_pagein_commit", "kvc_prefill_workspace_bytes", "kvc_prefill",
-    "kvc_rotary_init", "kvc_append_qk",
+    "kvc_rotary_init", "kvc_append_qk", "kvc_decode_attention_scored", "kvc_prefill_scored",
 )
 
 
@@ -71,6 +71,11 @@ class KvcQk(ctypes.Structure):
         ("rotary", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
         ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
     ]
+
+
+class KvcScore(ctypes.Structure):
+    """Mirror of `kvc_score` in include/kvc.h (make one with `make_score`)."""
+    _fields_ = [("slopes", ctypes.c_void_p), ("start", ctypes.c_void_p), ("softcap", ctypes.c_float)]
 
 
 class KvcError(RuntimeError):
@@ -119,6 +124,8 @@ def lib() -> ctypes.CDLL:
         L.kvc_pagein_issue.argtypes = [vp, dp, vp, vp, i32, vp, vp, vp, vp]
         L.kvc_pagein_commit.argtypes = [vp, dp, i32, i32, vp, vp, vp, vp, vp]
         L.kvc_rotary_init.argtypes = [vp]
+        L.kvc_decode_attention_scored.argtypes = [dp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.kvc_prefill_scored.argtypes = [dp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_append_qk.argtypes = [dp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_strerror.argtypes = [ctypes.c_int]
         L.kvc_strerror.restype = ctypes.c_char_p
@@ -395,6 +402,54 @@ def decode_attention(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tenso
     return out
 
 
+def make_score(softcap: float = 0.0, slopes: torch.Tensor | None = None,
+               start: torch.Tensor | None = None) -> KvcScore:
+    """Score modifiers (kvc_score): keeps the tensors alive.  slopes fp32 [q_heads]; start int32, [batch]
+    for `decode_attention_scored`, [batch, T] for `prefill_scored`."""
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32)
+    if start is not None:
+        _need(start, "start", torch.int32)
+    sc = KvcScore(_ptr(slopes), _ptr(start), float(softcap))
+    sc.keep = (slopes, start)
+    return sc
+
+
+def _need_score(d: KvcDesc, score: KvcScore, T: int):
+    slopes, start = score.keep
+    if slopes is not None and slopes.numel() != d.q_heads:
+        raise ValueError(f"score: slopes must have {d.q_heads} elements, got {slopes.numel()}")
+    if start is not None and start.numel() != d.batch * T:
+        raise ValueError(f"score: start must have {d.batch * T} elements, got {start.numel()}")
+    _on_current_device(slopes, start)
+
+
+def decode_attention_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
+                            workspace: torch.Tensor, score: KvcScore, block_table: torch.Tensor | None = None,
+                            valid_bits: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """kvc_decode_attention_scored: decode_attention with capped, biased scores and a first position."""
+    dt = desc_dtype(d)
+    _need_cache(d, cache)
+    _need(q, "q", dt, d.batch * d.q_heads * d.head_dim)
+    _need(pos, "pos", torch.int32, d.batch)
+    _need(workspace, "workspace", torch.uint8)
+    if block_table is not None:
+        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
+    if valid_bits is not None:
+        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
+    if out is None:
+        out = torch.empty((d.batch, d.q_heads, d.head_dim), dtype=dt, device=q.device)
+    _need(out, "out", dt, d.batch * d.q_heads * d.head_dim)
+    _need_score(d, score, 1)
+    _on_current_device(cache, q, pos, workspace, block_table, valid_bits, out)
+    _check(lib().kvc_decode_attention_scored(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(pos),
+                                             _ptr(block_table), _ptr(valid_bits), ctypes.byref(score), _ptr(out),
+                                             _ptr(workspace), workspace.numel(), _stream(stream)),
+           "kvc_decode_attention_scored")
+    return out
+
+
 def decode_step(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor,
                 v_new: torch.Tensor, pos: torch.Tensor, workspace: torch.Tensor,
                 block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
@@ -459,6 +514,37 @@ def prefill(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new:
                              _ptr(pos0), _ptr(block_table), _ptr(valid_bits), _ptr(out), _ptr(workspace),
                              workspace.numel(), _stream(stream)),
            "kvc_prefill")
+    return out
+
+
+def prefill_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor,
+                   v_new: torch.Tensor, pos0: torch.Tensor, workspace: torch.Tensor, score: KvcScore,
+                   block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvc_prefill_scored: prefill with capped, biased scores and a first position for each token."""
+    dt = desc_dtype(d)
+    _need_cache(d, cache)
+    _need(q, "q", dt)
+    if q.numel() % (d.batch * d.q_heads * d.head_dim):
+        raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    T = q.numel() // (d.batch * d.q_heads * d.head_dim)
+    _need(k_new, "k_new", dt, d.batch * T * d.kv_heads * d.head_dim)
+    _need(v_new, "v_new", dt, d.batch * T * d.kv_heads * d.head_dim)
+    _need(pos0, "pos0", torch.int32, d.batch)
+    _need(workspace, "workspace", torch.uint8)
+    if block_table is not None:
+        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
+    if valid_bits is not None:
+        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
+    if out is None:
+        out = torch.empty((d.batch, T, d.q_heads, d.head_dim), dtype=dt, device=q.device)
+    _need(out, "out", dt, d.batch * T * d.q_heads * d.head_dim)
+    _need_score(d, score, T)
+    _on_current_device(cache, q, k_new, v_new, pos0, workspace, block_table, valid_bits, out)
+    _check(lib().kvc_prefill_scored(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                    int(T), _ptr(pos0), _ptr(block_table), _ptr(valid_bits), ctypes.byref(score),
+                                    _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "kvc_prefill_scored")
     return out
 
 

@@ -43,3 +43,11 @@
     KVC_INST_MMA(256, 1, PG, RD, true) \
     KVC_INST_MMA(256, 2, PG, RD, true) \
     KVC_INST_MMA(256, 4, PG, RD, true)
+
+// scores with modifiers (kvc_decode_attention_scored)
+#define KVC_INST_SCORE_F32(D, GH, PG) \
+    template cudaError_t kvc::launch_decode_t<float, D, GH, PG, false, true>(const kvc::DecodeParams&, dim3, cudaStream_t);
+#define KVC_INST_SCORE_MMA(D, GH, PG, Q8)                                                                  \
+    template cudaError_t kvc::launch_decode_mma_t<D, GH, PG, false, Q8, true>(const kvc::DecodeParams&,      \
+                                                                              const kvc::KvTensorMaps&, dim3, \
+                                                                              cudaStream_t);

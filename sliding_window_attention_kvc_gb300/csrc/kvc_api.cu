@@ -9,15 +9,17 @@
 
 namespace kvc {
 
-template <typename Elt, int D, int GH, bool PAGED, bool READ>
+template <typename Elt, int D, int GH, bool PAGED, bool READ, bool SCORE = false>
 cudaError_t launch_decode_t(const DecodeParams& p, dim3 grid, cudaStream_t stream);
-template <int D, int GH, bool PAGED, bool READ, bool Q8>
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream);
 
-cudaError_t launch_decode(int dtype, int D, int gh, bool paged, bool rd, const DecodeParams& p, dim3 grid,
+cudaError_t launch_decode(int dtype, int D, int gh, bool paged, bool rd, bool scored, const DecodeParams& p, dim3 grid,
                           cudaStream_t s) {
-#define KVC_CASE(E, DD, GG, PG, RD) \
-    if (D == DD && gh == GG && paged == PG && rd == RD) return launch_decode_t<E, DD, GG, PG, RD>(p, grid, s);
+#define KVC_CASE(E, DD, GG, PG, RD)                                                     \
+    if (D == DD && gh == GG && paged == PG && rd == RD)                                 \
+        return (scored && !RD) ? launch_decode_t<E, DD, GG, PG, false, !RD>(p, grid, s) \
+                               : launch_decode_t<E, DD, GG, PG, RD>(p, grid, s);
 #define KVC_CASES(E, PG, RD)                                                         \
     KVC_CASE(E, 64, 1, PG, RD) KVC_CASE(E, 64, 2, PG, RD) KVC_CASE(E, 64, 4, PG, RD)    \
     KVC_CASE(E, 128, 1, PG, RD) KVC_CASE(E, 128, 2, PG, RD) KVC_CASE(E, 128, 4, PG, RD) \
@@ -32,11 +34,12 @@ cudaError_t launch_decode(int dtype, int D, int gh, bool paged, bool rd, const D
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_decode_mma(int D, int gh, bool paged, bool rd, bool q8, const DecodeParams& p,
+cudaError_t launch_decode_mma(int D, int gh, bool paged, bool rd, bool q8, bool scored, const DecodeParams& p,
                               const KvTensorMaps& maps, dim3 grid, cudaStream_t s) {
-#define KVC_CASE(DD, GG, PG, RD, Q)                                       \
-    if (D == DD && gh == GG && paged == PG && rd == RD && q8 == Q)        \
-        return launch_decode_mma_t<DD, GG, PG, RD, Q>(p, maps, grid, s);
+#define KVC_CASE(DD, GG, PG, RD, Q)                                                               \
+    if (D == DD && gh == GG && paged == PG && rd == RD && q8 == Q)                                \
+        return (scored && !RD) ? launch_decode_mma_t<DD, GG, PG, false, Q, !RD>(p, maps, grid, s) \
+                               : launch_decode_mma_t<DD, GG, PG, RD, Q>(p, maps, grid, s);
 #define KVC_CASES(PG, RD)                                                                        \
     KVC_CASE(64, 1, PG, RD, false) KVC_CASE(64, 2, PG, RD, false) KVC_CASE(64, 4, PG, RD, false)    \
     KVC_CASE(128, 1, PG, RD, false) KVC_CASE(128, 2, PG, RD, false) KVC_CASE(128, 4, PG, RD, false) \
@@ -246,13 +249,34 @@ static int decode_args(const kvc_desc* d, const void* cache, int32_t layer, cons
     return KVC_OK;
 }
 
+// Score modifiers (kvc_score) as the kernels take them; NULL: none.
+static int score_params(const kvc_desc* d, const kvc_score* sc, ScoreParams* out) {
+    *out = ScoreParams{};
+    if (!sc) return KVC_OK;
+    if (!(sc->softcap >= 0.f) || !std::isfinite(sc->softcap)) return KVC_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(sc->slopes) | reinterpret_cast<uintptr_t>(sc->start)) & 3u) return KVC_ERR_ALIGN;
+    // read-time rotation moves keys from step to step: no distances to a key's position
+    if (d->rope == KVC_ROPE_READ_INCACHE) return KVC_ERR_UNSUPPORTED;
+    const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
+    out->scale2 = scale * 1.4426950408889634f;
+    if (sc->softcap > 0.f) {
+        out->cap2 = sc->softcap * 1.4426950408889634f;
+        out->cap_in = (float)(2.0 * 1.4426950408889634 * scale / sc->softcap);
+    }
+    out->slopes = sc->slopes;
+    out->start = sc->start;
+    return KVC_OK;
+}
+
 static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, const void* q, const void* k_new,
                        const void* v_new, const int32_t* pos, const int32_t* block_table,
                        const uint32_t* valid_bits, void* out, void* workspace, size_t workspace_bytes,
-                       void* stream) {
+                       void* stream, const kvc_score* score = nullptr) {
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
+    ScoreParams sp;
+    if ((rc = score_params(d, score, &sp))) return rc;
     if ((rc = decode_args(d, cache, layer, q, pos, block_table, out))) return rc;
     if (!workspace) return KVC_ERR_NULL;
     if (!aligned16(workspace)) return KVC_ERR_ALIGN;
@@ -300,7 +324,8 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     p.max_items = w.items;
     p.rope = d->rope;
     const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
-    p.q_scale = scale * 1.4426950408889634f;   // log2(e): softmax in base 2
+    p.q_scale = score ? 1.f : scale * 1.4426950408889634f;   // log2(e): softmax in base 2
+    p.score = sp;
     if (d->rope != KVC_ROPE_NONE) fill_theta(d->head_dim, d->rope_base, p.theta, p.theta_f);
 
     dim3 grid(d->dtype != KVC_F32 ? w.ctas : w.items, d->kv_heads, g.nsub);
@@ -311,7 +336,8 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     // one paged sequence on the tensor-core kernel: its CTAs plan their own
     // shares from the block table and write the step's token themselves
     // (the CTAs bulk-copy the table and the valid words: 16-byte aligned buffers)
-    p.self_plan = (paged && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
+    // (a start is left to the planning kernel, which drops the blocks below it)
+    p.self_plan = (paged && !sp.start && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
                    (d->num_blocks + 31) / 32 <= kSelfPlanValidWords && aligned16(block_table) &&
                    (!valid_bits || aligned16(valid_bits))) ? 1 : 0;
     if (p.self_plan) {
@@ -325,6 +351,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         pp.pos = pos;
         pp.table = block_table;
         pp.valid = valid_bits;
+        pp.start = sp.start;
         pp.err = p.err;
         pp.seq_off = reinterpret_cast<long long*>(ws + w.plan_acc);
         pp.seq_rows = reinterpret_cast<int32_t*>(ws + w.plan_acc + (size_t)d->batch * 8);
@@ -377,11 +404,13 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     }
     const bool rd = d->rope == KVC_ROPE_READ_INCACHE;
     if (d->dtype != KVC_F32) {
-        if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, p, maps, grid, s) != cudaSuccess)
+        if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, score != nullptr, p, maps, grid, s) !=
+            cudaSuccess)
             return KVC_ERR_CUDA;
         return KVC_OK;
     }
-    if (launch_decode(d->dtype, d->head_dim, g.GH, paged, rd, p, grid, s) != cudaSuccess) return KVC_ERR_CUDA;
+    if (launch_decode(d->dtype, d->head_dim, g.GH, paged, rd, score != nullptr, p, grid, s) != cudaSuccess)
+        return KVC_ERR_CUDA;
     return KVC_OK;
 }
 
@@ -506,21 +535,24 @@ KVC_API size_t kvc_prefill_workspace_bytes(const kvc_desc* d, int32_t T) {
     return prefill_stage_offset(d, g) + prefill_stage_bytes(d, T);
 }
 
-KVC_API int kvc_prefill(const kvc_desc* d, void* cache, int32_t layer, const void* q, const void* k_new,
+static int prefill_impl(const kvc_desc* d, void* cache, int32_t layer, const void* q, const void* k_new,
                         const void* v_new, int32_t T, const int32_t* pos0, const int32_t* block_table,
-                        const uint32_t* valid_bits, void* out, void* workspace, size_t workspace_bytes,
-                        void* stream) {
+                        const uint32_t* valid_bits, const kvc_score* score, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream) {
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
+    ScoreParams sp;
+    if ((rc = score_params(d, score, &sp))) return rc;
     if (d->dtype == KVC_F32) return KVC_ERR_UNSUPPORTED;
     const bool q8 = d->dtype == KVC_I8;
     const bool paged_l = d->layout == KVC_LAYOUT_PAGED;
     // the warp-specialised kernel: 128-row Q tiles of whole GQA groups, paged
     // blocks that pack a 64-key tile, chunks no longer than the window
-    const bool ws_kernel = 128 % g.G == 0 &&
+    // (with modified scores any group of up to 128 heads: its tiles leave the odd rows empty)
+    const bool ws_kernel = (score ? g.G <= 128 : 128 % g.G == 0) &&
                            (paged_l ? (d->block_size % 8 == 0 && 64 % d->block_size == 0) : T <= d->window);
-    if (!ws_kernel && (q8 || (d->head_dim != 64 && d->head_dim != 128) || g.G > 64)) return KVC_ERR_UNSUPPORTED;
+    if (!ws_kernel && (score || q8 || (d->head_dim != 64 && d->head_dim != 128) || g.G > 64)) return KVC_ERR_UNSUPPORTED;
     if (!cache || !q || !k_new || !v_new || !pos0 || !out || !workspace) return KVC_ERR_NULL;
     const bool paged = d->layout == KVC_LAYOUT_PAGED;
     if (paged && !block_table) return KVC_ERR_NULL;
@@ -609,20 +641,47 @@ KVC_API int kvc_prefill(const kvc_desc* d, void* cache, int32_t layer, const voi
     pp.rope = d->rope;
     pp.layer = layer;
     const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
-    pp.q_scale = scale * 1.4426950408889634f;
+    pp.q_scale = score ? 1.f : scale * 1.4426950408889634f;
+    pp.score = sp;
     pp.scales = ap.scales;
     pp.sc_layer_off = ap.sc_layer_off;
     pp.sc_kv_off = ap.sc_kv_off;
     pp.half_rows = half_rows;
     if (d->rope != KVC_ROPE_NONE) fill_theta(d->head_dim, d->rope_base, pp.theta, nullptr);
     if (ws_kernel) {
-        if (launch_prefill_ws(d->head_dim, q8, pp, pm, s) != cudaSuccess) return KVC_ERR_CUDA;
+        if (launch_prefill_ws(d->head_dim, q8, score != nullptr, pp, pm, s) != cudaSuccess) return KVC_ERR_CUDA;
     } else if (launch_prefill(d->head_dim, g.G, pp, s) != cudaSuccess) {
         return KVC_ERR_CUDA;
     }
     // 3. the chunk appended
     if (launch_append(d->dtype, ap, s) != cudaSuccess) return KVC_ERR_CUDA;
     return KVC_OK;
+}
+
+KVC_API int kvc_prefill(const kvc_desc* d, void* cache, int32_t layer, const void* q, const void* k_new,
+                        const void* v_new, int32_t T, const int32_t* pos0, const int32_t* block_table,
+                        const uint32_t* valid_bits, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    return prefill_impl(d, cache, layer, q, k_new, v_new, T, pos0, block_table, valid_bits, nullptr, out, workspace,
+                        workspace_bytes, stream);
+}
+
+KVC_API int kvc_prefill_scored(const kvc_desc* d, void* cache, int32_t layer, const void* q, const void* k_new,
+                               const void* v_new, int32_t T, const int32_t* pos0, const int32_t* block_table,
+                               const uint32_t* valid_bits, const kvc_score* score, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    if (!score) return KVC_ERR_NULL;
+    return prefill_impl(d, cache, layer, q, k_new, v_new, T, pos0, block_table, valid_bits, score, out, workspace,
+                        workspace_bytes, stream);
+}
+
+KVC_API int kvc_decode_attention_scored(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                        const int32_t* pos, const int32_t* block_table, const uint32_t* valid_bits,
+                                        const kvc_score* score, void* out, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+    if (!score) return KVC_ERR_NULL;
+    return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
+                       workspace_bytes, stream, score);
 }
 
 KVC_API int kvc_decode_attention(const kvc_desc* d, const void* cache, int32_t layer, const void* q,

@@ -144,7 +144,24 @@ __device__ __forceinline__ int incache_of_slot(int s, int t, int S, int W, int C
     return shift > 0 ? p - shift : p;
 }
 
-template <typename Elt, int D, int GH, bool PAGED, bool READ>
+// Position held by live slot s of a ring / sink+ring cache at time t.
+__device__ __forceinline__ int abs_of_slot(int s, int t, int S, int W) {
+    return s < S ? s : t - (int)(((long long)t - s) % W);
+}
+
+// Scores with modifiers (kvc_score), base 2: x = q . k unscaled, d = p - t.
+// tanh(y) = 1 - 2 / (e^(2 y) + 1): one exponential and one reciprocal, both
+// with relative error near 2^-23, so the capped score is off by a few 2^-23 cap
+// (tanh.approx would leave 2^-11 of it); its limits +-1 hold as 2^(..) goes to
+// inf or 0.
+__device__ __forceinline__ float scored(const ScoreParams& sp, float x, float slope2, int d) {
+    const float y = sp.cap2 > 0.f ? sp.cap2 - __fdividef(2.f * sp.cap2, exp2f(x * sp.cap_in) + 1.f) : x * sp.scale2;
+    return fmaf(slope2, (float)d, y);
+}
+
+// SCORE: scores with modifiers (p.score; no read-time RoPE): positions of the
+// staged rows go with them, and rows below the sequence's start are masked.
+template <typename Elt, int D, int GH, bool PAGED, bool READ, bool SCORE>
 __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
     using S = DecodeShape<Elt, D>;
     using SM = DecodeSmem<Elt, D, GH, READ>;
@@ -152,6 +169,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     constexpr int NST = kvc::kStages;
     constexpr int CH = S::kCh, DPL = S::kDpl, LPR = S::kLpr, T = S::kT, NRG = S::kRowGroups;
     constexpr int HALF = S::kHalf;
+    static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
+    static_assert(!SCORE || T <= 32, "one lane per staged row");
+    __shared__ int s_pos[SCORE ? NST : 1][SCORE ? T : 1];
 
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* stage_base = smem + SM::kStages;
@@ -242,6 +262,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                         rot[s * HALF + i] = make_float2(c, sn);
                     }
                 }
+                if constexpr (SCORE) {
+                    if (lane < n) s_pos[s][lane] = abs_of_slot(r + lane, t, p.sinks, p.window);
+                }
                 __syncwarp();
                 if (lane == 0) {
                     meta[s].nrows = n;
@@ -290,6 +313,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                             fill = 0;
                         }
                         const int n = min(take, T - fill);
+                        if constexpr (SCORE) {
+                            if (lane < n) s_pos[s][fill + lane] = (lb + src) * p.bs + row + lane;
+                            __syncwarp();
+                        }
                         if (lane == 0) {
                             const uint32_t bytes = (uint32_t)n * S::kRowBytes;
                             unsigned char* dst = stage_base + (size_t)s * S::kStageBytes + (size_t)fill * S::kRowBytes;
@@ -403,6 +430,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
         }
     }
 
+    float slope2[GH];
+    int start = 0;
+    if constexpr (SCORE) {
+        if (p.score.start) start = p.score.start[b];
+#pragma unroll
+        for (int h = 0; h < GH; ++h)
+            slope2[h] = p.score.slopes ? p.score.slopes[kvh * p.G + z * GH + h] * 1.4426950408889634f : 0.f;
+    }
+
     float m[GH], l[GH], o[GH][DPL];
 #pragma unroll
     for (int h = 0; h < GH; ++h) {
@@ -427,7 +463,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < S::kRpg; ++k) {
             const int r = rg + k * NRG;
-            const bool vr = r < nrows;
+            bool vr = r < nrows;
+            if constexpr (SCORE) vr = vr && s_pos[s][r] >= start;
             float kf[DPL];
             if (vr) {
                 const uint4 wa = *reinterpret_cast<const uint4*>(Ks + r * S::kRowBytes + sl * 16);
@@ -460,6 +497,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                 for (int j = 0; j < DPL; ++j) d = fmaf(q[h][j], kf[j], d);
 #pragma unroll
                 for (int off = LPR / 2; off >= 1; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                if constexpr (SCORE) d = scored(p.score, d, slope2[h], vr ? s_pos[s][r] - qpos : 0);
                 sc[k][h] = vr ? d : -INFINITY;
             }
         }
@@ -489,7 +527,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < S::kRpg; ++k) {
             const int r = rg + k * NRG;
-            if (r < nrows) {
+            bool vr = r < nrows;
+            if constexpr (SCORE) vr = vr && s_pos[s][r] >= start;
+            if (vr) {
                 float vf[DPL];
                 const uint4 wa = *reinterpret_cast<const uint4*>(Vs + r * S::kRowBytes + sl * 16);
                 const uint4 wb = *reinterpret_cast<const uint4*>(Vs + r * S::kRowBytes + (sl + LPR) * 16);
@@ -590,10 +630,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     }
 }
 
-template <typename Elt, int D, int GH, bool PAGED, bool READ>
+template <typename Elt, int D, int GH, bool PAGED, bool READ, bool SCORE = false>
 cudaError_t launch_decode_t(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
     using SM = DecodeSmem<Elt, D, GH, READ>;
-    auto kern = decode_kernel<Elt, D, GH, PAGED, READ>;
+    auto kern = decode_kernel<Elt, D, GH, PAGED, READ, SCORE>;
     // The shared-memory opt-in is per device: remember which devices have it.
     static std::atomic<unsigned long long> configured{0};
     int dev = 0;

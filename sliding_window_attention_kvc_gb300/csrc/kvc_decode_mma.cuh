@@ -573,7 +573,12 @@ __device__ __noinline__ void append_token_warp(const DecodeParams& p, long long 
     }
 }
 
-template <int D, int GH, bool PAGED, bool READ, bool Q8>
+// SCORE: scores with modifiers (p.score; no read-time RoPE).  q enters the
+// products as it is (rotated when BAKED), the scale and the modifiers are
+// applied to the scores; runs are cut where positions are not consecutive
+// (window layouts), so that a sub-tile's first position places its rows; runs
+// wholly below the sequence's start are not copied.
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE>
 // Two CTAs (ten warps) per SM: three warps share a sub-partition's 16K
 // registers, so a thread may hold at most 168.
 __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, READ, D))
@@ -582,6 +587,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
     using SM = MmaSmem<D, GH, READ, Q8, PAGED>;
     static_assert(!(READ && Q8 && PAGED), "paged caches take no read-time RoPE");
     static_assert(!Q8 || D >= 128, "INT8 rows are whole 128-byte column blocks");
+    static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
     constexpr int NST = S::kStages, NSUB = S::kNsub, HALF = S::kHalf;
 
     extern __shared__ unsigned char smem_raw[];
@@ -969,11 +975,11 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
         // (1..16) from K-half row urow, sub-tile `rank` after the stage's
         // current fill (lanes of one call take distinct ranks below the room).
         constexpr int kSubCopy = S::kBoxes * 2 * 16 * 128;
-        auto emit_sub_lane = [&](long long urow, int n, int rank, int newrow, bool ef) {
+        auto emit_sub_lane = [&](long long urow, int n, int rank, int ip0, int newrow, bool ef) {
             const int s = it % NST;
             const int f = fill + rank;
             meta[s].nrows[f] = n;
-            meta[s].ip0[f] = 0;
+            meta[s].ip0[f] = ip0;
             meta[s].newrow[f] = newrow;
             meta[s].base[f] = run_off + rank * kSubCopy;
             meta[s].ld[f] = 16;
@@ -1083,6 +1089,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                     // the sink/window boundary and the ring's wrap; they (and their
                     // angles) are computed afresh at those points and every 32 runs
                     int ip_next = 0, prev_n = 0, since = 0;
+                    const int start_b = (SCORE && p.score.start) ? p.score.start[b] : 0;
                     for (int r = r0; r < r1 && ok;) {
                         const int room = ensure_room();
                         if (!room) {
@@ -1106,6 +1113,16 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                             ++since;
                             ip_next = ip0 + n;
                             prev_n = n;
+                        }
+                        if constexpr (SCORE) {
+                            // neither does one whose rows' positions are consecutive
+                            const int seg_end = r < p.sinks ? p.sinks : (r <= h_slot ? h_slot + 1 : C);
+                            n = min(n, seg_end - r);
+                            ip0 = abs_of_slot(r, t_b, p.sinks, p.window);
+                            if (ip0 + n - 1 < start_b) {
+                                r += n;
+                                continue;
+                            }
                         }
                         const int newrow = (p.k_new && t_b >= 0 && h_slot >= r && h_slot < r + n) ? h_slot - r : -1;
                         emit_run(base_row + r, n, ip0, newrow, exact, evict_first);
@@ -1192,7 +1209,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                             break;
                         }
                         const int n = min(take, 16 * room);
-                        emit_run(blk + row, n, 0, newrow_of(lb, row, n), true, evict_first);
+                        emit_run(blk + row, n, SCORE ? lb * p.bs + row : 0, newrow_of(lb, row, n), true, evict_first);
                         take -= n;
                         rem -= n;
                         row += n;
@@ -1230,7 +1247,9 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                         const int rank = __popc(pending & ((1u << lane) - 1u));
                         const bool mine = ((pending >> lane) & 1u) && rank < room;
                         const unsigned emitted = __ballot_sync(0xffffffffu, mine);
-                        if (mine) emit_sub_lane(urow, take, rank, newrow_of(my_lb, row0, take), my_ef);
+                        if (mine)
+                            emit_sub_lane(urow, take, rank, SCORE ? my_lb * p.bs + row0 : 0,
+                                          newrow_of(my_lb, row0, take), my_ef);
                         __syncwarp();
                         fill += __popc(emitted);
                         run_off += __popc(emitted) * kSubCopy;
@@ -1263,7 +1282,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                                 break;
                             }
                             const int n = min(take, 16 * room);
-                            emit_run(blk + row, n, 0, newrow_of(lb + src, row, n), true, bef);
+                            emit_run(blk + row, n, SCORE ? (lb + src) * p.bs + row : 0, newrow_of(lb + src, row, n), true,
+                                     bef);
                             take -= n;
                             rem -= n;
                             row += n;
@@ -1447,6 +1467,9 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
     // so far (the accumulator is rescaled when it grows and multiplied back at
     // the end), so weights stay in [0, 1]
     float qexp = 1.f, S_run = 0.f, rS = 0.f;   // rS = 1 / S_run
+    // SCORE: this lane's q head's slope (base 2), the sequence's start, and the query's position
+    float slope2 = 0.f;
+    int start = 0, t_q = 0;
 
     // q of sequence seg.b as mma A fragments: row g = q head (zero for g >= GH),
     // per k-step columns 16 ks + 2c (+1) and 16 ks + 8 + 2c (+1); rotated,
@@ -1464,6 +1487,11 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
         }
         const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
                                     ((long long)seg.b * p.Hq + kvh * p.G + z * GH + g) * D;
+        if constexpr (SCORE) {
+            t_q = qpos;
+            start = p.score.start ? p.score.start[seg.b] : 0;
+            slope2 = (p.score.slopes && g < GH) ? p.score.slopes[kvh * p.G + z * GH + g] * 1.4426950408889634f : 0.f;
+        }
         csync.sync(p.err);                      // everyone is done with the previous qcs
         if (p.rope != kRopeNone) {
             for (int i = ctid; i < HALF; i += NCT) {
@@ -1888,6 +1916,25 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                 __syncwarp();
             }
 
+            // SCORE: rows of the sub-tile below the start (positions run on from ip0)
+            int lo_rows = 0;
+            if constexpr (SCORE) {
+                lo_rows = start - meta[s].ip0[tg];
+                lo_rows = lo_rows < 0 ? 0 : (lo_rows > S::kSub ? S::kSub : lo_rows);
+                if (!Q8 && lo_rows > 0) {
+                    // they may hold anything too: zero this warp's V columns there
+                    constexpr int BPW = S::kBoxes / S::kDsplit;
+                    const int per_box = lo_rows * 8;
+                    for (int idx = lane; idx < per_box * BPW; idx += 32) {
+                        const int bxl = idx / per_box, rem = idx % per_box;
+                        *reinterpret_cast<uint4*>(Vs + (hd * BPW + bxl) * bstride + (rem / 8) * 128 + (rem % 8) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    wrote = true;
+                    __syncwarp();
+                }
+            }
+
             // ---- S = Q K^T over the 16 rows: two 8-token n-tiles --------------
             float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
             uint4 vw[2][2];          // INT8: V code chunks of tokens 2c, 2c + 1, 2c + 8, 2c + 9
@@ -1963,7 +2010,16 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (!READ) sv[e] *= scl[tk[e]] * qexp;   // (READ: the K scale is in the tile)
-                    vsc[e] = tk[e] < nrows ? vscl[tk[e]] : 0.f;
+                    vsc[e] = (tk[e] < nrows && (!SCORE || tk[e] >= lo_rows)) ? vscl[tk[e]] : 0.f;
+                }
+            }
+            if constexpr (SCORE) {
+                const int d0 = meta[s].ip0[tg] + tk0 - t_q;
+                const int off[4] = {0, 1, 8, 9};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sv[e] = scored(p.score, sv[e], slope2, d0 + off[e]);
+                    if (tk0 + off[e] < lo_rows) sv[e] = -INFINITY;
                 }
             }
             if (tk0 >= nrows) sv[0] = -INFINITY;
@@ -2068,14 +2124,14 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
     }
 }
 
-template <int D, int GH, bool PAGED, bool READ, bool Q8>
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream) {
     using SM = MmaSmem<D, GH, READ, Q8, PAGED>;
     // the resident CTAs per SM that __launch_bounds__ plans for must fit in
     // shared memory (228 KB per SM, 1 KB of it reserved per CTA)
     constexpr int kCtasPerSm = decode_ctas_per_sm(Q8, PAGED, READ, D);
     static_assert(kCtasPerSm * (SM::kTotal + 1024) <= 233472, "shared memory for the planned CTAs per SM");
-    auto kern = decode_mma_kernel<D, GH, PAGED, READ, Q8>;
+    auto kern = decode_mma_kernel<D, GH, PAGED, READ, Q8, SCORE>;
     // few (sequence, kv head, group) units: narrow column chunks, more CTAs
     // each; many: 128 columns a CTA (measured: 64-column chunks 0.5 us slower
     // on the 64-sequence paged batch, 16-column ones 14 us)

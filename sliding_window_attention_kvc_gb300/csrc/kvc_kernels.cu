@@ -263,8 +263,9 @@ __device__ __forceinline__ T plan_block_scan(T v, T* s_warp, T* total) {
 // Attended rows of kPlanPerThread logical blocks lb[j] < nb of one sequence
 // (as paged_block_rows) whose table entries phys[j] are already loaded: every
 // valid-bit load is issued before any is used.
+// Blocks wholly below position `start` are not attended.
 __device__ __forceinline__ void plan_rows_of(const uint32_t* valid, uint32_t* err, const int* lb, int t, int nb,
-                                             int bs, int num_blocks, const int* phys, int* rows) {
+                                             int bs, int num_blocks, int start, const int* phys, int* rows) {
     uint32_t word[kPlanPerThread];
 #pragma unroll
     for (int j = 0; j < kPlanPerThread; ++j) {
@@ -279,17 +280,17 @@ __device__ __forceinline__ void plan_rows_of(const uint32_t* valid, uint32_t* er
         } else if (lb[j] < nb && phys[j] >= 0 && ((word[j] >> (phys[j] & 31)) & 1u)) {
             r = lb[j] == t / bs ? (t - lb[j] * bs + 1) : bs;
         }
-        rows[j] = r;
+        rows[j] = (long long)(lb[j] + 1) * bs <= start ? 0 : r;
     }
 }
 
 // The same, loading the table entries first (all in flight together).
 __device__ __forceinline__ void plan_block_rows(const int32_t* trow, const uint32_t* valid, uint32_t* err,
-                                                const int* lb, int t, int nb, int bs, int num_blocks, int* rows,
-                                                int* phys) {
+                                                const int* lb, int t, int nb, int bs, int num_blocks, int start,
+                                                int* rows, int* phys) {
 #pragma unroll
     for (int j = 0; j < kPlanPerThread; ++j) phys[j] = lb[j] < nb ? __ldg(trow + lb[j]) : -1;
-    plan_rows_of(valid, err, lb, t, nb, bs, num_blocks, phys, rows);
+    plan_rows_of(valid, err, lb, t, nb, bs, num_blocks, start, phys, rows);
 }
 
 __device__ __forceinline__ void plan_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const __grid_c
     // it waits for this grid to complete before it reads anything
     plan_pdl_launch();
     const int32_t* trow = p.table + (long long)b * p.maxb;
+    const int start = p.start ? p.start[b] : 0;
     constexpr int kChunk = kPlanThreads * kPlanPerThread;
     __shared__ int s_tok_phys;
 
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const __grid_c
         const int traw = __ldg(p.pos);
         const int t = clamp_paged_t(traw, p.maxb, p.bs);
         const int nb = t < 0 ? 0 : t / p.bs + 1;
-        plan_rows_of(p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, ph, v);
+        plan_rows_of(p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, start, ph, v);
         int tsum = 0;
 #pragma unroll
         for (int j = 0; j < kPlanPerThread; ++j) {
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const __grid_c
         int lbs[kPlanPerThread], v[kPlanPerThread], ph[kPlanPerThread];
 #pragma unroll
         for (int j = 0; j < kPlanPerThread; ++j) lbs[j] = base + j * kPlanThreads + tid;
-        plan_block_rows(trow, p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, v, ph);
+        plan_block_rows(trow, p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, start, v, ph);
 #pragma unroll
         for (int j = 0; j < kPlanPerThread; ++j) sum += v[j];
     }
@@ -532,6 +534,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_items_kernel(const __grid_c
     // its own wait (this grid launches only after that): the rows of the first
     // pass are loaded before waiting for plan_count_kernel's results.
     const int32_t* trow = p.table + (long long)b * p.maxb;
+    const int start = p.start ? __ldg(p.start + b) : 0;
     const int traw = __ldg(p.pos + b);
     const int t = clamp_paged_t(traw, p.maxb, p.bs);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_items_kernel(const __grid_c
     int lbs[kPlanPerThread], v[kPlanPerThread], ph[kPlanPerThread];
 #pragma unroll
     for (int j = 0; j < kPlanPerThread; ++j) lbs[j] = tid * kPlanPerThread + j;
-    plan_block_rows(trow, p.valid, nullptr, lbs, t, nb, p.bs, p.num_blocks, v, ph);
+    plan_block_rows(trow, p.valid, nullptr, lbs, t, nb, p.bs, p.num_blocks, start, v, ph);
     // No early trigger here: the decode grid fills every SM (two CTAs each)
     // and must not launch while plan CTAs still hold registers, or its last
     // CTAs start only when others finish.
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_items_kernel(const __grid_c
         if (base > 0) {
 #pragma unroll
             for (int j = 0; j < kPlanPerThread; ++j) lbs[j] = lb0 + j;
-            plan_block_rows(trow, p.valid, nullptr, lbs, t, nb, p.bs, p.num_blocks, v, ph);
+            plan_block_rows(trow, p.valid, nullptr, lbs, t, nb, p.bs, p.num_blocks, start, v, ph);
         }
         int tsum = 0;
 #pragma unroll
@@ -607,6 +610,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(const __grid_co
     // the first pass (all of them, not only those the position reaches) and,
     // on a bf16 cache, the step's new token.
     const int traw = p.pos[b];
+    const int start = p.start ? p.start[b] : 0;
     int ph0[kPlanPerThread];
 #pragma unroll
     for (int j = 0; j < kPlanPerThread; ++j) {
@@ -645,9 +649,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(const __grid_co
         if (base == 0) {
 #pragma unroll
             for (int j = 0; j < kPlanPerThread; ++j) ph[j] = lbs[j] < nb ? ph0[j] : -1;
-            plan_rows_of(p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, ph, v);
+            plan_rows_of(p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, start, ph, v);
         } else {
-            plan_block_rows(trow, p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, v, ph);
+            plan_block_rows(trow, p.valid, p.err, lbs, t, nb, p.bs, p.num_blocks, start, v, ph);
         }
         uint32_t m[kPlanPerThread];
 #pragma unroll

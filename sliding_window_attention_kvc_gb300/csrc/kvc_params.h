@@ -72,6 +72,17 @@ struct WorkspaceLayout {
     int ctas;            // persistent CTAs per (kv head, q-head group) that claim the shares
 };
 
+// Score modifiers (kvc_score) in base-2 units: s = cap2 tanh(x / cap) (cap2 =
+// cap log2 e; x the scaled score, s = x log2 e when cap2 = 0) - slope log2 e
+// (t - p), keys p >= start.  q enters the products unscaled.
+struct ScoreParams {
+    float scale2;               // softmax scale * log2(e)
+    float cap2;                 // softcap * log2(e), 0: none
+    float cap_in;               // 2 log2(e) * softmax scale / softcap: tanh(x / cap) = 1 - 2 / (2^(cap_in q.k) + 1)
+    const float* slopes;        // [Hq], may be null
+    const int32_t* start;       // decode [B], prefill [B, T]; may be null
+};
+
 struct DecodeParams {
     const void* cache;          // whole cache tensor
     const void* q;              // [B, Hq, D]
@@ -112,6 +123,7 @@ struct DecodeParams {
     float q_scale;              // softmax scale * log2(e)
     float theta_f[kMaxHalfDim];     // RoPE frequencies, fp32 (small in-tile angles)
     unsigned long long theta[kMaxHalfDim];   // RoPE frequencies as turns, fixed point: theta_i / (2 pi) * 2^64
+    ScoreParams score;          // kvc_decode_attention_scored
 };
 
 struct PlanParams {
@@ -131,6 +143,7 @@ struct PlanParams {
                           // attended blocks of the sequence before block 32 g)
     int dir_groups;
     uint32_t* refs;       // plan_rows_kernel: [num_blocks] += 1 per sequence attending the block
+    const int32_t* start; // [B]: blocks wholly below it are not attended; may be null
     int B, bs, num_blocks, maxb, max_items, ctas;
     // the step's new token (kvc_decode_step); k_new == null: none
     void* cache;
@@ -183,6 +196,7 @@ struct PrefillParams {
     long long sc_kv_off;        // INT8: from the K half's scales to the V half's (rows of a half)
     long long half_rows;        // rows of a K (or V) half of a layer
     unsigned long long theta[kMaxHalfDim];   // theta_i / (2 pi) * 2^64 (see rope_cos_sin)
+    ScoreParams score;          // kvc_prefill_scored
 };
 
 // Tensor maps of the warp-specialised prefill (kvc_prefill_ws.cu), bf16 rows,
@@ -256,11 +270,12 @@ struct KvTensorMaps {
 };
 
 // Launchers (return a cudaError_t from the launch).
-cudaError_t launch_decode(int dtype, int head_dim, int gh, bool paged, bool read_rope,
+// (scored: kvc_decode_attention_scored, no read-time RoPE)
+cudaError_t launch_decode(int dtype, int head_dim, int gh, bool paged, bool read_rope, bool scored,
                           const DecodeParams& p, dim3 grid, cudaStream_t stream);
 // bf16 and INT8 (q8) caches: tensor-core kernel fed by TMA tensor copies through `maps`.
-cudaError_t launch_decode_mma(int head_dim, int gh, bool paged, bool read_rope, bool q8, const DecodeParams& p,
-                              const KvTensorMaps& maps, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_mma(int head_dim, int gh, bool paged, bool read_rope, bool q8, bool scored,
+                              const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_plan_rows(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_append(int dtype, const AppendParams& p, cudaStream_t stream);
@@ -270,7 +285,7 @@ cudaError_t launch_prefill_stage(const AppendParams& p, void* kst, void* vst, cu
 cudaError_t launch_prefill(int head_dim, int g, const PrefillParams& p, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, cudaStream_t stream);   // head_dim 128, tcgen05
 // head_dim 64 / 128 / 256, warp-specialised tcgen05 with TMA tiles
-cudaError_t launch_prefill_ws(int head_dim, bool q8, const PrefillParams& p, const PrefillMaps& maps,
+cudaError_t launch_prefill_ws(int head_dim, bool q8, bool scored, const PrefillParams& p, const PrefillMaps& maps,
                               cudaStream_t stream);
 cudaError_t launch_valid_write(const TableParams& p, cudaStream_t stream);
 cudaError_t launch_block_prepare(int elt, const BlockParams& p, cudaStream_t stream);

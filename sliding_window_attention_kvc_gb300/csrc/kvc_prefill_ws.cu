@@ -77,6 +77,7 @@ struct alignas(16) WsStageMeta {
     int kbase;               // kMaskRange: position of key 0
     int sc_off;              // INT8 cache tile: row 0's scale in the stage's scale area
     int pos[kWsKeys];        // position of each row, -1 = none
+    float rel[kWsKeys];      // modified scores: position less pos0, for the distance bias
 };
 
 // the barriers follow the stages' records: whole 16-byte records keep them aligned
@@ -190,6 +191,17 @@ __device__ __forceinline__ float2 ws_ex2_pair(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ float ws_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float ws_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // try_wait with a suspend-time hint: a thread whose phase is not complete
 // sleeps until it completes (or the hint, 0.1 ms, runs out) instead of coming
 // back to re-issue the test, which would take issue slots from the softmax warps
@@ -217,10 +229,16 @@ __device__ __forceinline__ bool ws_wait(uint64_t* bar, uint32_t parity, volatile
 
 }  // namespace
 
-template <int D, bool READ, bool Q8>
+// SCORE: scores with modifiers (p.score; no read-time RoPE): q is staged
+// unscaled, the softmax warps apply scale, cap and bias to the scores; keys
+// below every start of the CTA's tokens are absent, tiles of none but these
+// are not loaded, and a GQA group need not divide 128 (rows past the last
+// whole token stay empty).
+template <int D, bool READ, bool Q8, bool SCORE>
 __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     prefill_ws_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ PrefillMaps maps) {
     static_assert(!Q8 || D >= 128, "INT8 rows are whole 128-code boxes");
+    static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
     using S = WsShape<D>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
     extern __shared__ unsigned char ws_raw[];
@@ -302,6 +320,23 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         // ============================ producer ==============================
         int idx = 0;
         bool ok = true;
+        // SCORE: the lowest and highest start of the CTA's tokens
+        int smin = 0, smax = 0;
+        if constexpr (SCORE) {
+            if (p.score.start && i_last >= i0) {
+                smin = 0x7fffffff;
+                for (int i = i0 + lane; i <= i_last; i += 32) {
+                    const int v = max(0, p.score.start[(long long)b * p.T + i]);
+                    smin = min(smin, v);
+                    smax = max(smax, v);
+                }
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) {
+                    smin = min(smin, __shfl_xor_sync(0xffffffffu, smin, off));
+                    smax = max(smax, __shfl_xor_sync(0xffffffffu, smax, off));
+                }
+            }
+        }
         // next stage: wait until the MMA thread is done with its last tile
         auto acquire = [&]() -> int {
             const int s = idx % NST;
@@ -316,11 +351,11 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         // with that slot (p = s for sinks), or none.
         auto slot_pos = [&](int s, bool sinks_only, bool no_sinks) -> int {
             if (s >= C || t0 < 0) return -1;
-            if (s < p.sinks) return (no_sinks || s > t0) ? -1 : s;
+            if (s < p.sinks) return (no_sinks || s > t0 || (SCORE && s < smin)) ? -1 : s;
             if (sinks_only || s > t0) return -1;
             const int q = t0 - (int)((unsigned)(t0 - s) % (unsigned)p.window);
             // window keys any token of the CTA can see
-            return q >= t_lo - p.window + 1 ? q : -1;
+            return q >= t_lo - p.window + 1 && (!SCORE || q >= smin) ? q : -1;
         };
         auto issue_slot_tile = [&](int slot0, int kind) {
             const int s = acquire();
@@ -331,6 +366,10 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 const int r = lane + 32 * u;
                 const int q = slot_pos(slot0 + r, kind == kTileSink, READ && kind == kTileSlot);
                 meta[s].pos[r] = q;
+                if constexpr (SCORE) {
+                    meta[s].rel[r] = (float)(q - pos0);
+                    partial |= q >= 0 && q < smax;
+                }
                 absent |= q < 0;
                 // seen by every row of the CTA: a sink, or in the window of its
                 // latest token (every key here is below the chunk's first position)
@@ -392,6 +431,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 const int nlb = t0 / bs + 1;
                 const int32_t* trow = p.table + (long long)b * p.maxb;
                 int fill = 0, s = 0;
+                int low = 0;                              // SCORE: the tile's lowest position
                 for (int base = 0; base < nlb && ok; base += 32) {
                     const int lb = base + lane;
                     int phys = lb < nlb ? __ldcg(trow + lb) : -1;
@@ -401,19 +441,24 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     }
                     bool att = phys >= 0;
                     if (att && p.valid) att = (__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u;
+                    if (SCORE && (long long)(lb + 1) * bs <= smin) att = false;
                     unsigned m = __ballot_sync(0xffffffffu, att);
                     while (m && ok) {
                         const int src = __ffs(m) - 1;
                         m &= m - 1;
                         const int ph = __shfl_sync(0xffffffffu, phys, src);
                         const int blb = base + src;
-                        if (fill == 0) s = acquire();
+                        if (fill == 0) {
+                            s = acquire();
+                            low = blb * bs;
+                        }
                         if (!ok) break;
                         if (Q8 && fill == 0 && lane == 0) meta[s].sc_off = 0;   // block rows: multiples of 8
                         // rows of this block: positions blb * bs + r, keys up to t0
                         for (int r = lane; r < bs; r += 32) {
                             const int q = blb * bs + r;
-                            meta[s].pos[fill * bs + r] = q <= t0 ? q : -1;
+                            meta[s].pos[fill * bs + r] = q <= t0 && (!SCORE || q >= smin) ? q : -1;
+                            if constexpr (SCORE) meta[s].rel[fill * bs + r] = (float)(q - pos0);
                         }
                         if (lane == 0) {
                             const int row = (int)(((long long)ph * p.Hkv + h) * bs);
@@ -445,9 +490,10 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                             __syncwarp();
                             if (lane == 0) {
                                 meta[s].kind = kTileBlocks;
-                                meta[s].any_absent = t0 < blb * bs + bs - 1;   // the last block's rows past t0
+                                // the last block's rows past t0 (SCORE: and rows below every start)
+                                meta[s].any_absent = t0 < blb * bs + bs - 1 || (SCORE && low < smin);
                                 // every cached key precedes every token of the chunk
-                                meta[s].mask = meta[s].any_absent ? kMaskKeys : kMaskNone;
+                                meta[s].mask = (meta[s].any_absent || (SCORE && low < smax)) ? kMaskKeys : kMaskNone;
                                 mbar_arrive(&bars->full[s]);
                             }
                             fill = 0;
@@ -470,6 +516,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             // the chunk's own rows, tokens 0 .. i_last, 64 to a tile
             for (int i_s = 0; i_s <= i_last && ok; i_s += kWsKeys) {
+                if (SCORE && pos0 + min(i_s + kWsKeys - 1, i_last) < smin) continue;   // no token sees this tile
                 const int s = acquire();
                 if (!ok) break;
                 int absent = 0;
@@ -477,8 +524,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 for (int u = 0; u < 2; ++u) {
                     const int r = lane + 32 * u;
                     const int i = i_s + r;
-                    const int q = (i <= i_last && pos0 + i >= 0) ? pos0 + i : -1;
+                    const int q = (i <= i_last && pos0 + i >= 0 && (!SCORE || pos0 + i >= smin)) ? pos0 + i : -1;
                     meta[s].pos[r] = q;
+                    if constexpr (SCORE) meta[s].rel[r] = (float)i;
                     absent |= q < 0;
                 }
                 absent = __any_sync(0xffffffffu, absent);
@@ -801,6 +849,14 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         write_q(sink_tile ? min(row_t, C - 1) : row_t);
 
         float m_run = -INFINITY, l_run = 0.f;
+        // SCORE: the row's slope (base 2), its bias at distance row_i, and its start
+        float slope2 = 0.f, bias0 = 0.f;
+        int start = 0;
+        if constexpr (SCORE) {
+            if (row_ok && p.score.slopes) slope2 = p.score.slopes[row_h] * 1.4426950408889634f;
+            bias0 = -slope2 * (float)row_i;
+            if (row_ok && p.score.start) start = max(0, p.score.start[(long long)b * p.T + row_i]);
+        }
         int j = 0;
         bool ok = true;
         for (;; ++j) {
@@ -827,6 +883,22 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             // masks: a key at position q is seen by the row at t iff q <= t and
             // (paged, or a sink q < S, or q in the window t - W + 1 .. t)
             const int mode = meta[s].mask;
+            if constexpr (SCORE) {
+                if (p.score.cap2 > 0.f) {
+                    // cap tanh(x / cap) = cap - 2 cap / (e^(2 x / cap) + 1), base 2
+#pragma unroll
+                    for (int k = 0; k < kWsKeys; ++k)
+                        sv[k] = fmaf(-2.f * p.score.cap2, ws_rcp(ws_ex2(sv[k] * p.score.cap_in) + 1.f), p.score.cap2);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] *= p.score.scale2;
+                }
+                if (p.score.slopes) {
+                    // slope (p - t) = slope (p - pos0) - slope (t - pos0)
+#pragma unroll
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] += fmaf(slope2, meta[s].rel[k], bias0);
+                }
+            }
             if (!row_ok) {
 #pragma unroll
                 for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
@@ -834,7 +906,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 // the chunk's own rows: key k at kbase + k is seen iff 0 <= kbase + k <= t
                 // (the window holds every chunk token, the chunk being no longer than it)
                 const int kb = meta[s].kbase;
-                const int klo = -kb, khi = row_t - kb;
+                const int klo = (SCORE ? start : 0) - kb, khi = row_t - kb;
 #pragma unroll
                 for (int k = 0; k < kWsKeys; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
             } else if (mode == kMaskKeys) {
@@ -843,6 +915,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     const int q = meta[s].pos[k];
                     bool allowed = q >= 0 && q <= row_t;
                     if (!paged) allowed = allowed && (q < p.sinks || q > row_t - p.window);
+                    if constexpr (SCORE) allowed = allowed && q >= start;
                     sv[k] = allowed ? sv[k] : -INFINITY;
                 }
             }
@@ -949,7 +1022,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TmemCols) : "memory");
 }
 
-template <int D, bool READ, bool Q8>
+template <int D, bool READ, bool Q8, bool SCORE>
 static cudaError_t launch_prefill_ws_t(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
     constexpr int kSmem = ws_smem_bytes<D>();
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -959,22 +1032,25 @@ static cudaError_t launch_prefill_ws_t(const PrefillParams& p, const PrefillMaps
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(prefill_ws_kernel<D, READ, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(prefill_ws_kernel<D, READ, Q8, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
     const int tok = kWsRows / p.G * WsShape<D>::NQ;
     dim3 grid((p.T + tok - 1) / tok, p.Hkv, p.B);
-    prefill_ws_kernel<D, READ, Q8><<<grid, WsShape<D>::Threads, kSmem, stream>>>(p, maps);
+    prefill_ws_kernel<D, READ, Q8, SCORE><<<grid, WsShape<D>::Threads, kSmem, stream>>>(p, maps);
     return cudaGetLastError();
 }
 
-cudaError_t launch_prefill_ws(int head_dim, bool q8, const PrefillParams& p, const PrefillMaps& maps,
+cudaError_t launch_prefill_ws(int head_dim, bool q8, bool scored, const PrefillParams& p, const PrefillMaps& maps,
                               cudaStream_t stream) {
-    if (p.G < 1 || kWsRows % p.G) return cudaErrorInvalidValue;
+    if (p.G < 1 || p.G > kWsRows || (!scored && kWsRows % p.G)) return cudaErrorInvalidValue;
     const bool rd = p.rope == kRopeRead;
-#define KVC_WS(DD, RD, Q) \
-    if (head_dim == DD && rd == RD && q8 == Q) return launch_prefill_ws_t<DD, RD, Q>(p, maps, stream);
+    if (scored && rd) return cudaErrorInvalidValue;
+#define KVC_WS(DD, RD, Q)                                                                 \
+    if (head_dim == DD && rd == RD && q8 == Q)                                            \
+        return (scored && !RD) ? launch_prefill_ws_t<DD, false, Q, !RD>(p, maps, stream)  \
+                               : launch_prefill_ws_t<DD, RD, Q, false>(p, maps, stream);
     KVC_WS(64, false, false) KVC_WS(64, true, false)
     KVC_WS(128, false, false) KVC_WS(128, true, false) KVC_WS(128, false, true) KVC_WS(128, true, true)
     KVC_WS(256, false, false) KVC_WS(256, true, false) KVC_WS(256, false, true) KVC_WS(256, true, true)

@@ -78,6 +78,8 @@ def attend(q, k, v, dist, see, scale, cap=0.0, slopes=None):
     """q [T, H, D], k / v [L, KV, D] float64, dist / see [T, L]; a row that sees nothing gives 0."""
     T, H, D = q.shape
     G = H // k.shape[1]
+    if not T or not k.shape[0]:
+        return torch.zeros_like(q), q.new_zeros(H, T, k.shape[0])
     k, v = k.repeat_interleave(G, 1), v.repeat_interleave(G, 1)
     s = torch.einsum("thd,lhd->htl", q, k) * scale
     if cap:

@@ -39,7 +39,7 @@ def _struct_fields(name):
 
 def test_structs_match_the_header(kvc):
     width = {"int32_t": ctypes.c_int32, "float": ctypes.c_float}
-    for name, cls in (("kvc_rotary", kvc.KvcRotary), ("kvc_qk", kvc.KvcQk)):
+    for name, cls in (("kvc_rotary", kvc.KvcRotary), ("kvc_qk", kvc.KvcQk), ("kvc_score", kvc.KvcScore)):
         fields = _struct_fields(name)
         assert len(fields) == len(cls._fields_), name
         for text, (field, t) in zip(fields, cls._fields_):
@@ -139,3 +139,36 @@ def test_append_qk_binding_checks(kvc):
         kvc.append_qk(d, x, 0, x[0], x, x, x, x, qk)
     with pytest.raises(ValueError, match="CUDA"):
         kvc.make_qk(d, q_weight=torch.zeros(128, dtype=torch.bfloat16))
+
+
+def test_scored_refusals(kvc):
+    L = kvc.lib()
+    none = kvc.KvcScore(None, None, 0.0)
+
+    def decode(score=none, cache=A, q=A, pos=A, out=A, layer=0, table=None, **kw):
+        d = _desc(kvc, **kw)
+        return L.kvc_decode_attention_scored(ctypes.byref(d), cache, layer, q, pos, table, None,
+                                             ctypes.byref(score) if score is not None else None, out, A,
+                                             kvc.workspace_bytes(d), None)
+
+    def prefill(score=none, T=16, table=None, n_ws=1 << 40, **kw):
+        d = _desc(kvc, **kw)
+        return L.kvc_prefill_scored(ctypes.byref(d), A, 0, A, A, A, T, A, table, None,
+                                    ctypes.byref(score) if score is not None else None, A, A, n_ws, None)
+
+    for call in (decode, prefill):
+        assert call(score=None) == kvc.KVC_ERR_NULL
+        for cap in (-1.0, float("nan"), float("inf")):
+            assert call(score=kvc.KvcScore(None, None, cap)) == kvc.KVC_ERR_ARG
+        assert call(score=kvc.KvcScore(A + 2, None, 0.0)) == kvc.KVC_ERR_ALIGN
+        assert call(score=kvc.KvcScore(None, A + 1, 0.0)) == kvc.KVC_ERR_ALIGN
+        assert call(rope="read_time") == kvc.KVC_ERR_UNSUPPORTED
+    assert decode(q=None) == kvc.KVC_ERR_NULL and decode(out=A + 4) == kvc.KVC_ERR_ALIGN
+    assert decode(layer=2) == kvc.KVC_ERR_ARG
+    paged = dict(layout="paged", window=0, block_size=16, num_blocks=10, max_blocks_per_seq=4)
+    assert decode(**paged) == kvc.KVC_ERR_NULL and prefill(**paged) == kvc.KVC_ERR_NULL
+    assert prefill(dtype="f32") == kvc.KVC_ERR_UNSUPPORTED
+    assert prefill(T=101) == kvc.KVC_ERR_UNSUPPORTED                       # longer than the window
+    assert prefill(q_heads=258) == kvc.KVC_ERR_UNSUPPORTED                 # a group of 129 heads
+    assert prefill(**dict(paged, block_size=12), table=A) == kvc.KVC_ERR_UNSUPPORTED
+    assert prefill(T=0) == kvc.KVC_ERR_ARG and prefill(n_ws=64) == kvc.KVC_ERR_WORKSPACE
