@@ -315,6 +315,27 @@ KVC_API int kvc_decode_attention_scored(const kvc_desc* d, const void* cache, in
                                         const kvc_score* score, void* out, void* workspace, size_t workspace_bytes,
                                         void* stream);
 
+/* kvc_decode_attention for a PAGED batch whose groups of sequences share a
+ * prefix (kvc_block_share): the shared keys and values are read and scored once
+ * for a whole group.  The results are kvc_decode_attention's, whatever the
+ * groups are (to the rounding of another order of sums): the call itself finds
+ * how many leading blocks the tables of a group's sequences have in common,
+ * among those that lie wholly at positions <= t for each of them.
+ *   group      [batch] int32: sequences with the same value 0 .. batch - 1 form
+ *              a group; below 0: alone.  batch or more sets KVC_DEV_BAD_ENTRY
+ *              (the sequence counts as alone).
+ *   workspace  kvc_shared_workspace_bytes(d) bytes (0 if `d` is refused), set
+ *              up by kvc_workspace_init; it serves the other decode calls too.
+ * bf16 caches, blocks whose size is a multiple of 8 and divides 64 or is a
+ * multiple of 64, at most 128 q heads for each kv head, else
+ * KVC_ERR_UNSUPPORTED; rope NONE or BAKED.  The shared part runs on the tcgen05
+ * tensor cores, one CTA per SM that holds its tensor memory while it runs. */
+KVC_API size_t kvc_shared_workspace_bytes(const kvc_desc* d);
+KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                        const int32_t* pos, const int32_t* group, const int32_t* block_table,
+                                        const uint32_t* valid_bits, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 /* One decode step: kvc_append of the token at pos[b] (n_new = 1), then
  * kvc_decode_attention at pos[b], with the same arguments and results as
  * that pair of calls.  For bf16 and INT8 caches, RING / SINK_RING and PAGED

@@ -40,6 +40,7 @@ ABI_FUNCTIONS = (
     "kvc_pager_create", "kvc_pager_destroy", "kvc_pager_plan", "kvc_pager_evict", "kvc_pagein_issue",
     "kvc_pagein_commit", "kvc_prefill_workspace_bytes", "kvc_prefill",
     "kvc_rotary_init", "kvc_append_qk", "kvc_decode_attention_scored", "kvc_prefill_scored",
+    "kvc_shared_workspace_bytes", "kvc_decode_attention_shared",
 )
 
 
@@ -124,6 +125,9 @@ def lib() -> ctypes.CDLL:
         L.kvc_pagein_issue.argtypes = [vp, dp, vp, vp, i32, vp, vp, vp, vp]
         L.kvc_pagein_commit.argtypes = [vp, dp, i32, i32, vp, vp, vp, vp, vp]
         L.kvc_rotary_init.argtypes = [vp]
+        L.kvc_shared_workspace_bytes.argtypes = [dp]
+        L.kvc_shared_workspace_bytes.restype = sz
+        L.kvc_decode_attention_shared.argtypes = [dp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_decode_attention_scored.argtypes = [dp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_prefill_scored.argtypes = [dp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_append_qk.argtypes = [dp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -131,6 +135,7 @@ def lib() -> ctypes.CDLL:
         L.kvc_strerror.restype = ctypes.c_char_p
         for name in ABI_FUNCTIONS:
             if name not in ("kvc_cache_bytes", "kvc_workspace_bytes", "kvc_prefill_workspace_bytes", "kvc_strerror",
+                            "kvc_shared_workspace_bytes",
                             "kvc_pager_create", "kvc_pager_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -447,6 +452,44 @@ def decode_attention_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
                                              _ptr(block_table), _ptr(valid_bits), ctypes.byref(score), _ptr(out),
                                              _ptr(workspace), workspace.numel(), _stream(stream)),
            "kvc_decode_attention_scored")
+    return out
+
+
+def shared_workspace_bytes(d: KvcDesc) -> int:
+    return int(lib().kvc_shared_workspace_bytes(ctypes.byref(d)))
+
+
+def alloc_shared_workspace(d: KvcDesc, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for kvc_decode_attention_shared (also a decode workspace)."""
+    n = shared_workspace_bytes(d)
+    if n == 0:
+        raise KvcError(KVC_ERR_DESC, "kvc_shared_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_attention_shared(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
+                            group: torch.Tensor, workspace: torch.Tensor, block_table: torch.Tensor,
+                            valid_bits: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """kvc_decode_attention_shared: decode_attention of a paged batch; the sequences of a group (int32 [batch],
+    below 0: alone) share leading blocks, whose keys and values are read once for the group."""
+    dt = desc_dtype(d)
+    _need_cache(d, cache)
+    _need(q, "q", dt, d.batch * d.q_heads * d.head_dim)
+    _need(pos, "pos", torch.int32, d.batch)
+    _need(group, "group", torch.int32, d.batch)
+    _need(workspace, "workspace", torch.uint8)
+    _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
+    if valid_bits is not None:
+        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
+    if out is None:
+        out = torch.empty((d.batch, d.q_heads, d.head_dim), dtype=dt, device=q.device)
+    _need(out, "out", dt, d.batch * d.q_heads * d.head_dim)
+    _on_current_device(cache, q, pos, group, workspace, block_table, valid_bits, out)
+    _check(lib().kvc_decode_attention_shared(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(pos),
+                                             _ptr(group), _ptr(block_table), _ptr(valid_bits), _ptr(out),
+                                             _ptr(workspace), workspace.numel(), _stream(stream)),
+           "kvc_decode_attention_shared")
     return out
 
 

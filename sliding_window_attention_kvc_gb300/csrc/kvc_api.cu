@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "kvc_host.h"
+#include "kvc_shared.h"
 
 namespace kvc {
 
@@ -192,7 +193,8 @@ int encode_q8_code_map(const kvc_desc* d, const Geo& g, const void* cache, int r
 }
 
 // Paged caches, for the warp-specialised prefill: {column, row, K|V, layer}
-// with boxes of one block (bs rows) of K or of V, 64 columns.
+// with boxes of one block (of 64 rows, when its blocks are larger) of K or of
+// V, 64 columns.  The shared-prefix decode uses it too.
 int encode_block_map(const kvc_desc* d, const Geo& g, const void* cache, CUtensorMap* map) {
     const unsigned long long half_rows = (unsigned long long)g.half_elems / d->head_dim;
     if (half_rows >= (1ull << 31)) return KVC_ERR_UNSUPPORTED;
@@ -201,7 +203,7 @@ int encode_block_map(const kvc_desc* d, const Geo& g, const void* cache, CUtenso
     const cuuint64_t row_bytes = (cuuint64_t)d->head_dim * 2, half_bytes = half_rows * row_bytes;
     const cuuint64_t dims[4] = {(cuuint64_t)d->head_dim, half_rows, 2, (cuuint64_t)d->layers};
     const cuuint64_t strides[3] = {row_bytes, half_bytes, 2 * half_bytes};
-    const cuuint32_t box[4] = {64, (cuuint32_t)d->block_size, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(d->block_size < 64 ? d->block_size : 64), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -268,10 +270,41 @@ static int score_params(const kvc_desc* d, const kvc_score* sc, ScoreParams* out
     return KVC_OK;
 }
 
+// kvc_decode_attention_shared: what it adds to the decode workspace, after it.
+struct SharedLayout {
+    size_t head, groups, seq, seq_group, members, gmin, start, part_ml, part_o, total;
+    long long alt_rows;
+};
+static SharedLayout shared_layout(const kvc_desc* d, const Geo& g) {
+    SharedLayout l{};
+    const size_t B = (size_t)d->batch;
+    const int nq = shared_q_tiles(d->head_dim);
+    size_t off = align_up(ws_layout(d, g).total, 256);
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, 256);
+        return at;
+    };
+    l.head = take(sizeof(SharedHead));
+    l.groups = take((B / 2 + 1) * sizeof(SharedGroup));
+    l.seq = take(B * sizeof(int4));
+    l.seq_group = take(B * sizeof(int2));
+    l.members = take(B * 4);
+    l.gmin = take(B * 4);
+    l.start = take(B * 4);
+    // a column's rows, one partial for each share it meets (a share's first
+    // column aside, every column starts in its share)
+    l.alt_rows = (long long)B * d->q_heads + (long long)kSharedCtas * nq * 128;
+    l.part_ml = take((size_t)(nq * l.alt_rows) * 8);
+    l.part_o = take((size_t)(nq * l.alt_rows) * d->head_dim * 4);
+    l.total = off;
+    return l;
+}
+
 static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, const void* q, const void* k_new,
                        const void* v_new, const int32_t* pos, const int32_t* block_table,
                        const uint32_t* valid_bits, void* out, void* workspace, size_t workspace_bytes,
-                       void* stream, const kvc_score* score = nullptr) {
+                       void* stream, const kvc_score* score = nullptr, const int32_t* group = nullptr) {
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
@@ -282,7 +315,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     if (!aligned16(workspace)) return KVC_ERR_ALIGN;
     const bool paged = d->layout == KVC_LAYOUT_PAGED;
     const WorkspaceLayout w = ws_layout(d, g);
-    if (workspace_bytes < w.total) return KVC_ERR_WORKSPACE;
+    if (workspace_bytes < (group ? shared_layout(d, g).total : w.total)) return KVC_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
 
@@ -336,8 +369,50 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     // one paged sequence on the tensor-core kernel: its CTAs plan their own
     // shares from the block table and write the step's token themselves
     // (the CTAs bulk-copy the table and the valid words: 16-byte aligned buffers)
+    // shared prefixes: laid out before anything else is planned; the sequences'
+    // own blocks begin behind them
+    SharedParams sh{};
+    CUtensorMap sh_map;
+    if (group) {
+        if ((rc = encode_block_map(d, g, cache, &sh_map))) return rc;
+        const SharedLayout l = shared_layout(d, g);
+        sh.q = q;
+        sh.pos = pos;
+        sh.group = group;
+        sh.table = block_table;
+        sh.valid = valid_bits;
+        sh.err = p.err;
+        sh.ticket = p.counters + (size_t)d->batch * d->kv_heads * g.nsub;
+        sh.head = reinterpret_cast<SharedHead*>(ws + l.head);
+        sh.groups = reinterpret_cast<SharedGroup*>(ws + l.groups);
+        sh.seq = reinterpret_cast<int4*>(ws + l.seq);
+        sh.seq_group = reinterpret_cast<int2*>(ws + l.seq_group);
+        sh.members = reinterpret_cast<int32_t*>(ws + l.members);
+        sh.gmin = reinterpret_cast<int32_t*>(ws + l.gmin);
+        sh.start = reinterpret_cast<int32_t*>(ws + l.start);
+        sh.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+        sh.part_o = reinterpret_cast<float*>(ws + l.part_o);
+        sh.alt_rows = l.alt_rows;
+        sh.B = d->batch;
+        sh.Hq = d->q_heads;
+        sh.Hkv = d->kv_heads;
+        sh.G = g.G;
+        sh.bs = d->block_size;
+        sh.num_blocks = d->num_blocks;
+        sh.maxb = d->max_blocks_per_seq;
+        sh.layer = layer;
+        sh.tq = 128 / g.G;
+        sh.mq = sh.tq * shared_q_tiles(d->head_dim);
+        sh.ctas = kSharedCtas;
+        sh.rope = d->rope;
+        sh.scale2 = p.q_scale;
+        for (int i = 0; i < d->head_dim / 2; ++i) sh.theta[i] = p.theta[i];
+        if (launch_shared_plan(sh, s) != cudaSuccess) return KVC_ERR_CUDA;
+        p.no_combine = 1;
+    }
+    const int32_t* const start = group ? sh.start : sp.start;
     // (a start is left to the planning kernel, which drops the blocks below it)
-    p.self_plan = (paged && !sp.start && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
+    p.self_plan = (paged && !start && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
                    (d->num_blocks + 31) / 32 <= kSelfPlanValidWords && aligned16(block_table) &&
                    (!valid_bits || aligned16(valid_bits))) ? 1 : 0;
     if (p.self_plan) {
@@ -351,7 +426,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         pp.pos = pos;
         pp.table = block_table;
         pp.valid = valid_bits;
-        pp.start = sp.start;
+        pp.start = start;
         pp.err = p.err;
         pp.seq_off = reinterpret_cast<long long*>(ws + w.plan_acc);
         pp.seq_rows = reinterpret_cast<int32_t*>(ws + w.plan_acc + (size_t)d->batch * 8);
@@ -403,10 +478,25 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         p.cta_items = pp.cta_items;
     }
     const bool rd = d->rope == KVC_ROPE_READ_INCACHE;
+    if (group && launch_shared_prefix(d->head_dim, sh, sh_map, s) != cudaSuccess) return KVC_ERR_CUDA;
     if (d->dtype != KVC_F32) {
         if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, score != nullptr, p, maps, grid, s) !=
             cudaSuccess)
             return KVC_ERR_CUDA;
+        if (group) {
+            SharedDecode dp{};
+            dp.part_ml = p.part_ml;
+            dp.part_o = p.part_o;
+            dp.seq_rows = p.seq_rows;
+            dp.counters = p.counters;
+            dp.refs = p.refs;
+            dp.out = out;
+            dp.num_blocks = d->num_blocks;
+            dp.nsplit = p.nsplit;
+            dp.max_items = p.max_items;
+            dp.ncounters = d->kv_heads * g.nsub;
+            if (launch_shared_combine(d->head_dim, sh, dp, s) != cudaSuccess) return KVC_ERR_CUDA;
+        }
         return KVC_OK;
     }
     if (launch_decode(d->dtype, d->head_dim, g.GH, paged, rd, score != nullptr, p, grid, s) != cudaSuccess)
@@ -682,6 +772,34 @@ KVC_API int kvc_decode_attention_scored(const kvc_desc* d, const void* cache, in
     if (!score) return KVC_ERR_NULL;
     return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
                        workspace_bytes, stream, score);
+}
+
+// What kvc_decode_attention_shared takes of a descriptor.
+static int shared_desc(const kvc_desc* d, const Geo& g) {
+    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if (d->dtype != KVC_BF16 || g.G > 128 || d->block_size % 8 ||
+        (d->block_size < 64 ? 64 % d->block_size : d->block_size % 64) || (long long)d->batch * d->q_heads > 0x7fffffffLL)
+        return KVC_ERR_UNSUPPORTED;
+    return KVC_OK;
+}
+
+KVC_API size_t kvc_shared_workspace_bytes(const kvc_desc* d) {
+    Geo g;
+    if (check_desc(d, &g) != KVC_OK || shared_desc(d, g) != KVC_OK) return 0;
+    return shared_layout(d, g).total;
+}
+
+KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                        const int32_t* pos, const int32_t* group, const int32_t* block_table,
+                                        const uint32_t* valid_bits, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if ((rc = shared_desc(d, g))) return rc;
+    if (!group) return KVC_ERR_NULL;
+    return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
+                       workspace_bytes, stream, nullptr, group);
 }
 
 KVC_API int kvc_decode_attention(const kvc_desc* d, const void* cache, int32_t layer, const void* q,

@@ -2163,6 +2163,7 @@ cudaError_t launch_decode_mma_t(const DecodeParams& p, const KvTensorMaps& maps,
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p, maps);
     if (e != cudaSuccess) return e;
+    if (p.no_combine) return cudaSuccess;
     cudaLaunchConfig_t ccfg = {};
     ccfg.gridDim = dim3(p.B, p.Hkv * p.nsub, D / (narrow ? 16 : kWide));
     ccfg.blockDim = dim3(kCombineThreads);

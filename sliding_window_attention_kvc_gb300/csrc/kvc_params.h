@@ -124,6 +124,7 @@ struct DecodeParams {
     float theta_f[kMaxHalfDim];     // RoPE frequencies, fp32 (small in-tile angles)
     unsigned long long theta[kMaxHalfDim];   // RoPE frequencies as turns, fixed point: theta_i / (2 pi) * 2^64
     ScoreParams score;          // kvc_decode_attention_scored
+    int no_combine;             // the caller joins the partials itself (kvc_decode_attention_shared)
 };
 
 struct PlanParams {

@@ -1,0 +1,898 @@
+// kvc_decode_attention_shared: decode attention of a paged batch whose groups
+// of sequences share a prefix (the same physical blocks at the head of their
+// tables).  softmax splits over any partition of the keys into partial results
+// (m, l, o), so the shared keys are scored once for a whole group -- the rows
+// of one matrix product are its members' q heads of a kv head -- and each
+// sequence's own keys by the ordinary decode kernel; a combine kernel joins
+// them:  M = max m_i,  out = sum o_i 2^(m_i - M) / sum l_i 2^(m_i - M).
+//
+//   shared_plan_kernel    one CTA per sequence: its place in its group, and how
+//                         many leading blocks its table shares with the first
+//                         member's; the last CTA to finish (an atomic ticket,
+//                         no waiting) takes each group's minimum and lays the
+//                         work out.
+//   (plan_rows_kernel)    the blocks behind the shared ones, per sequence.
+//   shared_prefix_kernel  the shared keys, on tcgen05 (below).
+//   (decode_mma_kernel)   the rest.
+//   shared_combine_kernel one warp per (sequence, q head).
+//
+// Prefix work.  A column is (group, kv head, up to NQ x 128 rows of members x q
+// heads); its keys are cut into tiles of 64.  All tiles of all columns, laid end
+// to end, are split into nearly equal contiguous shares, one per CTA (one CTA per SM);
+// the part of a column in a share is a segment and leaves one partial per row.
+// What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for 4 x
+// 64 x 128 x D flops a Q tile, so up to one Q tile the bytes bound, beyond it
+// the softmax.
+// Rows that are never there (members x heads below 128) cost nothing but
+// tensor-core time.  A column of one Q tile gives both softmax warpgroups the
+// same rows and alternate tiles, each with sums of its own (two partials): the
+// latency of one tile's softmax, which a single warpgroup would wait out, is
+// what a CTA with few rows spends its time on.
+#include <atomic>
+
+#include "kvc_decode.cuh"
+#include "kvc_shared.h"
+#include "kvc_tc.cuh"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kShPlanThreads = 256;
+constexpr int kShSoftmax0 = 4;              // first softmax warp
+constexpr float kShLazy = 8.f;
+
+__device__ __forceinline__ void sh_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void sh_pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+// Sums of three counts and a minimum over the CTA (every thread gets them).
+struct ShScan {
+    int below, rank, n, leader;
+};
+__device__ __forceinline__ ShScan sh_reduce(ShScan v, ShScan* s_w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        v.below += __shfl_xor_sync(0xffffffffu, v.below, off);
+        v.rank += __shfl_xor_sync(0xffffffffu, v.rank, off);
+        v.n += __shfl_xor_sync(0xffffffffu, v.n, off);
+        v.leader = min(v.leader, __shfl_xor_sync(0xffffffffu, v.leader, off));
+    }
+    if (lane == 0) s_w[warp] = v;
+    __syncthreads();
+    ShScan r = s_w[0];
+    for (int w = 1; w < kShPlanThreads / 32; ++w) {
+        r.below += s_w[w].below;
+        r.rank += s_w[w].rank;
+        r.n += s_w[w].n;
+        r.leader = min(r.leader, s_w[w].leader);
+    }
+    __syncthreads();
+    return r;
+}
+
+__global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __grid_constant__ SharedParams p) {
+    __shared__ ShScan s_w[kShPlanThreads / 32];
+    __shared__ int s_common, s_last;
+    __shared__ long long s_u[kShPlanThreads / 32], s_r[kShPlanThreads / 32];
+    __shared__ int s_g[kShPlanThreads / 32];
+    const int tid = threadIdx.x, b = blockIdx.x;
+    sh_pdl_wait();
+    sh_pdl_launch();
+    // this sequence's place: the members of lower group ids before its group,
+    // its rank in the group, the group's size and first member
+    const int gid = p.group[b];
+    const bool grouped = gid >= 0 && gid < p.B;
+    if (gid >= p.B && tid == 0) set_error(p.err, 0x10u /* KVC_DEV_BAD_ENTRY */);
+    ShScan c{0, 0, 0, p.B};
+    if (grouped) {
+        for (int o = tid; o < p.B; o += kShPlanThreads) {
+            const int og = p.group[o];
+            if (og >= 0 && og < gid) ++c.below;
+            if (og == gid) {
+                ++c.n;
+                if (o < b) ++c.rank;
+                c.leader = min(c.leader, o);
+            }
+        }
+    }
+    c = sh_reduce(c, s_w);
+    // leading blocks wholly at positions <= t here and for the first member,
+    // whose entries equal the first member's
+    if (grouped && c.n > 1) {
+        auto full_blocks = [&](int s) {
+            const int t = clamp_paged_t(p.pos[s], p.maxb, p.bs);
+            return t < 0 ? 0 : (int)(((long long)t + 1) / p.bs);
+        };
+        const int nb = min(full_blocks(b), full_blocks(c.leader));
+        if (tid == 0) s_common = nb;
+        __syncthreads();
+        const int32_t* mine = p.table + (long long)b * p.maxb;
+        const int32_t* lead = p.table + (long long)c.leader * p.maxb;
+        int first = nb;
+        for (int i = tid; i < nb; i += kShPlanThreads)
+            if (mine[i] != lead[i]) {
+                first = i;
+                break;
+            }
+        if (first < nb) atomicMin(&s_common, first);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.seq[b] = make_int4(grouped && c.n > 1 ? c.below : -1, c.rank, c.n, grouped && c.n > 1 ? s_common : 0);
+        if (grouped) p.members[c.below + c.rank] = b;
+        __threadfence();
+        s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // the last CTA: each group's common blocks, kept at its place in the member list
+    for (int o = tid; o < p.B; o += kShPlanThreads) p.gmin[o] = 0x7fffffff;
+    __syncthreads();
+    for (int o = tid; o < p.B; o += kShPlanThreads) {
+        const int4 s = __ldcg(&p.seq[o]);
+        if (s.x >= 0) atomicMin(&p.gmin[s.x], s.w);
+    }
+    __syncthreads();
+    // groups with something to share, in member-list order: their units (tiles of
+    // every column) and partial rows before them
+    long long run_u = 0, run_r = 0;
+    int run_g = 0;
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int base = 0; base < p.B; base += kShPlanThreads) {
+        const int o = base + tid;
+        // place o of the member list begins a group iff its member has rank 0
+        int4 s = make_int4(-1, 0, 0, 0);
+        int lead = -1;
+        if (o < p.B && __ldcg(&p.gmin[o]) != 0x7fffffff) {
+            lead = __ldcg(&p.members[o]);
+            s = __ldcg(&p.seq[lead]);
+        }
+        int common = lead >= 0 ? __ldcg(&p.gmin[o]) : 0;
+        const bool real = lead >= 0 && common > 0;
+        SharedGroup g{};
+        long long u = 0, r = 0;
+        if (real) {
+            g.n = s.z;
+            g.off = o;
+            g.leader = lead;
+            g.rows = common * p.bs;
+            g.kt = (g.rows + kWsKeys - 1) / kWsKeys;
+            g.mt = (g.n + p.mq - 1) / p.mq;
+            u = (long long)p.Hkv * g.mt * g.kt;
+            r = (long long)p.Hkv * g.n * p.G;
+        }
+        long long iu = u, ir = r;
+        int ig = real ? 1 : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long a = __shfl_up_sync(0xffffffffu, iu, off), bb = __shfl_up_sync(0xffffffffu, ir, off);
+            const int gg = __shfl_up_sync(0xffffffffu, ig, off);
+            if (lane >= off) {
+                iu += a;
+                ir += bb;
+                ig += gg;
+            }
+        }
+        if (lane == 31) {
+            s_u[warp] = iu;
+            s_r[warp] = ir;
+            s_g[warp] = ig;
+        }
+        __syncthreads();
+        long long cu = run_u, cr = run_r;
+        int cg = run_g;
+        for (int w = 0; w < kShPlanThreads / 32; ++w) {
+            if (w < warp) {
+                cu += s_u[w];
+                cr += s_r[w];
+                cg += s_g[w];
+            }
+            run_u += s_u[w];
+            run_r += s_r[w];
+            run_g += s_g[w];
+        }
+        if (real) {
+            g.units0 = cu + iu - u;
+            g.rows0 = cr + ir - r;
+            p.groups[cg + ig - 1] = g;
+            p.gmin[o] = cg + ig - 1;          // its index, for the members below
+        } else if (o < p.B) {
+            p.gmin[o] = -1;
+        }
+        __syncthreads();
+    }
+    // each sequence's group and the position its own keys begin at
+    for (int o = tid; o < p.B; o += kShPlanThreads) {
+        const int4 s = __ldcg(&p.seq[o]);
+        const int gi = s.x >= 0 ? p.gmin[s.x] : -1;
+        p.seq_group[o] = make_int2(gi, s.y);
+        p.start[o] = gi >= 0 ? p.groups[gi].rows : 0;
+    }
+    if (tid == 0) {
+        p.head->units = run_u;
+        p.head->ngroups = run_g;
+        p.head->shares = (int)min((long long)p.ctas, (run_u + kSharedMinTiles - 1) / kSharedMinTiles);
+        *p.ticket = 0u;                       // ready for the next call
+    }
+}
+
+// ---------------------------------------------------------------------------
+// prefix
+// ---------------------------------------------------------------------------
+template <int D>
+struct PxShape {
+    static constexpr int NQ = shared_q_tiles(D);
+    static constexpr int STAGES = D == 64 ? 6 : (D == 128 ? 4 : 2);
+    static constexpr int CB = D / 64;                          // 64-column blocks of a row
+    static constexpr int QBytes = kWsRows * D * 2;             // one Q tile
+    static constexpr int KVBlock = 2 * kWsKeys * 128;          // one column block of K and V
+    static constexpr int StageBytes = CB * KVBlock;
+    static constexpr int OffQ = 0;
+    static constexpr int OffStage = OffQ + NQ * QBytes;
+    static constexpr int OffMeta = OffStage + STAGES * StageBytes;
+    static constexpr int TmemCols = 512;
+    static constexpr int SCol0 = NQ * D;                       // S buffers after the O tiles
+    static_assert(NQ * D + NQ * 2 * kWsKeys <= TmemCols, "TMEM columns");
+    static constexpr int Threads = 32 * (kShSoftmax0 + 4 * NQ);
+};
+
+struct alignas(16) PxStageMeta {
+    unsigned long long present;     // rows of the tile that hold a key
+    unsigned long long pad;
+};
+
+struct PxBars {
+    uint64_t full[6], ready[6], empty[6];
+    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_ready[2], fin;
+    uint32_t tmem;
+    int abort;
+};
+
+template <int D>
+constexpr int px_smem_bytes() {
+    using S = PxShape<D>;
+    return S::OffMeta + S::STAGES * (int)sizeof(PxStageMeta) + (int)sizeof(PxBars) + 1024;
+}
+
+// One segment: tiles tile0 .. tile0 + nt - 1 of a column.
+struct PxSegment {
+    int h, m0, members, off, leader, rows;     // kv head, first member's rank and members, the group's list and prefix
+    int tile0, nt;
+    int alt;                                   // one Q tile's rows: the warpgroups take alternate tiles
+    long long row0;                            // partial row of the column's first row, before the share's own offset
+    __device__ __forceinline__ bool active(int i, int t) const { return !alt || (t & 1) == i; }
+    __device__ __forceinline__ int local(int t) const { return alt ? t >> 1 : t; }
+    __device__ __forceinline__ int tiles(int i) const { return alt ? (nt + 1 - i) >> 1 : nt; }
+};
+
+// The segment that begins at unit u of a share ending at hi (a whole warp's call).
+template <int D>
+__device__ __forceinline__ PxSegment px_segment(const SharedParams& p, int ngroups, long long u, long long hi) {
+    const int lane = threadIdx.x & 31;
+    int gi = 0;
+    for (int base = 0; base < ngroups; base += 32) {
+        const unsigned le = __ballot_sync(0xffffffffu, base + lane < ngroups && __ldcg(&p.groups[base + lane].units0) <= u);
+        if (le) gi = base + 31 - __clz(le);
+        if (le != 0xffffffffu) break;
+    }
+    const SharedGroup* g = p.groups + gi;
+    const int kt = __ldcg(&g->kt), mt = __ldcg(&g->mt), n = __ldcg(&g->n);
+    const long long v = u - __ldcg(&g->units0);
+    const int col = (int)(v / kt);
+    PxSegment s;
+    s.tile0 = (int)(v - (long long)col * kt);
+    s.nt = (int)min((long long)(kt - s.tile0), hi - u);
+    s.h = col / mt;
+    s.m0 = (col - s.h * mt) * p.mq;
+    s.members = min(p.mq, n - s.m0);
+    s.off = __ldcg(&g->off);
+    s.leader = __ldcg(&g->leader);
+    s.rows = __ldcg(&g->rows);
+    s.alt = PxShape<D>::NQ == 2 && s.members <= p.tq;
+    s.row0 = __ldcg(&g->rows0) + ((long long)s.h * n + s.m0) * p.G;
+    return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PxShape<D>::Threads, 1)
+    shared_prefix_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ CUtensorMap map) {
+    using S = PxShape<D>;
+    constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
+    extern __shared__ unsigned char px_raw[];
+    const uint32_t raw_u = smem_u32(px_raw);
+    unsigned char* sm = px_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
+    const uint32_t sm_u = smem_u32(sm);
+    PxStageMeta* meta = reinterpret_cast<PxStageMeta*>(sm + S::OffMeta);
+    PxBars* bars = reinterpret_cast<PxBars*>(sm + S::OffMeta + NST * sizeof(PxStageMeta));
+    volatile int* abort = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->ready[s], 64);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&bars->s_full[i][u], 1);
+                mbar_init(&bars->s_free[i][u], 4);
+            }
+            mbar_init(&bars->p_full[i], kWsRows);
+            mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->q_ready[i], kWsRows);
+        }
+        mbar_init(&bars->fin, 1);
+        bars->abort = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&map);
+    }
+    sh_pdl_wait();
+    sh_pdl_launch();
+    const int ngroups = __ldcg(&p.head->ngroups), shares = __ldcg(&p.head->shares);
+    const long long units = __ldcg(&p.head->units);
+    const int x = blockIdx.x;
+    if (x >= shares || units <= 0) return;           // (uniform: before the tensor memory is taken)
+    const long long lo = div_nonneg((long long)x * units, shares), hi = div_nonneg((long long)(x + 1) * units, shares);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem)),
+                     "r"(S::TmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    ws_fence_before();
+    __syncthreads();
+    ws_fence_after();
+    const uint32_t tmem = bars->tmem;
+    auto give_up = [&]() {
+        if (!*abort) {
+            bars->abort = 1;
+            set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+        }
+    };
+
+    if (warp == 0) {
+        // ============================ producer ==============================
+        int idx = 0;
+        bool ok = true;
+        const int bs = p.bs;
+        const int box = bs < kWsKeys ? bs : kWsKeys;            // rows of one copy
+        const int per = kWsKeys / box;                          // copies of a tile
+        for (long long u = lo; u < hi && ok;) {
+            const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
+            const int32_t* trow = p.table + (long long)sg.leader * p.maxb;
+            const int ncopy = (sg.rows + box - 1) / box;        // of the whole prefix
+            // 32 copies at a time, one per lane: 32 / per tiles
+            for (int t0 = 0; t0 < sg.nt && ok; t0 += 32 / per) {
+                const int cp = (sg.tile0 + t0) * per + lane;    // this lane's copy: rows cp * box ..
+                int row = -1;
+                if (cp < ncopy) {
+                    const int r0 = cp * box, lb = r0 / bs;
+                    const int phys = __ldcg(trow + lb);
+                    bool att = phys >= 0;
+                    if (phys >= p.num_blocks) {
+                        set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+                        att = false;
+                    }
+                    if (att && p.valid) att = (__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u;
+                    if (att) row = (int)(((long long)phys * p.Hkv + sg.h) * bs + (r0 - lb * bs));
+                }
+                const unsigned have = __ballot_sync(0xffffffffu, row >= 0);
+                for (int k = 0; k < 32 / per && t0 + k < sg.nt; ++k) {
+                    const int s = idx % NST;
+                    if (idx >= NST && !ws_wait(&bars->empty[s], ((idx / NST) - 1) & 1, abort)) {
+                        if (lane == 0) give_up();
+                        ok = false;
+                        break;
+                    }
+                    const unsigned mine = (have >> (k * per)) & ((per == 32) ? 0xffffffffu : ((1u << per) - 1u));
+                    const int j = lane - k * per;
+                    if (j >= 0 && j < per && row >= 0) {
+                        mbar_expect_tx(&bars->full[s], (uint32_t)(box * D * 4));
+                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes + j * box * 128;
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                            for (int kv = 0; kv < 2; ++kv)
+                                tma_load_4d(dst + cb * S::KVBlock + kv * kWsKeys * 128, &map, cb * 64, row, kv,
+                                            p.layer, &bars->full[s]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        unsigned long long present = 0;
+                        for (int c = 0; c < per; ++c)
+                            if ((mine >> c) & 1u)
+                                present |= (box == 64 ? ~0ull : ((1ull << box) - 1)) << (c * box);
+                        meta[s].present = present;
+                        mbar_arrive(&bars->full[s]);
+                    }
+                    ++idx;
+                }
+            }
+            u += sg.nt;
+        }
+        // never leave with copies landing in shared memory
+        if (!ok && lane == 0)
+            for (int k = (idx > NST ? idx - NST : 0); k < idx; ++k) mbar_wait(&bars->full[k % NST], (k / NST) & 1);
+    } else if (warp == 2 || warp == 3) {
+        // ============================ fix-up ===============================
+        // V rows without a key may hold anything: zero them
+        const int ft = tid - 64;
+        const int nt = (int)(hi - lo);
+        for (int j = 0; j < nt; ++j) {
+            const int s = j % NST;
+            if (!ws_wait(&bars->full[s], (j / NST) & 1, abort)) {
+                give_up();
+                break;
+            }
+            if (!((meta[s].present >> ft) & 1ull)) {
+                unsigned char* st = sm + S::OffStage + s * S::StageBytes + kWsKeys * 128 + ft * 128;
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch)
+                        *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(&bars->ready[s]);
+        }
+    } else if (warp == 1) {
+        // =========================== MMA issuer =============================
+        constexpr uint32_t kIdescS = ws_idesc(kWsRows, kWsKeys, 0);
+        constexpr uint32_t kIdescO = ws_idesc(kWsRows, D, 1);
+        constexpr int LA = NST >= 3 ? 2 : 1;           // tiles that S runs ahead of P V
+        bool ok = true;
+        int idx0 = 0;                                  // tiles of the segments before
+        int base[2] = {0, 0};                          // ... and of each Q tile
+        int loads[2] = {0, 0};                         // segments each Q tile was loaded for
+        for (long long u = lo; u < hi;) {
+            const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
+            if (lane == 0 && ok) {
+                for (int i = 0; i < NQ && ok; ++i)
+                    if (sg.tiles(i) > 0 && !ws_wait(&bars->q_ready[i], loads[i] & 1, abort)) ok = false;
+                auto issue_s = [&](int t) -> bool {
+                    const int s = (idx0 + t) % NST;
+                    if (!ws_wait(&bars->ready[s], ((idx0 + t) / NST) & 1, abort)) return false;
+                    for (int i = 0; i < NQ; ++i) {
+                        if (!sg.active(i, t)) continue;
+                        const int j = base[i] + sg.local(t);
+                        if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) return false;
+                        ws_fence_after();
+                        const uint32_t q_u = sm_u + S::OffQ + i * S::QBytes;
+                        const uint32_t k_u = sm_u + S::OffStage + s * S::StageBytes;
+                        const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t within = (ks & 3) * 32;
+                            ws_mma(d, ws_sdesc(q_u + (ks >> 2) * (kWsRows * 128) + within, 16, 1024),
+                                   ws_sdesc(k_u + (ks >> 2) * S::KVBlock + within, 16, 1024), kIdescS, ks > 0);
+                        }
+                        ws_commit(&bars->s_full[i][j & 1]);
+                    }
+                    return true;
+                };
+                int issued = 0;
+                while (ok && issued < LA && issued < sg.nt) {
+                    ok = issue_s(issued);
+                    ++issued;
+                }
+                for (int t = 0; t < sg.nt && ok; ++t) {
+                    const int s = (idx0 + t) % NST;
+                    for (int i = 0; i < NQ && ok; ++i) {
+                        if (!sg.active(i, t)) continue;
+                        const int lt = sg.local(t), j = base[i] + lt;
+                        if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        ws_fence_after();
+                        // P_i in the S buffer it came from (bf16 pairs)
+                        const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
+                        const uint32_t v_u = sm_u + S::OffStage + s * S::StageBytes + kWsKeys * 128;
+#pragma unroll
+                        for (int ks = 0; ks < kWsKeys / 16; ++ks)
+                            ws_mma_ts(tmem + (uint32_t)(i * D), p_t + (uint32_t)(ks * 8),
+                                      ws_sdesc(v_u + ks * 16 * 128, S::KVBlock, 1024), kIdescO, (lt > 0 || ks > 0));
+                        ws_commit(&bars->o_done[i]);
+                    }
+                    if (!ok) break;
+                    ws_commit(&bars->empty[s]);            // K and V of the tile are done with
+                    if (issued < sg.nt) {
+                        ok = issue_s(issued);
+                        ++issued;
+                    }
+                }
+                if (!ok) give_up();
+            }
+            __syncwarp();
+            idx0 += sg.nt;
+            for (int i = 0; i < NQ; ++i) {
+                base[i] += sg.tiles(i);
+                loads[i] += sg.tiles(i) > 0;
+            }
+            u += sg.nt;
+        }
+        if (lane == 0) {
+            // every product this thread issued is done before TMEM is freed
+            ws_commit(&bars->fin);
+            if (!mbar_wait(&bars->fin, 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+        }
+        __syncwarp();
+    } else if (warp >= kShSoftmax0) {
+        // ============================ softmax ==============================
+        const int qi = (warp - kShSoftmax0) >> 2;          // Q tile
+        const int r = tid - (kShSoftmax0 + 4 * qi) * 32;   // row = TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
+        const int tl = r / p.G, gq = r - tl * p.G;
+        bool ok = true;
+        int idx0 = 0, base = 0;
+        for (long long u = lo; u < hi && ok;) {
+            const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
+            const int ml = (sg.alt ? 0 : qi * p.tq) + tl;  // the row's member of the column
+            const bool row_ok = tl < p.tq && ml < sg.members;
+            const int mb = row_ok ? __ldcg(p.members + sg.off + sg.m0 + ml) : 0;
+            const int qh = sg.h * p.G + gq;
+            const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
+            // Q row, rotated at its position when BAKED, unscaled bf16
+            if (nt > 0) {
+                const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + ((long long)mb * p.Hq + qh) * D;
+                const bool rot = p.rope != kRopeNone && row_ok;
+                const int qpos = rot ? clamp_paged_t(p.pos[mb], p.maxb, p.bs) : 0;
+#pragma unroll 1
+                for (int cbk = 0; cbk < D / 16; ++cbk) {
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                    if (row_ok) {
+                        a = *reinterpret_cast<const uint4*>(qrow + 8 * cbk);
+                        b = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * cbk);
+                    }
+                    if (rot) {
+                        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float y[2], z[2];
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const float x1 = __uint_as_float(w ? aw[e] & 0xffff0000u : aw[e] << 16);
+                                const float x2 = __uint_as_float(w ? bw[e] & 0xffff0000u : bw[e] << 16);
+                                float cs, sn;
+                                rope_cos_sin((long long)qpos, p.theta[8 * cbk + 2 * e + w], &cs, &sn);
+                                y[w] = x1 * cs - x2 * sn;
+                                z[w] = x1 * sn + x2 * cs;
+                            }
+                            aw[e] = pack_bf16x2(y[0], y[1]);
+                            bw[e] = pack_bf16x2(z[0], z[1]);
+                        }
+                        a = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+                        b = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+                    }
+                    // Q tile: [column block][128 rows][128 B], 128-byte swizzle
+                    const int c1 = cbk, c2 = cbk + D / 16;
+                    *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + r * 128 + (((c1 ^ r) & 7) << 4)) = a;
+                    *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + r * 128 + (((c2 ^ r) & 7) << 4)) = b;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->q_ready[qi]);
+            }
+            float m_run = -INFINITY, l_run = 0.f;          // m in base-2 units of the scaled scores
+            for (int lt = 0; lt < nt; ++lt) {
+                const int j = base + lt;
+                if (!ws_wait(&bars->s_full[qi][j & 1], (j >> 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                ws_fence_after();
+                float sv[kWsKeys];
+                const uint32_t scol = S::SCol0 + (uint32_t)((qi * 2 + (j & 1)) * kWsKeys);
+                ws_ld32(lane_base + scol, sv);
+                ws_ld32(lane_base + scol + 32, sv + 32);
+                ws_wait_ld();
+                ws_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
+                const int gt = idx0 + (sg.alt ? 2 * lt + qi : lt);
+                if (!ws_wait(&bars->ready[gt % NST], (gt / NST) & 1, abort)) {    // the stage's meta
+                    ok = false;
+                    break;
+                }
+                const unsigned long long present = meta[gt % NST].present;
+                if (present != ~0ull) {
+#pragma unroll
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] = ((present >> k) & 1ull) ? sv[k] : -INFINITY;
+                }
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kWsKeys; k += 4)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) mq[w] = fmaxf(mq[w], sv[k + w]);
+                const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * p.scale2;
+                float mn = m_run, alpha = 1.f;
+                if (mx > m_run + kShLazy) {
+                    mn = mx;
+                    alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                }
+                const float nmn = mn == -INFINITY ? 0.f : -mn;
+                float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < kWsKeys; k += 2) {
+                    const float2 d2 = __ffma2_rn(make_float2(sv[k], sv[k + 1]), make_float2(p.scale2, p.scale2),
+                                                 make_float2(nmn, nmn));
+                    const float2 e2 = ws_ex2_pair(d2.x, d2.y);
+                    sv[k] = e2.x;
+                    sv[k + 1] = e2.y;
+                    ls2[(k >> 1) & 3] = __fadd2_rn(ls2[(k >> 1) & 3], e2);
+                }
+                const float2 lsa = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
+                l_run = l_run * alpha + (lsa.x + lsa.y);
+                m_run = mn;
+                // P V of the previous tile is done: P's buffer and O are free
+                if (lt > 0 && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                ws_fence_after();
+                if (lt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int c4 = 0; c4 < D / 32; ++c4) {
+                        float ov[32];
+                        ws_ld32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
+                        ws_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+                        ws_st32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
+                    }
+                    ws_wait_st();
+                }
+                {
+                    float pw[kWsKeys / 2];
+#pragma unroll
+                    for (int k2 = 0; k2 < kWsKeys / 2; ++k2)
+                        pw[k2] = __uint_as_float(pack_bf16x2(sv[2 * k2], sv[2 * k2 + 1]));
+                    ws_st32(lane_base + scol, pw);
+                }
+                ws_wait_st();
+                ws_fence_before();
+                mbar_arrive(&bars->p_full[qi]);
+            }
+            if (!ok) {
+                give_up();
+                break;
+            }
+            // the last P V, then the partial (m, l, o) of each row
+            if (nt > 0) {
+                if (!ws_wait(&bars->o_done[qi], (base + nt - 1) & 1, abort)) {
+                    give_up();
+                    break;
+                }
+                ws_fence_after();
+            }
+            const long long prow = sg.row0 + (long long)x * (NQ * kWsRows) + (sg.alt ? 0 : qi * p.tq * p.G) +
+                                   (long long)tl * p.G + gq + (sg.alt && qi ? p.alt_rows : 0);
+            if (row_ok) p.part_ml[prow] = make_float2(m_run, l_run);
+            if (nt > 0) {
+                float* dst = p.part_o + prow * D;
+#pragma unroll 1
+                for (int c4 = 0; c4 < D / 32; ++c4) {
+                    float ov[32];
+                    ws_ld32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
+                    ws_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4*>(dst + 32 * c4 + k) =
+                                make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+                    }
+                }
+                // O is read: the next segment's first product may overwrite it
+                // (it waits for this warpgroup's next P)
+                ws_fence_before();
+            }
+            idx0 += sg.nt;
+            base += nt;
+            u += sg.nt;
+        }
+    }
+
+    // the MMA thread has waited for all of its products (its last commit)
+    ws_fence_before();
+    __syncthreads();
+    ws_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TmemCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// combine
+// ---------------------------------------------------------------------------
+constexpr int kShCombineWarps = 8;
+
+// One warp per (sequence, q head): lane l holds columns l D / 32 ...  The parts
+// are the decode kernel's slots of the sequence, then the shares of its prefix
+// column (two each when its warpgroups took alternate tiles).
+template <int D>
+__global__ void __launch_bounds__(kShCombineWarps * 32)
+    shared_combine_kernel(const __grid_constant__ SharedParams p, const __grid_constant__ SharedDecode dp) {
+    constexpr int NC = D / 32;
+    sh_pdl_launch();
+    sh_pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int w = blockIdx.x * kShCombineWarps + (threadIdx.x >> 5);
+    // ready the decode kernel's counters and the reader counts for the next call
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < dp.num_blocks;
+         i += (long long)gridDim.x * blockDim.x)
+        dp.refs[i] = 0u;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < dp.ncounters; i += blockDim.x) dp.counters[i] = 0u;
+    if (w >= p.B * p.Hq) return;
+    const int b = w / p.Hq, qh = w - b * p.Hq;
+    // the decode slots of sequence b, as its kernel cut them
+    long long tot = 0, before = 0, rb = 0;
+    for (int base = 0; base < p.B; base += 32) {
+        const long long st = base + lane < p.B ? (long long)__ldcg(dp.seq_rows + base + lane) : 0;
+        tot += st;
+        if (base + lane < b) before += st;
+        if (base + lane == b) rb += st;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        tot += __shfl_xor_sync(0xffffffffu, tot, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+        rb += __shfl_xor_sync(0xffffffffu, rb, off);
+    }
+    const int2 fl = paged_seq_shares(before, rb, tot, paged_share_count(tot, dp.nsplit));
+    const int first = fl.x + b;
+    int nd = fl.y - fl.x + 1;
+    if (first < 0 || nd < 1 || first + nd > dp.max_items) {
+        if (lane == 0) index_fault(p.err, 21, first);
+        return;
+    }
+    // the shares of its prefix column
+    const int2 sg = __ldcg(p.seq_group + b);
+    int np = 0, fx = 0, alt = 0;
+    long long prow = 0;
+    if (sg.x >= 0) {
+        const SharedGroup* g = p.groups + sg.x;
+        const int kt = __ldcg(&g->kt), mt = __ldcg(&g->mt), n = __ldcg(&g->n), h = qh / p.G;
+        const int m = sg.y / p.mq;
+        const long long units = __ldcg(&p.head->units);
+        const int shares = __ldcg(&p.head->shares);
+        const long long u0 = __ldcg(&g->units0) + ((long long)h * mt + m) * kt;
+        fx = streamk_share_of(u0, units, shares);
+        np = streamk_share_of(u0 + kt - 1, units, shares) - fx + 1;
+        alt = shared_q_tiles(D) == 2 && min(p.mq, n - m * p.mq) <= p.tq;
+        prow = __ldcg(&g->rows0) + ((long long)h * n + sg.y) * p.G + qh % p.G;
+        if (alt) np *= 2;
+    }
+    const int parts = nd + np;
+    constexpr int RT = shared_q_tiles(D) * kWsRows;
+    auto slot = [&](int k, const float2** ml) -> const float* {
+        if (k < nd) {
+            const long long s = (long long)(first + k) * p.Hq + qh;
+            *ml = dp.part_ml + s;
+            return dp.part_o + s * D;
+        }
+        const int j = k - nd, sx = fx + (alt ? j >> 1 : j);
+        const long long s = prow + (long long)sx * RT + ((alt && (j & 1)) ? p.alt_rows : 0);
+        *ml = p.part_ml + s;
+        return p.part_o + s * D;
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) {
+        const float2* ml;
+        slot(k, &ml);
+        M = fmaxf(M, __ldcg(ml).x);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f, acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+    for (int base = 0; base < parts; base += 32) {
+        float e = 0.f;
+        if (base + lane < parts) {
+            const float2* ml;
+            slot(base + lane, &ml);
+            const float2 v = __ldcg(ml);
+            if (v.x != -INFINITY) {
+                e = exp2f(v.x - M);
+                L += v.y * e;
+            }
+        }
+        const int cnt = min(32, parts - base);
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k) {
+            const float ek = __shfl_sync(0xffffffffu, e, k);
+            if (ek == 0.f) continue;                 // an empty part's o may hold anything
+            const float2* ml;
+            const float* o = slot(base + k, &ml) + lane * NC;
+            if constexpr (NC == 2) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+                acc[0] = fmaf(v.x, ek, acc[0]);
+                acc[1] = fmaf(v.y, ek, acc[1]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC; c += 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(o + c));
+                    acc[c] = fmaf(v.x, ek, acc[c]);
+                    acc[c + 1] = fmaf(v.y, ek, acc[c + 1]);
+                    acc[c + 2] = fmaf(v.z, ek, acc[c + 2]);
+                    acc[c + 3] = fmaf(v.w, ek, acc[c + 3]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dp.out) + ((long long)b * p.Hq + qh) * D + lane * NC;
+#pragma unroll
+    for (int c = 0; c < NC; c += 2)
+        *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+}
+
+cudaLaunchConfig_t sh_config(dim3 grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int D>
+cudaError_t launch_prefix_t(const SharedParams& p, const CUtensorMap& map, cudaStream_t stream) {
+    constexpr int kSmem = px_smem_bytes<D>();
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(shared_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = sh_config(dim3(p.ctas), PxShape<D>::Threads, kSmem, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, shared_prefix_kernel<D>, p, map);
+}
+
+template <int D>
+cudaError_t launch_combine_t(const SharedParams& p, const SharedDecode& dp, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const long long warps = (long long)p.B * p.Hq;
+    const cudaLaunchConfig_t cfg = sh_config(dim3((unsigned)((warps + kShCombineWarps - 1) / kShCombineWarps)),
+                                             kShCombineWarps * 32, 0, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, shared_combine_kernel<D>, p, dp);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = sh_config(dim3(p.B), kShPlanThreads, 0, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, shared_plan_kernel, p);
+}
+
+cudaError_t launch_shared_prefix(int D, const SharedParams& p, const CUtensorMap& map, cudaStream_t stream) {
+    return D == 64 ? launch_prefix_t<64>(p, map, stream)
+                   : (D == 128 ? launch_prefix_t<128>(p, map, stream) : launch_prefix_t<256>(p, map, stream));
+}
+
+cudaError_t launch_shared_combine(int D, const SharedParams& p, const SharedDecode& dp, cudaStream_t stream) {
+    return D == 64 ? launch_combine_t<64>(p, dp, stream)
+                   : (D == 128 ? launch_combine_t<128>(p, dp, stream) : launch_combine_t<256>(p, dp, stream));
+}
+
+}  // namespace kvc

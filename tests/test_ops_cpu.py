@@ -172,3 +172,29 @@ def test_scored_refusals(kvc):
     assert prefill(q_heads=258) == kvc.KVC_ERR_UNSUPPORTED                 # a group of 129 heads
     assert prefill(**dict(paged, block_size=12), table=A) == kvc.KVC_ERR_UNSUPPORTED
     assert prefill(T=0) == kvc.KVC_ERR_ARG and prefill(n_ws=64) == kvc.KVC_ERR_WORKSPACE
+
+
+def test_shared_refusals(kvc):
+    L = kvc.lib()
+    base = dict(layout="paged", window=0, block_size=16, num_blocks=10, max_blocks_per_seq=4)
+
+    def call(q=A, pos=A, group=A, table=A, out=A, ws=A, layer=0, short=0, cache=A, **kw):
+        d = _desc(kvc, **dict(base, **kw))
+        n = max(kvc.shared_workspace_bytes(d), 1 << 30) if not short else kvc.shared_workspace_bytes(d) - short
+        return L.kvc_decode_attention_shared(ctypes.byref(d), cache, layer, q, pos, group, table, None, out, ws, n, None)
+
+    for name in ("cache", "q", "pos", "group", "table", "out", "ws"):
+        assert call(**{name: None}) == kvc.KVC_ERR_NULL, name
+    for name in ("cache", "q", "out", "ws"):
+        assert call(**{name: A + 8}) == kvc.KVC_ERR_ALIGN, name
+    assert call(layer=2) == kvc.KVC_ERR_ARG and call(short=1) == kvc.KVC_ERR_WORKSPACE
+    for kw in (dict(dtype="f32"), dict(dtype="i8"), dict(block_size=12), dict(block_size=48), dict(block_size=100),
+               dict(q_heads=258)):
+        assert call(**kw) == kvc.KVC_ERR_UNSUPPORTED, kw
+        assert kvc.shared_workspace_bytes(_desc(kvc, **dict(base, **kw))) == 0
+    d = _desc(kvc)
+    assert L.kvc_decode_attention_shared(ctypes.byref(d), A, 0, A, A, A, A, None, A, A, 1 << 30, None) == kvc.KVC_ERR_DESC
+    assert kvc.shared_workspace_bytes(d) == 0
+    with pytest.raises(kvc.KvcError):
+        kvc.alloc_shared_workspace(d)
+    assert kvc.shared_workspace_bytes(_desc(kvc, **base)) > kvc.workspace_bytes(_desc(kvc, **base))
