@@ -229,6 +229,68 @@ def _need_cache(d: KvcDesc, cache: torch.Tensor):
     _need(cache, "cache", cache_dtype(d))
 
 
+class _Sizes:
+    """What the binding checks of a descriptor's tensors, worked out once for each descriptor's bytes: a step's
+    call takes a few microseconds on the GPU, and reading a dozen descriptor fields costs as much."""
+    __slots__ = ("act", "cache", "cache_bytes", "B", "H", "KV", "D", "q", "kv", "table", "valid", "shape")
+
+    def __init__(self, d: KvcDesc):
+        self.act, self.cache, self.cache_bytes = desc_dtype(d), cache_dtype(d), cache_bytes(d)
+        self.B, self.H, self.KV, self.D = d.batch, d.q_heads, d.kv_heads, d.head_dim
+        self.q, self.kv = self.B * self.H * self.D, self.B * self.KV * self.D
+        self.table, self.valid = self.B * d.max_blocks_per_seq, (d.num_blocks + 31) // 32
+        self.shape = (self.B, self.H, self.D)
+
+
+_sizes: dict = {}
+
+
+def _sizes_of(d: KvcDesc) -> _Sizes:
+    key = bytes(d)
+    z = _sizes.get(key)
+    if z is None:
+        if len(_sizes) >= 256:
+            _sizes.clear()
+        z = _sizes[key] = _Sizes(d)
+    return z
+
+
+def _on_device(t: torch.Tensor, dev: int, name: str):
+    """The library launches on the current device: every tensor of a call lies there."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _take(t: torch.Tensor, name: str, dtype, numel, dev: int) -> int:
+    """The address of a dense tensor of the call, checked (`numel` None: any size)."""
+    try:
+        if (t.dtype == dtype and t.is_contiguous() and t.get_device() == dev >= 0
+                and (numel is None or t.numel() == numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, numel)
+    _on_device(t, dev, name)
+    return t.data_ptr()
+
+
+def _take_cache(z: _Sizes, cache: torch.Tensor, dev: int) -> int:
+    if isinstance(cache, torch.Tensor) and cache.numel() * cache.element_size() < z.cache_bytes:
+        raise ValueError(f"cache holds {cache.numel() * cache.element_size()} bytes, the descriptor needs {z.cache_bytes}")
+    return _take(cache, "cache", z.cache, None, dev)
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle (None: the current one of device `dev`)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def alloc_cache(d: KvcDesc, device="cuda", fill=None) -> torch.Tensor:
     """Caller-owned cache tensor of the layout's shape (uninitialised unless `fill`).
 
@@ -318,34 +380,27 @@ def make_qk(d: KvcDesc, rotary: KvcRotary | None = None, q_weight: torch.Tensor 
     return qk
 
 
-def _need_tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: int) -> int:
-    """[B, n, heads, D] with dense heads and one stride between tokens (n = 1: [B, heads, D] too);
-    returns that stride in elements."""
+def _tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: int, dev: int) -> tuple:
+    """Address and token stride (elements) of a tensor [B, n, heads, D] with dense heads and one stride
+    between tokens (n = 1: [B, heads, D] too)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, st = t.shape, t.stride()
+    _on_device(t, dev, name)
+    shape, st = tuple(t.shape), t.stride()
     if len(shape) == 3 and n == 1:
-        shape, st = (shape[0], 1) + tuple(shape[1:]), (st[0], st[0]) + tuple(st[1:])
-    if tuple(shape) != (B, n, heads, D):
+        shape, st = (shape[0], 1, shape[1], shape[2]), (st[0], st[0], st[1], st[2])
+    if shape != (B, n, heads, D):
         raise ValueError(f"{name} must be [{B}, {n}, {heads}, {D}], got {tuple(t.shape)}")
-    if (D > 1 and st[3] != 1) or (heads > 1 and st[2] != D):
+    if st[3] != 1 or (heads > 1 and st[2] != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     stride = st[1] if n > 1 else (st[0] if B > 1 else heads * D)
     if (B > 1 and n > 1 and st[0] != n * stride) or not heads * D <= stride < 2 ** 31:
         raise ValueError(f"{name}: tokens must lie at one stride of at least {heads * D} elements")
-    return stride
-
-
-def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor of a call lies there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr(), stride
 
 
 def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -356,30 +411,27 @@ def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_ne
 
     q [batch, n_new, q_heads, D], k_new / v_new [batch, n_new, kv_heads, D] (or without n_new for one
     token); they may be views of one packed projection.  q_out: dense, like q (None: a new tensor)."""
-    dt = desc_dtype(d)
+    z, dev = _sizes_of(d), _current_device()
     n_new = 1 if q.dim() == 3 else q.shape[1] if q.dim() == 4 else -1
     if n_new < 1:
         raise ValueError("q must be [batch, n_new, q_heads, head_dim]")
-    qs = _need_tokens(q, "q", dt, d.batch, n_new, d.q_heads, d.head_dim)
-    ks = _need_tokens(k_new, "k_new", dt, d.batch, n_new, d.kv_heads, d.head_dim)
-    vs = _need_tokens(v_new, "v_new", dt, d.batch, n_new, d.kv_heads, d.head_dim)
-    _need_cache(d, cache)
-    _need(pos, "pos", torch.int32, d.batch)
-    _need(workspace, "workspace", torch.uint8)
-    if n_tok is not None:
-        _need(n_tok, "n_tok", torch.int32, d.batch)
-    if block_table is not None:
-        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
+    qp, qs = _tokens(q, "q", z.act, z.B, n_new, z.H, z.D, dev)
+    kp, ks = _tokens(k_new, "k_new", z.act, z.B, n_new, z.KV, z.D, dev)
+    vp, vs = _tokens(v_new, "v_new", z.act, z.B, n_new, z.KV, z.D, dev)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    _need(q_out, "q_out", dt, q.numel())
-    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        q_out = torch.empty(q.shape, dtype=z.act, device=q.device)
+    out = _take(q_out, "q_out", z.act, z.q * n_new, dev)
+    if out == qp and not q.is_contiguous():
         raise ValueError("q_out may be q itself only when q is contiguous")
-    _on_current_device(cache, q, k_new, v_new, pos, workspace, n_tok, block_table, q_out)
-    _check(lib().kvc_append_qk(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new), qs, ks,
-                               vs, n_new, _ptr(pos), _ptr(n_tok), _ptr(block_table), ctypes.byref(qk), _ptr(q_out),
-                               _ptr(workspace), workspace.numel(), _stream(stream)),
-           "kvc_append_qk")
+    rc = lib().kvc_append_qk(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, kp, vp, qs, ks, vs, n_new,
+        _take(pos, "pos", torch.int32, z.B, dev),
+        None if n_tok is None else _take(n_tok, "n_tok", torch.int32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
+        ctypes.byref(qk), out, _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_append_qk")
     return q_out
 
 
@@ -420,13 +472,16 @@ def make_score(softcap: float = 0.0, slopes: torch.Tensor | None = None,
     return sc
 
 
-def _need_score(d: KvcDesc, score: KvcScore, T: int):
+def _need_score(z: _Sizes, score: KvcScore, T: int, dev: int):
     slopes, start = score.keep
-    if slopes is not None and slopes.numel() != d.q_heads:
-        raise ValueError(f"score: slopes must have {d.q_heads} elements, got {slopes.numel()}")
-    if start is not None and start.numel() != d.batch * T:
-        raise ValueError(f"score: start must have {d.batch * T} elements, got {start.numel()}")
-    _on_current_device(slopes, start)
+    if slopes is not None:
+        if slopes.numel() != z.H:
+            raise ValueError(f"score: slopes must have {z.H} elements, got {slopes.numel()}")
+        _on_device(slopes, dev, "slopes")
+    if start is not None:
+        if start.numel() != z.B * T:
+            raise ValueError(f"score: start must have {z.B * T} elements, got {start.numel()}")
+        _on_device(start, dev, "start")
 
 
 def decode_attention_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
@@ -434,24 +489,19 @@ def decode_attention_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
                             valid_bits: torch.Tensor | None = None, out: torch.Tensor | None = None,
                             stream=None) -> torch.Tensor:
     """kvc_decode_attention_scored: decode_attention with capped, biased scores and a first position."""
-    dt = desc_dtype(d)
-    _need_cache(d, cache)
-    _need(q, "q", dt, d.batch * d.q_heads * d.head_dim)
-    _need(pos, "pos", torch.int32, d.batch)
-    _need(workspace, "workspace", torch.uint8)
-    if block_table is not None:
-        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
-    if valid_bits is not None:
-        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
+    z, dev = _sizes_of(d), _current_device()
+    qp = _take(q, "q", z.act, z.q, dev)
     if out is None:
-        out = torch.empty((d.batch, d.q_heads, d.head_dim), dtype=dt, device=q.device)
-    _need(out, "out", dt, d.batch * d.q_heads * d.head_dim)
-    _need_score(d, score, 1)
-    _on_current_device(cache, q, pos, workspace, block_table, valid_bits, out)
-    _check(lib().kvc_decode_attention_scored(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(pos),
-                                             _ptr(block_table), _ptr(valid_bits), ctypes.byref(score), _ptr(out),
-                                             _ptr(workspace), workspace.numel(), _stream(stream)),
-           "kvc_decode_attention_scored")
+        out = torch.empty(z.shape, dtype=z.act, device=q.device)
+    _need_score(z, score, 1, dev)
+    rc = lib().kvc_decode_attention_scored(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", torch.int32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
+        ctypes.byref(score), _take(out, "out", z.act, z.q, dev),
+        _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_decode_attention_scored")
     return out
 
 
@@ -473,23 +523,18 @@ def decode_attention_shared(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
                             stream=None) -> torch.Tensor:
     """kvc_decode_attention_shared: decode_attention of a paged batch; the sequences of a group (int32 [batch],
     below 0: alone) share leading blocks, whose keys and values are read once for the group."""
-    dt = desc_dtype(d)
-    _need_cache(d, cache)
-    _need(q, "q", dt, d.batch * d.q_heads * d.head_dim)
-    _need(pos, "pos", torch.int32, d.batch)
-    _need(group, "group", torch.int32, d.batch)
-    _need(workspace, "workspace", torch.uint8)
-    _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
-    if valid_bits is not None:
-        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
+    z, dev = _sizes_of(d), _current_device()
+    qp = _take(q, "q", z.act, z.q, dev)
     if out is None:
-        out = torch.empty((d.batch, d.q_heads, d.head_dim), dtype=dt, device=q.device)
-    _need(out, "out", dt, d.batch * d.q_heads * d.head_dim)
-    _on_current_device(cache, q, pos, group, workspace, block_table, valid_bits, out)
-    _check(lib().kvc_decode_attention_shared(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(pos),
-                                             _ptr(group), _ptr(block_table), _ptr(valid_bits), _ptr(out),
-                                             _ptr(workspace), workspace.numel(), _stream(stream)),
-           "kvc_decode_attention_shared")
+        out = torch.empty(z.shape, dtype=z.act, device=q.device)
+    rc = lib().kvc_decode_attention_shared(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", torch.int32, z.B, dev),
+        _take(group, "group", torch.int32, z.B, dev), _take(block_table, "block_table", torch.int32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
+        _take(out, "out", z.act, z.q, dev), _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_decode_attention_shared")
     return out
 
 
@@ -565,29 +610,23 @@ def prefill_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor,
                    block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kvc_prefill_scored: prefill with capped, biased scores and a first position for each token."""
-    dt = desc_dtype(d)
-    _need_cache(d, cache)
-    _need(q, "q", dt)
-    if q.numel() % (d.batch * d.q_heads * d.head_dim):
+    z, dev = _sizes_of(d), _current_device()
+    qp = _take(q, "q", z.act, None, dev)
+    T = q.numel() // z.q
+    if q.numel() != T * z.q:
         raise ValueError("q must be [batch, T, q_heads, head_dim]")
-    T = q.numel() // (d.batch * d.q_heads * d.head_dim)
-    _need(k_new, "k_new", dt, d.batch * T * d.kv_heads * d.head_dim)
-    _need(v_new, "v_new", dt, d.batch * T * d.kv_heads * d.head_dim)
-    _need(pos0, "pos0", torch.int32, d.batch)
-    _need(workspace, "workspace", torch.uint8)
-    if block_table is not None:
-        _need(block_table, "block_table", torch.int32, d.batch * d.max_blocks_per_seq)
-    if valid_bits is not None:
-        _need(valid_bits, "valid_bits", torch.int32, (d.num_blocks + 31) // 32)
     if out is None:
-        out = torch.empty((d.batch, T, d.q_heads, d.head_dim), dtype=dt, device=q.device)
-    _need(out, "out", dt, d.batch * T * d.q_heads * d.head_dim)
-    _need_score(d, score, T)
-    _on_current_device(cache, q, k_new, v_new, pos0, workspace, block_table, valid_bits, out)
-    _check(lib().kvc_prefill_scored(ctypes.byref(d), _ptr(cache), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                    int(T), _ptr(pos0), _ptr(block_table), _ptr(valid_bits), ctypes.byref(score),
-                                    _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
-           "kvc_prefill_scored")
+        out = torch.empty((z.B, T, z.H, z.D), dtype=z.act, device=q.device)
+    _need_score(z, score, T, dev)
+    rc = lib().kvc_prefill_scored(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(k_new, "k_new", z.act, z.kv * T, dev),
+        _take(v_new, "v_new", z.act, z.kv * T, dev), T, _take(pos0, "pos0", torch.int32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
+        ctypes.byref(score), _take(out, "out", z.act, z.q * T, dev),
+        _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_prefill_scored")
     return out
 
 
