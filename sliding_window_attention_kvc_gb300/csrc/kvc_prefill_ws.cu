@@ -75,8 +75,8 @@ struct alignas(16) WsStageMeta {
     int mask;                // kMaskNone / kMaskRange / kMaskKeys
     int kbase;               // kMaskRange: position of key 0
     int sc_off;              // INT8 cache tile: row 0's scale in the stage's scale area
-    int pos[kWsKeys];        // position of each row, -1 = none
-    float rel[kWsKeys];      // modified scores: position less pos0, for the distance bias
+    alignas(16) int pos[kWsKeys];   // position of each row, -1 = none
+    alignas(16) float rel[kWsKeys]; // modified scores: position less pos0, for the distance bias
 };
 
 // the barriers follow the stages' records: whole 16-byte records keep them aligned
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
                                         (((long long)b * p.T + (row_ok ? row_i : 0)) * p.Hq + row_h) * D;
             const bool rot = p.rope != kRopeNone && row_ok;
-#pragma unroll 1
+#pragma unroll (SCORE ? 4 : 1)
             for (int cbk = 0; cbk < D / 16; ++cbk) {
                 uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
                 if (row_ok) {
@@ -758,70 +758,129 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             // masks: a key at position q is seen by the row at t iff q <= t and
             // (paged, or a sink q < S, or q in the window t - W + 1 .. t)
             const int mode = meta[s].mask;
+            float mn, alpha;
             if constexpr (SCORE) {
+                // s = A v + B in base 2: v = q . k, or with a cap v = -1 / (2^(cap_in q.k) + 1)
+                // and s = 2 cap2 v + cap2 (cap tanh(x / cap) = cap - 2 cap / (e^(2 x / cap) + 1));
+                // a distance bias differs from key to key and is added to every v
+                float A = p.score.scale2, B = 0.f;
                 if (p.score.cap2 > 0.f) {
-                    // cap tanh(x / cap) = cap - 2 cap / (e^(2 x / cap) + 1), base 2
+                    const float2 ci = make_float2(p.score.cap_in, p.score.cap_in), neg = make_float2(-1.f, -1.f);
 #pragma unroll
-                    for (int k = 0; k < kWsKeys; ++k)
-                        sv[k] = fmaf(-2.f * p.score.cap2, ws_rcp(ws_ex2(sv[k] * p.score.cap_in) + 1.f), p.score.cap2);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kWsKeys; ++k) sv[k] *= p.score.scale2;
+                    for (int k = 0; k < kWsKeys; k += 2) {
+                        const float2 y = __fmul2_rn(make_float2(sv[k], sv[k + 1]), ci);
+                        const float2 e = __ffma2_rn(make_float2(ws_ex2(y.x), ws_ex2(y.y)), neg, neg);
+                        sv[k] = ws_rcp(e.x);
+                        sv[k + 1] = ws_rcp(e.y);
+                    }
+                    A = 2.f * p.score.cap2;
+                    B = p.score.cap2;
                 }
                 if (p.score.slopes) {
                     // slope (p - t) = slope (p - pos0) - slope (t - pos0)
+                    const float2 A2 = make_float2(A, A), sl = make_float2(slope2, slope2);
+                    const float2 b2 = make_float2(bias0 + B, bias0 + B);
 #pragma unroll
-                    for (int k = 0; k < kWsKeys; ++k) sv[k] += fmaf(slope2, meta[s].rel[k], bias0);
+                    for (int k = 0; k < kWsKeys; k += 4) {
+                        const float4 rel = *reinterpret_cast<const float4*>(&meta[s].rel[k]);
+                        const float2 x0 = __ffma2_rn(make_float2(sv[k], sv[k + 1]), A2,
+                                                     __ffma2_rn(make_float2(rel.x, rel.y), sl, b2));
+                        const float2 x1 = __ffma2_rn(make_float2(sv[k + 2], sv[k + 3]), A2,
+                                                     __ffma2_rn(make_float2(rel.z, rel.w), sl, b2));
+                        sv[k] = x0.x;
+                        sv[k + 1] = x0.y;
+                        sv[k + 2] = x1.x;
+                        sv[k + 3] = x1.y;
+                    }
+                    A = 1.f;
+                    B = 0.f;
                 }
-            }
-            if (!row_ok) {
+                // masks: the keys a row sees, a bit each
+                if (!row_ok) {
 #pragma unroll
-                for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
-            } else if (mode == kMaskRange) {
-                // the chunk's own rows: key k at kbase + k is seen iff 0 <= kbase + k <= t
-                // (the window holds every chunk token, the chunk being no longer than it)
-                const int kb = meta[s].kbase;
-                const int klo = (SCORE ? start : 0) - kb, khi = row_t - kb;
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
+                } else if (mode == kMaskRange) {
+                    const int kb = meta[s].kbase;
+                    const int klo = start - kb, khi = row_t - kb;
 #pragma unroll
-                for (int k = 0; k < kWsKeys; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
-            } else if (mode == kMaskKeys) {
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
+                } else if (mode == kMaskKeys) {
+                    const int from = paged ? start : max(start, row_t - p.window + 1);   // (sinks below it too)
 #pragma unroll
-                for (int k = 0; k < kWsKeys; ++k) {
-                    const int q = meta[s].pos[k];
-                    bool allowed = q >= 0 && q <= row_t;
-                    if (!paged) allowed = allowed && (q < p.sinks || q > row_t - p.window);
-                    if constexpr (SCORE) allowed = allowed && q >= start;
-                    sv[k] = allowed ? sv[k] : -INFINITY;
+                    for (int k = 0; k < kWsKeys; k += 4) {
+                        const int4 q4 = *reinterpret_cast<const int4*>(&meta[s].pos[k]);
+                        const int qk[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int q = qk[u];
+                            const bool allowed = q >= 0 && q <= row_t && (q >= from || (q < p.sinks && q >= start));
+                            sv[k + u] = allowed ? sv[k + u] : -INFINITY;
+                        }
+                    }
                 }
-            }
-            // four independent chains (latency, not issue slots, is what the
-            // softmax warps wait on)
-            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const float vmax = ws_max64(sv);
+                const float mx = vmax == -INFINITY ? -INFINITY : fmaf(vmax, A, B);
+                mn = m_run;
+                alpha = 1.f;
+                if (mx > m_run + kWsLazy) {
+                    mn = mx;
+                    alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                }
+                // fp32 exponentials: on this part they cost what a pair of fp16 ones and
+                // its conversions do
+                const float ls = ws_exp64(sv, A, mn == -INFINITY ? 0.f : B - mn);
+                l_run = l_run * alpha + ls;
+                m_run = mn;
+            } else {
+                if (!row_ok) {
 #pragma unroll
-            for (int k = 0; k < kWsKeys; k += 4)
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
+                } else if (mode == kMaskRange) {
+                    // the chunk's own rows: key k at kbase + k is seen iff 0 <= kbase + k <= t
+                    // (the window holds every chunk token, the chunk being no longer than it)
+                    const int kb = meta[s].kbase;
+                    const int klo = -kb, khi = row_t - kb;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) mq[u] = fmaxf(mq[u], sv[k + u]);
-            const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-            float mn = m_run, alpha = 1.f;
-            if (mx > m_run + kWsLazy) {
-                mn = mx;
-                alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
-            }
-            // p = 2^(s - m) (exactly 0 for a masked key: 2^-inf), summed in pairs
-            const float nmn = mn == -INFINITY ? 0.f : -mn;
-            float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                             make_float2(0.f, 0.f)};
+                    for (int k = 0; k < kWsKeys; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
+                } else if (mode == kMaskKeys) {
 #pragma unroll
-            for (int k = 0; k < kWsKeys; k += 2) {
-                const float2 d2 = __fadd2_rn(make_float2(sv[k], sv[k + 1]), make_float2(nmn, nmn));
-                const float2 e2 = ws_ex2_pair(d2.x, d2.y);
-                sv[k] = e2.x;
-                sv[k + 1] = e2.y;
-                ls2[(k >> 1) & 3] = __fadd2_rn(ls2[(k >> 1) & 3], e2);
+                    for (int k = 0; k < kWsKeys; ++k) {
+                        const int q = meta[s].pos[k];
+                        bool allowed = q >= 0 && q <= row_t;
+                        if (!paged) allowed = allowed && (q < p.sinks || q > row_t - p.window);
+                        sv[k] = allowed ? sv[k] : -INFINITY;
+                    }
+                }
+                // four independent chains (latency, not issue slots, is what the
+                // softmax warps wait on)
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kWsKeys; k += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mq[u] = fmaxf(mq[u], sv[k + u]);
+                const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                mn = m_run;
+                alpha = 1.f;
+                if (mx > m_run + kWsLazy) {
+                    mn = mx;
+                    alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                }
+                // p = 2^(s - m) (exactly 0 for a masked key: 2^-inf), summed in pairs
+                const float nmn = mn == -INFINITY ? 0.f : -mn;
+                float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < kWsKeys; k += 2) {
+                    const float2 d2 = __fadd2_rn(make_float2(sv[k], sv[k + 1]), make_float2(nmn, nmn));
+                    const float2 e2 = ws_ex2_pair(d2.x, d2.y);
+                    sv[k] = e2.x;
+                    sv[k + 1] = e2.y;
+                    ls2[(k >> 1) & 3] = __fadd2_rn(ls2[(k >> 1) & 3], e2);
+                }
+                const float2 lsa = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
+                l_run = l_run * alpha + (lsa.x + lsa.y);
+                m_run = mn;
             }
-            const float2 lsa = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
-            l_run = l_run * alpha + (lsa.x + lsa.y);
-            m_run = mn;
             // P V of the previous tile is done: P's buffer and O are free
             if (j > 0 && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
                 ok = false;

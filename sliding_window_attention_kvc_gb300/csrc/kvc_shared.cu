@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + ((long long)mb * p.Hq + qh) * D;
                 const bool rot = p.rope != kRopeNone && row_ok;
                 const int qpos = rot ? clamp_paged_t(p.pos[mb], p.maxb, p.bs) : 0;
-#pragma unroll 1
+#pragma unroll 4
                 for (int cbk = 0; cbk < D / 16; ++cbk) {
                     uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
                     if (row_ok) {
@@ -605,41 +605,24 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
 #pragma unroll
                     for (int k = 0; k < kWsKeys; ++k) sv[k] = ((present >> k) & 1ull) ? sv[k] : -INFINITY;
                 }
-                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < kWsKeys; k += 4)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) mq[w] = fmaxf(mq[w], sv[k + w]);
-                const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * p.scale2;
+                const float mx = ws_max64(sv) * p.scale2;
                 float mn = m_run, alpha = 1.f;
                 if (mx > m_run + kShLazy) {
                     mn = mx;
                     alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
                 }
-                const float nmn = mn == -INFINITY ? 0.f : -mn;
-                float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                 make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int k = 0; k < kWsKeys; k += 2) {
-                    const float2 d2 = __ffma2_rn(make_float2(sv[k], sv[k + 1]), make_float2(p.scale2, p.scale2),
-                                                 make_float2(nmn, nmn));
-                    // (fp32 exponentials: rounding the arguments to fp16 and taking two at
-                    // once left 3.2e-3 of the result against 1.9e-3 on the eight-reader groups)
-                    const float2 e2 = make_float2(ws_ex2(d2.x), ws_ex2(d2.y));
-                    sv[k] = e2.x;
-                    sv[k + 1] = e2.y;
-                    ls2[(k >> 1) & 3] = __fadd2_rn(ls2[(k >> 1) & 3], e2);
-                }
-                const float2 lsa = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
-                l_run = l_run * alpha + (lsa.x + lsa.y);
+                // (fp32 exponentials: rounding the arguments to fp16 and taking two at
+                // once left 3.2e-3 of the result against 1.9e-3 on the eight-reader groups)
+                const float ls = ws_exp64(sv, p.scale2, mn == -INFINITY ? 0.f : -mn);
+                l_run = l_run * alpha + ls;
                 m_run = mn;
-                // P V of the previous tile is done: P's buffer and O are free
+                // P V of the previous tile is done: O is free
                 if (lt > 0 && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
-                ws_fence_after();
                 if (lt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    ws_fence_after();
 #pragma unroll 1
                     for (int c4 = 0; c4 < D / 32; ++c4) {
                         float ov[32];

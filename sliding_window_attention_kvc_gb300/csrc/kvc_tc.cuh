@@ -109,6 +109,40 @@ __device__ __forceinline__ float ws_rcp(float x) {
     return y;
 }
 
+__device__ __forceinline__ float ws_max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Largest of 64 values, in four chains of three-input maxima.
+__device__ __forceinline__ float ws_max64(const float (&v)[kWsKeys]) {
+    float m[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        m[u] = ws_max3(v[16 * u], v[16 * u + 1], v[16 * u + 2]);
+#pragma unroll
+        for (int k = 3; k < 15; k += 2) m[u] = ws_max3(m[u], v[16 * u + k], v[16 * u + k + 1]);
+        m[u] = fmaxf(m[u], v[16 * u + 15]);
+    }
+    return fmaxf(ws_max3(m[0], m[1], m[2]), m[3]);
+}
+
+// p_k = 2^(a v_k + c) in place (a masked key's v = -inf gives 0); returns their sum.
+__device__ __forceinline__ float ws_exp64(float (&v)[kWsKeys], float a, float c) {
+    float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 a2 = make_float2(a, a), c2 = make_float2(c, c);
+#pragma unroll
+    for (int k = 0; k < kWsKeys; k += 2) {
+        const float2 d = __ffma2_rn(make_float2(v[k], v[k + 1]), a2, c2);
+        v[k] = ws_ex2(d.x);
+        v[k + 1] = ws_ex2(d.y);
+        ls[(k >> 1) & 3] = __fadd2_rn(ls[(k >> 1) & 3], make_float2(v[k], v[k + 1]));
+    }
+    const float2 s = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
+    return s.x + s.y;
+}
+
 // try_wait with a suspend-time hint: a thread whose phase is not complete
 // sleeps until it completes (or the hint, 0.1 ms, runs out) instead of coming
 // back to re-issue the test, which would take issue slots from the softmax warps
