@@ -578,30 +578,31 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = ws_idesc(kWsRows, kWsKeys, 0);
-            constexpr uint32_t kIdescO = ws_idesc(kWsRows, D, 1);
+        // the whole warp walks the tiles (its values stay uniform); lane 0 issues
+        {
             bool ok = true;
             int nt = 0x7fffffff;
-            auto stage_u = [&](int j) { return sm_u + S::OffStage + (j % NST) * S::StageBytes; };
+            uint64_t qd[NQ];
+            for (int i = 0; i < NQ; ++i) qd[i] = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+            const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
+            const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
+            auto stage_d = [&](int j) { return (uint64_t)(((j % NST) * S::StageBytes) >> 4); };
             // S_i(j) = Q_i K_j^T
             auto issue_s = [&](int j) {
-                for (int i = 0; i < NQ && ok; ++i) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    if (!ok) break;
                     if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) {
                         ok = false;
                         break;
                     }
                     ws_fence_after();
-                    const uint32_t q_u = sm_u + S::OffQ + i * S::QBytes;
-                    const uint32_t k_u = stage_u(j);
                     const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t within = (ks & 3) * 32;
-                        ws_mma(d, ws_sdesc(q_u + (ks >> 2) * (kWsRows * 128) + within, 16, 1024),
-                               ws_sdesc(k_u + (ks >> 2) * S::KVBlock + within, 16, 1024), kIdescS, ks > 0);
+                    if (lane == 0) {
+                        ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i], kd0 + stage_d(j));
+                        ws_commit(&bars->s_full[i][j & 1]);
                     }
-                    ws_commit(&bars->s_full[i][j & 1]);
+                    __syncwarp();
                 }
             };
             // S of tile t for every Q tile, once its keys are in place; false at
@@ -633,7 +634,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             int j = 0;
             for (; ok && j < issued; ++j) {
                 // O_i += P_i V_j
-                for (int i = 0; i < NQ && ok; ++i) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
                     if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
                         ok = false;
                         break;
@@ -642,30 +644,32 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     // P_i(j) in the S buffer it came from (bf16 pairs, 32 columns);
                     // S of tile j + 2 reuses that buffer, issued after this P V
                     const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                    const uint32_t v_u = stage_u(j) + kWsKeys * 128;
-#pragma unroll
-                    for (int ks = 0; ks < kWsKeys / 16; ++ks)
-                        ws_mma_ts(tmem + (uint32_t)(i * D), p_t + (uint32_t)(ks * 8),
-                                  ws_sdesc(v_u + ks * 16 * 128, S::KVBlock, 1024), kIdescO, (j > 0 || ks > 0));
-                    ws_commit(&bars->o_done[i]);
+                    if (lane == 0) {
+                        ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + stage_d(j), j > 0);
+                        ws_commit(&bars->o_done[i]);
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
-                ws_commit(&bars->empty[j % NST]);       // K and V of tile j are done with
+                if (lane == 0) ws_commit(&bars->empty[j % NST]);       // K and V of tile j are done with
                 if (issued == j + LA && try_issue(issued)) ++issued;
             }
             if (*abort) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
             nt = j;
-            if (ok) {
-                // the end: the softmax warps learn the tile count at the S slot
-                // they wait on next (every S before it has been consumed)
-                bars->ntiles = nt;
-                for (int i = 0; i < NQ; ++i) mbar_arrive(&bars->s_full[i][nt & 1]);
-            } else {
-                give_up();
+            if (lane == 0) {
+                if (ok) {
+                    // the end: the softmax warps learn the tile count at the S slot
+                    // they wait on next (every S before it has been consumed)
+                    bars->ntiles = nt;
+                    for (int i = 0; i < NQ; ++i) mbar_arrive(&bars->s_full[i][nt & 1]);
+                } else {
+                    give_up();
+                }
+                // every product this thread issued is done before TMEM is freed
+                ws_commit(&bars->fin);
+                if (!mbar_wait(&bars->fin, 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
             }
-            // every product this thread issued is done before TMEM is freed
-            ws_commit(&bars->fin);
-            if (!mbar_wait(&bars->fin, 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
         }
         __syncwarp();
     } else if (warp >= kWsSoftmax0 && warp < kWsSoftmax0 + 4 * NQ) {
@@ -765,14 +769,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 // a distance bias differs from key to key and is added to every v
                 float A = p.score.scale2, B = 0.f;
                 if (p.score.cap2 > 0.f) {
-                    const float2 ci = make_float2(p.score.cap_in, p.score.cap_in), neg = make_float2(-1.f, -1.f);
-#pragma unroll
-                    for (int k = 0; k < kWsKeys; k += 2) {
-                        const float2 y = __fmul2_rn(make_float2(sv[k], sv[k + 1]), ci);
-                        const float2 e = __ffma2_rn(make_float2(ws_ex2(y.x), ws_ex2(y.y)), neg, neg);
-                        sv[k] = ws_rcp(e.x);
-                        sv[k + 1] = ws_rcp(e.y);
-                    }
+                    ws_cap(sv, p.score.cap_in);
                     A = 2.f * p.score.cap2;
                     B = p.score.cap2;
                 }
@@ -795,15 +792,15 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     A = 1.f;
                     B = 0.f;
                 }
-                // masks: the keys a row sees, a bit each
-                if (!row_ok) {
+                // masks
+                if (mode == kMaskRange) {
+                    // the chunk's own rows: key k at kbase + k (the window holds every chunk token)
+                    const int kb = meta[s].kbase;
+                    const int klo = row_ok ? start - kb : kWsKeys, khi = row_t - kb;
+                    if (!__all_sync(0xffffffffu, klo <= 0 && khi >= kWsKeys - 1)) ws_mask_range(sv, klo, khi);
+                } else if (!row_ok) {
 #pragma unroll
                     for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
-                } else if (mode == kMaskRange) {
-                    const int kb = meta[s].kbase;
-                    const int klo = start - kb, khi = row_t - kb;
-#pragma unroll
-                    for (int k = 0; k < kWsKeys; ++k) sv[k] = (k >= klo && k <= khi) ? sv[k] : -INFINITY;
                 } else if (mode == kMaskKeys) {
                     const int from = paged ? start : max(start, row_t - p.window + 1);   // (sinks below it too)
 #pragma unroll

@@ -443,36 +443,37 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        constexpr uint32_t kIdescS = ws_idesc(kWsRows, kWsKeys, 0);
-        constexpr uint32_t kIdescO = ws_idesc(kWsRows, D, 1);
+        // (the whole warp walks the tiles, its values stay uniform; lane 0 issues)
         constexpr int LA = NST >= 3 ? 2 : 1;           // tiles that S runs ahead of P V
         bool ok = true;
         int idx0 = 0;                                  // tiles of the segments before
         int base[2] = {0, 0};                          // ... and of each Q tile
         int loads[2] = {0, 0};                         // segments each Q tile was loaded for
+        uint64_t qd[NQ];
+        for (int i = 0; i < NQ; ++i) qd[i] = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
+        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
         for (long long u = lo; u < hi;) {
             const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
-            if (lane == 0 && ok) {
+            if (ok) {
                 for (int i = 0; i < NQ && ok; ++i)
                     if (sg.tiles(i) > 0 && !ws_wait(&bars->q_ready[i], loads[i] & 1, abort)) ok = false;
                 auto issue_s = [&](int t) -> bool {
                     const int s = (idx0 + t) % NST;
                     if (!ws_wait(&bars->ready[s], ((idx0 + t) / NST) & 1, abort)) return false;
+#pragma unroll
                     for (int i = 0; i < NQ; ++i) {
                         if (!sg.active(i, t)) continue;
                         const int j = base[i] + sg.local(t);
                         if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) return false;
                         ws_fence_after();
-                        const uint32_t q_u = sm_u + S::OffQ + i * S::QBytes;
-                        const uint32_t k_u = sm_u + S::OffStage + s * S::StageBytes;
                         const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t within = (ks & 3) * 32;
-                            ws_mma(d, ws_sdesc(q_u + (ks >> 2) * (kWsRows * 128) + within, 16, 1024),
-                                   ws_sdesc(k_u + (ks >> 2) * S::KVBlock + within, 16, 1024), kIdescS, ks > 0);
+                        if (lane == 0) {
+                            ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i],
+                                                                     kd0 + (uint64_t)((s * S::StageBytes) >> 4));
+                            ws_commit(&bars->s_full[i][j & 1]);
                         }
-                        ws_commit(&bars->s_full[i][j & 1]);
+                        __syncwarp();
                     }
                     return true;
                 };
@@ -483,31 +484,34 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 }
                 for (int t = 0; t < sg.nt && ok; ++t) {
                     const int s = (idx0 + t) % NST;
-                    for (int i = 0; i < NQ && ok; ++i) {
-                        if (!sg.active(i, t)) continue;
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) {
+                        if (!ok || !sg.active(i, t)) continue;
                         const int lt = sg.local(t), j = base[i] + lt;
                         if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
                             ok = false;
-                            break;
+                            continue;
                         }
                         ws_fence_after();
                         // P_i in the S buffer it came from (bf16 pairs)
                         const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                        const uint32_t v_u = sm_u + S::OffStage + s * S::StageBytes + kWsKeys * 128;
-#pragma unroll
-                        for (int ks = 0; ks < kWsKeys / 16; ++ks)
-                            ws_mma_ts(tmem + (uint32_t)(i * D), p_t + (uint32_t)(ks * 8),
-                                      ws_sdesc(v_u + ks * 16 * 128, S::KVBlock, 1024), kIdescO, (lt > 0 || ks > 0));
-                        ws_commit(&bars->o_done[i]);
+                        if (lane == 0) {
+                            ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + (uint64_t)((s * S::StageBytes) >> 4),
+                                           lt > 0);
+                            ws_commit(&bars->o_done[i]);
+                        }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    ws_commit(&bars->empty[s]);            // K and V of the tile are done with
+                    if (lane == 0) ws_commit(&bars->empty[s]);     // K and V of the tile are done with
+                    __syncwarp();
                     if (issued < sg.nt) {
                         ok = issue_s(issued);
                         ++issued;
                     }
                 }
-                if (!ok) give_up();
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok && lane == 0) give_up();
             }
             __syncwarp();
             idx0 += sg.nt;

@@ -43,6 +43,31 @@ __device__ __forceinline__ void ws_commit(uint64_t* bar) {
                  : "memory");
 }
 
+// S[128 x 64] = Q[128 x D] K[64 x D]^T, both in shared memory; qd, kd: descriptors
+// of their first column blocks (QB and KB bytes between blocks).  A descriptor's
+// address field counts 16 bytes and never carries out of its 14 bits here, so
+// the k-steps add constants: a thread that builds descriptors anew for each
+// product spends more time on them than the tensor cores on the product.
+template <int D, int QB, int KB>
+__device__ __forceinline__ void ws_issue_s(uint32_t d_tmem, uint64_t qd, uint64_t kd) {
+    constexpr uint32_t idesc = ws_idesc(kWsRows, kWsKeys, 0);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+        ws_mma(d_tmem, qd + (uint64_t)(((ks >> 2) * QB + (ks & 3) * 32) >> 4),
+               kd + (uint64_t)(((ks >> 2) * KB + (ks & 3) * 32) >> 4), idesc, ks > 0);
+}
+
+// O[128 x D] (+)= P[128 x 64] V[64 x D]: P in tensor memory (bf16 pairs), vd: the
+// descriptor of V's rows 0 .. 15; `more`: accumulate onto O.
+template <int D>
+__device__ __forceinline__ void ws_issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t vd, uint32_t more) {
+    constexpr uint32_t idesc = ws_idesc(kWsRows, D, 1);
+#pragma unroll
+    for (int ks = 0; ks < kWsKeys / 16; ++ks)
+        ws_mma_ts(d_tmem, p_tmem + (uint32_t)(ks * 8), vd + (uint64_t)((ks * 16 * 128) >> 4), idesc,
+                  ks > 0 ? 1u : more);
+}
+
 __device__ __forceinline__ void ws_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void ws_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -141,6 +166,46 @@ __device__ __forceinline__ float ws_exp64(float (&v)[kWsKeys], float a, float c)
     }
     const float2 s = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
     return s.x + s.y;
+}
+
+// v = -1 / (2^(ci x) + 1) in place, the argument of a capped score (cap tanh =
+// 2 cap v + cap).  Reciprocals run at half the exponentials' rate here: four
+// denominators share one, 1 / a = b (c d) / (a b c d) and so on (measured: 64 keys of
+// two warps 1583 -> 1100 cycles).  Exponents are held to 30 so that no product
+// overflows: tanh is 1 - 2^-29 there, 1 in fp32; a NaN counts as 30 too, so that the garbage of
+// an absent key does not reach its neighbours.
+template <int N>
+__device__ __forceinline__ void ws_cap(float (&v)[N], float ci) {
+    const float2 c2 = make_float2(ci, ci), one = make_float2(1.f, 1.f);
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+        const float2 y0 = __fmul2_rn(make_float2(v[k], v[k + 1]), c2), y1 = __fmul2_rn(make_float2(v[k + 2], v[k + 3]), c2);
+        const float2 e0 = __fadd2_rn(make_float2(ws_ex2(fminf(y0.x, 30.f)), ws_ex2(fminf(y0.y, 30.f))), one);
+        const float2 e1 = __fadd2_rn(make_float2(ws_ex2(fminf(y1.x, 30.f)), ws_ex2(fminf(y1.y, 30.f))), one);
+        const float2 pq = __fmul2_rn(make_float2(e0.x, e1.x), make_float2(e0.y, e1.y));    // a b, c d
+        const float r = -ws_rcp(pq.x * pq.y);
+        const float2 rp = __fmul2_rn(make_float2(r, r), make_float2(pq.y, pq.x));          // -1 / (a b), -1 / (c d)
+        const float2 x0 = __fmul2_rn(make_float2(e0.y, e0.x), make_float2(rp.x, rp.x));
+        const float2 x1 = __fmul2_rn(make_float2(e1.y, e1.x), make_float2(rp.y, rp.y));
+        v[k] = x0.x;
+        v[k + 1] = x0.y;
+        v[k + 2] = x1.x;
+        v[k + 3] = x1.y;
+    }
+}
+
+// Keys lo .. hi of a tile of N stay, the others become -inf (as bits of one word:
+// two compares a key took three times as long).
+template <int N>
+__device__ __forceinline__ void ws_mask_range(float (&v)[N], int lo, int hi) {
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) {
+        const int l = lo - 32 * w, h = hi - 32 * w;
+        uint32_t m = h >= 31 ? 0xffffffffu : (h < 0 ? 0u : (2u << h) - 1u);
+        m &= l <= 0 ? 0xffffffffu : (l > 31 ? 0u : 0xffffffffu << l);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[32 * w + k] = ((m >> k) & 1u) ? v[32 * w + k] : -INFINITY;
+    }
 }
 
 // try_wait with a suspend-time hint: a thread whose phase is not complete
