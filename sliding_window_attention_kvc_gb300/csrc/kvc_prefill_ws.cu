@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], 64);
+            mbar_init(&bars->ready[s], 2);
             mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 mbar_init(&bars->s_full[i][u], 1);
                 mbar_init(&bars->s_free[i][u], 4);
             }
-            mbar_init(&bars->p_full[i], kWsRows);
+            mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
         }
@@ -573,7 +573,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 }
                 if (wrote) fence_proxy_async_smem();
             }
-            mbar_arrive(&bars->ready[s]);
+            // (one arrival a warp: arrivals on one barrier are made one after the other)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->ready[s]);
             if (kind == kTileEnd) break;
         }
     } else if (warp == 1) {
@@ -684,48 +686,58 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
 
-        // Q row: rotated at qpos, scaled by q_scale (softmax scale * log2 e), bf16
-        auto write_q = [&](long long qpos) {
-            const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
-                                        (((long long)b * p.T + (row_ok ? row_i : 0)) * p.Hq + row_h) * D;
-            const bool rot = p.rope != kRopeNone && row_ok;
-#pragma unroll (SCORE ? 4 : 1)
-            for (int cbk = 0; cbk < D / 16; ++cbk) {
+        // The Q tile: rotated at its position (a sink tile's at min(t, C - 1)), scaled by
+        // q_scale (softmax scale * log2 e, or 1), bf16.  D / 16 lanes share a row, so
+        // that a load covers whole lines (a row a thread took 6 us of each CTA).
+        auto write_q = [&](bool at_sinks) {
+            constexpr int LPR = D / 16, RPW = 32 / LPR;
+            const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
+#pragma unroll (READ ? 1 : 4)
+            for (int it = 0; it < 32 / RPW; ++it) {
+                const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
+                const int rtl = rr / G, ri = i0 + qi * tq + rtl, rt = pos0 + ri;
+                const bool rok = rtl < tq && ri < p.T && rt >= 0;
                 uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                if (row_ok) {
-                    lo = *reinterpret_cast<const uint4*>(qrow + 8 * cbk);
-                    hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * cbk);
+                if (rok) {
+                    const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
+                                                (((long long)b * p.T + ri) * p.Hq + h * G + (rr - rtl * G)) * D;
+                    lo = *reinterpret_cast<const uint4*>(qrow + 8 * c);
+                    hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c);
                 }
-                const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                uint32_t lo2[4], hi2[4];
+                const bool rot = p.rope != kRopeNone && rok;
+                if (!SCORE || rot) {
+                    const long long qpos = at_sinks ? min(rt, C - 1) : rt;
+                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                    uint32_t lo2[4], hi2[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
-                    float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
-                    if (rot) {
+                    for (int e = 0; e < 4; ++e) {
+                        float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
+                        float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
+                        if (rot) {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float cs, sn;
-                            rope_cos_sin(qpos, p.theta[8 * cbk + 2 * e + u], &cs, &sn);
-                            const float x1 = x[u], x2 = y[u];
-                            x[u] = x1 * cs - x2 * sn;
-                            y[u] = x1 * sn + x2 * cs;
+                            for (int u = 0; u < 2; ++u) {
+                                float cs, sn;
+                                rope_cos_sin(qpos, p.theta[8 * c + 2 * e + u], &cs, &sn);
+                                const float x1 = x[u], x2 = y[u];
+                                x[u] = x1 * cs - x2 * sn;
+                                y[u] = x1 * sn + x2 * cs;
+                            }
                         }
+                        lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
+                        hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
                     }
-                    lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
-                    hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
+                    lo = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                    hi = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
                 }
                 // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-                const int c1 = cbk, c2 = cbk + D / 16;
-                *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + r * 128 + (((c1 ^ r) & 7) << 4)) =
-                    make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
-                *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + r * 128 + (((c2 ^ r) & 7) << 4)) =
-                    make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
+                const int c1 = c, c2 = c + D / 16;
+                *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = lo;
+                *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = hi;
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars->q_ready[qi]);
         };
-        write_q(sink_tile ? min(row_t, C - 1) : row_t);
+        write_q(sink_tile);
 
         float m_run = -INFINITY, l_run = 0.f;
         // SCORE: the row's slope (base 2), its bias at distance row_i, and its start
@@ -753,7 +765,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             ws_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
-            if (READ && sink_tile && j == 0) write_q(row_t);     // S of the sink tile is out of TMEM
+            if (READ && sink_tile && j == 0) write_q(false);     // S of the sink tile is out of TMEM
             const int s = j % NST;
             if (!ws_wait(&bars->ready[s], (j / NST) & 1, abort)) {    // the stage's meta
                 ok = false;
@@ -906,7 +918,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             ws_wait_st();
             ws_fence_before();
-            mbar_arrive(&bars->p_full[qi]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[qi]);
         }
         if (!ok) give_up();
         // the last P V, then O / l to the output
@@ -921,8 +934,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         ws_fence_after();
         if (!*abort) {
             const float inv = (have_o && l_run > 0.f) ? 1.f / l_run : 0.f;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (((long long)b * p.T + row_i) * p.Hq + row_h) * D;
-            const bool store = tl < tq && row_i < p.T;
+            // through the Q tile's shared memory (its products are done), so that
+            // whole rows go out
 #pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
                 float ov[32];
@@ -930,17 +943,30 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     ws_ld32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
                     ws_wait_ld();
                 }
-                if (store) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        uint32_t w[4];
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = (have_o && row_ok) ? pack_bf16x2(ov[8 * q4 + 2 * e] * inv, ov[8 * q4 + 2 * e + 1] * inv)
-                                                      : 0u;
-                        *reinterpret_cast<uint4*>(dst + 32 * c4 + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = (have_o && row_ok) ? pack_bf16x2(ov[8 * q4 + 2 * e] * inv, ov[8 * q4 + 2 * e + 1] * inv)
+                                                  : 0u;
+                    const int ch = 4 * c4 + q4;
+                    *reinterpret_cast<uint4*>(Qs + (ch >> 3) * (kWsRows * 128) + r * 128 + (((ch ^ r) & 7) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
+            }
+            __syncwarp();
+            constexpr int LPR = D / 8, RPW = 32 / LPR;
+            const int ch = lane % LPR;
+#pragma unroll 4
+            for (int it = 0; it < 32 / RPW; ++it) {
+                const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
+                const int rtl = rr / G, ri = i0 + qi * tq + rtl;
+                if (rtl < tq && ri < p.T)
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                              (((long long)b * p.T + ri) * p.Hq + h * G + (rr - rtl * G)) * D + 8 * ch) =
+                        *reinterpret_cast<const uint4*>(Qs + (ch >> 3) * (kWsRows * 128) + rr * 128 +
+                                                        (((ch ^ rr) & 7) << 4));
             }
         }
     }

@@ -259,6 +259,28 @@ constexpr int px_smem_bytes() {
     return S::OffMeta + S::STAGES * (int)sizeof(PxStageMeta) + (int)sizeof(PxBars) + 1024;
 }
 
+// Eight rotation pairs (elements of lo with those of hi) of a bf16 row at `pos`.
+__device__ __forceinline__ void px_rotate8(uint4& lo, uint4& hi, long long pos, const unsigned long long* turns) {
+    uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float y[2], z[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const float x1 = __uint_as_float(w ? a[e] & 0xffff0000u : a[e] << 16);
+            const float x2 = __uint_as_float(w ? b[e] & 0xffff0000u : b[e] << 16);
+            float cs, sn;
+            rope_cos_sin(pos, turns[2 * e + w], &cs, &sn);
+            y[w] = x1 * cs - x2 * sn;
+            z[w] = x1 * sn + x2 * cs;
+        }
+        a[e] = pack_bf16x2(y[0], y[1]);
+        b[e] = pack_bf16x2(z[0], z[1]);
+    }
+    lo = make_uint4(a[0], a[1], a[2], a[3]);
+    hi = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
 // One segment: tiles tile0 .. tile0 + nt - 1 of a column.
 struct PxSegment {
     int h, m0, members, off, leader, rows;     // kv head, first member's rank and members, the group's list and prefix
@@ -315,7 +337,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], 64);
+            mbar_init(&bars->ready[s], 2);
             mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -323,7 +345,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 mbar_init(&bars->s_full[i][u], 1);
                 mbar_init(&bars->s_free[i][u], 4);
             }
-            mbar_init(&bars->p_full[i], kWsRows);
+            mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
         }
@@ -439,7 +461,9 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                         *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
-            mbar_arrive(&bars->ready[s]);
+            // (one arrival a warp: arrivals on one barrier are made one after the other)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->ready[s]);
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
@@ -540,45 +564,31 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
             const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
             const int ml = (sg.alt ? 0 : qi * p.tq) + tl;  // the row's member of the column
             const bool row_ok = tl < p.tq && ml < sg.members;
-            const int mb = row_ok ? __ldcg(p.members + sg.off + sg.m0 + ml) : 0;
-            const int qh = sg.h * p.G + gq;
             const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
             // Q row, rotated at its position when BAKED, unscaled bf16
             if (nt > 0) {
-                const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + ((long long)mb * p.Hq + qh) * D;
-                const bool rot = p.rope != kRopeNone && row_ok;
-                const int qpos = rot ? clamp_paged_t(p.pos[mb], p.maxb, p.bs) : 0;
+                // (D / 16 lanes share a row: a load covers whole lines)
+                constexpr int LPR = D / 16, RPW = 32 / LPR;
+                const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
 #pragma unroll 4
-                for (int cbk = 0; cbk < D / 16; ++cbk) {
+                for (int it = 0; it < 32 / RPW; ++it) {
+                    const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
+                    const int rtl = rr / p.G, rm = (sg.alt ? 0 : qi * p.tq) + rtl;
+                    const bool rok = rtl < p.tq && rm < sg.members;
                     uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                    if (row_ok) {
-                        a = *reinterpret_cast<const uint4*>(qrow + 8 * cbk);
-                        b = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * cbk);
-                    }
-                    if (rot) {
-                        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float y[2], z[2];
-#pragma unroll
-                            for (int w = 0; w < 2; ++w) {
-                                const float x1 = __uint_as_float(w ? aw[e] & 0xffff0000u : aw[e] << 16);
-                                const float x2 = __uint_as_float(w ? bw[e] & 0xffff0000u : bw[e] << 16);
-                                float cs, sn;
-                                rope_cos_sin((long long)qpos, p.theta[8 * cbk + 2 * e + w], &cs, &sn);
-                                y[w] = x1 * cs - x2 * sn;
-                                z[w] = x1 * sn + x2 * cs;
-                            }
-                            aw[e] = pack_bf16x2(y[0], y[1]);
-                            bw[e] = pack_bf16x2(z[0], z[1]);
-                        }
-                        a = make_uint4(aw[0], aw[1], aw[2], aw[3]);
-                        b = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+                    if (rok) {
+                        const int mb = __ldcg(p.members + sg.off + sg.m0 + rm);
+                        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
+                                                    ((long long)mb * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
+                        a = *reinterpret_cast<const uint4*>(qrow + 8 * c);
+                        b = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c);
+                        if (p.rope != kRopeNone)
+                            px_rotate8(a, b, clamp_paged_t(p.pos[mb], p.maxb, p.bs), p.theta + 8 * c);
                     }
                     // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-                    const int c1 = cbk, c2 = cbk + D / 16;
-                    *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + r * 128 + (((c1 ^ r) & 7) << 4)) = a;
-                    *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + r * 128 + (((c2 ^ r) & 7) << 4)) = b;
+                    const int c1 = c, c2 = c + D / 16;
+                    *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = a;
+                    *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = b;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->q_ready[qi]);
@@ -647,7 +657,8 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 }
                 ws_wait_st();
                 ws_fence_before();
-                mbar_arrive(&bars->p_full[qi]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[qi]);
             }
             if (!ok) {
                 give_up();
