@@ -256,8 +256,8 @@ typedef struct kvc_qk {
  *                 b are real, those behind them padding (NULL: all n_new).
  *   q_out         [batch, n_new, q_heads, head_dim] dense; may be q itself
  *                 when q is dense, otherwise it overlaps no input.
- * Padding tokens and tokens at negative positions are not read; their q_out
- * rows stay as they were.  Device errors as in kvc_append (the token's q_out
+ * Padding tokens and tokens at negative positions may hold anything; their
+ * q_out rows stay as they were.  Device errors as in kvc_append (the token's q_out
  * is written all the same).  All arithmetic is fp32 and every stored value is
  * rounded once.  All pointers are 16-byte aligned but pos, n_tok and
  * block_table. */

@@ -212,6 +212,23 @@ int encode_block_map(const kvc_desc* d, const Geo& g, const void* cache, CUtenso
                : KVC_ERR_CUDA;
 }
 
+// The caller's K or V of the chunk [batch][T][kv head][D] as {column, kv head,
+// batch * T}, boxes of 64 columns of 64 tokens of one kv head.
+int encode_rows_map(const kvc_desc* d, const void* rows, long long T, CUtensorMap* map) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KVC_ERR_CUDA;
+    const cuuint64_t D = (cuuint64_t)d->head_dim;
+    const cuuint64_t dims[3] = {D, (cuuint64_t)d->kv_heads, (cuuint64_t)(d->batch * T)};
+    const cuuint64_t strides[2] = {D * 2, (cuuint64_t)d->kv_heads * D * 2};
+    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
 // The chunk's staged rows, K [batch][T][kv head][D] then V at kv_bytes past
 // it: {64 columns, kv head, batch * T, K|V, column block}, boxes of 64 tokens
 // of one kv head, K and V, every column.
@@ -700,9 +717,13 @@ static int prefill_impl(const kvc_desc* d, void* cache, int32_t layer, const voi
             pm.slot = km.run[kRunMaps - 1];                 // 64-row runs
         }
         if ((rc = encode_stage_map(d, kst, T, prefill_stage_bytes(d, T) / 2, &pm.stage))) return rc;
+        // modified scores over rows stored as they come: read where they lie
+        pm.direct = score && d->dtype == KVC_BF16 && d->rope == KVC_ROPE_NONE;
+        if (pm.direct && ((rc = encode_rows_map(d, k_new, T, &pm.stage_k)) || (rc = encode_rows_map(d, v_new, T, &pm.stage_v))))
+            return rc;
     }
     // 1. the chunk's rows as the cache will hold them (INT8: as it reads them back)
-    if (launch_prefill_stage(ap, kst, vst, s) != cudaSuccess) return KVC_ERR_CUDA;
+    if (!pm.direct && launch_prefill_stage(ap, kst, vst, s) != cudaSuccess) return KVC_ERR_CUDA;
     // 2. attention: earlier keys from the cache as it stands, the chunk's from the stage
     PrefillParams pp{};
     pp.cache = cache;
@@ -744,7 +765,8 @@ static int prefill_impl(const kvc_desc* d, void* cache, int32_t layer, const voi
         return KVC_ERR_CUDA;
     }
     // 3. the chunk appended
-    if (launch_append(d->dtype, ap, s) != cudaSuccess) return KVC_ERR_CUDA;
+    if ((pm.direct ? launch_append_rows(d->dtype, ap, s) : launch_append(d->dtype, ap, s)) != cudaSuccess)
+        return KVC_ERR_CUDA;
     return KVC_OK;
 }
 

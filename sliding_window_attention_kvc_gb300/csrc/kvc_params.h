@@ -211,9 +211,14 @@ struct PrefillParams {
 //          {64 columns, kv head, batch * T, K|V, column block}, 64 tokens.
 // INT8 caches: slot and block are code maps {D bytes, row, K|V, layer} with
 // boxes of 128 codes of 64 rows (slot) or one block (block), no swizzle.
+//   stage_k, stage_v  (direct) the chunk's own K and V as the caller holds them
+//          [batch][T][kv head][D]: {column, kv head, batch * T}, 64 columns of 64
+//          tokens of one kv head.
 struct PrefillMaps {
     CUtensorMap slot, block, stage;
+    CUtensorMap stage_k, stage_v;
     int slot_whole;
+    int direct;      // rows that the cache stores as they come (bf16, no rotation) are not staged
 };
 
 struct TableParams {
@@ -280,6 +285,8 @@ cudaError_t launch_decode_mma(int head_dim, int gh, bool paged, bool read_rope, 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_plan_rows(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_append(int dtype, const AppendParams& p, cudaStream_t stream);
+// the same without rotation (a.rope is ignored), 16 bytes a lane (16-byte aligned rows)
+cudaError_t launch_append_rows(int dtype, const AppendParams& a, cudaStream_t stream);
 cudaError_t launch_table_write(const TableParams& p, cudaStream_t stream);
 // kvc_prefill: the chunk's rows staged (K rotated as stored), then attention.
 cudaError_t launch_prefill_stage(const AppendParams& p, void* kst, void* vst, cudaStream_t stream);

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             tma_prefetch_desc(&maps.block);
         else
             tma_prefetch_desc(&maps.slot);
-        tma_prefetch_desc(&maps.stage);
+        tma_prefetch_desc(SCORE && maps.direct ? &maps.stage_k : &maps.stage);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem)),
@@ -413,7 +413,16 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     meta[s].kbase = pos0 + i_s;
                     unsigned char* dst = sm + S::OffStage + s * S::StageBytes;
                     mbar_expect_tx(&bars->full[s], (uint32_t)S::StageBytes);
-                    tma_load_5d(dst, &maps.stage, 0, h, b * p.T + i_s, 0, 0, &bars->full[s]);
+                    if (SCORE && maps.direct) {
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) {
+                            tma_load_3d(dst + cb * S::KVBlock, &maps.stage_k, cb * 64, h, b * p.T + i_s, &bars->full[s]);
+                            tma_load_3d(dst + cb * S::KVBlock + kWsKeys * 128, &maps.stage_v, cb * 64, h, b * p.T + i_s,
+                                        &bars->full[s]);
+                        }
+                    } else {
+                        tma_load_5d(dst, &maps.stage, 0, h, b * p.T + i_s, 0, 0, &bars->full[s]);
+                    }
                     mbar_arrive(&bars->full[s]);
                 }
                 ++idx;

@@ -82,8 +82,10 @@ template <> struct QkVec<float> {
 };
 
 // Act: element type of q, k, v, q_out and the weights; Q8: an INT8 cache.
+// Four CTAs an SM: with the 119 registers it would take by itself (two CTAs) a
+// prompt of 11.5k tokens ran at 2.3 TB/s, for want of loads in flight.
 template <typename Act, int D, bool Q8>
-__global__ void __launch_bounds__(kQkThreads) append_qk_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, 4) append_qk_kernel(const __grid_constant__ QkParams p) {
     constexpr int LPR = D / 8;                    // lanes of a row
     constexpr int RP = kQkThreads / LPR;          // rows the CTA visits at once
     __shared__ float2 s_cs[kMaxHalfDim];
@@ -94,6 +96,24 @@ __global__ void __launch_bounds__(kQkThreads) append_qk_kernel(const __grid_cons
     const int tid = threadIdx.x;
     const int lr = tid % LPR, r0 = tid / LPR;
     const int i_tok = blockIdx.x, b = blockIdx.y;
+    const int R = p.Hq + 2 * p.Hkv;
+    const int first = blockIdx.z * p.rows_per_z, end = min(R, first + p.rows_per_z);
+    const long long tok = (long long)b * p.n_new + i_tok;
+    auto row_at = [&](int r) -> const Act* {
+        return (r < p.Hq ? static_cast<const Act*>(p.q) + tok * p.q_stride + (long long)r * D
+                         : (r < p.Hq + p.Hkv ? static_cast<const Act*>(p.k) + tok * p.k_stride + (long long)(r - p.Hq) * D
+                                             : static_cast<const Act*>(p.v) + tok * p.v_stride +
+                                                   (long long)(r - p.Hq - p.Hkv) * D)) + lr * 8;
+    };
+    QkVec<Act> x[kQkBatch];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kQkBatch; ++u)
+            if (base + u * RP < end) x[u].load(row_at(base + u * RP));
+    };
+    // the rows first: they need neither the count nor the position
+    load(first + r0);
+
     const int n = p.n_tok ? min(p.n_tok[b], p.n_new) : p.n_new;
     const int t0 = p.pos[b];
     const long long pos = (long long)t0 + i_tok;
@@ -128,77 +148,24 @@ __global__ void __launch_bounds__(kQkThreads) append_qk_kernel(const __grid_cons
         head_stride = (long long)p.bs * D;
     }
 
-    const int R = p.Hq + 2 * p.Hkv;
-    const int first = blockIdx.z * p.rows_per_z, end = min(R, first + p.rows_per_z);
-    const long long tok = (long long)b * p.n_new + i_tok;
-    const Act* const qs = static_cast<const Act*>(p.q) + tok * p.q_stride + lr * 8;
-    const Act* const ks = static_cast<const Act*>(p.k) + tok * p.k_stride + lr * 8;
-    const Act* const vs = static_cast<const Act*>(p.v) + tok * p.v_stride + lr * 8;
+    // the token's sines and cosines, once for all its heads
     const int half = p.rot >> 1;
-
-    // this lane's weights and rotation, the same for every row
-    float wq[8], wk[8];
-    float c[8], s[8];                             // neighbour pairs use the first four
-    bool ready = false;
+    if (p.rot) {
+        for (int i = tid; i < half; i += kQkThreads) {
+            float cc, ss;
+            rope_cos_sin(pos, p.turns[i], &cc, &ss);
+            s_cs[i] = make_float2(cc * p.mag, ss * p.mag);
+        }
+        __syncthreads();
+    }
     const int hc = half >> 3;                     // halves of whole chunks: chunks of a half
     const bool chunks = p.rot && !p.interleaved && (half & 7) == 0;
+    // pair index of this lane's value j (interleaved: of its pair j), and the sign of
+    // its sine: y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin
+    const int i0 = p.interleaved ? lr * 4 : (lr * 8 < half ? lr * 8 : lr * 8 - half);
 
     for (int base = first + r0; base - r0 < end; base += kQkBatch * RP) {
-        QkVec<Act> x[kQkBatch];
-#pragma unroll
-        for (int u = 0; u < kQkBatch; ++u) {
-            const int r = base + u * RP;
-            if (r < end)
-                x[u].load(r < p.Hq ? qs + (long long)r * D
-                                   : (r < p.Hq + p.Hkv ? ks + (long long)(r - p.Hq) * D
-                                                       : vs + (long long)(r - p.Hq - p.Hkv) * D));
-        }
-        if (!ready) {
-            // while the rows arrive: the token's sines and cosines, and the weights
-            ready = true;
-            if (p.rot) {
-                for (int i = tid; i < half; i += kQkThreads) {
-                    float cc, ss;
-                    rope_cos_sin(pos, p.turns[i], &cc, &ss);
-                    s_cs[i] = make_float2(cc * p.mag, ss * p.mag);
-                }
-            }
-            if (p.qw) {
-                QkVec<Act> w;
-                w.load(static_cast<const Act*>(p.qw) + lr * 8);
-                w.get(wq);
-            }
-            if (p.kw) {
-                QkVec<Act> w;
-                w.load(static_cast<const Act*>(p.kw) + lr * 8);
-                w.get(wk);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                wq[j] = p.qw ? wq[j] + p.offset : 1.f;
-                wk[j] = p.kw ? wk[j] + p.offset : 1.f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[j] = 1.f;
-                s[j] = 0.f;
-                int i = -1;
-                float sign = 1.f;
-                if (p.interleaved) {
-                    if (j < 4 && lr * 8 + 2 * j < p.rot) i = lr * 4 + j;
-                } else if (lr * 8 + j < p.rot) {
-                    const int e = lr * 8 + j;
-                    i = e < half ? e : e - half;
-                    sign = e < half ? -1.f : 1.f;   // y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin
-                }
-                if (i >= 0) {
-                    const float2 cs = s_cs[i];
-                    c[j] = cs.x;
-                    s[j] = cs.y * sign;
-                }
-            }
-        }
+        if (base != first + r0) load(base);
 #pragma unroll
         for (int u = 0; u < kQkBatch; ++u) {
             const int r = base + u * RP;
@@ -219,10 +186,15 @@ __global__ void __launch_bounds__(kQkThreads) append_qk_kernel(const __grid_cons
                 for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
 #pragma unroll
                 for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-                if (!isv && (isq ? p.qw : p.kw)) {
+                const void* wp = isq ? p.qw : p.kw;
+                if (!isv && wp) {
+                    const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+                    QkVec<Act> wv;                 // (the same few lines for every row: from L1)
+                    wv.load(static_cast<const Act*>(wp) + lr * 8);
+                    float w[8];
+                    wv.get(w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= rs * (isq ? wq[j] : wk[j]);
+                    for (int j = 0; j < 8; ++j) f[j] *= rs * (w[j] + p.offset);
                 }
             }
             if (p.rot) {
@@ -230,35 +202,41 @@ __global__ void __launch_bounds__(kQkThreads) append_qk_kernel(const __grid_cons
                     if (!isv) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float a = f[2 * j], bb = f[2 * j + 1];
-                            f[2 * j] = a * c[j] - bb * s[j];
-                            f[2 * j + 1] = a * s[j] + bb * c[j];
+                            if (lr * 8 + 2 * j < p.rot) {
+                                const float2 cs = s_cs[i0 + j];
+                                const float a = f[2 * j], bb = f[2 * j + 1];
+                                f[2 * j] = a * cs.x - bb * cs.y;
+                                f[2 * j + 1] = a * cs.y + bb * cs.x;
+                            }
+                        }
+                    }
+                } else if (chunks) {
+                    const int src = lr < hc ? lr + hc : (lr < 2 * hc ? lr - hc : lr);
+                    const float sign = lr < hc ? -1.f : 1.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float o = __shfl_sync(0xffffffffu, f[j], src, LPR);
+                        if (!isv && lr < 2 * hc) {
+                            const float2 cs = s_cs[i0 + j];
+                            f[j] = f[j] * cs.x + o * (sign * cs.y);
                         }
                     }
                 } else {
-                    float o[8];
-                    if (chunks) {
-                        const int src = lr < hc ? lr + hc : (lr < 2 * hc ? lr - hc : lr);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float v = __shfl_sync(0xffffffffu, f[j], src, LPR);
-                            o[j] = lr < 2 * hc ? v : 0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) s_row[r0][lr * 8 + j] = f[j];
-                        __syncwarp();
+                    for (int j = 0; j < 8; ++j) s_row[r0][lr * 8 + j] = f[j];
+                    __syncwarp();
+                    if (!isv) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int e = lr * 8 + j;
-                            o[j] = e < p.rot ? s_row[r0][e < half ? e + half : e - half] : 0.f;
+                            if (e < p.rot) {
+                                const float2 cs = s_cs[e < half ? e : e - half];
+                                const float o = s_row[r0][e < half ? e + half : e - half];
+                                f[j] = f[j] * cs.x + o * (e < half ? -cs.y : cs.y);
+                            }
                         }
-                        __syncwarp();
                     }
-                    if (!isv) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = f[j] * c[j] + o[j] * s[j];
-                    }
+                    __syncwarp();
                 }
             }
             float amax = 0.f;
@@ -309,7 +287,56 @@ cudaError_t launch_qk(const QkParams& p, dim3 grid, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, append_qk_kernel<Act, D, Q8>, p);
 }
 
+// The grid: one CTA per token; few tokens: a token's rows over several CTAs, so
+// that two CTAs per SM are busy.
+cudaError_t dispatch_qk(int dtype, int D, int B, QkParams& p, cudaStream_t s) {
+    const int R = p.Hq + 2 * p.Hkv, RP = kQkThreads / (D / 8);
+    const long long tokens = (long long)B * p.n_new;
+    int parts = (R + RP - 1) / RP;
+    if (tokens * parts > 2 * 152) parts = (int)((2 * 152 + tokens - 1) / tokens);
+    if (parts > 65535) parts = 65535;
+    p.rows_per_z = ((R + parts - 1) / parts + RP - 1) / RP * RP;
+    const dim3 grid(p.n_new, B, (R + p.rows_per_z - 1) / p.rows_per_z);
+    cudaError_t e = cudaErrorInvalidValue;
+#define KVC_QK(DD)                                                               \
+    if (D == DD)                                                                 \
+        e = dtype == KVC_F32 ? launch_qk<float, DD, false>(p, grid, s)           \
+            : dtype == KVC_BF16 ? launch_qk<__nv_bfloat16, DD, false>(p, grid, s) \
+                                : launch_qk<__nv_bfloat16, DD, true>(p, grid, s);
+    KVC_QK(64)
+    KVC_QK(128)
+    KVC_QK(256)
+#undef KVC_QK
+    return e;
+}
+
 }  // namespace
+
+cudaError_t launch_append_rows(int dtype, const AppendParams& a, cudaStream_t stream) {
+    QkParams p{};
+    p.k = a.k_new;
+    p.v = a.v_new;
+    p.cache = a.cache;
+    p.scales = a.scales;
+    p.pos = a.pos;
+    p.table = a.table;
+    p.err = a.err;
+    p.layer_off = a.layer_off;
+    p.kv_off = a.kv_off;
+    p.sc_layer_off = a.sc_layer_off;
+    p.sc_kv_off = a.sc_kv_off;
+    p.k_stride = p.v_stride = (long long)a.Hkv * a.D;
+    p.n_new = a.n_new;
+    p.Hkv = a.Hkv;
+    p.layout = a.layout;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.capacity = a.capacity;
+    p.bs = a.bs;
+    p.num_blocks = a.num_blocks;
+    p.maxb = a.maxb;
+    return dispatch_qk(dtype, a.D, a.B, p, stream);
+}
 
 }  // namespace kvc
 
@@ -434,26 +461,7 @@ KVC_API int kvc_append_qk(const kvc_desc* d, void* cache, int32_t layer, const v
         p.mag = rot->magnitude;
         for (int i = 0; i < rot->dim / 2; ++i) p.turns[i] = rot->turns[i];
     }
-    // one CTA per token; few tokens: a token's rows over several CTAs, so that
-    // two CTAs per SM are busy
-    const int R = d->q_heads + 2 * d->kv_heads, RP = kQkThreads / (d->head_dim / 8);
-    const long long tokens = (long long)d->batch * n_new;
-    int parts = (R + RP - 1) / RP;
-    if (tokens * parts > 2 * 152) parts = (int)((2 * 152 + tokens - 1) / tokens);
-    if (parts > 65535) parts = 65535;
-    p.rows_per_z = ((R + parts - 1) / parts + RP - 1) / RP * RP;
-    const dim3 grid(n_new, d->batch, (R + p.rows_per_z - 1) / p.rows_per_z);
-    cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = cudaErrorInvalidValue;
-#define KVC_QK(DD)                                                                   \
-    if (d->head_dim == DD)                                                           \
-        e = d->dtype == KVC_F32 ? launch_qk<float, DD, false>(p, grid, s)            \
-            : d->dtype == KVC_BF16 ? launch_qk<__nv_bfloat16, DD, false>(p, grid, s) \
-                                   : launch_qk<__nv_bfloat16, DD, true>(p, grid, s);
-    KVC_QK(64)
-    KVC_QK(128)
-    KVC_QK(256)
-#undef KVC_QK
+    const cudaError_t e = dispatch_qk(d->dtype, d->head_dim, d->batch, p, (cudaStream_t)stream);
     return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
