@@ -23,8 +23,11 @@ namespace kvc {
 
 namespace {
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 64;
+constexpr int kQkCtas = 12;          // CTAs an SM
 constexpr int kQkBatch = 4;          // rows a thread keeps in flight
+// How a row's pairs lie: neighbours; halves of whole 8-value chunks; any halves.
+enum : int { kRotNone = 0, kRotPairs = 1, kRotChunks = 2, kRotAny = 3 };
 
 struct QkParams {
     const void* q;
@@ -45,7 +48,7 @@ struct QkParams {
     int layout, window, sinks, capacity, bs, num_blocks, maxb;
     int rows_per_z;                  // rows (heads of q, k, v) of one CTA
     int rot;                         // rotated values of a row (even), 0: none
-    int interleaved;
+    int mode;                        // kRotNone ...
     float eps, offset, mag;
     unsigned long long turns[kMaxHalfDim];
 };
@@ -81,11 +84,93 @@ template <> struct QkVec<float> {
     }
 };
 
-// Act: element type of q, k, v, q_out and the weights; Q8: an INT8 cache.
-// Four CTAs an SM: with the 119 registers it would take by itself (two CTAs) a
-// prompt of 11.5k tokens ran at 2.3 TB/s, for want of loads in flight.
+// A row of K (from f) or V (as loaded, in x; INT8: from f) to element offset `at` of the K
+// half; every lane of a warp calls.
 template <typename Act, int D, bool Q8>
-__global__ void __launch_bounds__(kQkThreads, 4) append_qk_kernel(const __grid_constant__ QkParams p) {
+__device__ __forceinline__ void qk_store(const QkParams& p, QkVec<Act>& x, const float (&f)[8], long long at, bool v,
+                                         bool write, int lr) {
+    const long long off = p.layer_off + at + (v ? p.kv_off : 0);
+    if constexpr (Q8) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+#pragma unroll
+        for (int o = D / 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (!write) return;
+        const float sc = __fdiv_rn(amax, 127.f);
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            lo |= ((uint32_t)q8_code(f[j], sc) & 0xffu) << (8 * j);
+            hi |= ((uint32_t)q8_code(f[4 + j], sc) & 0xffu) << (8 * j);
+        }
+        *reinterpret_cast<uint2*>(static_cast<int8_t*>(p.cache) + off + lr * 8) = make_uint2(lo, hi);
+        if (lr == 0) p.scales[p.sc_layer_off + at / D + (v ? p.sc_kv_off : 0)] = sc;
+    } else if (write) {
+        if (!v) x.put(f);
+        x.store(static_cast<Act*>(p.cache) + off + lr * 8);
+    }
+}
+
+// One head's row in 8 values a lane, by every lane of a warp at once: norm (ss: the
+// row's sum of squares over its lanes), then rotation.  w: this lane's weights; c,
+// s: its cosines and (signed) sines, interleaved: of its four pairs.
+template <int D>
+__device__ __forceinline__ void qk_row(float (&f)[8], bool norm, const float (&w)[8], float eps, int mode,
+                                       const float (&c)[8], const float (&s)[8], int src, bool rotated, float* row,
+                                       int lr, int half, int rot) {
+    constexpr int LPR = D / 8;
+    float2* const g = reinterpret_cast<float2*>(f);
+    if (norm) {
+        float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q = __ffma2_rn(g[j], g[j], q);
+        float ss = q.x + q.y;
+#pragma unroll
+        for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const float rs = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            g[j] = __fmul2_rn(__fmul2_rn(g[j], make_float2(rs, rs)), make_float2(w[2 * j], w[2 * j + 1]));
+    }
+    if (mode == kRotPairs) {
+        if (rotated) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = f[2 * j], y = f[2 * j + 1];
+                f[2 * j] = x * c[j] - y * s[j];
+                f[2 * j + 1] = x * s[j] + y * c[j];
+            }
+        }
+    } else if (mode == kRotChunks) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, f[j], src, LPR);
+        if (rotated) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * c[j] + o[j] * s[j];
+        }
+    } else if (mode == kRotAny) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) row[lr * 8 + j] = f[j];
+        __syncwarp();
+        if (rotated) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = lr * 8 + j;
+                if (e < rot) f[j] = f[j] * c[j] + row[e < half ? e + half : e - half] * s[j];
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Act: element type of q, k, v, q_out and the weights; Q8: an INT8 cache.  Two
+// warps a token: what a lane needs for every row (weights, sines, cosines) is in
+// registers and serves a dozen rows.  With eight warps a token, three rows a
+// thread, a prompt of 11.5k tokens spent 67% of the issue slots at 3.3 TB/s.
+template <typename Act, int D, bool Q8>
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) append_qk_kernel(const __grid_constant__ QkParams p) {
     constexpr int LPR = D / 8;                    // lanes of a row
     constexpr int RP = kQkThreads / LPR;          // rows the CTA visits at once
     __shared__ float2 s_cs[kMaxHalfDim];
@@ -96,23 +181,23 @@ __global__ void __launch_bounds__(kQkThreads, 4) append_qk_kernel(const __grid_c
     const int tid = threadIdx.x;
     const int lr = tid % LPR, r0 = tid / LPR;
     const int i_tok = blockIdx.x, b = blockIdx.y;
-    const int R = p.Hq + 2 * p.Hkv;
-    const int first = blockIdx.z * p.rows_per_z, end = min(R, first + p.rows_per_z);
+    const int first = blockIdx.z * p.rows_per_z, end = min(p.Hq + 2 * p.Hkv, first + p.rows_per_z);
     const long long tok = (long long)b * p.n_new + i_tok;
-    auto row_at = [&](int r) -> const Act* {
-        return (r < p.Hq ? static_cast<const Act*>(p.q) + tok * p.q_stride + (long long)r * D
-                         : (r < p.Hq + p.Hkv ? static_cast<const Act*>(p.k) + tok * p.k_stride + (long long)(r - p.Hq) * D
-                                             : static_cast<const Act*>(p.v) + tok * p.v_stride +
-                                                   (long long)(r - p.Hq - p.Hkv) * D)) + lr * 8;
-    };
+    // the CTA's heads of q, of k and of v
+    const int q0 = first, q1 = min(end, p.Hq);
+    const int k0 = max(first, p.Hq) - p.Hq, k1 = min(end, p.Hq + p.Hkv) - p.Hq;
+    const int v0 = max(first - p.Hq - p.Hkv, 0), v1 = end - p.Hq - p.Hkv;
+    const Act* const qs = static_cast<const Act*>(p.q) + tok * p.q_stride + lr * 8;
+    const Act* const ks = static_cast<const Act*>(p.k) + tok * p.k_stride + lr * 8;
+    const Act* const vs = static_cast<const Act*>(p.v) + tok * p.v_stride + lr * 8;
     QkVec<Act> x[kQkBatch];
-    auto load = [&](int base) {
+    auto load = [&](const Act* src, int base, int hi) {
 #pragma unroll
         for (int u = 0; u < kQkBatch; ++u)
-            if (base + u * RP < end) x[u].load(row_at(base + u * RP));
+            if (base + u * RP + r0 < hi) x[u].load(src + (long long)(base + u * RP + r0) * D);
     };
-    // the rows first: they need neither the count nor the position
-    load(first + r0);
+    // the first rows need neither the count nor the position
+    if (q0 < q1) load(qs, q0, q1);
 
     const int n = p.n_tok ? min(p.n_tok[b], p.n_new) : p.n_new;
     const int t0 = p.pos[b];
@@ -150,125 +235,92 @@ __global__ void __launch_bounds__(kQkThreads, 4) append_qk_kernel(const __grid_c
 
     // the token's sines and cosines, once for all its heads
     const int half = p.rot >> 1;
-    if (p.rot) {
+    const int hc = half >> 3;                     // halves of whole chunks: chunks of a half
+    float c[8], s[8];
+    bool rotated = false;
+    if (p.mode != kRotNone) {
         for (int i = tid; i < half; i += kQkThreads) {
             float cc, ss;
             rope_cos_sin(pos, p.turns[i], &cc, &ss);
             s_cs[i] = make_float2(cc * p.mag, ss * p.mag);
         }
         __syncthreads();
+        rotated = lr * 8 < p.rot;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[j] = 1.f;
+            s[j] = 0.f;
+            int i = -1;
+            float sign = 1.f;
+            if (p.mode == kRotPairs) {
+                if (j < 4 && lr * 8 + 2 * j < p.rot) i = lr * 4 + j;
+            } else if (lr * 8 + j < p.rot) {
+                // y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin
+                const int e = lr * 8 + j;
+                i = e < half ? e : e - half;
+                sign = e < half ? -1.f : 1.f;
+            }
+            if (i >= 0) {
+                const float2 cs = s_cs[i];
+                c[j] = cs.x;
+                s[j] = cs.y * sign;
+            }
+        }
     }
-    const int hc = half >> 3;                     // halves of whole chunks: chunks of a half
-    const bool chunks = p.rot && !p.interleaved && (half & 7) == 0;
-    // pair index of this lane's value j (interleaved: of its pair j), and the sign of
-    // its sine: y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin
-    const int i0 = p.interleaved ? lr * 4 : (lr * 8 < half ? lr * 8 : lr * 8 - half);
+    const int src = lr < hc ? lr + hc : (lr < 2 * hc ? lr - hc : lr);
+    float w[8];
+    auto weights = [&](const void* wp) {
+        if (!wp) return;
+        QkVec<Act> wv;
+        wv.load(static_cast<const Act*>(wp) + lr * 8);
+        wv.get(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] += p.offset;
+    };
 
-    for (int base = first + r0; base - r0 < end; base += kQkBatch * RP) {
-        if (base != first + r0) load(base);
+    if (q0 < q1) {
+        weights(p.qw);
+        Act* const dst = static_cast<Act*>(p.q_out) + tok * p.Hq * D + lr * 8;
+        for (int base = q0; base < q1; base += kQkBatch * RP) {
+            if (base != q0) load(qs, base, q1);
+#pragma unroll
+            for (int u = 0; u < kQkBatch; ++u) {
+                if (base + u * RP >= q1) break;   // (uniform: a warp's rows share its shuffles)
+                const int r = base + u * RP + r0;
+                float f[8];
+                x[u].get(f);
+                qk_row<D>(f, p.qw, w, p.eps, p.mode, c, s, src, rotated, s_row[r0], lr, half, p.rot);
+                if (r < q1) {
+                    x[u].put(f);
+                    x[u].store(dst + (long long)r * D);
+                }
+            }
+        }
+    }
+    if (k0 < k1) {
+        weights(p.kw);
+        for (int base = k0; base < k1; base += kQkBatch * RP) {
+            load(ks, base, k1);
+#pragma unroll
+            for (int u = 0; u < kQkBatch; ++u) {
+                if (base + u * RP >= k1) break;
+                const int r = base + u * RP + r0;
+                float f[8];
+                x[u].get(f);
+                qk_row<D>(f, p.kw, w, p.eps, p.mode, c, s, src, rotated, s_row[r0], lr, half, p.rot);
+                qk_store<Act, D, Q8>(p, x[u], f, row_base + r * head_stride, false, keep && r < k1, lr);
+            }
+        }
+    }
+    for (int base = v0; base < v1; base += kQkBatch * RP) {
+        load(vs, base, v1);
 #pragma unroll
         for (int u = 0; u < kQkBatch; ++u) {
-            const int r = base + u * RP;
-            // (a warp's rows share the loop: its shuffles run for all of them or none)
-            if (base - r0 + u * RP >= end) break;
-            const bool in = r < end;
-            const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
+            if (base + u * RP >= v1) break;
+            const int r = base + u * RP + r0;
             float f[8];
-            if (in) {
-                x[u].get(f);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = 0.f;
-            }
-            if (p.qw || p.kw) {
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-#pragma unroll
-                for (int off = LPR / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                const void* wp = isq ? p.qw : p.kw;
-                if (!isv && wp) {
-                    const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-                    QkVec<Act> wv;                 // (the same few lines for every row: from L1)
-                    wv.load(static_cast<const Act*>(wp) + lr * 8);
-                    float w[8];
-                    wv.get(w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= rs * (w[j] + p.offset);
-                }
-            }
-            if (p.rot) {
-                if (p.interleaved) {
-                    if (!isv) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (lr * 8 + 2 * j < p.rot) {
-                                const float2 cs = s_cs[i0 + j];
-                                const float a = f[2 * j], bb = f[2 * j + 1];
-                                f[2 * j] = a * cs.x - bb * cs.y;
-                                f[2 * j + 1] = a * cs.y + bb * cs.x;
-                            }
-                        }
-                    }
-                } else if (chunks) {
-                    const int src = lr < hc ? lr + hc : (lr < 2 * hc ? lr - hc : lr);
-                    const float sign = lr < hc ? -1.f : 1.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float o = __shfl_sync(0xffffffffu, f[j], src, LPR);
-                        if (!isv && lr < 2 * hc) {
-                            const float2 cs = s_cs[i0 + j];
-                            f[j] = f[j] * cs.x + o * (sign * cs.y);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s_row[r0][lr * 8 + j] = f[j];
-                    __syncwarp();
-                    if (!isv) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int e = lr * 8 + j;
-                            if (e < p.rot) {
-                                const float2 cs = s_cs[e < half ? e : e - half];
-                                const float o = s_row[r0][e < half ? e + half : e - half];
-                                f[j] = f[j] * cs.x + o * (e < half ? -cs.y : cs.y);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            float amax = 0.f;
-            if constexpr (Q8) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-#pragma unroll
-                for (int off = LPR / 2; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            }
-            if (!in) continue;
-            if (isq) {
-                x[u].put(f);
-                x[u].store(static_cast<Act*>(p.q_out) + (tok * p.Hq + r) * D + lr * 8);
-            } else if (keep) {
-                const int h = isv ? r - p.Hq - p.Hkv : r - p.Hq;
-                const long long off = p.layer_off + row_base + h * head_stride + (isv ? p.kv_off : 0);
-                if constexpr (Q8) {
-                    const float sc = __fdiv_rn(amax, 127.f);
-                    uint32_t lo = 0, hi = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        lo |= ((uint32_t)q8_code(f[j], sc) & 0xffu) << (8 * j);
-                        hi |= ((uint32_t)q8_code(f[4 + j], sc) & 0xffu) << (8 * j);
-                    }
-                    *reinterpret_cast<uint2*>(static_cast<int8_t*>(p.cache) + off + lr * 8) = make_uint2(lo, hi);
-                    if (lr == 0)
-                        p.scales[p.sc_layer_off + (row_base + h * head_stride) / D + (isv ? p.sc_kv_off : 0)] = sc;
-                } else {
-                    x[u].put(f);
-                    x[u].store(static_cast<Act*>(p.cache) + off + lr * 8);
-                }
-            }
+            if constexpr (Q8) x[u].get(f);
+            qk_store<Act, D, Q8>(p, x[u], f, row_base + r * head_stride, true, keep && r < v1, lr);
         }
     }
 }
@@ -288,12 +340,12 @@ cudaError_t launch_qk(const QkParams& p, dim3 grid, cudaStream_t stream) {
 }
 
 // The grid: one CTA per token; few tokens: a token's rows over several CTAs, so
-// that two CTAs per SM are busy.
+// that every SM has eight.
 cudaError_t dispatch_qk(int dtype, int D, int B, QkParams& p, cudaStream_t s) {
     const int R = p.Hq + 2 * p.Hkv, RP = kQkThreads / (D / 8);
     const long long tokens = (long long)B * p.n_new;
     int parts = (R + RP - 1) / RP;
-    if (tokens * parts > 2 * 152) parts = (int)((2 * 152 + tokens - 1) / tokens);
+    if (tokens * parts > 8 * 152) parts = (int)((8 * 152 + tokens - 1) / tokens);
     if (parts > 65535) parts = 65535;
     p.rows_per_z = ((R + parts - 1) / parts + RP - 1) / RP * RP;
     const dim3 grid(p.n_new, B, (R + p.rows_per_z - 1) / p.rows_per_z);
@@ -457,7 +509,7 @@ KVC_API int kvc_append_qk(const kvc_desc* d, void* cache, int32_t layer, const v
     p.offset = qk->weight_offset;
     if (rotates) {
         p.rot = rot->dim;
-        p.interleaved = rot->pairs == KVC_PAIRS_INTERLEAVED;
+        p.mode = rot->pairs == KVC_PAIRS_INTERLEAVED ? kRotPairs : (rot->dim % 16 == 0 ? kRotChunks : kRotAny);
         p.mag = rot->magnitude;
         for (int i = 0; i < rot->dim / 2; ++i) p.turns[i] = rot->turns[i];
     }
