@@ -243,6 +243,7 @@ class _Sizes:
 
 
 _sizes: dict = {}
+_INT32, _UINT8 = torch.int32, torch.uint8
 
 
 def _sizes_of(d: KvcDesc) -> _Sizes:
@@ -264,8 +265,8 @@ def _on_device(t: torch.Tensor, dev: int, name: str):
 def _take(t: torch.Tensor, name: str, dtype, numel, dev: int) -> int:
     """The address of a dense tensor of the call, checked (`numel` None: any size)."""
     try:
-        if (t.dtype == dtype and t.is_contiguous() and t.get_device() == dev >= 0
-                and (numel is None or t.numel() == numel)):
+        if (t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and (numel is None or t.numel() == numel)
+                and dev >= 0):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -275,13 +276,14 @@ def _take(t: torch.Tensor, name: str, dtype, numel, dev: int) -> int:
 
 
 def _take_cache(z: _Sizes, cache: torch.Tensor, dev: int) -> int:
-    if isinstance(cache, torch.Tensor) and cache.numel() * cache.element_size() < z.cache_bytes:
+    if isinstance(cache, torch.Tensor) and cache.nbytes < z.cache_bytes:
         raise ValueError(f"cache holds {cache.numel() * cache.element_size()} bytes, the descriptor needs {z.cache_bytes}")
     return _take(cache, "cache", z.cache, None, dev)
 
 
-def _current_device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+def _device_of(q: torch.Tensor) -> int:
+    """The current device, for a call whose first tensor is q (-1: q is no CUDA tensor, which its own check reports)."""
+    return torch._C._cuda_getDevice() if isinstance(q, torch.Tensor) and q.is_cuda else -1
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -385,12 +387,13 @@ def _tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: in
     between tokens (n = 1: [B, heads, D] too)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev or dev < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _on_device(t, dev, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _on_device(t, dev, name)
-    shape, st = tuple(t.shape), t.stride()
+    shape, st = t.shape, t.stride()
     if len(shape) == 3 and n == 1:
         shape, st = (shape[0], 1, shape[1], shape[2]), (st[0], st[0], st[1], st[2])
     if shape != (B, n, heads, D):
@@ -411,7 +414,7 @@ def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_ne
 
     q [batch, n_new, q_heads, D], k_new / v_new [batch, n_new, kv_heads, D] (or without n_new for one
     token); they may be views of one packed projection.  q_out: dense, like q (None: a new tensor)."""
-    z, dev = _sizes_of(d), _current_device()
+    z, dev = _sizes_of(d), _device_of(q)
     n_new = 1 if q.dim() == 3 else q.shape[1] if q.dim() == 4 else -1
     if n_new < 1:
         raise ValueError("q must be [batch, n_new, q_heads, head_dim]")
@@ -425,10 +428,10 @@ def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_ne
         raise ValueError("q_out may be q itself only when q is contiguous")
     rc = lib().kvc_append_qk(
         ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, kp, vp, qs, ks, vs, n_new,
-        _take(pos, "pos", torch.int32, z.B, dev),
-        None if n_tok is None else _take(n_tok, "n_tok", torch.int32, z.B, dev),
-        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
-        ctypes.byref(qk), out, _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        _take(pos, "pos", _INT32, z.B, dev),
+        None if n_tok is None else _take(n_tok, "n_tok", _INT32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", _INT32, z.table, dev),
+        ctypes.byref(qk), out, _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(),
         _raw_stream(stream, dev))
     if rc:
         raise KvcError(rc, "kvc_append_qk")
@@ -489,17 +492,17 @@ def decode_attention_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
                             valid_bits: torch.Tensor | None = None, out: torch.Tensor | None = None,
                             stream=None) -> torch.Tensor:
     """kvc_decode_attention_scored: decode_attention with capped, biased scores and a first position."""
-    z, dev = _sizes_of(d), _current_device()
+    z, dev = _sizes_of(d), _device_of(q)
     qp = _take(q, "q", z.act, z.q, dev)
     if out is None:
         out = torch.empty(z.shape, dtype=z.act, device=q.device)
     _need_score(z, score, 1, dev)
     rc = lib().kvc_decode_attention_scored(
-        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", torch.int32, z.B, dev),
-        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
-        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", _INT32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
         ctypes.byref(score), _take(out, "out", z.act, z.q, dev),
-        _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         raise KvcError(rc, "kvc_decode_attention_scored")
     return out
@@ -523,15 +526,15 @@ def decode_attention_shared(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
                             stream=None) -> torch.Tensor:
     """kvc_decode_attention_shared: decode_attention of a paged batch; the sequences of a group (int32 [batch],
     below 0: alone) share leading blocks, whose keys and values are read once for the group."""
-    z, dev = _sizes_of(d), _current_device()
+    z, dev = _sizes_of(d), _device_of(q)
     qp = _take(q, "q", z.act, z.q, dev)
     if out is None:
         out = torch.empty(z.shape, dtype=z.act, device=q.device)
     rc = lib().kvc_decode_attention_shared(
-        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", torch.int32, z.B, dev),
-        _take(group, "group", torch.int32, z.B, dev), _take(block_table, "block_table", torch.int32, z.table, dev),
-        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
-        _take(out, "out", z.act, z.q, dev), _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", _INT32, z.B, dev),
+        _take(group, "group", _INT32, z.B, dev), _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
+        _take(out, "out", z.act, z.q, dev), _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(),
         _raw_stream(stream, dev))
     if rc:
         raise KvcError(rc, "kvc_decode_attention_shared")
@@ -610,7 +613,7 @@ def prefill_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor,
                    block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kvc_prefill_scored: prefill with capped, biased scores and a first position for each token."""
-    z, dev = _sizes_of(d), _current_device()
+    z, dev = _sizes_of(d), _device_of(q)
     qp = _take(q, "q", z.act, None, dev)
     T = q.numel() // z.q
     if q.numel() != T * z.q:
@@ -620,11 +623,11 @@ def prefill_scored(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor,
     _need_score(z, score, T, dev)
     rc = lib().kvc_prefill_scored(
         ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(k_new, "k_new", z.act, z.kv * T, dev),
-        _take(v_new, "v_new", z.act, z.kv * T, dev), T, _take(pos0, "pos0", torch.int32, z.B, dev),
-        None if block_table is None else _take(block_table, "block_table", torch.int32, z.table, dev),
-        None if valid_bits is None else _take(valid_bits, "valid_bits", torch.int32, z.valid, dev),
+        _take(v_new, "v_new", z.act, z.kv * T, dev), T, _take(pos0, "pos0", _INT32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
         ctypes.byref(score), _take(out, "out", z.act, z.q * T, dev),
-        _take(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         raise KvcError(rc, "kvc_prefill_scored")
     return out
