@@ -420,11 +420,16 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         sh.layer = layer;
         sh.tq = 128 / g.G;
         sh.mq = sh.tq * shared_q_tiles(d->head_dim);
+        sh.full_units = shared_q_tiles(d->head_dim);
         sh.ctas = kSharedCtas;
         sh.rope = d->rope;
         sh.scale2 = p.q_scale;
         for (int i = 0; i < d->head_dim / 2; ++i) sh.theta[i] = p.theta[i];
-        if (launch_shared_plan(sh, s) != cudaSuccess) return KVC_ERR_CUDA;
+        // the prefix before the plan of the rest: that plan needs only the first
+        // kernel's results, which are there once the prefix kernel lets it launch, and
+        // runs beside it
+        if (launch_shared_plan(sh, s) != cudaSuccess || launch_shared_prefix(d->head_dim, sh, sh_map, s) != cudaSuccess)
+            return KVC_ERR_CUDA;
         p.no_combine = 1;
     }
     const int32_t* const start = group ? sh.start : sp.start;
@@ -444,6 +449,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         pp.table = block_table;
         pp.valid = valid_bits;
         pp.start = start;
+        pp.late_wait = group != nullptr;
         pp.err = p.err;
         pp.seq_off = reinterpret_cast<long long*>(ws + w.plan_acc);
         pp.seq_rows = reinterpret_cast<int32_t*>(ws + w.plan_acc + (size_t)d->batch * 8);
@@ -495,7 +501,6 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         p.cta_items = pp.cta_items;
     }
     const bool rd = d->rope == KVC_ROPE_READ_INCACHE;
-    if (group && launch_shared_prefix(d->head_dim, sh, sh_map, s) != cudaSuccess) return KVC_ERR_CUDA;
     if (d->dtype != KVC_F32) {
         if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, score != nullptr, p, maps, grid, s) !=
             cudaSuccess)

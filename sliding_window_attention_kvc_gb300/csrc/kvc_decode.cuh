@@ -188,6 +188,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     const int tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     const int item = blockIdx.x, kvh = blockIdx.y, z = blockIdx.z;
+    if constexpr (SCORE) {
+        // launched while the previous kernel in the stream drains (launch_decode_t)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
 
     // ---- which sequence, which rows --------------------------------------
     int b, first_item, nparts;
@@ -579,6 +584,29 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     }
     named_sync(1, kConsumerWarps * 32);
 
+    if constexpr (SCORE) {
+        if (nparts == 1) {
+            // one part: its own result, without the partial's round trip
+            for (int idx = ctid; idx < GH * D; idx += kConsumerWarps * 32) {
+                const int h = idx / D, d = idx % D;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, merge_ml[w * GH + h].x);
+                float L = 0.f, O = 0.f;
+#pragma unroll
+                for (int w = 0; w < kConsumerWarps; ++w) {
+                    const float2 ml = merge_ml[w * GH + h];
+                    const float e = (ml.x == M) ? 1.f : exp2f(ml.x - M);
+                    L += ml.y * e;
+                    O += merge_o[(w * GH + h) * D + d] * e;
+                }
+                static_cast<Elt*>(p.out)[((long long)b * p.Hq + kvh * p.G + z * GH + h) * D + d] =
+                    TR::from_f32(L > 0.f ? O / L : 0.f);
+            }
+            return;
+        }
+    }
+
     // ---- merge the warps, write this CTA's partial ------------------------
     for (int idx = ctid; idx < GH * D; idx += kConsumerWarps * 32) {
         const int h = idx / D, d = idx % D;
@@ -644,6 +672,19 @@ cudaError_t launch_decode_t(const DecodeParams& p, dim3 grid, cudaStream_t strea
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_relaxed);
+    }
+    if constexpr (SCORE) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kDecodeThreads);
+        cfg.dynamicSmemBytes = SM::kTotal;
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p);
     }
     kern<<<grid, kDecodeThreads, SM::kTotal, stream>>>(p);
     return cudaGetLastError();

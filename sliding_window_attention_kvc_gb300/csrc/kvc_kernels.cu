@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(const __grid_co
     __shared__ int s_tok_phys;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x;
-    plan_pdl_wait();            // positions, table, valid bits may come from the previous kernel
+    if (!p.late_wait) plan_pdl_wait();            // positions, table, valid bits may come from the previous kernel
     // the decode kernel may launch now: it waits for this grid to complete
     // before it reads anything
     plan_pdl_launch();
@@ -734,6 +734,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(const __grid_co
     int rb = 0;
     plan_block_scan<int>(sum, s_wi, &rb);
     if (tid == 0) p.seq_rows[b] = rb;
+    // this grid's end is then the end of the one before it too, for the kernels behind
+    if (p.late_wait) plan_pdl_wait();
 }
 
 cudaError_t launch_plan_rows(const PlanParams& p, cudaStream_t stream) {

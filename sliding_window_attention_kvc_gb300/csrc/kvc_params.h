@@ -145,6 +145,8 @@ struct PlanParams {
     int dir_groups;
     uint32_t* refs;       // plan_rows_kernel: [num_blocks] += 1 per sequence attending the block
     const int32_t* start; // [B]: blocks wholly below it are not attended; may be null
+    int late_wait;        // plan_rows_kernel: everything it reads is ready when it may launch; it waits
+                          // for the kernel before it only at its end (kvc_decode_attention_shared)
     int B, bs, num_blocks, maxb, max_items, ctas;
     // the step's new token (kvc_decode_step); k_new == null: none
     void* cache;

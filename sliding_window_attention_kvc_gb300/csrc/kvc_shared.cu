@@ -17,9 +17,10 @@
 //   shared_combine_kernel one warp per (sequence, q head).
 //
 // Prefix work.  A column is (group, kv head, up to NQ x 128 rows of members x q
-// heads); its keys are cut into tiles of 64.  All tiles of all columns, laid end
-// to end, are split into nearly equal contiguous shares, one per CTA (one CTA per SM);
-// the part of a column in a share is a segment and leaves one partial per row.
+// heads); its keys are cut into tiles of 64, a unit of work for each Q tile.  All
+// units of all columns, laid end to end, are split into nearly equal contiguous
+// shares, one per CTA (one CTA per SM); the part of a column in a share is a
+// segment and leaves one partial per row.
 // What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for 4 x
 // 64 x 128 x D flops a Q tile, so up to one Q tile the bytes bound, beyond it
 // the softmax.
@@ -163,7 +164,10 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
             g.rows = common * p.bs;
             g.kt = (g.rows + kWsKeys - 1) / kWsKeys;
             g.mt = (g.n + p.mq - 1) / p.mq;
-            u = (long long)p.Hkv * g.mt * g.kt;
+            // the columns of a kv head: full ones of two units a tile, and a last one
+            const int last = g.n - (g.mt - 1) * p.mq;
+            g.hu = g.kt * ((g.mt - 1) * p.full_units + (last <= p.tq ? 1 : p.full_units));
+            u = (long long)p.Hkv * g.hu;
             r = (long long)p.Hkv * g.n * p.G;
         }
         long long iu = u, ir = r;
@@ -284,7 +288,8 @@ __device__ __forceinline__ void px_rotate8(uint4& lo, uint4& hi, long long pos, 
 // One segment: tiles tile0 .. tile0 + nt - 1 of a column.
 struct PxSegment {
     int h, m0, members, off, leader, rows;     // kv head, first member's rank and members, the group's list and prefix
-    int tile0, nt;
+    int tile0, nt;                             // nt may be 0: one unit of a tile that begins in the share before
+    long long units;
     int alt;                                   // one Q tile's rows: the warpgroups take alternate tiles
     long long row0;                            // partial row of the column's first row, before the share's own offset
     __device__ __forceinline__ bool active(int i, int t) const { return !alt || (t & 1) == i; }
@@ -303,15 +308,21 @@ __device__ __forceinline__ PxSegment px_segment(const SharedParams& p, int ngrou
         if (le != 0xffffffffu) break;
     }
     const SharedGroup* g = p.groups + gi;
-    const int kt = __ldcg(&g->kt), mt = __ldcg(&g->mt), n = __ldcg(&g->n);
-    const long long v = u - __ldcg(&g->units0);
-    const int col = (int)(v / kt);
+    const int kt = __ldcg(&g->kt), n = __ldcg(&g->n), hu = __ldcg(&g->hu);
+    long long v = u - __ldcg(&g->units0);
     PxSegment s;
-    s.tile0 = (int)(v - (long long)col * kt);
-    s.nt = (int)min((long long)(kt - s.tile0), hi - u);
-    s.h = col / mt;
-    s.m0 = (col - s.h * mt) * p.mq;
+    s.h = (int)(v / hu);
+    v -= (long long)s.h * hu;
+    const int m = (int)(v / ((long long)kt * p.full_units));     // every column but a head's last is full
+    v -= (long long)m * kt * p.full_units;
+    s.m0 = m * p.mq;
     s.members = min(p.mq, n - s.m0);
+    // units to tiles: a tile belongs to the share that holds its first unit
+    const int per = s.members <= p.tq ? 1 : p.full_units;
+    const long long take = min((long long)kt * per - v, hi - u);
+    s.units = take;
+    s.tile0 = (int)((v + per - 1) / per);
+    s.nt = (int)((v + take + per - 1) / per) - s.tile0;
     s.off = __ldcg(&g->off);
     s.leader = __ldcg(&g->leader);
     s.rows = __ldcg(&g->rows);
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                     ++idx;
                 }
             }
-            u += sg.nt;
+            u += sg.units;
         }
         // never leave with copies landing in shared memory
         if (!ok && lane == 0)
@@ -445,11 +456,16 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
         // ============================ fix-up ===============================
         // V rows without a key may hold anything: zero them
         const int ft = tid - 64;
-        const int nt = (int)(hi - lo);
-        for (int j = 0; j < nt; ++j) {
+        int j = 0;
+        bool ok = true;
+        for (long long u = lo; u < hi && ok;) {
+            const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
+            u += sg.units;
+            for (const int end = j + sg.nt; j < end; ++j) {
             const int s = j % NST;
             if (!ws_wait(&bars->full[s], (j / NST) & 1, abort)) {
                 give_up();
+                ok = false;
                 break;
             }
             if (!((meta[s].present >> ft) & 1ull)) {
@@ -464,6 +480,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
             // (one arrival a warp: arrivals on one barrier are made one after the other)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->ready[s]);
+            }
         }
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 base[i] += sg.tiles(i);
                 loads[i] += sg.tiles(i) > 0;
             }
-            u += sg.nt;
+            u += sg.units;
         }
         if (lane == 0) {
             // every product this thread issued is done before TMEM is freed
@@ -695,7 +712,7 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
             }
             idx0 += sg.nt;
             base += nt;
-            u += sg.nt;
+            u += sg.units;
         }
     }
 
@@ -758,14 +775,15 @@ __global__ void __launch_bounds__(kShCombineWarps * 32)
     long long prow = 0;
     if (sg.x >= 0) {
         const SharedGroup* g = p.groups + sg.x;
-        const int kt = __ldcg(&g->kt), mt = __ldcg(&g->mt), n = __ldcg(&g->n), h = qh / p.G;
+        const int kt = __ldcg(&g->kt), n = __ldcg(&g->n), h = qh / p.G;
         const int m = sg.y / p.mq;
         const long long units = __ldcg(&p.head->units);
         const int shares = __ldcg(&p.head->shares);
-        const long long u0 = __ldcg(&g->units0) + ((long long)h * mt + m) * kt;
+        const bool one = min(p.mq, n - m * p.mq) <= p.tq;
+        const long long u0 = __ldcg(&g->units0) + (long long)h * __ldcg(&g->hu) + (long long)m * kt * p.full_units;
         fx = streamk_share_of(u0, units, shares);
-        np = streamk_share_of(u0 + kt - 1, units, shares) - fx + 1;
-        alt = shared_q_tiles(D) == 2 && min(p.mq, n - m * p.mq) <= p.tq;
+        np = streamk_share_of(u0 + (long long)kt * (one ? 1 : p.full_units) - 1, units, shares) - fx + 1;
+        alt = shared_q_tiles(D) == 2 && one;
         prow = __ldcg(&g->rows0) + ((long long)h * n + sg.y) * p.G + qh % p.G;
         if (alt) np *= 2;
     }

@@ -9,20 +9,21 @@ namespace kvc {
 // Q tiles of 128 rows of one column: head_dim 256 leaves tensor memory for one.
 __host__ __device__ constexpr int shared_q_tiles(int D) { return D == 256 ? 1 : 2; }
 constexpr int kSharedCtas = 152;                // one prefix CTA per SM
-// Fewest 64-key tiles of a share: below that, a share's partials and its start
+// Fewest units of a share: below that, a share's partials and its start
 // (a q load, the first copies) cost more than the tiles it takes off the others.
 constexpr int kSharedMinTiles = 2;
 
 struct SharedGroup {
-    long long units0;     // tiles of the groups before
+    long long units0;     // units of the groups before
     long long rows0;      // partial rows of the groups before
     int kt, mt;           // tiles of a column; columns of a kv head
     int n, off, leader;   // members, their place in the member list, the first of them
     int rows;             // shared rows (whole blocks)
+    int hu;               // units of a kv head
 };
 
 struct SharedHead {
-    long long units;      // tiles of all columns
+    long long units;      // of all columns
     int ngroups, shares;
 };
 
@@ -47,6 +48,7 @@ struct SharedParams {
     long long alt_rows;             // rows from a column's partials to those of its second warpgroup
     int B, Hq, Hkv, G, bs, num_blocks, maxb, layer;
     int tq, mq;                     // members of a Q tile, of a column
+    int full_units;                 // units a tile of a full column: its Q tiles
     int ctas;
     int rope;
     float scale2;                   // softmax scale * log2(e)
