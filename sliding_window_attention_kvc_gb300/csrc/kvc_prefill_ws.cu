@@ -84,7 +84,7 @@ static_assert(sizeof(WsStageMeta) % 16 == 0, "stage records keep the barriers al
 
 struct WsBars {
     uint64_t full[4], ready[4], empty[4];
-    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_ready[2], fin;
+    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_ready[2], fin[2];
     uint64_t fixb;           // INT8 with read-time RoPE: the fix-up threads, between expansion and rotation
     uint32_t tmem;
     int ntiles;              // set when the producer's end marker reaches the MMA thread
@@ -116,6 +116,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
     using S = WsShape<D>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
+    // modified scores over bf16 rows: an issuing warp for each Q tile, the second in the
+    // place of a fix-up warp, which has little to do
+    constexpr bool TWO = SCORE && !Q8;
     extern __shared__ unsigned char ws_raw[];
     const uint32_t raw_u = smem_u32(ws_raw);
     unsigned char* sm = ws_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
@@ -143,8 +146,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], 2);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->ready[s], TWO ? 1 : 2);
+            mbar_init(&bars->empty[s], TWO ? NQ : 1);
         }
         for (int i = 0; i < 2; ++i) {
             for (int u = 0; u < 2; ++u) {
@@ -155,7 +158,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
         }
-        mbar_init(&bars->fin, 1);
+        mbar_init(&bars->fin[0], 1);
+        mbar_init(&bars->fin[1], 1);
         mbar_init(&bars->fixb, 64);
         bars->ntiles = 0x7fffffff;
         bars->abort = 0;
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         // never leave with copies landing in shared memory
         if (!ok && lane == 0)
             for (int k = (idx > NST ? idx - NST : 0); k < idx; ++k) mbar_wait(&bars->full[k % NST], (k / NST) & 1);
-    } else if (warp == 2 || warp == 3) {
+    } else if (warp == 2 || (!TWO && warp == 3)) {
         // ============================ fix-up ===============================
         const int ft = tid - 64;                       // 0 .. 63
         uint32_t fix_phase = 0;
@@ -502,15 +506,17 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     }
                 }
                 if (meta[s].any_absent) {
-                    // V rows of absent keys to zero: 64 threads, one row each
-                    if (meta[s].pos[ft] < 0) {
+                    // V rows of absent keys to zero: 64 threads, one row each (32: two)
+#pragma unroll 1
+                    for (int r = ft; r < kWsKeys; r += TWO ? 32 : 64)
+                        if (meta[s].pos[r] < 0) {
 #pragma unroll
-                        for (int cb = 0; cb < CB; ++cb)
+                            for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                            for (int ch = 0; ch < 8; ++ch)
-                                *reinterpret_cast<uint4*>(st + cb * S::KVBlock + kWsKeys * 128 + ft * 128 + ch * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                    }
+                                for (int ch = 0; ch < 8; ++ch)
+                                    *reinterpret_cast<uint4*>(st + cb * S::KVBlock + kWsKeys * 128 + r * 128 + ch * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        }
                     wrote = true;
                 }
                 if constexpr (READ && Q8) {
@@ -587,6 +593,71 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             if (lane == 0) mbar_arrive(&bars->ready[s]);
             if (kind == kTileEnd) break;
         }
+    } else if (TWO && (warp == 1 || (NQ == 2 && warp == 3))) {
+        // ================== MMA issuers, one for each Q tile =================
+        // S_i = Q_i K^T a tile ahead of O_i += P_i V.  (One thread for both took 3300 to
+        // 4100 cycles a tile of both, 1460 of them on products: the waits and commits
+        // of one now pass while the other's products run.)  The whole warp walks the
+        // tiles, its values stay uniform; lane 0 issues.
+        const int i = warp >> 1;
+        const uint64_t qd = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
+        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
+        const uint32_t s_t = tmem + S::SCol0 + (uint32_t)(i * 2 * kWsKeys), o_t = tmem + (uint32_t)(i * D);
+        bool ok = ws_wait(&bars->q_ready[i], 0, abort);
+        int ns = 0, npv = 0, nt = 0x7fffffff;              // S issued, P V issued, tiles
+        long long c0 = clock64();
+        while (ok && npv < nt) {
+            // (each barrier's phases are asked for in order)
+            if (ns < nt && ns < npv + 2 && ws_test(&bars->ready[ns % NST], (ns / NST) & 1)) {
+                const int s = ns % NST;
+                if (meta[s].kind == kTileEnd) {
+                    nt = ns;
+                } else {
+                    ws_fence_after();
+                    if (lane == 0) {
+                        ws_issue_s<D, kWsRows * 128, S::KVBlock>(s_t + (uint32_t)((ns & 1) * kWsKeys), qd,
+                                                                 kd0 + (uint64_t)((s * S::StageBytes) >> 4));
+                        ws_commit(&bars->s_full[i][ns & 1]);
+                    }
+                    __syncwarp();
+                    ++ns;
+                }
+                c0 = clock64();
+                continue;
+            }
+            if (npv < ns && ws_test(&bars->p_full[i], npv & 1)) {
+                ws_fence_after();
+                const int s = npv % NST;
+                if (lane == 0) {
+                    // P_i in the S buffer it came from (bf16 pairs, 32 columns)
+                    ws_issue_pv<D>(o_t, s_t + (uint32_t)((npv & 1) * kWsKeys),
+                                   vd0 + (uint64_t)((s * S::StageBytes) >> 4), npv > 0);
+                    ws_commit(&bars->o_done[i]);
+                    ws_commit(&bars->empty[s]);            // this Q tile is done with the tile's K and V
+                }
+                __syncwarp();
+                ++npv;
+                c0 = clock64();
+                continue;
+            }
+            if (*abort || clock64() - c0 > kWaitCycles) ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) {
+            if (ok) {
+                // the end: the softmax warps learn the tile count at the S slot they wait
+                // on next (every S before it has been consumed)
+                bars->ntiles = nt;
+                mbar_arrive(&bars->s_full[i][nt & 1]);
+            } else {
+                give_up();
+            }
+            // every product this thread issued is done before TMEM is freed
+            ws_commit(&bars->fin[i]);
+            if (!mbar_wait(&bars->fin[i], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
         // the whole warp walks the tiles (its values stay uniform); lane 0 issues
@@ -678,8 +749,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     give_up();
                 }
                 // every product this thread issued is done before TMEM is freed
-                ws_commit(&bars->fin);
-                if (!mbar_wait(&bars->fin, 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+                ws_commit(&bars->fin[0]);
+                if (!mbar_wait(&bars->fin[0], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
             }
         }
         __syncwarp();
@@ -773,7 +844,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             ws_wait_ld();
             ws_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
+            if (!TWO && lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
             if (READ && sink_tile && j == 0) write_q(false);     // S of the sink tile is out of TMEM
             const int s = j % NST;
             if (!ws_wait(&bars->ready[s], (j / NST) & 1, abort)) {    // the stage's meta

@@ -252,7 +252,7 @@ struct alignas(16) PxStageMeta {
 
 struct PxBars {
     uint64_t full[6], ready[6], empty[6];
-    uint64_t s_full[2][2], s_free[2][2], p_full[2], o_done[2], q_ready[2], fin;
+    uint64_t s_full[2][2], p_full[2], o_done[2], q_ready[2], fin[2];
     uint32_t tmem;
     int abort;
 };
@@ -292,8 +292,6 @@ struct PxSegment {
     long long units;
     int alt;                                   // one Q tile's rows: the warpgroups take alternate tiles
     long long row0;                            // partial row of the column's first row, before the share's own offset
-    __device__ __forceinline__ bool active(int i, int t) const { return !alt || (t & 1) == i; }
-    __device__ __forceinline__ int local(int t) const { return alt ? t >> 1 : t; }
     __device__ __forceinline__ int tiles(int i) const { return alt ? (nt + 1 - i) >> 1 : nt; }
 };
 
@@ -348,19 +346,18 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], 2);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->ready[s], 1);
+            mbar_init(&bars->empty[s], NQ);
         }
         for (int i = 0; i < 2; ++i) {
             for (int u = 0; u < 2; ++u) {
                 mbar_init(&bars->s_full[i][u], 1);
-                mbar_init(&bars->s_free[i][u], 4);
             }
             mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
+            mbar_init(&bars->fin[i], 1);
         }
-        mbar_init(&bars->fin, 1);
         bars->abort = 0;
         mbar_fence_init();
         tma_prefetch_desc(&map);
@@ -452,120 +449,117 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
         // never leave with copies landing in shared memory
         if (!ok && lane == 0)
             for (int k = (idx > NST ? idx - NST : 0); k < idx; ++k) mbar_wait(&bars->full[k % NST], (k / NST) & 1);
-    } else if (warp == 2 || warp == 3) {
+    } else if (warp == 2) {
         // ============================ fix-up ===============================
         // V rows without a key may hold anything: zero them
-        const int ft = tid - 64;
         int j = 0;
         bool ok = true;
         for (long long u = lo; u < hi && ok;) {
             const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
             u += sg.units;
             for (const int end = j + sg.nt; j < end; ++j) {
-            const int s = j % NST;
-            if (!ws_wait(&bars->full[s], (j / NST) & 1, abort)) {
-                give_up();
-                ok = false;
-                break;
-            }
-            if (!((meta[s].present >> ft) & 1ull)) {
-                unsigned char* st = sm + S::OffStage + s * S::StageBytes + kWsKeys * 128 + ft * 128;
+                const int s = j % NST;
+                if (!ws_wait(&bars->full[s], (j / NST) & 1, abort)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const unsigned long long present = meta[s].present;
+                if (present != ~0ull) {
+#pragma unroll 1
+                    for (int r = lane; r < kWsKeys; r += 32) {
+                        if ((present >> r) & 1ull) continue;
+                        unsigned char* st = sm + S::OffStage + s * S::StageBytes + kWsKeys * 128 + r * 128;
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
+                        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                    for (int ch = 0; ch < 8; ++ch)
-                        *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-            }
-            // (one arrival a warp: arrivals on one barrier are made one after the other)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->ready[s]);
+                            for (int ch = 0; ch < 8; ++ch)
+                                *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                // (one arrival a warp: arrivals on one barrier are made one after the other)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->ready[s]);
             }
         }
-    } else if (warp == 1) {
-        // =========================== MMA issuer =============================
-        // (the whole warp walks the tiles, its values stay uniform; lane 0 issues)
-        constexpr int LA = NST >= 3 ? 2 : 1;           // tiles that S runs ahead of P V
+    } else if (warp == 1 || (NQ == 2 && warp == 3)) {
+        // ========================== MMA issuers =============================
+        // One warp for each Q tile: S_i = Q_i K^T a tile ahead of O_i += P_i V.  (One
+        // thread for both spent 3270 cycles a tile of both, 1460 of them on products:
+        // the waits and commits of one now pass while the other's products run.)  The
+        // whole warp walks the tiles, its values stay uniform; lane 0 issues.
+        const int i = warp >> 1;
         bool ok = true;
-        int idx0 = 0;                                  // tiles of the segments before
-        int base[2] = {0, 0};                          // ... and of each Q tile
-        int loads[2] = {0, 0};                         // segments each Q tile was loaded for
-        uint64_t qd[NQ];
-        for (int i = 0; i < NQ; ++i) qd[i] = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        int idx0 = 0, base = 0, loads = 0;             // tiles of the segments before; of this Q tile; its loads
+        const uint64_t qd = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
         const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
         const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
-        for (long long u = lo; u < hi;) {
+        const uint32_t s0 = tmem + S::SCol0 + (uint32_t)(i * 2 * kWsKeys), o_t = tmem + (uint32_t)(i * D);
+        for (long long u = lo; u < hi && ok;) {
             const PxSegment sg = px_segment<D>(p, ngroups, u, hi);
-            if (ok) {
-                for (int i = 0; i < NQ && ok; ++i)
-                    if (sg.tiles(i) > 0 && !ws_wait(&bars->q_ready[i], loads[i] & 1, abort)) ok = false;
-                auto issue_s = [&](int t) -> bool {
-                    const int s = (idx0 + t) % NST;
-                    if (!ws_wait(&bars->ready[s], ((idx0 + t) / NST) & 1, abort)) return false;
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        if (!sg.active(i, t)) continue;
-                        const int j = base[i] + sg.local(t);
-                        if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) return false;
-                        ws_fence_after();
-                        const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                        if (lane == 0) {
-                            ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i],
-                                                                     kd0 + (uint64_t)((s * S::StageBytes) >> 4));
-                            ws_commit(&bars->s_full[i][j & 1]);
-                        }
-                        __syncwarp();
-                    }
-                    return true;
-                };
-                int issued = 0;
-                while (ok && issued < LA && issued < sg.nt) {
-                    ok = issue_s(issued);
-                    ++issued;
-                }
-                for (int t = 0; t < sg.nt && ok; ++t) {
-                    const int s = (idx0 + t) % NST;
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        if (!ok || !sg.active(i, t)) continue;
-                        const int lt = sg.local(t), j = base[i] + lt;
-                        if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
-                            ok = false;
-                            continue;
-                        }
-                        ws_fence_after();
-                        // P_i in the S buffer it came from (bf16 pairs)
-                        const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                        if (lane == 0) {
-                            ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + (uint64_t)((s * S::StageBytes) >> 4),
-                                           lt > 0);
-                            ws_commit(&bars->o_done[i]);
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    if (lane == 0) ws_commit(&bars->empty[s]);     // K and V of the tile are done with
-                    __syncwarp();
-                    if (issued < sg.nt) {
-                        ok = issue_s(issued);
-                        ++issued;
-                    }
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok && lane == 0) give_up();
+            const int own = sg.tiles(i), others = sg.nt - own;
+            if (own > 0) {
+                ok = ws_wait(&bars->q_ready[i], loads & 1, abort);
+                ++loads;
             }
+            int ns = 0, npv = 0, nother = 0;           // S issued, P V issued, the other Q tile's tiles passed
+            long long t0 = clock64();
+            while (ok && (npv < own || nother < others)) {
+                // (each barrier's phases are asked for in order)
+                if (ns < own && ns < npv + 2) {
+                    const int t = idx0 + (sg.alt ? 2 * ns + i : ns), s = t % NST;
+                    if (ws_test(&bars->ready[s], (t / NST) & 1)) {
+                        ws_fence_after();
+                        if (lane == 0) {
+                            ws_issue_s<D, kWsRows * 128, S::KVBlock>(s0 + (uint32_t)(((base + ns) & 1) * kWsKeys), qd,
+                                                                     kd0 + (uint64_t)((s * S::StageBytes) >> 4));
+                            ws_commit(&bars->s_full[i][(base + ns) & 1]);
+                        }
+                        __syncwarp();
+                        ++ns;
+                        t0 = clock64();
+                        continue;
+                    }
+                }
+                if (npv < ns && ws_test(&bars->p_full[i], (base + npv) & 1)) {
+                    ws_fence_after();
+                    const int t = idx0 + (sg.alt ? 2 * npv + i : npv), s = t % NST;
+                    if (lane == 0) {
+                        // P_i in the S buffer it came from (bf16 pairs)
+                        ws_issue_pv<D>(o_t, s0 + (uint32_t)(((base + npv) & 1) * kWsKeys),
+                                       vd0 + (uint64_t)((s * S::StageBytes) >> 4), npv > 0);
+                        ws_commit(&bars->o_done[i]);
+                        ws_commit(&bars->empty[s]);        // this Q tile is done with the tile's K and V
+                    }
+                    __syncwarp();
+                    ++npv;
+                    t0 = clock64();
+                    continue;
+                }
+                if (nother < others) {
+                    const int t = idx0 + 2 * nother + (i ^ 1), s = t % NST;
+                    if (ws_test(&bars->ready[s], (t / NST) & 1)) {
+                        if (lane == 0) mbar_arrive(&bars->empty[s]);
+                        __syncwarp();
+                        ++nother;
+                        t0 = clock64();
+                        continue;
+                    }
+                }
+                if (*abort || clock64() - t0 > kWaitCycles) ok = false;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok && lane == 0) give_up();
             __syncwarp();
             idx0 += sg.nt;
-            for (int i = 0; i < NQ; ++i) {
-                base[i] += sg.tiles(i);
-                loads[i] += sg.tiles(i) > 0;
-            }
+            base += own;
             u += sg.units;
         }
         if (lane == 0) {
             // every product this thread issued is done before TMEM is freed
-            ws_commit(&bars->fin);
-            if (!mbar_wait(&bars->fin, 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+            ws_commit(&bars->fin[i]);
+            if (!mbar_wait(&bars->fin[i], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
         }
         __syncwarp();
     } else if (warp >= kShSoftmax0) {
@@ -623,9 +617,6 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                 ws_ld32(lane_base + scol, sv);
                 ws_ld32(lane_base + scol + 32, sv + 32);
                 ws_wait_ld();
-                ws_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
                 const int gt = idx0 + (sg.alt ? 2 * lt + qi : lt);
                 if (!ws_wait(&bars->ready[gt % NST], (gt / NST) & 1, abort)) {    // the stage's meta
                     ok = false;
