@@ -764,8 +764,11 @@ static int prefill_impl(const kvc_desc* d, void* cache, int32_t layer, const voi
     pp.sc_kv_off = ap.sc_kv_off;
     pp.half_rows = half_rows;
     if (d->rope != KVC_ROPE_NONE) fill_theta(d->head_dim, d->rope_base, pp.theta, nullptr);
-    if (ws_kernel) {
-        if (launch_prefill_ws(d->head_dim, q8, score != nullptr, pp, pm, s) != cudaSuccess) return KVC_ERR_CUDA;
+    if (score) {
+        if ((q8 ? launch_prefill_score_i8 : launch_prefill_score_bf16)(d->head_dim, pp, pm, s) != cudaSuccess)
+            return KVC_ERR_CUDA;
+    } else if (ws_kernel) {
+        if (launch_prefill_ws(d->head_dim, q8, pp, pm, s) != cudaSuccess) return KVC_ERR_CUDA;
     } else if (launch_prefill(d->head_dim, g.G, pp, s) != cudaSuccess) {
         return KVC_ERR_CUDA;
     }

@@ -295,8 +295,11 @@ cudaError_t launch_prefill_stage(const AppendParams& p, void* kst, void* vst, cu
 cudaError_t launch_prefill(int head_dim, int g, const PrefillParams& p, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, cudaStream_t stream);   // head_dim 128, tcgen05
 // head_dim 64 / 128 / 256, warp-specialised tcgen05 with TMA tiles
-cudaError_t launch_prefill_ws(int head_dim, bool q8, bool scored, const PrefillParams& p, const PrefillMaps& maps,
+cudaError_t launch_prefill_ws(int head_dim, bool q8, const PrefillParams& p, const PrefillMaps& maps,
                               cudaStream_t stream);
+// the same with modified scores (kvc_prefill_scored)
+cudaError_t launch_prefill_score_bf16(int head_dim, const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);
+cudaError_t launch_prefill_score_i8(int head_dim, const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);
 cudaError_t launch_valid_write(const TableParams& p, cudaStream_t stream);
 cudaError_t launch_block_prepare(int elt, const BlockParams& p, cudaStream_t stream);
 cudaError_t launch_block_share(const BlockParams& p, int n, cudaStream_t stream);
