@@ -299,7 +299,49 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             ++idx;
         };
+        // the chunk's own rows, tokens i_s .. i_s + 63
+        auto issue_stage_tile = [&](int i_s) {
+            if (SCORE && pos0 + min(i_s + kWsKeys - 1, i_last) < smin) return;   // no token sees this tile
+            const int s = acquire();
+            if (!ok) return;
+            int absent = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = lane + 32 * u;
+                const int i = i_s + r;
+                const int q = (i <= i_last && pos0 + i >= 0 && (!SCORE || pos0 + i >= smin)) ? pos0 + i : -1;
+                meta[s].pos[r] = q;
+                if constexpr (SCORE) meta[s].rel[r] = (float)i;
+                absent |= q < 0;
+            }
+            absent = __any_sync(0xffffffffu, absent);
+            __syncwarp();
+            if (lane == 0) {
+                meta[s].kind = kTileStage;
+                meta[s].any_absent = absent;
+                meta[s].mask = kMaskRange;
+                meta[s].kbase = pos0 + i_s;
+                unsigned char* dst = sm + S::OffStage + s * S::StageBytes;
+                mbar_expect_tx(&bars->full[s], (uint32_t)S::StageBytes);
+                if (SCORE && maps.direct) {
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) {
+                        tma_load_3d(dst + cb * S::KVBlock, &maps.stage_k, cb * 64, h, b * p.T + i_s, &bars->full[s]);
+                        tma_load_3d(dst + cb * S::KVBlock + kWsKeys * 128, &maps.stage_v, cb * 64, h, b * p.T + i_s,
+                                    &bars->full[s]);
+                    }
+                } else {
+                    tma_load_5d(dst, &maps.stage, 0, h, b * p.T + i_s, 0, 0, &bars->full[s]);
+                }
+                mbar_arrive(&bars->full[s]);
+            }
+            ++idx;
+        };
         if (t_hi >= 0) {
+            // modified scores take the chunk first and backwards: a distance bias favours
+            // near keys, and a reference maximum found at once need not move again
+            if (SCORE)
+                for (int i_s = i_last / kWsKeys * kWsKeys; i_s >= 0 && ok; i_s -= kWsKeys) issue_stage_tile(i_s);
             if (!paged) {
                 if (sink_tile) issue_slot_tile(0, kTileSink);
                 // slot tiles with at least one key the CTA can see
@@ -400,44 +442,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     ++idx;
                 }
             }
-            // the chunk's own rows, tokens 0 .. i_last, 64 to a tile
-            for (int i_s = 0; i_s <= i_last && ok; i_s += kWsKeys) {
-                if (SCORE && pos0 + min(i_s + kWsKeys - 1, i_last) < smin) continue;   // no token sees this tile
-                const int s = acquire();
-                if (!ok) break;
-                int absent = 0;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int r = lane + 32 * u;
-                    const int i = i_s + r;
-                    const int q = (i <= i_last && pos0 + i >= 0 && (!SCORE || pos0 + i >= smin)) ? pos0 + i : -1;
-                    meta[s].pos[r] = q;
-                    if constexpr (SCORE) meta[s].rel[r] = (float)i;
-                    absent |= q < 0;
-                }
-                absent = __any_sync(0xffffffffu, absent);
-                __syncwarp();
-                if (lane == 0) {
-                    meta[s].kind = kTileStage;
-                    meta[s].any_absent = absent;
-                    meta[s].mask = kMaskRange;
-                    meta[s].kbase = pos0 + i_s;
-                    unsigned char* dst = sm + S::OffStage + s * S::StageBytes;
-                    mbar_expect_tx(&bars->full[s], (uint32_t)S::StageBytes);
-                    if (SCORE && maps.direct) {
-#pragma unroll
-                        for (int cb = 0; cb < CB; ++cb) {
-                            tma_load_3d(dst + cb * S::KVBlock, &maps.stage_k, cb * 64, h, b * p.T + i_s, &bars->full[s]);
-                            tma_load_3d(dst + cb * S::KVBlock + kWsKeys * 128, &maps.stage_v, cb * 64, h, b * p.T + i_s,
-                                        &bars->full[s]);
-                        }
-                    } else {
-                        tma_load_5d(dst, &maps.stage, 0, h, b * p.T + i_s, 0, 0, &bars->full[s]);
-                    }
-                    mbar_arrive(&bars->full[s]);
-                }
-                ++idx;
-            }
+            if (!SCORE)
+                for (int i_s = 0; i_s <= i_last && ok; i_s += kWsKeys) issue_stage_tile(i_s);
         }
         // end marker
         if (ok) {
