@@ -42,7 +42,9 @@ constexpr float kWsLazy = 8.f;
 
 // Score modifiers a kernel is built for: a branch for each inside one kernel held the
 // softmax to a schedule two to three times as long as the branch taken alone.
-enum : int { kModPlain = 0, kModScore = 1, kModCap = 2, kModBias = 4 };
+// kModFixed: capped scores alone, with a cap small enough that 2^score fits every
+// sum and product as it is: the reference maximum stays 0, and no maximum is sought.
+enum : int { kModPlain = 0, kModScore = 1, kModCap = 2, kModBias = 4, kModFixed = 8 };
 
 enum : int { kTileSlot = 0, kTileSink = 1, kTileBlocks = 2, kTileStage = 3, kTileEnd = 4 };
 
@@ -118,7 +120,9 @@ __device__ __forceinline__ int ws_off(int r, int ch) {    // K row r, 16-byte ch
 template <int D, bool READ, bool Q8, int MOD>
 __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     prefill_ws_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ PrefillMaps maps) {
-    constexpr bool SCORE = MOD != kModPlain, CAP = (MOD & kModCap) != 0, BIAS = (MOD & kModBias) != 0;
+    constexpr bool SCORE = MOD != kModPlain, CAP = (MOD & kModCap) != 0, BIAS = (MOD & kModBias) != 0,
+                   FIXED = (MOD & kModFixed) != 0;
+    static_assert(!FIXED || (CAP && !BIAS), "a fixed reference needs bounded scores");
     static_assert(!Q8 || D >= 128, "INT8 rows are whole 128-code boxes");
     static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
     using S = WsShape<D>;
@@ -920,13 +924,16 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                         }
                     }
                 }
-                const float vmax = ws_max64(sv);
-                const float mx = vmax == -INFINITY ? -INFINITY : fmaf(vmax, A, B);
-                mn = m_run;
+                mn = 0.f;
                 alpha = 1.f;
-                if (mx > m_run + kWsLazy) {
-                    mn = mx;
-                    alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                if constexpr (!FIXED) {
+                    const float vmax = ws_max64(sv);
+                    const float mx = vmax == -INFINITY ? -INFINITY : fmaf(vmax, A, B);
+                    mn = m_run;
+                    if (mx > m_run + kWsLazy) {
+                        mn = mx;
+                        alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                    }
                 }
                 // fp32 exponentials: on this part they cost what a pair of fp16 ones and
                 // its conversions do
@@ -989,7 +996,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 break;
             }
             ws_fence_after();
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (!FIXED && j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
                 for (int c4 = 0; c4 < D / 32; ++c4) {
                     float ov[32];

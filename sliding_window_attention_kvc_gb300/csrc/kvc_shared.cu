@@ -684,18 +684,35 @@ __global__ void __launch_bounds__(PxShape<D>::Threads, 1)
                                    (long long)tl * p.G + gq + (sg.alt && qi ? p.alt_rows : 0);
             if (row_ok) p.part_ml[prow] = make_float2(m_run, l_run);
             if (nt > 0) {
-                float* dst = p.part_o + prow * D;
+                // through the Q tile's shared memory (its products are done), each row in the
+                // place of its own q (which this warp alone writes), CP columns at a time, so
+                // that whole lines go out
+                constexpr int CP = D == 64 ? 32 : 64, CPL = CP / 4;            // 16-byte chunks of a staged row
+                auto stg = [&](int row, int ch) {
+                    return reinterpret_cast<float4*>(Qs + (ch >> 3) * (kWsRows * 128) + row * 128 + (((ch ^ row) & 7) << 4));
+                };
+                const long long row_a = prow - ((long long)tl * p.G + gq);     // the column's row 0 of this Q tile
 #pragma unroll 1
-                for (int c4 = 0; c4 < D / 32; ++c4) {
-                    float ov[32];
-                    ws_ld32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
-                    ws_wait_ld();
-                    if (row_ok) {
+                for (int c6 = 0; c6 < D / CP; ++c6) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4*>(dst + 32 * c4 + k) =
-                                make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+                    for (int hf = 0; hf < CP / 32; ++hf) {
+                        float ov[32];
+                        ws_ld32(lane_base + (uint32_t)(qi * D + CP * c6 + 32 * hf), ov);
+                        ws_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *stg(r, 8 * hf + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
                     }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int it = 0; it < CPL; ++it) {
+                        const int rr = (warp & 3) * 32 + (32 / CPL) * it + lane / CPL, ch = lane % CPL;
+                        const int rtl = rr / p.G;
+                        if (rtl < p.tq && (sg.alt ? 0 : qi * p.tq) + rtl < sg.members)
+                            *reinterpret_cast<float4*>(p.part_o + (row_a + rr) * D + CP * c6 + 4 * ch) =
+                                *stg(rr, ch);
+                    }
+                    __syncwarp();
                 }
                 // O is read: the next segment's first product may overwrite it
                 // (it waits for this warpgroup's next P)
