@@ -374,7 +374,13 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     p.max_items = w.items;
     p.rope = d->rope;
     const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
-    p.q_scale = score ? 1.f : scale * 1.4426950408889634f;   // log2(e): softmax in base 2
+    // log2(e): softmax in base 2.  With modified scores, and in a group, where the tensor
+    // cores score the shared keys, q enters the products as it is and fp32 scores are scaled:
+    // q scaled and rounded to bf16 made the shared form's error twice the outputs' rounding
+    // (0.0031 of their size instead of 0.0017; groups of 8, 2049 .. 8192 keys)
+    const bool scored = score || group;
+    if (group) sp.scale2 = scale * 1.4426950408889634f;
+    p.q_scale = scored ? 1.f : scale * 1.4426950408889634f;
     p.score = sp;
     if (d->rope != KVC_ROPE_NONE) fill_theta(d->head_dim, d->rope_base, p.theta, p.theta_f);
 
@@ -423,7 +429,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         sh.full_units = shared_q_tiles(d->head_dim);
         sh.ctas = kSharedCtas;
         sh.rope = d->rope;
-        sh.scale2 = p.q_scale;
+        sh.scale2 = sp.scale2;
         for (int i = 0; i < d->head_dim / 2; ++i) sh.theta[i] = p.theta[i];
         // the prefix before the plan of the rest: that plan needs only the first
         // kernel's results, which are there once the prefix kernel lets it launch, and
@@ -502,7 +508,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     }
     const bool rd = d->rope == KVC_ROPE_READ_INCACHE;
     if (d->dtype != KVC_F32) {
-        if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, score != nullptr, p, maps, grid, s) !=
+        if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, scored, p, maps, grid, s) !=
             cudaSuccess)
             return KVC_ERR_CUDA;
         if (group) {
