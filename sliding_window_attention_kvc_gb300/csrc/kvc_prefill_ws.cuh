@@ -13,22 +13,25 @@
 //          valid blocks, packed 64 / bs to a tile); then the chunk's own rows
 //          from the staged copy, 64 tokens to a tile.  It records each row's
 //          position (-1: no key).
-//   1      issues every tcgen05.mma (one thread):  S_i = Q_i K^T  into one of
-//          two S buffers per Q tile, then O_i += P_i V; S of tile j + 1 is
-//          issued before P V of tile j, so the softmax of one tile overlaps the
-//          products of the next.
-//   2-3    fix-up: zero the V rows of absent keys (they may hold anything) and,
-//          for read-time RoPE, rotate the raw K rows at their positions.
+//   1 (3)  issue the tcgen05.mma (one thread of the warp):  S_i = Q_i K^T  into
+//          one of two S buffers per Q tile, then O_i += P_i V; S of tile j + 1
+//          is issued before P V of tile j, so the softmax of one tile overlaps
+//          the products of the next.  Two issuing warps, one for each Q tile,
+//          when one fix-up warp will do (bf16 rows without read-time RoPE).
+//   2 (3)  fix-up: zero the V rows of absent keys (they may hold anything),
+//          expand INT8 rows and, for read-time RoPE, rotate the raw K rows at
+//          their positions.
 //   4-7    softmax of Q tile 0 (one thread per row): masks (window, sinks,
 //   (8-11)  causal), online softmax in base 2 with a lazy reference max (moved
 //          only when a tile's max exceeds it by more than 8: probabilities stay
-//          below 2^8), bf16 P into shared memory, O rescaled in TMEM when the
-//          reference moved; at the end O / l to the output.
+//          below 2^8), bf16 P into the S buffer it came from, O rescaled in TMEM
+//          when the reference moved; at the end O / l to the output.
 // Every wait is bounded (~1 s); a timeout sets KVC_DEV_TIMEOUT and every role
 // stops; the CTA waits for its copies and products before freeing TMEM.
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "kvc_decode.cuh"
 #include "kvc_tc.cuh"
@@ -42,8 +45,13 @@ constexpr float kWsLazy = 8.f;
 
 // Score modifiers a kernel is built for: a branch for each inside one kernel held the
 // softmax to a schedule two to three times as long as the branch taken alone.
-// kModFixed: capped scores alone, with a cap small enough that 2^score fits every
-// sum and product as it is: the reference maximum stays 0, and no maximum is sought.
+// kModFixed: capped scores alone, |s| <= cap2 <= kWsFixedCap in base 2: the reference
+// is a constant and no maximum is sought.  It is the cap itself (weights <= 1, as with
+// a sought maximum) while the smallest weight, 2^(-2 cap2), stays at or above 2^-100;
+// with larger caps that smallest weight is kept there and the largest grows to 2^50:
+// values up to 2^57 in magnitude still sum over 2^20 keys.  (8 rings of 4096, 256 tokens,
+// cap 20: 258 us with the maximum, 232 us without.)
+constexpr float kWsFixedCap = 75.f;
 enum : int { kModPlain = 0, kModScore = 1, kModCap = 2, kModBias = 4, kModFixed = 8 };
 
 enum : int { kTileSlot = 0, kTileSink = 1, kTileBlocks = 2, kTileStage = 3, kTileEnd = 4 };
@@ -127,9 +135,14 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
     using S = WsShape<D>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
-    // modified scores over bf16 rows: an issuing warp for each Q tile, the second in the
-    // place of a fix-up warp, which has little to do
-    constexpr bool TWO = SCORE && !Q8;
+    // bf16 rows taken as they lie: an issuing warp for each Q tile, the second in the
+    // place of a fix-up warp, which has little to do (plain ring, 128-token chunks: 138 ->
+    // 127 us)
+    constexpr bool TWO = !READ && !Q8;
+    // read-time RoPE: the issuing thread runs alone and each thread arrives for itself
+    // (sink ring, 128-token chunks: 1.24 ms; a whole issuing warp and an arrival a warp,
+    // best elsewhere: 1.28)
+    constexpr bool ALONE = READ;
     extern __shared__ unsigned char ws_raw[];
     const uint32_t raw_u = smem_u32(ws_raw);
     unsigned char* sm = ws_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], TWO ? 1 : 2);
+            mbar_init(&bars->ready[s], TWO ? 1 : (ALONE ? 64 : 2));
             mbar_init(&bars->empty[s], TWO ? NQ : 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -165,7 +178,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 mbar_init(&bars->s_full[i][u], 1);
                 mbar_init(&bars->s_free[i][u], 4);
             }
-            mbar_init(&bars->p_full[i], 4);
+            mbar_init(&bars->p_full[i], ALONE ? kWsRows : 4);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
         }
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             // (one arrival a warp: arrivals on one barrier are made one after the other)
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->ready[s]);
+            if (ALONE || lane == 0) mbar_arrive(&bars->ready[s]);
             if (kind == kTileEnd) break;
         }
     } else if (TWO && (warp == 1 || (NQ == 2 && warp == 3))) {
@@ -677,8 +690,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        // the whole warp walks the tiles (its values stay uniform); lane 0 issues
-        {
+        // the whole warp walks the tiles (its values stay uniform) and lane 0 issues, or
+        // lane 0 walks them alone
+        if (!ALONE || lane == 0) {
             bool ok = true;
             int nt = 0x7fffffff;
             uint64_t qd[NQ];
@@ -701,7 +715,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                         ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i], kd0 + stage_d(j));
                         ws_commit(&bars->s_full[i][j & 1]);
                     }
-                    __syncwarp();
+                    if (!ALONE) __syncwarp();
                 }
             };
             // S of tile t for every Q tile, once its keys are in place; false at
@@ -747,14 +761,14 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                         ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + stage_d(j), j > 0);
                         ws_commit(&bars->o_done[i]);
                     }
-                    __syncwarp();
+                    if (!ALONE) __syncwarp();
                 }
                 if (!ok) break;
                 if (lane == 0) ws_commit(&bars->empty[j % NST]);       // K and V of tile j are done with
                 if (issued == j + LA && try_issue(issued)) ++issued;
             }
             if (*abort) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
+            if (!ALONE) ok = __all_sync(0xffffffffu, ok);
             nt = j;
             if (lane == 0) {
                 if (ok) {
@@ -786,50 +800,60 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         // The Q tile: rotated at its position (a sink tile's at min(t, C - 1)), scaled by
         // q_scale (softmax scale * log2 e, or 1), bf16.  D / 16 lanes share a row, so
         // that a load covers whole lines (a row a thread took 6 us of each CTA).
-        auto write_q = [&](bool at_sinks) {
-            constexpr int LPR = D / 16, RPW = 32 / LPR;
-            const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
-#pragma unroll (READ ? 1 : 4)
-            for (int it = 0; it < 32 / RPW; ++it) {
-                const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
-                const int rtl = rr / G, ri = i0 + qi * tq + rtl, rt = pos0 + ri;
-                const bool rok = rtl < tq && ri < p.T && rt >= 0;
-                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                if (rok) {
-                    const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
-                                                (((long long)b * p.T + ri) * p.Hq + h * G + (rr - rtl * G)) * D;
-                    lo = *reinterpret_cast<const uint4*>(qrow + 8 * c);
-                    hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c);
-                }
-                const bool rot = p.rope != kRopeNone && rok;
-                if (!SCORE || rot) {
-                    const long long qpos = at_sinks ? min(rt, C - 1) : rt;
-                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                    uint32_t lo2[4], hi2[4];
+        constexpr int QLPR = D / 16, QRPW = 32 / QLPR;
+        const int qc = lane % QLPR;                    // 8-column chunk, paired with qc + D / 16
+        auto write_q_rows = [&](int it, bool at_sinks, auto rotated, const float* th) {
+            const int rr = (warp & 3) * 32 + it * QRPW + lane / QLPR;
+            const int rtl = rr / G, ri = i0 + qi * tq + rtl, rt = pos0 + ri;
+            const bool rok = rtl < tq && ri < p.T && rt >= 0;
+            uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+            if (rok) {
+                const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
+                                            (((long long)b * p.T + ri) * p.Hq + h * G + (rr - rtl * G)) * D;
+                lo = *reinterpret_cast<const uint4*>(qrow + 8 * qc);
+                hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * qc);
+            }
+            if (!SCORE || rotated.value) {
+                const long long qpos = at_sinks ? min(rt, C - 1) : rt;
+                const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                uint32_t lo2[4], hi2[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
-                        float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
-                        if (rot) {
+                for (int e = 0; e < 4; ++e) {
+                    float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
+                    float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
+                    if (rotated.value && rok) {
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                float cs, sn;
-                                rope_cos_sin(qpos, p.theta[8 * c + 2 * e + u], &cs, &sn);
-                                const float x1 = x[u], x2 = y[u];
-                                x[u] = x1 * cs - x2 * sn;
-                                y[u] = x1 * sn + x2 * cs;
-                            }
+                        for (int u = 0; u < 2; ++u) {
+                            float cs, sn;
+                            rope_cos_sin(qpos, th[2 * e + u], &cs, &sn);
+                            const float x1 = x[u], x2 = y[u];
+                            x[u] = x1 * cs - x2 * sn;
+                            y[u] = x1 * sn + x2 * cs;
                         }
-                        lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
-                        hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
                     }
-                    lo = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
-                    hi = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
+                    lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
+                    hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
                 }
-                // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-                const int c1 = c, c2 = c + D / 16;
-                *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = lo;
-                *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = hi;
+                lo = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                hi = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
+            }
+            // Q tile: [column block][128 rows][128 B], 128-byte swizzle
+            const int c1 = qc, c2 = qc + D / 16;
+            *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = lo;
+            *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = hi;
+        };
+        auto write_q = [&](bool at_sinks) {
+            if (p.rope == kRopeNone) {
+#pragma unroll 4
+                for (int it = 0; it < 32 / QRPW; ++it) write_q_rows(it, at_sinks, std::false_type{}, nullptr);
+            } else {
+                // (the lane's frequencies are read once: lanes read different ones; unrolled,
+                // the rotations took 13 us more of each CTA)
+                float th[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) th[e] = p.theta[8 * qc + e];
+#pragma unroll 1
+                for (int it = 0; it < 32 / QRPW; ++it) write_q_rows(it, at_sinks, std::true_type{}, th);
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars->q_ready[qi]);
@@ -905,7 +929,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 if (mode == kMaskRange) {
                     // the chunk's own rows: key k at kbase + k (the window holds every chunk token)
                     const int kb = meta[s].kbase;
-                    const int klo = row_ok ? start - kb : kWsKeys, khi = row_t - kb;
+                    const int klo = row_ok ? (int)min((long long)start - kb, (long long)kWsKeys) : kWsKeys;
+                    const int khi = row_t - kb;
                     if (!__all_sync(0xffffffffu, klo <= 0 && khi >= kWsKeys - 1)) ws_mask_range(sv, klo, khi);
                 } else if (!row_ok) {
 #pragma unroll
@@ -924,7 +949,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                         }
                     }
                 }
-                mn = 0.f;
+                mn = fmaxf(100.f - p.score.cap2, 0.f);
+                mn = fminf(p.score.cap2, mn);
                 alpha = 1.f;
                 if constexpr (!FIXED) {
                     const float vmax = ws_max64(sv);
@@ -941,6 +967,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 l_run = l_run * alpha + ls;
                 m_run = mn;
             } else {
+                // (masks and maxima as the modified scores have them made read-time RoPE 1.25 ->
+                // 1.32 ms and a paged INT8 batch 1.37 -> 1.53: this schedule is left alone)
                 if (!row_ok) {
 #pragma unroll
                     for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
@@ -1018,8 +1046,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             ws_wait_st();
             ws_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[qi]);
+            if (!ALONE) __syncwarp();
+            if (ALONE || lane == 0) mbar_arrive(&bars->p_full[qi]);
         }
         if (!ok) give_up();
         // the last P V, then O / l to the output

@@ -7,10 +7,8 @@ namespace kvc {
 cudaError_t launch_prefill_score_i8(int head_dim, const PrefillParams& p, const PrefillMaps& maps,
                                     cudaStream_t stream) {
     if (p.G < 1 || p.G > kWsRows || p.rope == kRopeRead) return cudaErrorInvalidValue;
-    // |s| <= 90 in base 2: 2^s and sums of 2^20 of them, times values below 2^10, stay
-    // inside fp32 (and bf16, which has its range)
     const int mod = (p.score.cap2 > 0.f ? kModCap : 0) | (p.score.slopes ? kModBias : 0) |
-                    (p.score.cap2 > 0.f && p.score.cap2 <= 90.f && !p.score.slopes ? kModFixed : 0);
+                    (p.score.cap2 > 0.f && p.score.cap2 <= kWsFixedCap && !p.score.slopes ? kModFixed : 0);
 #define KVC_WS(DD, M) \
     if (head_dim == DD && mod == (M)) return launch_prefill_ws_t<DD, false, true, kModScore | (M)>(p, maps, stream);
 #define KVC_WS_ALL(DD) KVC_WS(DD, 0) KVC_WS(DD, kModCap) KVC_WS(DD, kModBias) KVC_WS(DD, kModCap | kModBias) \
