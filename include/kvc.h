@@ -297,8 +297,12 @@ KVC_API int kvc_decode_attention(const kvc_desc* d, const void* cache, int32_t l
  *     s = s - slopes[h] * (t - p)             slopes not NULL
  * and keys below the query's start are not attended (sinks among them): the
  * document it belongs to begins there.  A value below 0 counts as 0.
+ * A softcap is 0 or KVC_SOFTCAP_MIN .. KVC_SOFTCAP_MAX (else KVC_ERR_ARG); a
+ * capped score is off by a few 2^-23 softcap.
  * Cached rows below every start of their sequence may hold anything; all other
  * rows up to the query's position hold finite values, as for kvc_prefill. */
+#define KVC_SOFTCAP_MIN 0.0009765625f
+#define KVC_SOFTCAP_MAX 1024.0f
 typedef struct kvc_score {
     const float* slopes;        /* [q_heads] or NULL */
     const int32_t* start;       /* decode [batch], prefill [batch, T]; or NULL */

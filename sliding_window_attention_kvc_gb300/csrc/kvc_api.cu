@@ -272,7 +272,8 @@ static int decode_args(const kvc_desc* d, const void* cache, int32_t layer, cons
 static int score_params(const kvc_desc* d, const kvc_score* sc, ScoreParams* out) {
     *out = ScoreParams{};
     if (!sc) return KVC_OK;
-    if (!(sc->softcap >= 0.f) || !std::isfinite(sc->softcap)) return KVC_ERR_ARG;
+    // (a cap's own rounding, a few 2^-23 of it, stays far below the scores' in this range)
+    if (!(sc->softcap == 0.f || (sc->softcap >= KVC_SOFTCAP_MIN && sc->softcap <= KVC_SOFTCAP_MAX))) return KVC_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(sc->slopes) | reinterpret_cast<uintptr_t>(sc->start)) & 3u) return KVC_ERR_ALIGN;
     // read-time rotation moves keys from step to step: no distances to a key's position
     if (d->rope == KVC_ROPE_READ_INCACHE) return KVC_ERR_UNSUPPORTED;

@@ -1489,7 +1489,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                                     ((long long)seg.b * p.Hq + kvh * p.G + z * GH + g) * D;
         if constexpr (SCORE) {
             t_q = qpos;
-            start = p.score.start ? p.score.start[seg.b] : 0;
+            start = p.score.start ? max(0, p.score.start[seg.b]) : 0;
             slope2 = (p.score.slopes && g < GH) ? p.score.slopes[kvh * p.G + z * GH + g] * 1.4426950408889634f : 0.f;
         }
         csync.sync(p.err);                      // everyone is done with the previous qcs

@@ -46,7 +46,8 @@ def _within(got, want, weight, rel, act):
     assert not bad.any(), (int(bad.sum()), float(((got.double() - want).abs() / tol).max()))
 
 
-def _decode(kvc, layout, dtype, lens, H=8, KV=2, D=128, cap=0.0, bias=False, start=None, dead=(), poison=True, **kw):
+def _decode(kvc, layout, dtype, lens, H=8, KV=2, D=128, cap=0.0, bias=False, start=None, dead=(), poison=True, more=0.0,
+            **kw):
     c = Built(kvc, layout, dtype, lens, H, KV, D, **kw)
     slopes = _slopes(H) if bias else None
     st = None if start is None else torch.tensor(start, dtype=torch.int32, device="cuda")
@@ -78,7 +79,7 @@ def _decode(kvc, layout, dtype, lens, H=8, KV=2, D=128, cap=0.0, bias=False, sta
         want, w = plain.attend(c.q[b].double()[None], k, v, dist, torch.ones_like(dist, dtype=torch.bool), c.scale,
                                cap, slopes)
         weight = torch.einsum("htl,lhd->thd", w, v.abs().repeat_interleave(H // KV, 1))
-        _within(out[b], want[0], weight[0], REL[dtype], c.act)
+        _within(out[b], want[0], weight[0], REL[dtype] + more, c.act)
     return c, out
 
 
@@ -196,7 +197,8 @@ def test_saturated_and_infinite_scores(kvc):
                 c.act)
 
 
-def _prefill(kvc, layout, dtype, lens, T, H=8, KV=2, D=128, cap=0.0, bias=False, docs=None, rope="none", seed=0, **kw):
+def _prefill(kvc, layout, dtype, lens, T, H=8, KV=2, D=128, cap=0.0, bias=False, docs=None, rope="none", seed=0, more=0.0,
+             **kw):
     """lens[b]: tokens cached before the chunk (negative: the chunk starts with padding)."""
     have = [max(0, n) for n in lens]
     c = Built(kvc, layout, dtype, have, H, KV, D, rope=rope, seed=seed, new=T, **kw)
@@ -245,7 +247,7 @@ def _prefill(kvc, layout, dtype, lens, T, H=8, KV=2, D=128, cap=0.0, bias=False,
         want, w = plain.attend(q[b, first:].double(), K, V, t[:, None] - p[None], see, c.scale, cap, slopes)
         weight = torch.einsum("htl,lhd->thd", w, V.abs().repeat_interleave(H // KV, 1))
         assert not out[b, :first].any()
-        _within(out[b, first:], want, weight, 2.0 ** -8 + 1.3e-2, c.act)
+        _within(out[b, first:], want, weight, 2.0 ** -8 + 1.3e-2 + more, c.act)
 
 
 @pytest.mark.parametrize("mods", MODS)
@@ -363,3 +365,64 @@ def test_norm_rotary_append_then_scored_attention(kvc):
             rel = REL["bf16"] + math.expm1(4 * 2.0 ** -7 * float(qk_sum) * D ** -0.5 * 0.02)
             _within(out[b], want[0], weight[0], rel, torch.bfloat16)
     assert kvc.get_error(ws) == 0
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -10, 1024.0])
+def test_smallest_and_largest_caps(kvc, cap):
+    more = 12 * 2.0 ** -23 * cap      # a capped score is off by 6 2^-23 cap, a weight by twice that
+    for dtype in ("bf16", "f32"):
+        _decode(kvc, "ring", dtype, lens=(70, 3), window=64, H=4, KV=2, D=64, cap=cap, more=more)
+    _prefill(kvc, "paged", "bf16", lens=(0, 70), T=40, cap=cap, more=more)        # a fixed reference, and a sought one
+    _prefill(kvc, "paged", "bf16", lens=(0, 70), T=40, cap=cap, bias=True, more=more)
+
+
+@pytest.mark.parametrize("cap", [0.5, 30.0, 34.0, 35.0, 51.0, 53.0, 80.0])
+@pytest.mark.parametrize("vmag", [1.0, 1e16, 1e-3])
+def test_prefill_scores_at_the_cap(kvc, cap, vmag):
+    """Scores at +cap and -cap: rows that see only the one, only the other, and both; large values."""
+    T, H, D, dev = 150, 4, 64, "cuda"
+    c = Built(kvc, "paged", "bf16", (0, 0, 0), H, 1, D, new=T)
+    g = torch.Generator(device=dev).manual_seed(3)
+    sign = torch.ones(3, T, device=dev)
+    sign[0] = -1
+    sign[2] = torch.where(torch.rand(T, generator=g, device=dev) < 0.5, 1.0, -1.0)
+    q = torch.full((3, T, H, D), 1000.0, device=dev, dtype=torch.bfloat16)
+    k = (sign[:, :, None, None] * torch.full((1, 1, 1, D), 1000.0, device=dev)).to(torch.bfloat16)
+    v = (torch.randn(3, T, 1, D, generator=g, device=dev) * vmag).to(torch.bfloat16)
+    pos0 = torch.zeros(3, dtype=torch.int32, device=dev)
+    ws = kvc.alloc_prefill_workspace(c.d, T)
+    out = kvc.prefill_scored(c.d, c.cache, c.layer, q, k, v, pos0, ws, kvc.make_score(cap), block_table=c.table)
+    assert kvc.get_error(ws) == 0
+    t = torch.arange(T, device=dev)
+    for b in range(3):
+        want, w = plain.attend(q[b].double(), k[b].double(), v[b].double(), t[:, None] - t[None], t[None] <= t[:, None],
+                               c.scale, cap)
+        weight = torch.einsum("htl,lhd->thd", w, v[b].double().abs().repeat_interleave(H, 1))
+        _within(out[b].double() / vmag, want / vmag, weight / vmag, 2.0 ** -8 + 1.3e-2, c.act)
+
+
+def test_starts_at_the_ends_of_the_range(kvc):
+    """The smallest and largest int32 as starts: nothing masked, everything masked."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    for dtype in ("bf16", "f32", "i8"):
+        _decode(kvc, "paged", dtype, lens=(90, 90, 90), start=(lo, hi, 5), bias=True)
+        _decode(kvc, "ring", dtype, lens=(300, 300, 300), window=100, start=(lo, hi, 250), cap=5.0)
+    _prefill(kvc, "paged", "bf16", lens=(0, -5, 70), T=66, docs=lambda b, i, n: (0, hi, lo, max(0, n + i))[i % 4])
+
+
+def test_calls_at_once_on_two_streams(kvc):
+    """Each with its own workspace: the results of the calls alone."""
+    a = Built(kvc, "paged", "bf16", (900, 333, 64), 8, 2, 128, seed=1)
+    b = Built(kvc, "ring", "bf16", (900, 333, 64), 8, 2, 128, window=512, seed=2)
+    sa, sb = kvc.make_score(9.0, _slopes(8)), kvc.make_score(0.0, _slopes(8))
+    ra = kvc.decode_attention_scored(a.d, a.cache, a.layer, a.q, a.pos, a.ws, sa, block_table=a.table)
+    rb = kvc.decode_attention_scored(b.d, b.cache, b.layer, b.q, b.pos, b.ws, sb)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    oa, ob = torch.empty_like(ra), torch.empty_like(rb)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        kvc.decode_attention_scored(a.d, a.cache, a.layer, a.q, a.pos, a.ws, sa, block_table=a.table, out=oa, stream=one)
+        kvc.decode_attention_scored(b.d, b.cache, b.layer, b.q, b.pos, b.ws, sb, out=ob, stream=two)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, ra) and torch.equal(ob, rb)
+    assert kvc.get_error(a.ws) == 0 and kvc.get_error(b.ws) == 0

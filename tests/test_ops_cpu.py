@@ -158,7 +158,7 @@ def test_scored_refusals(kvc):
 
     for call in (decode, prefill):
         assert call(score=None) == kvc.KVC_ERR_NULL
-        for cap in (-1.0, float("nan"), float("inf")):
+        for cap in (-1.0, float("nan"), float("inf"), 1e-4, 2000.0):
             assert call(score=kvc.KvcScore(None, None, cap)) == kvc.KVC_ERR_ARG
         assert call(score=kvc.KvcScore(A + 2, None, 0.0)) == kvc.KVC_ERR_ALIGN
         assert call(score=kvc.KvcScore(None, A + 1, 0.0)) == kvc.KVC_ERR_ALIGN
