@@ -381,10 +381,10 @@ class ClockSampler:
 # capture per workload, and the digest of the kernel's sources
 # (KERNEL_TRAFFIC_FILES) they were taken on: reported only while those
 # sources are unchanged.
-KERNEL_TRAFFIC = {"ring_bf16": 137679616, "sink_window_bf16": 543395584,
-                  "paged_shared_prefix_bf16": 842048256, "long_context_pool_bf16": 156166144,
-                  "ring_int8": 70007552}
-KERNEL_TRAFFIC_SOURCES = "24d6eacb67dbe03dc8e15f6823c3bd723a1a13f551c9d31eef08d159a6fe4904"
+KERNEL_TRAFFIC = {"ring_bf16": 137616896, "sink_window_bf16": 542781696,
+                  "paged_shared_prefix_bf16": 841274624, "long_context_pool_bf16": 155708928,
+                  "ring_int8": 69713408}
+KERNEL_TRAFFIC_SOURCES = "b8db15a401bb29e10f930184b73f5e1c2b67888b8add4cbd2f257de78c328743"
 
 
 # the sources decode_mma_kernel and its launch are built from

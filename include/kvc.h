@@ -399,7 +399,8 @@ KVC_API int kvc_prefill(const kvc_desc* d, void* cache, int32_t layer, const voi
  * themselves.  bf16 and INT8 caches, any GQA group of up to 128 heads, rope
  * NONE or BAKED; window layouts take chunks no longer than the window, paged
  * ones blocks whose size is a multiple of 8 dividing 64 (else
- * KVC_ERR_UNSUPPORTED).  Workspace as for kvc_prefill. */
+ * KVC_ERR_UNSUPPORTED).  With a softcap and no slopes, values beyond 2^57 in
+ * magnitude may overflow the sums.  Workspace as for kvc_prefill. */
 KVC_API int kvc_prefill_scored(const kvc_desc* d, void* cache, int32_t layer, const void* q,
                                const void* k_new, const void* v_new, int32_t T, const int32_t* pos0,
                                const int32_t* block_table, const uint32_t* valid_bits, const kvc_score* score,

@@ -377,8 +377,8 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
     // log2(e): softmax in base 2.  With modified scores, and in a group, where the tensor
     // cores score the shared keys, q enters the products as it is and fp32 scores are scaled:
-    // q scaled and rounded to bf16 made the shared form's error twice the outputs' rounding
-    // (0.0031 of their size instead of 0.0017; groups of 8, 2049 .. 8192 keys)
+    // with q scaled and rounded to bf16 first the shared form was off by 0.0031 of the
+    // outputs' size instead of 0.0020 (groups of 8, 2049 .. 8192 keys)
     const bool scored = score || group;
     if (group) sp.scale2 = scale * 1.4426950408889634f;
     p.q_scale = scored ? 1.f : scale * 1.4426950408889634f;

@@ -161,6 +161,7 @@ __device__ __forceinline__ float scored(const ScoreParams& sp, float x, float sl
 
 // SCORE: scores with modifiers (p.score; no read-time RoPE): positions of the
 // staged rows go with them, and rows below the sequence's start are masked.
+// (One sink cache of 64 rows, 4 heads of 64: 6.9 us, a launch and its latencies.)
 template <typename Elt, int D, int GH, bool PAGED, bool READ, bool SCORE>
 __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
     using S = DecodeShape<Elt, D>;

@@ -202,7 +202,7 @@ struct PrefillParams {
     ScoreParams score;          // kvc_prefill_scored
 };
 
-// Tensor maps of the warp-specialised prefill (kvc_prefill_ws.cu), bf16 rows,
+// Tensor maps of the warp-specialised prefill (kvc_prefill_ws.cuh), bf16 rows,
 // 64-column boxes, 128-byte swizzle:
 //   slot   window caches: 64 consecutive rows of a K half with their V rows,
 //          5-D {64 columns, row, K|V, layer, column block} (slot_whole) or

@@ -171,7 +171,7 @@ __device__ __forceinline__ float ws_exp64(float (&v)[kWsKeys], float a, float c)
 // v = -1 / (2^(ci x) + 1) in place, the argument of a capped score (cap tanh =
 // 2 cap v + cap).  Reciprocals run at half the exponentials' rate here: four
 // denominators share one, 1 / a = b (c d) / (a b c d) and so on (measured: 64 keys of
-// two warps 1583 -> 1100 cycles).  Exponents are held to 30 so that no product
+// two warps 1590 -> 1001 cycles).  Exponents are held to 30 so that no product
 // overflows: tanh is 1 - 2^-29 there, 1 in fp32; a NaN counts as 30 too, so that the garbage of
 // an absent key does not reach its neighbours.
 template <int N>
