@@ -198,7 +198,7 @@ def test_saturated_and_infinite_scores(kvc):
 
 
 def _prefill(kvc, layout, dtype, lens, T, H=8, KV=2, D=128, cap=0.0, bias=False, docs=None, rope="none", seed=0, more=0.0,
-             **kw):
+             dead=lambda b, j: False, **kw):
     """lens[b]: tokens cached before the chunk (negative: the chunk starts with padding)."""
     have = [max(0, n) for n in lens]
     c = Built(kvc, layout, dtype, have, H, KV, D, rope=rope, seed=seed, new=T, **kw)
@@ -218,20 +218,31 @@ def _prefill(kvc, layout, dtype, lens, T, H=8, KV=2, D=128, cap=0.0, bias=False,
     ws = kvc.alloc_prefill_workspace(c.d, T)
     out = torch.full_like(q, float("nan"))
     ref_cache = c.cache.clone()
+    valid = None
+    if layout == "paged":      # dead(b, j): logical block j of sequence b, wholly cached, is not resident
+        mask = torch.ones(c.d.num_blocks, dtype=torch.bool)
+        for b in range(B):
+            for j in range(have[b] // c.bs):
+                if dead(b, j):
+                    mask[int(c.table[b, j])] = False
+        valid = kvc.pack_valid_bits(mask).cuda() if not mask.all() else None
     kvc.prefill_scored(c.d, c.cache, c.layer, q, k, v, pos0, ws, kvc.make_score(cap, slopes, start),
-                       block_table=c.table, out=out)
+                       block_table=c.table, valid_bits=valid, out=out)
     assert kvc.get_error(ws) == 0
     kvc.append(c.d, ref_cache, c.layer, k, v, pos0, ws, block_table=c.table)
     assert torch.equal(c.cache.view(torch.uint8), ref_cache.view(torch.uint8))
     k64, v64 = k.double(), v.double()
     if dtype == "i8":     # the chunk's rows as the cache reads them back, bf16 of code * scale
         for x in (k64, v64):
-            s = (x.abs().amax(-1, keepdim=True).float() / 127).double()
-            x.copy_(((x / s).round().clamp(-127, 127) * s).to(torch.bfloat16).double())
+            s = x.abs().amax(-1, keepdim=True).float() / 127
+            code = (x.float() / s).round().clamp(-127, 127).double()       # the format's fp32 quotient
+            x.copy_((code * s.double()).to(torch.bfloat16).double())
     for b in range(B):
         old = plain.attended(layout, have[b] - 1, c.window, c.sinks)
         if start is not None:
             old = [p for p in old if p >= int(start[b].min())]
+        if layout == "paged":
+            old = [p for p in old if (p // c.bs + 1) * c.bs > have[b] or not dead(b, p // c.bs)]
         kc, vc = c.rows(b, old) if old else (k64[b, :0], v64[b, :0])
         if dtype == "i8" and old:
             kc, vc = kc.to(torch.bfloat16).double(), vc.to(torch.bfloat16).double()
@@ -426,3 +437,21 @@ def test_calls_at_once_on_two_streams(kvc):
     torch.cuda.synchronize()
     assert torch.equal(oa, ra) and torch.equal(ob, rb)
     assert kvc.get_error(a.ws) == 0 and kvc.get_error(b.ws) == 0
+
+
+@pytest.mark.parametrize("dtype,bs", [("bf16", 16), ("bf16", 64), ("i8", 16)])
+@pytest.mark.parametrize("mods", [dict(cap=6.0), dict(bias=True), dict(cap=6.0, bias=True)])
+def test_prefill_absent_blocks(kvc, dtype, bs, mods):
+    """Cached blocks that are not resident, some, all but one, all."""
+    _prefill(kvc, "paged", dtype, lens=(400, 333, 200), T=70, bs=bs,
+             dead=lambda b, j: (j % 3 == 1, j != 2, True)[b], **mods)
+    _prefill(kvc, "paged", dtype, lens=(400, 333, 200), T=70, bs=bs, dead=lambda b, j: j % 2 == b % 2,
+             docs=lambda b, i, n: max(0, n - 150 + 3 * i), **mods)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (256, "bf16"), (256, "i8")])
+def test_long_chunks_of_other_head_dims(kvc, D, dtype):
+    """More tiles than stages before, inside and behind the chunk's diagonal."""
+    for mods in (dict(cap=20.0), dict(bias=True)):
+        _prefill(kvc, "paged", dtype, lens=(0, 900), T=520, D=D, H=4, KV=1, **mods)
+        _prefill(kvc, "sink_ring", dtype, lens=(40, 2000), T=520, D=D, H=4, KV=1, window=600, sinks=4, **mods)

@@ -287,3 +287,19 @@ def test_offsets_past_32_bits(kvc):
             tol = REL * weight + 2.0 ** -8 * (want[0].abs() + REL * weight) + 1e-6
             assert ((got[b].double() - want[0]).abs() <= tol).all()
     assert kvc.get_error(ws) == 0
+
+
+def test_calls_at_once_on_two_streams(kvc):
+    """Each with its own workspace: the results of the calls alone."""
+    runs = [_run(kvc, [900, 700, 655, 40, 333], [0, 0, 0, 1, 1], [(range(3), 40), ((3, 4), 2)]),
+            _run(kvc, [2100, 2060], [1, 1], [(range(2), 128)], H=16)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty_like(r[3]) for r in runs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (c, ws, gt, _), s, o in zip(runs, streams, outs):
+            kvc.decode_attention_shared(c.d, c.cache, c.layer, c.q, c.pos, gt, ws, c.table, out=o, stream=s)
+    torch.cuda.synchronize()
+    for (c, ws, gt, want), o in zip(runs, outs):
+        assert torch.equal(o, want)
+        assert kvc.get_error(ws) == 0
