@@ -384,7 +384,7 @@ class ClockSampler:
 KERNEL_TRAFFIC = {"ring_bf16": 137616896, "sink_window_bf16": 542781696,
                   "paged_shared_prefix_bf16": 841274624, "long_context_pool_bf16": 155708928,
                   "ring_int8": 69713408}
-KERNEL_TRAFFIC_SOURCES = "b8db15a401bb29e10f930184b73f5e1c2b67888b8add4cbd2f257de78c328743"
+KERNEL_TRAFFIC_SOURCES = "a6ae3a09964a74264a89253764b7c4c84ab0875e82a572af8d66bdfc3407721e"
 
 
 # the sources decode_mma_kernel and its launch are built from

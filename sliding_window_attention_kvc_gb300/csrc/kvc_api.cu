@@ -835,6 +835,7 @@ KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, in
     if (rc) return rc;
     if ((rc = shared_desc(d, g))) return rc;
     if (!group) return KVC_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(group) & 3u) return KVC_ERR_ALIGN;
     return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
                        workspace_bytes, stream, nullptr, group);
 }

@@ -579,7 +579,7 @@ __device__ __noinline__ void append_token_warp(const DecodeParams& p, long long 
 // (window layouts), so that a sub-tile's first position places its rows; runs
 // wholly below the sequence's start are not copied.  Paged bf16 batch of 64, 1008 MB of
 // attended rows, distance bias and starts: 166 us, 0.89 of the measured bandwidth;
-// 8 rings of 4096, cap: 27 us, 0.73.
+// 8 rings of 4096, cap: 27 us, 0.73 (31 replayed from a graph).
 template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE>
 // Two CTAs (ten warps) per SM: three warps share a sub-partition's 16K
 // registers, so a thread may hold at most 168.

@@ -50,7 +50,7 @@ constexpr float kWsLazy = 8.f;
 // a sought maximum) while the smallest weight, 2^(-2 cap2), stays at or above 2^-100;
 // with larger caps that smallest weight is kept there and the largest grows to 2^50:
 // values up to 2^57 in magnitude still sum over 2^20 keys.  (8 rings of 4096, 256 tokens,
-// cap 20: 258 us with the maximum, 232 us without.)
+// cap 20: 258 us with the maximum, 229 us without.)
 constexpr float kWsFixedCap = 75.f;
 enum : int { kModPlain = 0, kModScore = 1, kModCap = 2, kModBias = 4, kModFixed = 8 };
 

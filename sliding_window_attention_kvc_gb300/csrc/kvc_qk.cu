@@ -18,7 +18,8 @@
 // while the rows' loads are in flight, and serve every head.
 //
 // One token a CTA of two warps, twelve CTAs an SM: eight ragged prompt
-// chunks of up to 2048 tokens, 32 / 8 heads of 128, bf16 paged, 303 MB: 61 us, 0.73 of the measured copy bandwidth.  Four
+// chunks of up to 2048 tokens, 32 / 8 heads of 128, bf16 paged, 303 MB: 61 us (65 replayed from a graph), 0.73 of
+// the measured copy bandwidth.  Four
 // warps took 96 us, CTAs that walk several tokens 117 us (their loads waited for the
 // rows before).  One token of each of 64 sequences: 6.2 us, of which the launch and one
 // dependent load each of position, table and rows are most.

@@ -31,10 +31,10 @@
 // what a CTA with few rows spends its time on.
 //
 // Measured (32 / 8 heads of 128, blocks of 16), whole call: 64 sequences in groups
-// of 8 with 2048 shared tokens and 2049 .. 8192 in all 183 us, 0.69 of the bytes'
+// of 8 with 2048 shared tokens and 2049 .. 8192 in all 185 us, 0.69 of the bytes'
 // time (the plan 8 us, the prefix 25 to 35, the sequences' own keys 130 at 0.9 of
-// bandwidth, the combine 5); 96 readers of one document 148 us, of which the prefix
-// 75 at the softmax's rate; six readers 38 us, five dependent launches.
+// bandwidth, the combine 5); 96 readers of one document 149 us, of which the prefix
+// 75 at the softmax's rate; six readers 41 us, five dependent launches.
 #include <atomic>
 
 #include "kvc_decode.cuh"

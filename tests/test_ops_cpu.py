@@ -187,6 +187,7 @@ def test_shared_refusals(kvc):
         assert call(**{name: None}) == kvc.KVC_ERR_NULL, name
     for name in ("cache", "q", "out", "ws"):
         assert call(**{name: A + 8}) == kvc.KVC_ERR_ALIGN, name
+    assert call(group=A + 2) == kvc.KVC_ERR_ALIGN
     assert call(layer=2) == kvc.KVC_ERR_ARG and call(short=1) == kvc.KVC_ERR_WORKSPACE
     for kw in (dict(dtype="f32"), dict(dtype="i8"), dict(block_size=12), dict(block_size=48), dict(block_size=100),
                dict(q_heads=258)):
