@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     // (sink ring, 128-token chunks: 1.24 ms; a whole issuing warp and an arrival a warp,
     // best elsewhere: 1.28)
     constexpr bool ALONE = READ;
+    static_assert(!(ALONE && TWO), "the arrivals a barrier counts are those its warps make");
     extern __shared__ unsigned char ws_raw[];
     const uint32_t raw_u = smem_u32(ws_raw);
     unsigned char* sm = ws_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
