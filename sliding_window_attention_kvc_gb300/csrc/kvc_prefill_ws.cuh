@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         // that a load covers whole lines (a row a thread took 6 us of each CTA).
         constexpr int QLPR = D / 16, QRPW = 32 / QLPR;
         const int qc = lane % QLPR;                    // 8-column chunk, paired with qc + D / 16
-        auto write_q_rows = [&](int it, bool at_sinks, auto rotated, const float* th) {
+        auto write_q_rows = [&](int it, bool at_sinks, auto rotated, const unsigned long long* th) {
             const int rr = (warp & 3) * 32 + it * QRPW + lane / QLPR;
             const int rtl = rr / G, ri = i0 + qi * tq + rtl, rt = pos0 + ri;
             const bool rok = rtl < tq && ri < p.T && rt >= 0;
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             } else {
                 // (the lane's frequencies are read once: lanes read different ones; unrolled,
                 // the rotations took 13 us more of each CTA)
-                float th[8];
+                unsigned long long th[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) th[e] = p.theta[8 * qc + e];
 #pragma unroll 1
