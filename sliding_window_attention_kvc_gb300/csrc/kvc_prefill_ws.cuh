@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             } else if (t0 >= 0) {
                 // paged: mapped and valid blocks holding positions <= t0, packed
                 const int bs = p.bs, per = kWsKeys / bs;
-                const int nlb = t0 / bs + 1;
+                // (positions past the table hold no key; the append reports them)
+                const int nlb = min(t0 / bs + 1, p.maxb);
                 const int32_t* trow = p.table + (long long)b * p.maxb;
                 int fill = 0, s = 0;
                 int low = 0;                              // SCORE: the tile's lowest position
