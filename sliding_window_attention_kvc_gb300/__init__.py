@@ -406,6 +406,18 @@ def _tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: in
     return t.data_ptr(), stride
 
 
+def _need_qk(z: _Sizes, qk: KvcQk, dev: int):
+    """The weights were checked against the descriptor they were given with; the call's may be another."""
+    for name, w in zip(("q_weight", "k_weight"), qk.keep[1:]):
+        if w is not None:
+            if w.dtype is not z.act:
+                raise TypeError(f"qk: {name} must be {z.act}, got {w.dtype}")
+            if w.numel() != z.D:
+                raise ValueError(f"qk: {name} must have {z.D} elements, got {w.numel()}")
+            if dev >= 0:                # (no CUDA tensor q: its own check reports it)
+                _on_device(w, dev, name)
+
+
 def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
               pos: torch.Tensor, workspace: torch.Tensor, qk: KvcQk, n_tok: torch.Tensor | None = None,
               block_table: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
@@ -418,6 +430,7 @@ def append_qk(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_ne
     n_new = 1 if q.dim() == 3 else q.shape[1] if q.dim() == 4 else -1
     if n_new < 1:
         raise ValueError("q must be [batch, n_new, q_heads, head_dim]")
+    _need_qk(z, qk, dev)
     qp, qs = _tokens(q, "q", z.act, z.B, n_new, z.H, z.D, dev)
     kp, ks = _tokens(k_new, "k_new", z.act, z.B, n_new, z.KV, z.D, dev)
     vp, vs = _tokens(v_new, "v_new", z.act, z.B, n_new, z.KV, z.D, dev)
