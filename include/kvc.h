@@ -205,9 +205,12 @@ KVC_API int kvc_append(const kvc_desc* d, void* cache, int32_t layer,
  *                     as the turns original_len f_i / (2 pi) go from slow to fast.
  *  magnitude  factor on the rotated values; 0: 1, and for YARN with factor > 1
  *             0.1 ln(factor) + 1.
- * kvc_rotary_init checks the fields (KVC_ERR_ARG), and fills in magnitude,
- * turns (the frequencies as 2^64ths of a turn, so that position * f_i is
- * reduced exactly) and ready.  Call it again after a change of any field. */
+ * kvc_rotary_init checks the fields (KVC_ERR_ARG), and fills in magnitude (if
+ * it is 0), turns (the frequencies as 2^64ths of a turn, so that position *
+ * f_i is reduced exactly), ready and filled.  Zero the struct before its fields
+ * are set, and call kvc_rotary_init again after a change of any of them: a
+ * magnitude that the call before filled in, and that is still there, counts as
+ * 0 and is worked out anew. */
 typedef enum { KVC_PAIRS_HALF = 0, KVC_PAIRS_INTERLEAVED = 1 } kvc_pairs;
 typedef enum { KVC_SCALING_NONE = 0, KVC_SCALING_LINEAR = 1, KVC_SCALING_YARN = 2, KVC_SCALING_BANDS = 3 }
     kvc_scaling;
@@ -223,6 +226,7 @@ typedef struct kvc_rotary {
     float magnitude;
     int32_t ready;              /* set by kvc_rotary_init */
     uint64_t turns[128];
+    float filled;               /* set by kvc_rotary_init: the magnitude it filled in, 0: the caller's own */
 } kvc_rotary;
 KVC_API int kvc_rotary_init(kvc_rotary* rotary);
 

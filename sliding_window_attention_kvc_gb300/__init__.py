@@ -62,7 +62,7 @@ class KvcRotary(ctypes.Structure):
         ("pairs", ctypes.c_int32), ("dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
         ("original_len", ctypes.c_int32), ("base", ctypes.c_float), ("factor", ctypes.c_float),
         ("fast", ctypes.c_float), ("slow", ctypes.c_float), ("magnitude", ctypes.c_float),
-        ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128),
+        ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128), ("filled", ctypes.c_float),
     ]
 
 

@@ -406,6 +406,8 @@ extern "C" {
 KVC_API int kvc_rotary_init(kvc_rotary* r) {
     if (!r) return KVC_ERR_NULL;
     r->ready = 0;
+    if (r->magnitude == r->filled) r->magnitude = 0.f;     // the last call's value, not the caller's
+    r->filled = 0.f;
     if (r->pairs != KVC_PAIRS_HALF && r->pairs != KVC_PAIRS_INTERLEAVED) return KVC_ERR_ARG;
     if (r->dim < 0 || r->dim > 2 * kMaxHalfDim || (r->dim & 1)) return KVC_ERR_ARG;
     if (r->scaling < KVC_SCALING_NONE || r->scaling > KVC_SCALING_BANDS) return KVC_ERR_ARG;
@@ -443,8 +445,8 @@ KVC_API int kvc_rotary_init(kvc_rotary* r) {
         r->turns[i] = (uint64_t)std::ldexp(turn, 64);
     }
     if (r->magnitude == 0.f)
-        r->magnitude = (r->scaling == KVC_SCALING_YARN && r->factor > 1.f)
-                           ? (float)(0.1 * std::log((double)r->factor) + 1.0) : 1.f;
+        r->magnitude = r->filled = (r->scaling == KVC_SCALING_YARN && r->factor > 1.f)
+                                       ? (float)(0.1 * std::log((double)r->factor) + 1.0) : 1.f;
     r->ready = 1;
     return KVC_OK;
 }
