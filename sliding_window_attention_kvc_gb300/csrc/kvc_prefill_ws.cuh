@@ -899,12 +899,53 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             const int mode = meta[s].mask;
             float mn, alpha;
             if constexpr (SCORE) {
+                // keys that the row does not attend become -inf (if `on`)
+                auto mask = [&](bool on) {
+                    if (mode == kMaskRange) {
+                        // the chunk's own rows: key k at kbase + k (the window holds every chunk token)
+                        const int kb = meta[s].kbase;
+                        int klo = row_ok ? (int)min((long long)start - kb, (long long)kWsKeys) : kWsKeys;
+                        int khi = row_t - kb;
+                        if (!on) {
+                            klo = 0;
+                            khi = kWsKeys;
+                        }
+                        if (!__all_sync(0xffffffffu, klo <= 0 && khi >= kWsKeys - 1)) ws_mask_range(sv, klo, khi);
+                    } else if (on && !row_ok) {
+#pragma unroll
+                        for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
+                    } else if (on && mode == kMaskKeys) {
+                        const int from = paged ? start : max(start, row_t - p.window + 1);   // (sinks below it too)
+#pragma unroll
+                        for (int k = 0; k < kWsKeys; k += 4) {
+                            const int4 q4 = *reinterpret_cast<const int4*>(&meta[s].pos[k]);
+                            const int qk[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int q = qk[u];
+                                const bool allowed = q >= 0 && q <= row_t && (q >= from || (q < p.sinks && q >= start));
+                                sv[k + u] = allowed ? sv[k + u] : -INFINITY;
+                            }
+                        }
+                    }
+                };
                 // s = A v + B in base 2: v = q . k, or with a cap v = -1 / (2^(cap_in q.k) + 1)
                 // and s = 2 cap2 v + cap2 (cap tanh(x / cap) = cap - 2 cap / (e^(2 x / cap) + 1));
                 // a distance bias differs from key to key and is added to every v
                 float A = p.score.scale2, B = 0.f;
                 if constexpr (CAP) {
-                    ws_cap(sv, p.score.cap_in);
+                    const float nan = ws_cap(sv, p.score.cap_in);
+                    // A NaN among a row's scores, which the cap passes on to its neighbours: the warp
+                    // once more, the keys that such a row does not attend masked first; a NaN that
+                    // is left is the row's own.  (Masked first in every tile with a mask: 8 rings of
+                    // 4096, cap: 228 -> 262 us.)
+                    if (__any_sync(0xffffffffu, nan != nan)) {
+                        ws_ld32(lane_base + scol, sv);
+                        ws_ld32(lane_base + scol + 32, sv + 32);
+                        ws_wait_ld();
+                        mask(nan != nan);
+                        ws_cap(sv, p.score.cap_in);
+                    }
                     A = 2.f * p.score.cap2;
                     B = p.score.cap2;
                 }
@@ -927,30 +968,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                     A = 1.f;
                     B = 0.f;
                 }
-                // masks
-                if (mode == kMaskRange) {
-                    // the chunk's own rows: key k at kbase + k (the window holds every chunk token)
-                    const int kb = meta[s].kbase;
-                    const int klo = row_ok ? (int)min((long long)start - kb, (long long)kWsKeys) : kWsKeys;
-                    const int khi = row_t - kb;
-                    if (!__all_sync(0xffffffffu, klo <= 0 && khi >= kWsKeys - 1)) ws_mask_range(sv, klo, khi);
-                } else if (!row_ok) {
-#pragma unroll
-                    for (int k = 0; k < kWsKeys; ++k) sv[k] = -INFINITY;
-                } else if (mode == kMaskKeys) {
-                    const int from = paged ? start : max(start, row_t - p.window + 1);   // (sinks below it too)
-#pragma unroll
-                    for (int k = 0; k < kWsKeys; k += 4) {
-                        const int4 q4 = *reinterpret_cast<const int4*>(&meta[s].pos[k]);
-                        const int qk[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int q = qk[u];
-                            const bool allowed = q >= 0 && q <= row_t && (q >= from || (q < p.sinks && q >= start));
-                            sv[k + u] = allowed ? sv[k + u] : -INFINITY;
-                        }
-                    }
-                }
+                mask(true);
                 mn = fmaxf(100.f - p.score.cap2, 0.f);
                 mn = fminf(p.score.cap2, mn);
                 alpha = 1.f;

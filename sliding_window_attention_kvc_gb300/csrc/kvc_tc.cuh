@@ -140,6 +140,12 @@ __device__ __forceinline__ float ws_max3(float a, float b, float c) {
     return y;
 }
 
+__device__ __forceinline__ float ws_max3_nan(float a, float b, float c) {    // NaN if one of them is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Largest of 64 values, in four chains of three-input maxima.
 __device__ __forceinline__ float ws_max64(const float (&v)[kWsKeys]) {
     float m[4];
@@ -168,20 +174,28 @@ __device__ __forceinline__ float ws_exp64(float (&v)[kWsKeys], float a, float c)
     return s.x + s.y;
 }
 
+__device__ __forceinline__ float ws_hold30(float x) {    // min(x, 30), NaN if x is
+    float y;
+    asm("min.NaN.f32 %0, %1, 0f41F00000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // v = -1 / (2^(ci x) + 1) in place, the argument of a capped score (cap tanh =
 // 2 cap v + cap).  Reciprocals run at half the exponentials' rate here: four
 // denominators share one, 1 / a = b (c d) / (a b c d) and so on (measured: 64 keys of
 // two warps 1590 -> 1001 cycles).  Exponents are held to 30 so that no product
-// overflows: tanh is 1 - 2^-29 there, 1 in fp32; a NaN counts as 30 too, so that the garbage of
-// an absent key does not reach its neighbours.
+// overflows: tanh is 1 - 2^-29 there, 1 in fp32.  A NaN goes to its three neighbours
+// too: one among the keys that the row attends makes its result NaN anyhow, others are to
+// be masked before the cap.  Returns NaN if a score was NaN.
 template <int N>
-__device__ __forceinline__ void ws_cap(float (&v)[N], float ci) {
+__device__ __forceinline__ float ws_cap(float (&v)[N], float ci) {
     const float2 c2 = make_float2(ci, ci), one = make_float2(1.f, 1.f);
+    float any = 0.f, last = 0.f;
 #pragma unroll
     for (int k = 0; k < N; k += 4) {
         const float2 y0 = __fmul2_rn(make_float2(v[k], v[k + 1]), c2), y1 = __fmul2_rn(make_float2(v[k + 2], v[k + 3]), c2);
-        const float2 e0 = __fadd2_rn(make_float2(ws_ex2(fminf(y0.x, 30.f)), ws_ex2(fminf(y0.y, 30.f))), one);
-        const float2 e1 = __fadd2_rn(make_float2(ws_ex2(fminf(y1.x, 30.f)), ws_ex2(fminf(y1.y, 30.f))), one);
+        const float2 e0 = __fadd2_rn(make_float2(ws_ex2(ws_hold30(y0.x)), ws_ex2(ws_hold30(y0.y))), one);
+        const float2 e1 = __fadd2_rn(make_float2(ws_ex2(ws_hold30(y1.x)), ws_ex2(ws_hold30(y1.y))), one);
         const float2 pq = __fmul2_rn(make_float2(e0.x, e1.x), make_float2(e0.y, e1.y));    // a b, c d
         const float r = -ws_rcp(pq.x * pq.y);
         const float2 rp = __fmul2_rn(make_float2(r, r), make_float2(pq.y, pq.x));          // -1 / (a b), -1 / (c d)
@@ -191,7 +205,12 @@ __device__ __forceinline__ void ws_cap(float (&v)[N], float ci) {
         v[k + 1] = x0.y;
         v[k + 2] = x1.x;
         v[k + 3] = x1.y;
+        if (k & 4)
+            any = ws_max3_nan(any, last, r);
+        else
+            last = r;
     }
+    return any;
 }
 
 // Keys lo .. hi of a tile of N stay, the others become -inf (as bits of one word:
