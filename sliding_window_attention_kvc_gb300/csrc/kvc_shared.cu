@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kShCombineWarps * 32)
             const float2* ml;
             slot(base + lane, &ml);
             const float2 v = __ldcg(ml);
-            if (v.x != -INFINITY) {
+            if (v.x != -INFINITY || v.y != v.y) {      // (NaN scores leave no maximum, but a sum of NaN)
                 e = exp2f(v.x - M);
                 L += v.y * e;
             }
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kShCombineWarps * 32)
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dp.out) + ((long long)b * p.Hq + qh) * D + lane * NC;
 #pragma unroll
     for (int c = 0; c < NC; c += 2)

@@ -109,3 +109,19 @@ def test_nan_query_and_keys_outside_the_document(kvc, mods):
     if not mods.get("softcap"):
         assert torch.equal(got[~touched], want[~touched])
     assert got[touched].isnan().all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,prefix", [((200, 190, 210, 130), 128), ((300, 257, 256, 256), 256)])
+def test_nan_query_of_a_shared_decode(kvc, D, lens, prefix):
+    """Groups of two; a sequence whose keys are all shared, and one alone."""
+    bs, tables, at = 16, [], prefix // 16
+    for n in lens:
+        own = -(-n // bs) - at
+        tables.append(list(range(at)) + [at + sum(len(t) - at for t in tables) + i for i in range(own)])
+    c = Built(kvc, "paged", "bf16", lens, 8, 2, D, bs=bs, tables=tables)
+    ws = kvc.alloc_shared_workspace(c.d)
+    group = torch.tensor([1, 1, 1, -1], dtype=torch.int32, device="cuda")
+    _nan_rows(lambda x: kvc.decode_attention_shared(c.d, c.cache, c.layer, x, c.pos, group, ws, c.table), c.q,
+              [(0, 0), (1, 5), (2, 7), (3, 2)])
+    assert kvc.get_error(ws) == 0
