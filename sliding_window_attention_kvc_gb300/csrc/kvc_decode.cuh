@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                     O += merge_o[(w * GH + h) * D + d] * e;
                 }
                 static_cast<Elt*>(p.out)[((long long)b * p.Hq + kvh * p.G + z * GH + h) * D + d] =
-                    TR::from_f32(L > 0.f ? O / L : 0.f);
+                    TR::from_f32(L == 0.f ? 0.f : O / L);
             }
             return;
         }
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                 L += ml.y * e;
                 O += __ldcg(&p.part_o[slot * D + d]) * e;
             }
-            out[((long long)b * p.Hq + qh) * D + d] = TR::from_f32(L > 0.f ? O / L : 0.f);
+            out[((long long)b * p.Hq + qh) * D + d] = TR::from_f32(L == 0.f ? 0.f : O / L);
         }
         if (ctid == 0) p.counters[cidx] = 0u;
     }

@@ -125,3 +125,26 @@ def test_nan_query_of_a_shared_decode(kvc, D, lens, prefix):
     _nan_rows(lambda x: kvc.decode_attention_shared(c.d, c.cache, c.layer, x, c.pos, group, ws, c.table), c.q,
               [(0, 0), (1, 5), (2, 7), (3, 2)])
     assert kvc.get_error(ws) == 0
+
+
+@pytest.mark.parametrize("plain", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("layout,kw", [("ring", dict(lens=(1, 50, 1200), window=64)),
+                                       ("ring", dict(lens=(1, 50, 9000), window=4096)),
+                                       ("paged", dict(lens=(1, 40, 1200), bs=16)), ("paged", dict(lens=(700,), bs=16))])
+def test_nan_query_of_a_decode(kvc, dtype, layout, kw, plain):
+    """One part and many, for the plain call as well."""
+    c = Built(kvc, layout, dtype, H=4, KV=2, D=128, **kw)
+    B = len(c.lens)
+    rows = [(b, (b + 1) % 4) for b in range(B)]
+    if plain:
+        _nan_rows(lambda x: kvc.decode_attention(c.d, c.cache, c.layer, x, c.pos, c.ws, block_table=c.table), c.q, rows)
+    else:
+        for mods in MODS:
+            start = torch.zeros(B, dtype=torch.int32, device="cuda")
+            score = _score(kvc, 4, mods, start)
+            run = lambda x: kvc.decode_attention_scored(c.d, c.cache, c.layer, x, c.pos, c.ws, score, block_table=c.table)
+            _nan_rows(run, c.q, rows)
+            start.fill_(2 ** 30)                  # nothing attended: zeros, whatever the query holds
+            assert not run(torch.full_like(c.q, NAN)).any()
+    assert kvc.get_error(c.ws) == 0
