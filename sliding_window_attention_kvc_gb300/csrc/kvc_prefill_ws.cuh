@@ -800,8 +800,39 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
 
         // The Q tile: rotated at its position (a sink tile's at min(t, C - 1)), scaled by
-        // q_scale (softmax scale * log2 e, or 1), bf16.  D / 16 lanes share a row, so
-        // that a load covers whole lines (a row a thread took 6 us of each CTA).
+        // q_scale (softmax scale * log2 e, or 1), bf16.
+        // 8-column chunk c of row rr and its partner c + D / 16 (lo, hi) to the tile,
+        // [column block][128 rows][128 B], 128-byte swizzle; th(k): frequency of pair 8 c + k
+        auto write_q_chunk = [&](int rr, int c, bool rok, long long qpos, auto rotated, auto th, uint4 lo, uint4 hi) {
+            if (!SCORE || rotated.value) {
+                const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                uint32_t lo2[4], hi2[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
+                    float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
+                    if (rotated.value && rok) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float cs, sn;
+                            rope_cos_sin(qpos, th(2 * e + u), &cs, &sn);
+                            const float x1 = x[u], x2 = y[u];
+                            x[u] = x1 * cs - x2 * sn;
+                            y[u] = x1 * sn + x2 * cs;
+                        }
+                    }
+                    lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
+                    hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
+                }
+                lo = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
+                hi = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
+            }
+            const int c2 = c + D / 16;
+            *reinterpret_cast<uint4*>(Qs + (c >> 3) * (kWsRows * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = lo;
+            *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = hi;
+        };
+        // D / 16 lanes share a row, so that a load covers whole lines (unrotated, a row a
+        // thread took 6 us of each CTA)
         constexpr int QLPR = D / 16, QRPW = 32 / QLPR;
         const int qc = lane % QLPR;                    // 8-column chunk, paired with qc + D / 16
         auto write_q_rows = [&](int it, bool at_sinks, auto rotated, const unsigned long long* th) {
@@ -815,39 +846,28 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 lo = *reinterpret_cast<const uint4*>(qrow + 8 * qc);
                 hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * qc);
             }
-            if (!SCORE || rotated.value) {
-                const long long qpos = at_sinks ? min(rt, C - 1) : rt;
-                const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                uint32_t lo2[4], hi2[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x[2] = {__uint_as_float(lw[e] << 16), __uint_as_float(lw[e] & 0xffff0000u)};
-                    float y[2] = {__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)};
-                    if (rotated.value && rok) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float cs, sn;
-                            rope_cos_sin(qpos, th[2 * e + u], &cs, &sn);
-                            const float x1 = x[u], x2 = y[u];
-                            x[u] = x1 * cs - x2 * sn;
-                            y[u] = x1 * sn + x2 * cs;
-                        }
-                    }
-                    lo2[e] = pack_bf16x2(x[0] * p.q_scale, x[1] * p.q_scale);
-                    hi2[e] = pack_bf16x2(y[0] * p.q_scale, y[1] * p.q_scale);
-                }
-                lo = make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
-                hi = make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
-            }
-            // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-            const int c1 = qc, c2 = qc + D / 16;
-            *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = lo;
-            *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = hi;
+            write_q_chunk(rr, qc, rok, at_sinks ? min(rt, C - 1) : rt, rotated, [&](int k) { return th[k]; }, lo, hi);
         };
         auto write_q = [&](bool at_sinks) {
             if (p.rope == kRopeNone) {
 #pragma unroll 4
                 for (int it = 0; it < 32 / QRPW; ++it) write_q_rows(it, at_sinks, std::false_type{}, nullptr);
+            } else if constexpr (!READ && !SCORE) {
+                // baked rows a thread each: the frequencies are then the same for the whole warp
+                // (paged, 64 x 128 tokens: 1.129 ms by whole lines, 1.122 so; INT8 1.339 and 1.334;
+                // ring, 8 x 128: 126 and 122.5 us.  Read-time RoPE is the other way round, 1.271
+                // by lines against 1.293 ms; modified scores within 3 % either way)
+                const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
+                                            (((long long)b * p.T + (row_ok ? row_i : 0)) * p.Hq + row_h) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                    if (row_ok) {
+                        lo = *reinterpret_cast<const uint4*>(qrow + 8 * c);
+                        hi = *reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c);
+                    }
+                    write_q_chunk(r, c, row_ok, row_t, std::true_type{}, [&](int k) { return p.theta[8 * c + k]; }, lo, hi);
+                }
             } else {
                 // (the lane's frequencies are read once: lanes read different ones; unrolled,
                 // the rotations took 13 us more of each CTA)
