@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
             g.mt = (g.n + p.mq - 1) / p.mq;
             // the columns of a kv head: full ones of two units a tile, and a last one
             const int last = g.n - (g.mt - 1) * p.mq;
-            g.hu = g.kt * ((g.mt - 1) * p.full_units + (last <= p.tq ? 1 : p.full_units));
-            u = (long long)p.Hkv * g.hu;
+            g.hu = (long long)g.kt * ((g.mt - 1) * p.full_units + (last <= p.tq ? 1 : p.full_units));
+            u = p.Hkv * g.hu;
             r = (long long)p.Hkv * g.n * p.G;
         }
         long long iu = u, ir = r;
@@ -312,11 +312,12 @@ __device__ __forceinline__ PxSegment px_segment(const SharedParams& p, int ngrou
         if (le != 0xffffffffu) break;
     }
     const SharedGroup* g = p.groups + gi;
-    const int kt = __ldcg(&g->kt), n = __ldcg(&g->n), hu = __ldcg(&g->hu);
+    const int kt = __ldcg(&g->kt), n = __ldcg(&g->n);
+    const long long hu = __ldcg(&g->hu);
     long long v = u - __ldcg(&g->units0);
     PxSegment s;
     s.h = (int)(v / hu);
-    v -= (long long)s.h * hu;
+    v -= s.h * hu;
     const int m = (int)(v / ((long long)kt * p.full_units));     // every column but a head's last is full
     v -= (long long)m * kt * p.full_units;
     s.m0 = m * p.mq;
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(kShCombineWarps * 32)
         const long long units = __ldcg(&p.head->units);
         const int shares = __ldcg(&p.head->shares);
         const bool one = min(p.mq, n - m * p.mq) <= p.tq;
-        const long long u0 = __ldcg(&g->units0) + (long long)h * __ldcg(&g->hu) + (long long)m * kt * p.full_units;
+        const long long u0 = __ldcg(&g->units0) + h * __ldcg(&g->hu) + (long long)m * kt * p.full_units;
         fx = streamk_share_of(u0, units, shares);
         np = streamk_share_of(u0 + (long long)kt * (one ? 1 : p.full_units) - 1, units, shares) - fx + 1;
         alt = shared_q_tiles(D) == 2 && one;

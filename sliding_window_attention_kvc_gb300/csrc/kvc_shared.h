@@ -19,7 +19,7 @@ struct SharedGroup {
     int kt, mt;           // tiles of a column; columns of a kv head
     int n, off, leader;   // members, their place in the member list, the first of them
     int rows;             // shared rows (whole blocks)
-    int hu;               // units of a kv head
+    long long hu;         // units of a kv head
 };
 
 struct SharedHead {
