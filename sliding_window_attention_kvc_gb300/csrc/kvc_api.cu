@@ -390,9 +390,6 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     // failure leaves the cache and the workspace untouched)
     KvTensorMaps maps;
     if (d->dtype != KVC_F32 && (rc = kv_maps_for(d, g, cache, &maps, &p.tma_whole))) return rc;
-    // one paged sequence on the tensor-core kernel: its CTAs plan their own
-    // shares from the block table and write the step's token themselves
-    // (the CTAs bulk-copy the table and the valid words: 16-byte aligned buffers)
     // shared prefixes: laid out before anything else is planned; the sequences'
     // own blocks begin behind them
     SharedParams sh{};
@@ -440,6 +437,9 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         p.no_combine = 1;
     }
     const int32_t* const start = group ? sh.start : sp.start;
+    // one paged sequence on the tensor-core kernel: its CTAs plan their own
+    // shares from the block table and write the step's token themselves
+    // (the CTAs bulk-copy the table and the valid words: 16-byte aligned buffers)
     // (a start is left to the planning kernel, which drops the blocks below it)
     p.self_plan = (paged && !start && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
                    (d->num_blocks + 31) / 32 <= kSelfPlanValidWords && aligned16(block_table) &&

@@ -50,7 +50,7 @@ constexpr float kWsLazy = 8.f;
 // a sought maximum) while the smallest weight, 2^(-2 cap2), stays at or above 2^-100;
 // with larger caps that smallest weight is kept there and the largest grows to 2^50:
 // values up to 2^57 in magnitude still sum over 2^20 keys.  (8 rings of 4096, 256 tokens,
-// cap 20: 258 us with the maximum, 229 us without.)
+// cap 20: 259 us with the maximum, 232 us without.)
 constexpr float kWsFixedCap = 75.f;
 enum : int { kModPlain = 0, kModScore = 1, kModCap = 2, kModBias = 4, kModFixed = 8 };
 
@@ -136,14 +136,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     using S = WsShape<D>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
     // bf16 rows taken as they lie: an issuing warp for each Q tile, the second in the
-    // place of a fix-up warp, which has little to do (plain ring, 128-token chunks: 138 ->
-    // 127 us)
+    // place of a fix-up warp, which has little to do (plain ring, 128-token chunks: 135 ->
+    // 122.5 us, paged 1.128 -> 1.123 ms; modified scores: 238 -> 232 and 198 -> 181 us)
     constexpr bool TWO = !READ && !Q8;
-    // read-time RoPE: the issuing thread runs alone and each thread arrives for itself
-    // (sink ring, 128-token chunks: 1.24 ms; a whole issuing warp and an arrival a warp,
-    // best elsewhere: 1.28)
-    constexpr bool ALONE = READ;
-    static_assert(!(ALONE && TWO), "the arrivals a barrier counts are those its warps make");
     extern __shared__ unsigned char ws_raw[];
     const uint32_t raw_u = smem_u32(ws_raw);
     unsigned char* sm = ws_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
@@ -171,7 +166,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], TWO ? 1 : (ALONE ? 64 : 2));
+            mbar_init(&bars->ready[s], TWO ? 1 : 2);
             mbar_init(&bars->empty[s], TWO ? NQ : 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -179,7 +174,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 mbar_init(&bars->s_full[i][u], 1);
                 mbar_init(&bars->s_free[i][u], 4);
             }
-            mbar_init(&bars->p_full[i], ALONE ? kWsRows : 4);
+            mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], kWsRows);
         }
@@ -622,7 +617,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             // (one arrival a warp: arrivals on one barrier are made one after the other)
             __syncwarp();
-            if (ALONE || lane == 0) mbar_arrive(&bars->ready[s]);
+            if (lane == 0) mbar_arrive(&bars->ready[s]);
             if (kind == kTileEnd) break;
         }
     } else if (TWO && (warp == 1 || (NQ == 2 && warp == 3))) {
@@ -692,99 +687,96 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // =========================== MMA issuer =============================
-        // the whole warp walks the tiles (its values stay uniform) and lane 0 issues, or
-        // lane 0 walks them alone
-        if (!ALONE || lane == 0) {
-            bool ok = true;
-            int nt = 0x7fffffff;
-            uint64_t qd[NQ];
-            for (int i = 0; i < NQ; ++i) qd[i] = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
-            const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
-            const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
-            auto stage_d = [&](int j) { return (uint64_t)(((j % NST) * S::StageBytes) >> 4); };
-            // S_i(j) = Q_i K_j^T
-            auto issue_s = [&](int j) {
+        // the whole warp walks the tiles (its values stay uniform) and lane 0 issues
+        bool ok = true;
+        int nt = 0x7fffffff;
+        uint64_t qd[NQ];
+        for (int i = 0; i < NQ; ++i) qd[i] = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
+        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
+        auto stage_d = [&](int j) { return (uint64_t)(((j % NST) * S::StageBytes) >> 4); };
+        // S_i(j) = Q_i K_j^T
+        auto issue_s = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    if (!ok) break;
-                    if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    ws_fence_after();
-                    const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                    if (lane == 0) {
-                        ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i], kd0 + stage_d(j));
-                        ws_commit(&bars->s_full[i][j & 1]);
-                    }
-                    if (!ALONE) __syncwarp();
-                }
-            };
-            // S of tile t for every Q tile, once its keys are in place; false at
-            // the end marker (nt = t) or when a wait gave up
-            auto try_issue = [&](int t) -> bool {
-                if (!ok || t >= nt) return false;
-                if (!ws_wait(&bars->ready[t % NST], (t / NST) & 1, abort)) {
-                    ok = false;
-                    return false;
-                }
-                if (meta[t % NST].kind == kTileEnd) {
-                    nt = t;
-                    return false;
-                }
-                for (int i = 0; i < NQ && ok; ++i) {
-                    // q at position 0, and (read-time RoPE) again past the sink tile
-                    if (t == 0 && !ws_wait(&bars->q_ready[i], 0, abort)) ok = false;
-                    if (READ && sink_tile && t == 1 && !ws_wait(&bars->q_ready[i], 1, abort)) ok = false;
-                }
-                if (ok) issue_s(t);
-                return ok;
-            };
-            // S runs LA tiles ahead of P V: each Q tile's next scores are queued
-            // on the tensor cores while its softmax works on the current ones.
-            // LA + 1 tiles are in flight, so the stages must hold them.
-            constexpr int LA = NST >= 3 ? 2 : 1;
-            int issued = 0;
-            while (issued < LA && try_issue(issued)) ++issued;
-            int j = 0;
-            for (; ok && j < issued; ++j) {
-                // O_i += P_i V_j
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    ws_fence_after();
-                    // P_i(j) in the S buffer it came from (bf16 pairs, 32 columns);
-                    // S of tile j + 2 reuses that buffer, issued after this P V
-                    const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
-                    if (lane == 0) {
-                        ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + stage_d(j), j > 0);
-                        ws_commit(&bars->o_done[i]);
-                    }
-                    if (!ALONE) __syncwarp();
-                }
+            for (int i = 0; i < NQ; ++i) {
                 if (!ok) break;
-                if (lane == 0) ws_commit(&bars->empty[j % NST]);       // K and V of tile j are done with
-                if (issued == j + LA && try_issue(issued)) ++issued;
-            }
-            if (*abort) ok = false;
-            if (!ALONE) ok = __all_sync(0xffffffffu, ok);
-            nt = j;
-            if (lane == 0) {
-                if (ok) {
-                    // the end: the softmax warps learn the tile count at the S slot
-                    // they wait on next (every S before it has been consumed)
-                    bars->ntiles = nt;
-                    for (int i = 0; i < NQ; ++i) mbar_arrive(&bars->s_full[i][nt & 1]);
-                } else {
-                    give_up();
+                if (j >= 2 && !ws_wait(&bars->s_free[i][j & 1], ((j >> 1) - 1) & 1, abort)) {
+                    ok = false;
+                    break;
                 }
-                // every product this thread issued is done before TMEM is freed
-                ws_commit(&bars->fin[0]);
-                if (!mbar_wait(&bars->fin[0], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+                ws_fence_after();
+                const uint32_t d = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
+                if (lane == 0) {
+                    ws_issue_s<D, kWsRows * 128, S::KVBlock>(d, qd[i], kd0 + stage_d(j));
+                    ws_commit(&bars->s_full[i][j & 1]);
+                }
+                __syncwarp();
             }
+        };
+        // S of tile t for every Q tile, once its keys are in place; false at
+        // the end marker (nt = t) or when a wait gave up
+        auto try_issue = [&](int t) -> bool {
+            if (!ok || t >= nt) return false;
+            if (!ws_wait(&bars->ready[t % NST], (t / NST) & 1, abort)) {
+                ok = false;
+                return false;
+            }
+            if (meta[t % NST].kind == kTileEnd) {
+                nt = t;
+                return false;
+            }
+            for (int i = 0; i < NQ && ok; ++i) {
+                // q at position 0, and (read-time RoPE) again past the sink tile
+                if (t == 0 && !ws_wait(&bars->q_ready[i], 0, abort)) ok = false;
+                if (READ && sink_tile && t == 1 && !ws_wait(&bars->q_ready[i], 1, abort)) ok = false;
+            }
+            if (ok) issue_s(t);
+            return ok;
+        };
+        // S runs LA tiles ahead of P V: each Q tile's next scores are queued
+        // on the tensor cores while its softmax works on the current ones.
+        // LA + 1 tiles are in flight, so the stages must hold them.
+        constexpr int LA = NST >= 3 ? 2 : 1;
+        int issued = 0;
+        while (issued < LA && try_issue(issued)) ++issued;
+        int j = 0;
+        for (; ok && j < issued; ++j) {
+            // O_i += P_i V_j
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                if (!ws_wait(&bars->p_full[i], j & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                ws_fence_after();
+                // P_i(j) in the S buffer it came from (bf16 pairs, 32 columns);
+                // S of tile j + 2 reuses that buffer, issued after this P V
+                const uint32_t p_t = tmem + S::SCol0 + (uint32_t)((i * 2 + (j & 1)) * kWsKeys);
+                if (lane == 0) {
+                    ws_issue_pv<D>(tmem + (uint32_t)(i * D), p_t, vd0 + stage_d(j), j > 0);
+                    ws_commit(&bars->o_done[i]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (lane == 0) ws_commit(&bars->empty[j % NST]);       // K and V of tile j are done with
+            if (issued == j + LA && try_issue(issued)) ++issued;
+        }
+        if (*abort) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        nt = j;
+        if (lane == 0) {
+            if (ok) {
+                // the end: the softmax warps learn the tile count at the S slot
+                // they wait on next (every S before it has been consumed)
+                bars->ntiles = nt;
+                for (int i = 0; i < NQ; ++i) mbar_arrive(&bars->s_full[i][nt & 1]);
+            } else {
+                give_up();
+            }
+            // every product this thread issued is done before TMEM is freed
+            ws_commit(&bars->fin[0]);
+            if (!mbar_wait(&bars->fin[0], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
         }
         __syncwarp();
     } else if (warp >= kWsSoftmax0 && warp < kWsSoftmax0 + 4 * NQ) {
@@ -1086,8 +1078,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             }
             ws_wait_st();
             ws_fence_before();
-            if (!ALONE) __syncwarp();
-            if (ALONE || lane == 0) mbar_arrive(&bars->p_full[qi]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[qi]);
         }
         if (!ok) give_up();
         // the last P V, then O / l to the output
