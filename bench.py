@@ -381,10 +381,10 @@ class ClockSampler:
 # capture per workload, and the digest of the kernel's sources
 # (KERNEL_TRAFFIC_FILES) they were taken on: reported only while those
 # sources are unchanged.
-KERNEL_TRAFFIC = {"ring_bf16": 137616896, "sink_window_bf16": 542781696,
-                  "paged_shared_prefix_bf16": 841274624, "long_context_pool_bf16": 155708928,
-                  "ring_int8": 69713408}
-KERNEL_TRAFFIC_SOURCES = "a6ae3a09964a74264a89253764b7c4c84ab0875e82a572af8d66bdfc3407721e"
+KERNEL_TRAFFIC = {"ring_bf16": 137129216, "sink_window_bf16": 542877184,
+                  "paged_shared_prefix_bf16": 840988672, "long_context_pool_bf16": 155721728,
+                  "ring_int8": 69624576}
+KERNEL_TRAFFIC_SOURCES = "1e94581e5a1e00e04622639553fdf43960b63803cf03b3d8628b9b7bd38d45d9"
 
 
 # the sources decode_mma_kernel and its launch are built from
