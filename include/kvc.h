@@ -337,9 +337,9 @@ KVC_API int kvc_decode_attention_scored(const kvc_desc* d, const void* cache, in
  * shared block from the L2 cache, is faster.
  *   group      [batch] int32: sequences with the same value 0 .. batch - 1 form
  *              a group; below 0: alone.  batch or more sets KVC_DEV_BAD_ENTRY
- *              (the sequence counts as alone).  A member without a whole block
- *              in common (an idle slot) leaves its group nothing to share: such
- *              sequences are given a group below 0.
+ *              (the sequence counts as alone).  Members without a whole block in
+ *              common with the group's first that has one (idle slots, another
+ *              prompt) count as alone; the others share what they all have.
  *   workspace  kvc_shared_workspace_bytes(d) bytes (0 if `d` is refused), set
  *              up by kvc_workspace_init; it serves the other decode calls too.
  * bf16 caches, blocks whose size is a multiple of 8 and divides 64 or is a

@@ -8,9 +8,9 @@
 //
 //   shared_plan_kernel    one CTA per sequence: its place in its group, and how
 //                         many leading blocks its table shares with the first
-//                         member's; the last CTA to finish (an atomic ticket,
-//                         no waiting) takes each group's minimum and lays the
-//                         work out.
+//                         member's that has any; the last CTA to finish (an atomic
+//                         ticket, no waiting) takes each group's minimum over the
+//                         members that share and lays the work out.
 //   (plan_rows_kernel)    the blocks behind the shared ones, per sequence.
 //   shared_prefix_kernel  the shared keys, on tcgen05 (below).
 //   (decode_mma_kernel)   the rest.
@@ -33,8 +33,11 @@
 // Measured (32 / 8 heads of 128, blocks of 16), whole call: 64 sequences in groups
 // of 8 with 2048 shared tokens and 2049 .. 8192 in all 185 us, 0.69 of the bytes'
 // time (the plan 8 us, the prefix 25 to 35, the sequences' own keys 130 at 0.9 of
-// bandwidth, the combine 5); 96 readers of one document 149 us, of which the prefix
-// 75 at the softmax's rate; six readers 41 us, five dependent launches.
+// bandwidth, the combine 5); 96 readers of one document 149 us, of which the prefix 75;
+// six readers 41 us, five dependent launches.  Plain decode of the same batches, which
+// takes a shared block from L2 for all sequences but the first (cold, us, plain / shared):
+// 179 / 200, 1087 / 155, 30 / 52; the shared form pays from about 150,000 shared tokens
+// mapped (sequences x prefix).
 #include <atomic>
 
 #include "kvc_decode.cuh"
@@ -89,8 +92,13 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
     const int tid = threadIdx.x, b = blockIdx.x;
     sh_pdl_wait();
     sh_pdl_launch();
-    // this sequence's place: the members of lower group ids before its group,
-    // its rank in the group, the group's size and first member
+    auto full_blocks = [&](int q) {                // blocks wholly at positions <= t of sequence q
+        const int t = clamp_paged_t(p.pos[q], p.maxb, p.bs);
+        return t < 0 ? 0 : (int)(((long long)t + 1) / p.bs);
+    };
+    // this sequence's place: the members of lower group ids before its group, its rank
+    // in the group, the group's size, and the first member that has a block to share (an
+    // idle one has none)
     const int gid = p.group[b];
     const bool grouped = gid >= 0 && gid < p.B;
     if (gid >= p.B && tid == 0) set_error(p.err, 0x10u /* KVC_DEV_BAD_ENTRY */);
@@ -102,18 +110,15 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
             if (og == gid) {
                 ++c.n;
                 if (o < b) ++c.rank;
-                c.leader = min(c.leader, o);
+                if (o < c.leader && full_blocks(o) > 0) c.leader = o;
             }
         }
     }
     c = sh_reduce(c, s_w);
-    // leading blocks wholly at positions <= t here and for the first member,
-    // whose entries equal the first member's
-    if (grouped && c.n > 1) {
-        auto full_blocks = [&](int s) {
-            const int t = clamp_paged_t(p.pos[s], p.maxb, p.bs);
-            return t < 0 ? 0 : (int)(((long long)t + 1) / p.bs);
-        };
+    // leading blocks wholly at positions <= t here and for that member, whose entries
+    // equal that member's
+    const bool placed = grouped && c.n > 1 && c.leader < p.B;
+    if (placed) {
         const int nb = min(full_blocks(b), full_blocks(c.leader));
         if (tid == 0) s_common = nb;
         __syncthreads();
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
         __syncthreads();
     }
     if (tid == 0) {
-        p.seq[b] = make_int4(grouped && c.n > 1 ? c.below : -1, c.rank, c.n, grouped && c.n > 1 ? s_common : 0);
+        p.seq[b] = make_int4(placed ? c.below : -1, c.rank, c.n, placed ? s_common : 0);
         if (grouped) p.members[c.below + c.rank] = b;
         __threadfence();
         s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
@@ -137,12 +142,23 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    // the last CTA: each group's common blocks, kept at its place in the member list
-    for (int o = tid; o < p.B; o += kShPlanThreads) p.gmin[o] = 0x7fffffff;
+    // the last CTA: the blocks that the members of a group have in common, how many have
+    // any and the first of them, kept at the group's place in the member list.  Members
+    // without (idle, or mapped elsewhere) take part in nothing but the tiles' rows: their
+    // own keys begin at 0, and the join does not read their part of the prefix.
+    for (int o = tid; o < p.B; o += kShPlanThreads) {
+        p.gmin[o] = 0x7fffffff;
+        p.start[o] = 0x7fffffff;
+        p.seq_group[o].x = 0;
+    }
     __syncthreads();
     for (int o = tid; o < p.B; o += kShPlanThreads) {
         const int4 s = __ldcg(&p.seq[o]);
-        if (s.x >= 0) atomicMin(&p.gmin[s.x], s.w);
+        if (s.x >= 0 && s.w > 0) {
+            atomicMin(&p.gmin[s.x], s.w);
+            atomicMin(&p.start[s.x], o);
+            atomicAdd(&p.seq_group[s.x].x, 1);
+        }
     }
     __syncthreads();
     // groups with something to share, in member-list order: their units (tiles of
@@ -152,15 +168,15 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
     const int lane = tid & 31, warp = tid >> 5;
     for (int base = 0; base < p.B; base += kShPlanThreads) {
         const int o = base + tid;
-        // place o of the member list begins a group iff its member has rank 0
+        // place o of the member list begins a group iff two of its members share
         int4 s = make_int4(-1, 0, 0, 0);
         int lead = -1;
-        if (o < p.B && __ldcg(&p.gmin[o]) != 0x7fffffff) {
-            lead = __ldcg(&p.members[o]);
+        if (o < p.B && __ldcg(&p.seq_group[o].x) > 1) {
+            lead = __ldcg(&p.start[o]);
             s = __ldcg(&p.seq[lead]);
         }
-        int common = lead >= 0 ? __ldcg(&p.gmin[o]) : 0;
-        const bool real = lead >= 0 && common > 0;
+        const int common = lead >= 0 ? __ldcg(&p.gmin[o]) : 0;
+        const bool real = lead >= 0;
         SharedGroup g{};
         long long u = 0, r = 0;
         if (real) {
@@ -219,7 +235,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const __gri
     // each sequence's group and the position its own keys begin at
     for (int o = tid; o < p.B; o += kShPlanThreads) {
         const int4 s = __ldcg(&p.seq[o]);
-        const int gi = s.x >= 0 ? p.gmin[s.x] : -1;
+        const int gi = s.x >= 0 && s.w > 0 ? p.gmin[s.x] : -1;
         p.seq_group[o] = make_int2(gi, s.y);
         p.start[o] = gi >= 0 ? p.groups[gi].rows : 0;
     }

@@ -17,7 +17,7 @@ struct SharedGroup {
     long long units0;     // units of the groups before
     long long rows0;      // partial rows of the groups before
     int kt, mt;           // tiles of a column; columns of a kv head
-    int n, off, leader;   // members, their place in the member list, the first of them
+    int n, off, leader;   // members, their place in the member list, the first that shares
     int rows;             // shared rows (whole blocks)
     long long hu;         // units of a kv head
 };
