@@ -86,3 +86,30 @@ def test_idle_members_of_many_groups(kvc):
     got = call([i % 30 for i in range(n)])
     want = call([-1 if i < 30 else i % 30 for i in range(n)])
     assert torch.equal(got, want) and not torch.equal(got, call([-1] * n))
+
+
+def test_thousands_of_sequences(kvc):
+    """A batch far wider than the plan's thread block, against the formula for some of its sequences and
+    against plain decode for all: two roundings of the weights and of the output, and plain decode's query
+    rounded after its scale (2^-8 sum |q_i k_i| scale, under 8 here, twice in a weight)."""
+    from tests import test_gpu_shared as shared
+
+    n, ng, bs = 4096, 500, 8
+    lens = [17 + (i * 13) % 23 for i in range(n)]
+    tables, at = [], 2 * ng
+    for i, m in enumerate(lens):
+        need = -(-m // bs)
+        g = i % ng
+        tables.append([2 * g, 2 * g + 1] + list(range(at, at + need - 2)))
+        at += need - 2
+    c = Built(kvc, "paged", "bf16", lens, 4, 1, 64, bs=bs, tables=tables, qstd=1.0)
+    ws = kvc.alloc_shared_workspace(c.d)
+    group = torch.tensor([i % ng for i in range(n)], dtype=torch.int32, device="cuda")
+    out = kvc.decode_attention_shared(c.d, c.cache, c.layer, c.q, c.pos, group, ws, c.table)
+    again = kvc.decode_attention_shared(c.d, c.cache, c.layer, c.q, c.pos, group, ws, c.table)
+    assert torch.equal(out, again) and kvc.get_error(ws) == 0
+    shared._check(c, out, skip=[b for b in range(n) if b % 97], rel=2.0 ** -8 + 1e-3)
+    ref = kvc.decode_attention(c.d, c.cache, c.layer, c.q, c.pos, c.ws, block_table=c.table)
+    vmax = float(c.v.abs().max())
+    rel = 2 * (2.0 ** -8 + 1e-3) + 2 * 8 * 2.0 ** -8
+    assert ((out.float() - ref.float()).abs() <= rel * vmax + 2.0 ** -7 * ref.float().abs()).all()
