@@ -407,8 +407,9 @@ def _tokens(t: torch.Tensor, name: str, dtype, B: int, n: int, heads: int, D: in
 
 
 def _need_qk(z: _Sizes, qk: KvcQk, dev: int):
-    """The weights were checked against the descriptor they were given with; the call's may be another."""
-    for name, w in zip(("q_weight", "k_weight"), qk.keep[1:]):
+    """The weights were checked against the descriptor they were given with; the call's may be another.
+    (A KvcQk filled in by hand holds addresses alone: they are the caller's, as in C.)"""
+    for name, w in zip(("q_weight", "k_weight"), getattr(qk, "keep", (None,))[1:]):
         if w is not None:
             if w.dtype is not z.act:
                 raise TypeError(f"qk: {name} must be {z.act}, got {w.dtype}")
