@@ -445,6 +445,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
                    (d->num_blocks + 31) / 32 <= kSelfPlanValidWords && aligned16(block_table) &&
                    (!valid_bits || aligned16(valid_bits))) ? 1 : 0;
     if (p.self_plan) {
+        if (p.nsplit > w.ctas) p.nsplit = w.ctas;      // each CTA takes the share of its index, none claims another
         p.seq_items = reinterpret_cast<int2*>(ws + w.plan_seq);
         p.n_items = reinterpret_cast<int32_t*>(ws + w.plan_total);
         p.items = reinterpret_cast<int4*>(ws + w.plan_items);
