@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
     const int t_lo = max(pos0 + i0, 0);
     const int t0 = pos0 - 1;                         // the cache holds positions <= t0
     // read-time RoPE: sink keys are scored with q at min(t, C - 1), so they form
-    // a tile of their own, first (only cached sinks: chunk tokens below C need none)
-    const bool sink_tile = READ && !paged && p.sinks > 0 && t0 >= 0 && t_hi >= 0;
+    // tiles of their own, first (only cached sinks: chunk tokens below C need none)
+    const int sink_tiles = READ && !paged && t0 >= 0 && t_hi >= 0 ? (min(p.sinks, t0 + 1) + kWsKeys - 1) / kWsKeys : 0;
 
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             if (SCORE)
                 for (int i_s = i_last / kWsKeys * kWsKeys; i_s >= 0 && ok; i_s -= kWsKeys) issue_stage_tile(i_s);
             if (!paged) {
-                if (sink_tile) issue_slot_tile(0, kTileSink);
+                for (int k = 0; k < sink_tiles && ok; ++k) issue_slot_tile(k * kWsKeys, kTileSink);
                 // slot tiles with at least one key the CTA can see
                 const int nslot = (C + kWsKeys - 1) / kWsKeys;
                 for (int k = 0; k < nslot && ok; ++k) {
@@ -726,9 +726,9 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
                 return false;
             }
             for (int i = 0; i < NQ && ok; ++i) {
-                // q at position 0, and (read-time RoPE) again past the sink tile
+                // q at position 0, and (read-time RoPE) again past the sink tiles
                 if (t == 0 && !ws_wait(&bars->q_ready[i], 0, abort)) ok = false;
-                if (READ && sink_tile && t == 1 && !ws_wait(&bars->q_ready[i], 1, abort)) ok = false;
+                if (READ && t > 0 && t == sink_tiles && !ws_wait(&bars->q_ready[i], 1, abort)) ok = false;
             }
             if (ok) issue_s(t);
             return ok;
@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             fence_proxy_async_smem();
             mbar_arrive(&bars->q_ready[qi]);
         };
-        write_q(sink_tile);
+        write_q(sink_tiles > 0);
 
         float m_run = -INFINITY, l_run = 0.f;
         // SCORE: the row's slope (base 2), its bias at distance row_i, and its start
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(WsShape<D>::Threads, 1)
             ws_fence_before();
             __syncwarp();
             if (!TWO && lane == 0) mbar_arrive(&bars->s_free[qi][j & 1]);
-            if (READ && sink_tile && j == 0) write_q(false);     // S of the sink tile is out of TMEM
+            if (READ && j == sink_tiles - 1) write_q(false);     // S of the last sink tile is out of TMEM
             const int s = j % NST;
             if (!ws_wait(&bars->ready[s], (j / NST) & 1, abort)) {    // the stage's meta
                 ok = false;
