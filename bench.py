@@ -381,10 +381,10 @@ class ClockSampler:
 # capture per workload, and the digest of the kernel's sources
 # (KERNEL_TRAFFIC_FILES) they were taken on: reported only while those
 # sources are unchanged.
-KERNEL_TRAFFIC = {"ring_bf16": 137129216, "sink_window_bf16": 542877184,
-                  "paged_shared_prefix_bf16": 840988672, "long_context_pool_bf16": 155721728,
-                  "ring_int8": 69624576}
-KERNEL_TRAFFIC_SOURCES = "1e94581e5a1e00e04622639553fdf43960b63803cf03b3d8628b9b7bd38d45d9"
+KERNEL_TRAFFIC = {"ring_bf16": 137129472, "sink_window_bf16": 542839552,
+                  "paged_shared_prefix_bf16": 842615808, "long_context_pool_bf16": 155723264,
+                  "ring_int8": 69640192}
+KERNEL_TRAFFIC_SOURCES = "493a159d06b4594331754d9e513fb8dd2901f99221b2fbc74c74f70b726fed74"
 
 
 # the sources decode_mma_kernel and its launch are built from
