@@ -352,6 +352,102 @@ KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, in
                                         const uint32_t* valid_bits, void* out, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/* Long caches read in part: every block of a PAGED cache keeps the ends of its
+ * keys, channel by channel; a decode step asks them which blocks can hold large
+ * scores, and attends those alone.  Every element type and rope NONE or BAKED
+ * (the keys as the cache stores them); kvc_decode_attention_selected bf16 and
+ * INT8 caches.
+ *
+ * Bounds of the blocks, caller-owned memory of kvc_bounds_bytes(d) bytes (0 if
+ * `d` is refused), 16-byte aligned: int8 codes [layers, num_blocks, kv_heads, 2,
+ * head_dim], at index 0 the largest key value of each channel, at 1 the
+ * smallest, then fp32 steps [layers, num_blocks, kv_heads]:
+ *     step = max over channels of max(|largest|, |smallest|) / 127,
+ *     codes ceil(largest / step) and floor(smallest / step), clamped to +-127
+ * (IEEE fp32 quotients; a step of 0 has codes 0), so that code * step bounds the
+ * keys from outside.
+ *
+ * kvc_block_bounds works them out for every logical block that holds one of the
+ * positions pos[b] .. pos[b] + n - 1 (n = n_tok[b], cut to 0 .. n_new; NULL:
+ * n_new), from the block's first row to position pos[b] + n - 1: call it after
+ * the append of those tokens, and after a block was copied (kvc_block_prepare)
+ * or brought in.  Positions below 0 are padding.  A block that several
+ * sequences map is written by each of them.  Keys are finite.  Device errors as
+ * in kvc_append.  Workspace: kvc_workspace_bytes(d). */
+KVC_API size_t kvc_bounds_bytes(const kvc_desc* d);
+KVC_API int kvc_block_bounds(const kvc_desc* d, const void* cache, int32_t layer, void* bounds, const int32_t* pos,
+                             int32_t n_new, const int32_t* n_tok, const int32_t* block_table, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The k blocks of each sequence and kv head that a query at pos[b] is to attend.
+ * With the query of a q head as codes c = rint(q / s_q), s_q = max|q| / 127
+ * (rotated first when BAKED), a block's score is
+ *     max over the kv head's q heads of  u * (s_q * step),
+ *     u = sum over channels of max(c * largest code, c * smallest code),
+ * u a whole number, the products fp32.  Candidates are the blocks 0 .. pos[b] /
+ * block_size that are mapped and resident.  The first `first` and the last
+ * `recent` of these numbers (mapped or not) are always in, the others by score,
+ * equal scores by the lowest number.
+ *   q        [batch, q_heads, head_dim], pre-RoPE, 16-byte aligned, finite.
+ *   k        1 .. 2^24; first >= 0, recent >= 1, first + recent <= k (else
+ *            KVC_ERR_ARG).  At most 128 q heads for each kv head.
+ *   blocks   [batch, kv_heads, k] int32, out: logical blocks, ascending, -1
+ *            behind the last.
+ *   workspace  kvc_select_workspace_bytes(d, k) bytes (0 if refused), set up by
+ *            kvc_workspace_init; it serves the other decode calls too. */
+KVC_API size_t kvc_select_workspace_bytes(const kvc_desc* d, int32_t k);
+KVC_API int kvc_select_blocks(const kvc_desc* d, const void* bounds, int32_t layer, const void* q, const int32_t* pos,
+                              int32_t k, int32_t first, int32_t recent, const int32_t* block_table,
+                              const uint32_t* valid_bits, int32_t* blocks, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* kvc_decode_attention over listed blocks of a PAGED bf16 or INT8 cache: the
+ * query of q head h attends the positions <= pos[b] of the blocks that
+ * blocks[b][h / (q_heads / kv_heads)] lists.
+ *   blocks   [batch, kv_heads, k] int32, ascending; negative entries are none.
+ *            An entry past the table, or not above those before it (a block
+ *            listed twice), sets KVC_DEV_BAD_ENTRY and is left out.  Blocks that
+ *            are unmapped, not resident or past the position are not attended.
+ *   workspace  kvc_select_workspace_bytes(d, k) bytes.
+ * An empty list gives zeros. */
+KVC_API int kvc_decode_attention_selected(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                          const int32_t* pos, const int32_t* blocks, int32_t k,
+                                          const int32_t* block_table, const uint32_t* valid_bits, void* out,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* kvc_decode_attention of a PAGED bf16 or INT8 cache that also adds up how much
+ * weight each block receives: for every entry of weights [batch,
+ * max_blocks_per_seq] fp32,
+ *     weights = decay * weights + sum over q heads and over the block's attended
+ *               positions of the softmax weight (0 for a block that is not
+ *               attended),
+ * in an order of sums that depends on nothing but the shapes.  decay 0 .. 1 (else
+ * KVC_ERR_ARG); with 0 the old values are not read.  One array can take several
+ * layers' calls, the decay given to the step's first.
+ *   workspace  kvc_weighed_workspace_bytes(d) bytes (0 if `d` is refused): the
+ *              decode workspace, which it serves as too, and a score for every q
+ *              head and position. */
+KVC_API size_t kvc_weighed_workspace_bytes(const kvc_desc* d);
+KVC_API int kvc_decode_attention_weighed(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                         const int32_t* pos, const int32_t* block_table, const uint32_t* valid_bits,
+                                         float decay, float* weights, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* The accepted path of a tree of drafted tokens, appended: token path[b][j] of
+ * the draft goes to position pos0[b] + j, for j < n_path[b], as kvc_append of
+ * those tokens would put it (any layout, element type and rope).
+ *   k_new, v_new  [batch, T, kv_heads, head_dim], pre-RoPE, 16-byte aligned.
+ *   path          [batch, P] int32, entries 0 .. T - 1; another among the first
+ *                 n_path[b] sets KVC_DEV_BAD_ENTRY and its position is not
+ *                 written.
+ *   n_path        [batch] int32 (NULL: P for all); above P counts as P
+ *                 (KVC_DEV_BAD_ENTRY), below 0 as 0.
+ * Sequences with pos0[b] < 0 append nothing.  Other device errors as in
+ * kvc_append.  Workspace: kvc_workspace_bytes(d). */
+KVC_API int kvc_append_path(const kvc_desc* d, void* cache, int32_t layer, const void* k_new, const void* v_new,
+                            int32_t T, const int32_t* pos0, const int32_t* path, int32_t P, const int32_t* n_path,
+                            const int32_t* block_table, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One decode step: kvc_append of the token at pos[b] (n_new = 1), then
  * kvc_decode_attention at pos[b], with the same arguments and results as
  * that pair of calls.  For bf16 and INT8 caches, RING / SINK_RING and PAGED
@@ -479,6 +575,22 @@ KVC_API int kvc_block_share(const kvc_desc* d, int32_t* block_table, int32_t* re
 KVC_API int kvc_block_release(const kvc_desc* d, int32_t* block_table, uint32_t* valid_bits, int32_t* refcount,
                               int32_t* free_list, int32_t* free_count, int32_t n, const int32_t* seq,
                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Blocks given back by weight: of each sequence's mapped blocks 0 .. pos[b] /
+ * block_size, those beyond `keep` go, the lightest (weights, as
+ * kvc_decode_attention_weighed adds them up) first, equal ones by the lowest
+ * number; the first `first` and the last `recent` of these numbers stay.  A block
+ * that goes is unmapped, its count drops by one and its weight becomes 0; blocks
+ * whose count reaches zero return to the free list in ascending block id and
+ * lose their valid bit (valid_bits may be NULL).  Later positions attend what is
+ * left.  A weight that is NaN counts as the heaviest.  Sequences with pos[b] < 0
+ * stay as they are.
+ *   weights  [batch, max_blocks_per_seq] fp32.
+ *   keep     >= first + recent, first >= 0, recent >= 1 (else KVC_ERR_ARG). */
+KVC_API int kvc_block_evict(const kvc_desc* d, float* weights, const int32_t* pos, int32_t keep, int32_t first,
+                            int32_t recent, int32_t* block_table, uint32_t* valid_bits, int32_t* refcount,
+                            int32_t* free_list, int32_t* free_count, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* Paging of a fixed pool of block slots between host memory and the device
  * ([pool] "KV cache paging": a fixed pool of resident slots; blocks move on

@@ -41,6 +41,9 @@ ABI_FUNCTIONS = (
     "kvc_pagein_commit", "kvc_prefill_workspace_bytes", "kvc_prefill",
     "kvc_rotary_init", "kvc_append_qk", "kvc_decode_attention_scored", "kvc_prefill_scored",
     "kvc_shared_workspace_bytes", "kvc_decode_attention_shared",
+    "kvc_bounds_bytes", "kvc_block_bounds", "kvc_select_workspace_bytes", "kvc_select_blocks",
+    "kvc_decode_attention_selected", "kvc_weighed_workspace_bytes", "kvc_decode_attention_weighed",
+    "kvc_block_evict", "kvc_append_path",
 )
 
 
@@ -131,11 +134,24 @@ def lib() -> ctypes.CDLL:
         L.kvc_decode_attention_scored.argtypes = [dp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_prefill_scored.argtypes = [dp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_append_qk.argtypes = [dp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.kvc_bounds_bytes.argtypes = [dp]
+        L.kvc_bounds_bytes.restype = sz
+        L.kvc_block_bounds.argtypes = [dp, vp, i32, vp, vp, i32, vp, vp, vp, sz, vp]
+        L.kvc_select_workspace_bytes.argtypes = [dp, i32]
+        L.kvc_select_workspace_bytes.restype = sz
+        L.kvc_select_blocks.argtypes = [dp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.kvc_decode_attention_selected.argtypes = [dp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+        L.kvc_weighed_workspace_bytes.argtypes = [dp]
+        L.kvc_weighed_workspace_bytes.restype = sz
+        L.kvc_decode_attention_weighed.argtypes = [dp, vp, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.kvc_block_evict.argtypes = [dp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.kvc_append_path.argtypes = [dp, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp, sz, vp]
         L.kvc_strerror.argtypes = [ctypes.c_int]
         L.kvc_strerror.restype = ctypes.c_char_p
         for name in ABI_FUNCTIONS:
             if name not in ("kvc_cache_bytes", "kvc_workspace_bytes", "kvc_prefill_workspace_bytes", "kvc_strerror",
-                            "kvc_shared_workspace_bytes",
+                            "kvc_shared_workspace_bytes", "kvc_bounds_bytes", "kvc_select_workspace_bytes",
+                            "kvc_weighed_workspace_bytes",
                             "kvc_pager_create", "kvc_pager_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -232,7 +248,7 @@ def _need_cache(d: KvcDesc, cache: torch.Tensor):
 class _Sizes:
     """What the binding checks of a descriptor's tensors, worked out once for each descriptor's bytes: a step's
     call takes a few microseconds on the GPU, and reading a dozen descriptor fields costs as much."""
-    __slots__ = ("act", "cache", "cache_bytes", "B", "H", "KV", "D", "q", "kv", "table", "valid", "shape")
+    __slots__ = ("act", "cache", "cache_bytes", "B", "H", "KV", "D", "q", "kv", "table", "valid", "shape", "bounds")
 
     def __init__(self, d: KvcDesc):
         self.act, self.cache, self.cache_bytes = desc_dtype(d), cache_dtype(d), cache_bytes(d)
@@ -240,6 +256,7 @@ class _Sizes:
         self.q, self.kv = self.B * self.H * self.D, self.B * self.KV * self.D
         self.table, self.valid = self.B * d.max_blocks_per_seq, (d.num_blocks + 31) // 32
         self.shape = (self.B, self.H, self.D)
+        self.bounds = bounds_bytes(d)
 
 
 _sizes: dict = {}
@@ -555,6 +572,163 @@ def decode_attention_shared(d: KvcDesc, cache: torch.Tensor, layer: int, q: torc
     return out
 
 
+def bounds_bytes(d: KvcDesc) -> int:
+    return int(lib().kvc_bounds_bytes(ctypes.byref(d)))
+
+
+def alloc_bounds(d: KvcDesc, device="cuda") -> torch.Tensor:
+    """Zero-filled bounds of a paged cache's blocks (kvc_block_bounds; `bounds_views` gives codes and steps)."""
+    n = bounds_bytes(d)
+    if n == 0:
+        raise KvcError(KVC_ERR_DESC, "kvc_bounds_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def bounds_views(d: KvcDesc, bounds: torch.Tensor):
+    """(codes int8 [layers, num_blocks, kv_heads, 2, D], largest and smallest; steps fp32 [layers, num_blocks,
+    kv_heads]) views of a bounds buffer."""
+    rows = d.layers * d.num_blocks * d.kv_heads
+    n = rows * 2 * d.head_dim
+    return (bounds[:n].view(torch.int8).view(d.layers, d.num_blocks, d.kv_heads, 2, d.head_dim),
+            bounds[n:n + 4 * rows].view(torch.float32).view(d.layers, d.num_blocks, d.kv_heads))
+
+
+def _take_bounds(z: _Sizes, bounds: torch.Tensor, dev: int) -> int:
+    if isinstance(bounds, torch.Tensor) and bounds.numel() < z.bounds:
+        raise ValueError(f"bounds holds {bounds.numel()} bytes, the descriptor needs {z.bounds}")
+    return _take(bounds, "bounds", _UINT8, None, dev)
+
+
+def block_bounds(d: KvcDesc, cache: torch.Tensor, layer: int, bounds: torch.Tensor, pos: torch.Tensor, n_new: int,
+                 workspace: torch.Tensor, block_table: torch.Tensor, n_tok: torch.Tensor | None = None, stream=None):
+    """kvc_block_bounds: the ends of the keys of every block that holds one of positions pos[b] .. pos[b] + n - 1
+    (n = n_tok[b], or n_new)."""
+    z, dev = _sizes_of(d), _device_of(cache)
+    rc = lib().kvc_block_bounds(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, _take_bounds(z, bounds, dev),
+        _take(pos, "pos", _INT32, z.B, dev), int(n_new),
+        None if n_tok is None else _take(n_tok, "n_tok", _INT32, z.B, dev),
+        _take(block_table, "block_table", _INT32, z.table, dev), _take(workspace, "workspace", _UINT8, None, dev),
+        workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_block_bounds")
+
+
+def select_workspace_bytes(d: KvcDesc, k: int) -> int:
+    return int(lib().kvc_select_workspace_bytes(ctypes.byref(d), int(k)))
+
+
+def alloc_select_workspace(d: KvcDesc, k: int, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for kvc_select_blocks and kvc_decode_attention_selected with up to k blocks (also a
+    decode workspace)."""
+    n = select_workspace_bytes(d, k)
+    if n == 0:
+        raise KvcError(KVC_ERR_DESC, "kvc_select_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def select_blocks(d: KvcDesc, bounds: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor, k: int,
+                  workspace: torch.Tensor, block_table: torch.Tensor, first: int = 1, recent: int = 1,
+                  valid_bits: torch.Tensor | None = None, blocks: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """kvc_select_blocks: q [batch, q_heads, D] -> logical blocks int32 [batch, kv_heads, k], ascending, -1 behind."""
+    z, dev = _sizes_of(d), _device_of(q)
+    qp = _take(q, "q", z.act, z.q, dev)
+    if blocks is None:
+        blocks = torch.empty((z.B, z.KV, max(int(k), 0)), dtype=_INT32, device=q.device)
+    rc = lib().kvc_select_blocks(
+        ctypes.byref(d), _take_bounds(z, bounds, dev), layer, qp, _take(pos, "pos", _INT32, z.B, dev), int(k),
+        int(first), int(recent), _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
+        _take(blocks, "blocks", _INT32, z.B * z.KV * max(int(k), 0), dev),
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_select_blocks")
+    return blocks
+
+
+def decode_attention_selected(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
+                              blocks: torch.Tensor, workspace: torch.Tensor, block_table: torch.Tensor,
+                              valid_bits: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """kvc_decode_attention_selected: decode_attention over the logical blocks int32 [batch, kv_heads, k] of each
+    kv head."""
+    z, dev = _sizes_of(d), _device_of(q)
+    qp = _take(q, "q", z.act, z.q, dev)
+    bp = _take(blocks, "blocks", _INT32, None, dev)
+    k = blocks.numel() // (z.B * z.KV)
+    if blocks.numel() != z.B * z.KV * k:
+        raise ValueError("blocks must be [batch, kv_heads, k]")
+    if out is None:
+        out = torch.empty(z.shape, dtype=z.act, device=q.device)
+    rc = lib().kvc_decode_attention_selected(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", _INT32, z.B, dev), bp, k,
+        _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
+        _take(out, "out", z.act, z.q, dev), _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_decode_attention_selected")
+    return out
+
+
+def weighed_workspace_bytes(d: KvcDesc) -> int:
+    return int(lib().kvc_weighed_workspace_bytes(ctypes.byref(d)))
+
+
+def alloc_weighed_workspace(d: KvcDesc, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for kvc_decode_attention_weighed (also a decode workspace)."""
+    n = weighed_workspace_bytes(d)
+    if n == 0:
+        raise KvcError(KVC_ERR_DESC, "kvc_weighed_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_attention_weighed(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, pos: torch.Tensor,
+                             weights: torch.Tensor, workspace: torch.Tensor, block_table: torch.Tensor,
+                             valid_bits: torch.Tensor | None = None, decay: float = 1.0,
+                             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvc_decode_attention_weighed: decode_attention that also adds each block's softmax weight, over all q
+    heads, to decay * weights (fp32 [batch, max_blocks_per_seq], updated in place)."""
+    z, dev = _sizes_of(d), _device_of(q)
+    qp = _take(q, "q", z.act, z.q, dev)
+    if out is None:
+        out = torch.empty(z.shape, dtype=z.act, device=q.device)
+    rc = lib().kvc_decode_attention_weighed(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(pos, "pos", _INT32, z.B, dev),
+        _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev), float(decay),
+        _take(weights, "weights", torch.float32, z.table, dev), _take(out, "out", z.act, z.q, dev),
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_decode_attention_weighed")
+    return out
+
+
+def append_path(d: KvcDesc, cache: torch.Tensor, layer: int, k_new: torch.Tensor, v_new: torch.Tensor,
+                pos0: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor | None, workspace: torch.Tensor,
+                block_table: torch.Tensor | None = None, stream=None):
+    """kvc_append_path: tokens path[b][j] of the draft k_new / v_new [batch, T, kv_heads, D] to positions
+    pos0[b] + j, j < n_path[b] (int32 [batch]; None: the whole path, int32 [batch, P])."""
+    z, dev = _sizes_of(d), _device_of(k_new)
+    kp = _take(k_new, "k_new", z.act, None, dev)
+    T = k_new.numel() // z.kv
+    if k_new.numel() != T * z.kv:
+        raise ValueError("k_new must be [batch, T, kv_heads, head_dim]")
+    pp = _take(path, "path", _INT32, None, dev)
+    P = path.numel() // z.B
+    if path.numel() != P * z.B:
+        raise ValueError("path must be [batch, P]")
+    rc = lib().kvc_append_path(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, kp, _take(v_new, "v_new", z.act, T * z.kv, dev), T,
+        _take(pos0, "pos0", _INT32, z.B, dev), pp, P,
+        None if n_path is None else _take(n_path, "n_path", _INT32, z.B, dev),
+        None if block_table is None else _take(block_table, "block_table", _INT32, z.table, dev),
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_append_path")
+
+
 def decode_step(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor,
                 v_new: torch.Tensor, pos: torch.Tensor, workspace: torch.Tensor,
                 block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
@@ -718,6 +892,23 @@ def block_release(d: KvcDesc, state: BlockState, seq: torch.Tensor, workspace: t
                                    _ptr(state.refcount), _ptr(state.free_list), _ptr(state.free_count), int(n),
                                    _ptr(seq), _ptr(workspace), workspace.numel(), _stream(stream)),
            "kvc_block_release")
+
+
+def block_evict(d: KvcDesc, state: BlockState, weights: torch.Tensor, pos: torch.Tensor, keep: int,
+                workspace: torch.Tensor, first: int = 1, recent: int = 1, stream=None):
+    """kvc_block_evict: each sequence's mapped blocks up to pos beyond `keep`, the lightest by weights (fp32
+    [batch, max_blocks_per_seq]), are given back."""
+    z, dev = _sizes_of(d), _device_of(weights)
+    rc = lib().kvc_block_evict(
+        ctypes.byref(d), _take(weights, "weights", torch.float32, z.table, dev), _take(pos, "pos", _INT32, z.B, dev),
+        int(keep), int(first), int(recent), _take(state.table, "state.table", _INT32, z.table, dev),
+        _take(state.valid_bits, "state.valid_bits", _INT32, z.valid, dev),
+        _take(state.refcount, "state.refcount", _INT32, d.num_blocks, dev),
+        _take(state.free_list, "state.free_list", _INT32, d.num_blocks, dev),
+        _take(state.free_count, "state.free_count", _INT32, 1, dev),
+        _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_block_evict")
 
 
 class Pager:

@@ -51,3 +51,26 @@
     template cudaError_t kvc::launch_decode_mma_t<D, GH, PG, false, Q8, true>(const kvc::DecodeParams&,      \
                                                                               const kvc::KvTensorMaps&, dim3, \
                                                                               cudaStream_t);
+
+// additions to a paged decode (kvc_decode_attention_selected, kvc_decode_attention_weighed)
+#define KVC_INST_EXT_MMA(D, GH, Q8, EXT)                                                                        \
+    template cudaError_t kvc::launch_decode_mma_t<D, GH, true, false, Q8, false, EXT>(const kvc::DecodeParams&,    \
+                                                                                      const kvc::KvTensorMaps&,    \
+                                                                                      dim3, cudaStream_t);
+#define KVC_INST_EXT_BF16(EXT)             \
+    KVC_INST_EXT_MMA(64, 1, false, EXT)    \
+    KVC_INST_EXT_MMA(64, 2, false, EXT)    \
+    KVC_INST_EXT_MMA(64, 4, false, EXT)    \
+    KVC_INST_EXT_MMA(128, 1, false, EXT)   \
+    KVC_INST_EXT_MMA(128, 2, false, EXT)   \
+    KVC_INST_EXT_MMA(128, 4, false, EXT)   \
+    KVC_INST_EXT_MMA(256, 1, false, EXT)   \
+    KVC_INST_EXT_MMA(256, 2, false, EXT)   \
+    KVC_INST_EXT_MMA(256, 4, false, EXT)
+#define KVC_INST_EXT_I8(EXT)              \
+    KVC_INST_EXT_MMA(128, 1, true, EXT)   \
+    KVC_INST_EXT_MMA(128, 2, true, EXT)   \
+    KVC_INST_EXT_MMA(128, 4, true, EXT)   \
+    KVC_INST_EXT_MMA(256, 1, true, EXT)   \
+    KVC_INST_EXT_MMA(256, 2, true, EXT)   \
+    KVC_INST_EXT_MMA(256, 4, true, EXT)

@@ -6,13 +6,15 @@
 #include <cuda_bf16.h>
 
 #include "kvc_host.h"
+#include "kvc_select.h"
 #include "kvc_shared.h"
+#include "kvc_tree.h"
 
 namespace kvc {
 
 template <typename Elt, int D, int GH, bool PAGED, bool READ, bool SCORE = false>
 cudaError_t launch_decode_t(const DecodeParams& p, dim3 grid, cudaStream_t stream);
-template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false>
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false, int EXT = kExtNone>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream);
 
 cudaError_t launch_decode(int dtype, int D, int gh, bool paged, bool rd, bool scored, const DecodeParams& p, dim3 grid,
@@ -56,6 +58,21 @@ cudaError_t launch_decode_mma(int D, int gh, bool paged, bool rd, bool q8, bool 
     KVC_CASES_Q8(true, false)
 #undef KVC_CASES_Q8
 #undef KVC_CASES
+#undef KVC_CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_ext(int D, int gh, bool q8, int ext, const DecodeParams& p, const KvTensorMaps& maps, dim3 grid,
+                              cudaStream_t s) {
+#define KVC_CASE(DD, GG, Q)                                                                                 \
+    if (D == DD && gh == GG && q8 == Q)                                                                     \
+        return ext == kExtSelect ? launch_decode_mma_t<DD, GG, true, false, Q, false, kExtSelect>(p, maps, grid, s) \
+                                 : launch_decode_mma_t<DD, GG, true, false, Q, false, kExtWeigh>(p, maps, grid, s);
+    KVC_CASE(64, 1, false) KVC_CASE(64, 2, false) KVC_CASE(64, 4, false)
+    KVC_CASE(128, 1, false) KVC_CASE(128, 2, false) KVC_CASE(128, 4, false)
+    KVC_CASE(256, 1, false) KVC_CASE(256, 2, false) KVC_CASE(256, 4, false)
+    KVC_CASE(128, 1, true) KVC_CASE(128, 2, true) KVC_CASE(128, 4, true)
+    KVC_CASE(256, 1, true) KVC_CASE(256, 2, true) KVC_CASE(256, 4, true)
 #undef KVC_CASE
     return cudaErrorInvalidValue;
 }
@@ -319,10 +336,49 @@ static SharedLayout shared_layout(const kvc_desc* d, const Geo& g) {
     return l;
 }
 
+// kvc_select_blocks and kvc_decode_attention_selected: what they add to the decode workspace, after it.
+struct SelectLayout {
+    size_t keys, list, rows, total;
+};
+static SelectLayout select_layout(const kvc_desc* d, const Geo& g, int k) {
+    SelectLayout l{};
+    const size_t units = (size_t)d->batch * d->kv_heads;
+    l.keys = align_up(ws_layout(d, g).total, 256);
+    l.list = align_up(l.keys + units * d->max_blocks_per_seq * 4, 256);
+    l.rows = align_up(l.list + units * k * 4, 256);
+    l.total = align_up(l.rows + units * 4, 256);
+    return l;
+}
+
+// kvc_decode_attention_weighed: every row's score of every q head, and the softmax statistics.
+struct WeighLayout {
+    size_t ml, scores, total;
+    long long stride;           // scores of a (sequence, q head)
+};
+static WeighLayout weigh_layout(const kvc_desc* d, const Geo& g) {
+    WeighLayout l{};
+    const size_t rows = (size_t)d->batch * d->q_heads;
+    l.stride = (long long)align_up((size_t)d->max_blocks_per_seq * d->block_size, 4);
+    l.ml = align_up(ws_layout(d, g).total, 256);
+    l.scores = align_up(l.ml + rows * 8, 256);
+    l.total = align_up(l.scores + rows * (size_t)l.stride * 4, 256);
+    return l;
+}
+
+// What kvc_decode_attention_selected and kvc_decode_attention_weighed add to a paged decode.
+struct DecodeMore {
+    int ext;                    // DecodeExt
+    const int32_t* blocks;      // kExtSelect: [B][Hkv][k]
+    int k;
+    float* weights;             // kExtWeigh: [B][maxb]
+    float decay;
+};
+
 static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, const void* q, const void* k_new,
                        const void* v_new, const int32_t* pos, const int32_t* block_table,
                        const uint32_t* valid_bits, void* out, void* workspace, size_t workspace_bytes,
-                       void* stream, const kvc_score* score = nullptr, const int32_t* group = nullptr) {
+                       void* stream, const kvc_score* score = nullptr, const int32_t* group = nullptr,
+                       const DecodeMore* more = nullptr) {
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
@@ -333,7 +389,12 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     if (!aligned16(workspace)) return KVC_ERR_ALIGN;
     const bool paged = d->layout == KVC_LAYOUT_PAGED;
     const WorkspaceLayout w = ws_layout(d, g);
-    if (workspace_bytes < (group ? shared_layout(d, g).total : w.total)) return KVC_ERR_WORKSPACE;
+    const bool selected = more && more->ext == kExtSelect, weighed = more && more->ext == kExtWeigh;
+    if (workspace_bytes < (group      ? shared_layout(d, g).total
+                           : selected ? select_layout(d, g, more->k).total
+                           : weighed  ? weigh_layout(d, g).total
+                                      : w.total))
+        return KVC_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
 
@@ -381,7 +442,8 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     // outputs' size instead of 0.0020 (groups of 8, 2049 .. 8192 keys)
     const bool scored = score || group;
     if (group) sp.scale2 = scale * 1.4426950408889634f;
-    p.q_scale = scored ? 1.f : scale * 1.4426950408889634f;
+    if (more) sp.scale2 = scale * 1.4426950408889634f;
+    p.q_scale = scored || more ? 1.f : scale * 1.4426950408889634f;
     p.score = sp;
     if (d->rope != KVC_ROPE_NONE) fill_theta(d->head_dim, d->rope_base, p.theta, p.theta_f);
 
@@ -441,7 +503,7 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
     // shares from the block table and write the step's token themselves
     // (the CTAs bulk-copy the table and the valid words: 16-byte aligned buffers)
     // (a start is left to the planning kernel, which drops the blocks below it)
-    p.self_plan = (paged && !start && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
+    p.self_plan = (paged && !start && !selected && d->dtype != KVC_F32 && d->batch == 1 && d->max_blocks_per_seq <= kSelfPlanMax &&
                    (d->num_blocks + 31) / 32 <= kSelfPlanValidWords && aligned16(block_table) &&
                    (!valid_bits || aligned16(valid_bits))) ? 1 : 0;
     if (p.self_plan) {
@@ -451,6 +513,26 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         p.items = reinterpret_cast<int4*>(ws + w.plan_items);
         p.item_info = reinterpret_cast<int4*>(ws + w.plan_info);
         p.cta_items = reinterpret_cast<int2*>(ws + w.plan_cta);
+    } else if (selected) {
+        const SelectLayout l = select_layout(d, g, more->k);
+        SelectPlanParams sl{};
+        sl.blocks = more->blocks;
+        sl.pos = pos;
+        sl.table = block_table;
+        sl.valid = valid_bits;
+        sl.err = p.err;
+        sl.list = reinterpret_cast<int32_t*>(ws + l.list);
+        sl.rows = reinterpret_cast<int32_t*>(ws + l.rows);
+        sl.B = d->batch;
+        sl.Hkv = d->kv_heads;
+        sl.bs = d->block_size;
+        sl.num_blocks = d->num_blocks;
+        sl.maxb = d->max_blocks_per_seq;
+        sl.k = more->k;
+        if (launch_select_plan(sl, s) != cudaSuccess) return KVC_ERR_CUDA;
+        p.seq_rows = sl.rows;
+        p.list = sl.list;
+        p.list_k = more->k;
     } else if (paged) {
         PlanParams pp{};
         pp.pos = pos;
@@ -509,6 +591,32 @@ static int decode_impl(const kvc_desc* d, const void* cache, int32_t layer, cons
         p.cta_items = pp.cta_items;
     }
     const bool rd = d->rope == KVC_ROPE_READ_INCACHE;
+    if (more) {
+        WeighParams wp{};
+        if (weighed) {
+            const WeighLayout l = weigh_layout(d, g);
+            p.scores = reinterpret_cast<float*>(ws + l.scores);
+            p.scores_stride = l.stride;
+            p.ml_out = reinterpret_cast<float2*>(ws + l.ml);
+            wp.scores = p.scores;
+            wp.ml = p.ml_out;
+            wp.pos = pos;
+            wp.table = block_table;
+            wp.valid = valid_bits;
+            wp.weights = more->weights;
+            wp.stride = l.stride;
+            wp.decay = more->decay;
+            wp.B = d->batch;
+            wp.Hq = d->q_heads;
+            wp.bs = d->block_size;
+            wp.num_blocks = d->num_blocks;
+            wp.maxb = d->max_blocks_per_seq;
+        }
+        if (launch_decode_ext(d->head_dim, g.GH, d->dtype == KVC_I8, more->ext, p, maps, grid, s) != cudaSuccess ||
+            (weighed && launch_weigh(wp, s) != cudaSuccess))
+            return KVC_ERR_CUDA;
+        return KVC_OK;
+    }
     if (d->dtype != KVC_F32) {
         if (launch_decode_mma(d->head_dim, g.GH, paged, rd, d->dtype == KVC_I8, scored, p, maps, grid, s) !=
             cudaSuccess)
@@ -986,6 +1094,241 @@ KVC_API int kvc_block_release(const kvc_desc* d, int32_t* block_table, uint32_t*
     p.free_count = free_count;
     p.src_seq = seq;
     return launch_block_release(p, n, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+// The bounds of a paged cache's blocks: codes, then steps (kvc_block_bounds).
+static size_t bounds_code_bytes(const kvc_desc* d) {
+    return (size_t)d->layers * d->num_blocks * d->kv_heads * 2 * d->head_dim;
+}
+
+KVC_API size_t kvc_bounds_bytes(const kvc_desc* d) {
+    Geo g;
+    if (check_desc(d, &g) != KVC_OK || d->layout != KVC_LAYOUT_PAGED) return 0;
+    return bounds_code_bytes(d) + (size_t)d->layers * d->num_blocks * d->kv_heads * 4;
+}
+
+KVC_API int kvc_block_bounds(const kvc_desc* d, const void* cache, int32_t layer, void* bounds, const int32_t* pos,
+                             int32_t n_new, const int32_t* n_tok, const int32_t* block_table, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if (!cache || !bounds || !pos || !block_table || !workspace) return KVC_ERR_NULL;
+    if (!aligned16(cache) || !aligned16(bounds) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(n_tok) & 3u))
+        return KVC_ERR_ALIGN;
+    if (layer < 0 || layer >= d->layers || n_new < 1) return KVC_ERR_ARG;
+    const WorkspaceLayout w = ws_layout(d, g);
+    if (workspace_bytes < w.total) return KVC_ERR_WORKSPACE;
+    const long long per = (long long)d->num_blocks * d->kv_heads;
+    BoundsParams p{};
+    p.cache = cache;
+    p.layer_off = (long long)layer * 2 * g.half_elems;
+    if (d->dtype == KVC_I8) {
+        p.scales = reinterpret_cast<const float*>(static_cast<const char*>(cache) +
+                                                  (size_t)d->layers * 2 * (size_t)g.half_elems);
+        p.sc_layer_off = (long long)layer * 2 * (g.half_elems / d->head_dim);
+    }
+    p.codes = static_cast<int8_t*>(bounds) + layer * per * 2 * d->head_dim;
+    p.steps = reinterpret_cast<float*>(static_cast<char*>(bounds) + bounds_code_bytes(d)) + layer * per;
+    p.pos = pos;
+    p.n_tok = n_tok;
+    p.table = block_table;
+    p.err = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + w.err);
+    p.B = d->batch;
+    p.Hkv = d->kv_heads;
+    p.bs = d->block_size;
+    p.num_blocks = d->num_blocks;
+    p.maxb = d->max_blocks_per_seq;
+    p.n_new = n_new;
+    // blocks that n_new tokens can touch; one more, past the table's end, for its error
+    const long long slots = ((long long)n_new + d->block_size - 2) / d->block_size + 1;
+    p.slots = (int)(slots <= d->max_blocks_per_seq ? slots : (long long)d->max_blocks_per_seq + 1);
+    if ((long long)p.slots * d->kv_heads > 0x7fffffffLL) return KVC_ERR_UNSUPPORTED;
+    return launch_block_bounds(d->dtype, d->head_dim, p, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+// What kvc_select_blocks and kvc_decode_attention_selected take of a descriptor and k.
+static int select_desc(const kvc_desc* d, const Geo& g, int32_t k) {
+    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if (g.G > 128) return KVC_ERR_UNSUPPORTED;
+    if (k < 1 || k > (1 << 24)) return KVC_ERR_ARG;
+    return KVC_OK;
+}
+
+KVC_API size_t kvc_select_workspace_bytes(const kvc_desc* d, int32_t k) {
+    Geo g;
+    if (check_desc(d, &g) != KVC_OK || select_desc(d, g, k) != KVC_OK) return 0;
+    return select_layout(d, g, k).total;
+}
+
+KVC_API int kvc_select_blocks(const kvc_desc* d, const void* bounds, int32_t layer, const void* q, const int32_t* pos,
+                              int32_t k, int32_t first, int32_t recent, const int32_t* block_table,
+                              const uint32_t* valid_bits, int32_t* blocks, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if ((rc = select_desc(d, g, k))) return rc;
+    if (!bounds || !q || !pos || !block_table || !blocks || !workspace) return KVC_ERR_NULL;
+    if (!aligned16(bounds) || !aligned16(q) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(blocks) & 3u))
+        return KVC_ERR_ALIGN;
+    if (layer < 0 || layer >= d->layers || first < 0 || recent < 1 || (long long)first + recent > k) return KVC_ERR_ARG;
+    const SelectLayout l = select_layout(d, g, k);
+    if (workspace_bytes < l.total) return KVC_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    const long long per = (long long)d->num_blocks * d->kv_heads;
+    SelectParams p{};
+    p.codes = static_cast<const int8_t*>(bounds) + layer * per * 2 * d->head_dim;
+    p.steps = reinterpret_cast<const float*>(static_cast<const char*>(bounds) + bounds_code_bytes(d)) + layer * per;
+    p.q = q;
+    p.pos = pos;
+    p.table = block_table;
+    p.valid = valid_bits;
+    p.err = reinterpret_cast<uint32_t*>(ws + ws_layout(d, g).err);
+    p.keys = reinterpret_cast<uint32_t*>(ws + l.keys);
+    p.blocks = blocks;
+    p.B = d->batch;
+    p.Hq = d->q_heads;
+    p.Hkv = d->kv_heads;
+    p.G = g.G;
+    p.bs = d->block_size;
+    p.num_blocks = d->num_blocks;
+    p.maxb = d->max_blocks_per_seq;
+    p.k = k;
+    p.first = first;
+    p.recent = recent;
+    p.rope = d->rope;
+    if (d->rope == KVC_ROPE_BAKED) fill_theta(d->head_dim, d->rope_base, p.theta, nullptr);
+    return launch_select(d->dtype, d->head_dim, p, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+KVC_API int kvc_decode_attention_selected(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                          const int32_t* pos, const int32_t* blocks, int32_t k,
+                                          const int32_t* block_table, const uint32_t* valid_bits, void* out,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if ((rc = select_desc(d, g, k))) return rc;
+    if (d->dtype == KVC_F32) return KVC_ERR_UNSUPPORTED;
+    if (!blocks) return KVC_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(blocks) & 3u) return KVC_ERR_ALIGN;
+    // (rows of a list, as of a sequence, are counted in 32 bits)
+    if ((long long)k * d->block_size > 0x7fffffffLL) return KVC_ERR_ARG;
+    DecodeMore more{};
+    more.ext = kExtSelect;
+    more.blocks = blocks;
+    more.k = k;
+    return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
+                       workspace_bytes, stream, nullptr, nullptr, &more);
+}
+
+KVC_API size_t kvc_weighed_workspace_bytes(const kvc_desc* d) {
+    Geo g;
+    if (check_desc(d, &g) != KVC_OK || d->layout != KVC_LAYOUT_PAGED || d->dtype == KVC_F32) return 0;
+    return weigh_layout(d, g).total;
+}
+
+KVC_API int kvc_decode_attention_weighed(const kvc_desc* d, const void* cache, int32_t layer, const void* q,
+                                         const int32_t* pos, const int32_t* block_table, const uint32_t* valid_bits,
+                                         float decay, float* weights, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if (d->dtype == KVC_F32) return KVC_ERR_UNSUPPORTED;
+    if (!weights) return KVC_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(weights) & 3u) return KVC_ERR_ALIGN;
+    if (!(decay >= 0.f && decay <= 1.f)) return KVC_ERR_ARG;
+    DecodeMore more{};
+    more.ext = kExtWeigh;
+    more.weights = weights;
+    more.decay = decay;
+    return decode_impl(d, cache, layer, q, nullptr, nullptr, pos, block_table, valid_bits, out, workspace,
+                       workspace_bytes, stream, nullptr, nullptr, &more);
+}
+
+KVC_API int kvc_block_evict(const kvc_desc* d, float* weights, const int32_t* pos, int32_t keep, int32_t first,
+                            int32_t recent, int32_t* block_table, uint32_t* valid_bits, int32_t* refcount,
+                            int32_t* free_list, int32_t* free_count, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if (!weights || !pos || !block_table || !refcount || !free_list || !free_count) return KVC_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(weights) & 3u) return KVC_ERR_ALIGN;
+    if (first < 0 || recent < 1 || (long long)first + recent > keep) return KVC_ERR_ARG;
+    kvc::BlockParams b;
+    if ((rc = block_params(d, g, workspace, workspace_bytes, &b))) return rc;
+    EvictParams p{};
+    p.weights = weights;
+    p.pos = pos;
+    p.table = block_table;
+    p.valid = valid_bits;
+    p.refcount = refcount;
+    p.free_list = free_list;
+    p.free_count = free_count;
+    p.err = b.err;
+    p.ticket = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + ws_layout(d, g).counters) +
+               (size_t)d->batch * d->kv_heads * g.nsub;
+    p.back = reinterpret_cast<uint32_t*>(b.flags);
+    p.B = d->batch;
+    p.bs = d->block_size;
+    p.num_blocks = d->num_blocks;
+    p.maxb = d->max_blocks_per_seq;
+    p.keep = keep;
+    p.first = first;
+    p.recent = recent;
+    return launch_block_evict(p, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+KVC_API int kvc_append_path(const kvc_desc* d, void* cache, int32_t layer, const void* k_new, const void* v_new,
+                            int32_t T, const int32_t* pos0, const int32_t* path, int32_t P, const int32_t* n_path,
+                            const int32_t* block_table, void* workspace, size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if (!cache || !k_new || !v_new || !pos0 || !path || !workspace) return KVC_ERR_NULL;
+    if (d->layout == KVC_LAYOUT_PAGED && !block_table) return KVC_ERR_NULL;
+    if (!aligned16(cache) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(workspace) ||
+        ((reinterpret_cast<uintptr_t>(path) | reinterpret_cast<uintptr_t>(n_path)) & 3u))
+        return KVC_ERR_ALIGN;
+    if (layer < 0 || layer >= d->layers || T < 1 || P < 1) return KVC_ERR_ARG;
+    const WorkspaceLayout w = ws_layout(d, g);
+    if (workspace_bytes < w.total) return KVC_ERR_WORKSPACE;
+    PathParams p{};
+    p.cache = cache;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.pos = pos0;
+    p.path = path;
+    p.n_path = n_path;
+    p.table = block_table;
+    p.err = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + w.err);
+    p.layer_off = (long long)layer * 2 * g.half_elems;
+    p.kv_off = g.half_elems;
+    if (d->dtype == KVC_I8) {
+        const long long half_rows = g.half_elems / d->head_dim;
+        p.scales = reinterpret_cast<float*>(static_cast<char*>(cache) + (size_t)d->layers * 2 * (size_t)g.half_elems);
+        p.sc_layer_off = (long long)layer * 2 * half_rows;
+        p.sc_kv_off = half_rows;
+    }
+    p.B = d->batch;
+    p.Hkv = d->kv_heads;
+    p.T = T;
+    p.P = P;
+    p.layout = d->layout;
+    p.window = d->window;
+    p.sinks = d->layout == KVC_LAYOUT_SINK_RING ? d->sinks : 0;
+    p.capacity = g.C;
+    p.bs = d->block_size;
+    p.num_blocks = d->num_blocks;
+    p.maxb = d->max_blocks_per_seq;
+    p.rope = d->rope;
+    if (d->rope == KVC_ROPE_BAKED) fill_theta(d->head_dim, d->rope_base, p.theta, nullptr);
+    return launch_append_path(d->dtype, d->head_dim, p, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
 KVC_API int kvc_get_error(void* workspace, void* stream) {

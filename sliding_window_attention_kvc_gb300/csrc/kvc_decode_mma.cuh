@@ -342,13 +342,13 @@ __device__ __forceinline__ void window_partition(const DecodeParams& p, int b, l
 
 // The same for a paged batch: its attended rows (plan_rows_kernel's seq_rows),
 // and those of the sequences before b.
-__device__ __forceinline__ void paged_partition(const DecodeParams& p, int b, long long* total, long long* Ob,
-                                                long long* Rb) {
+__device__ __forceinline__ void paged_partition(const DecodeParams& p, const int32_t* seq_rows, int b,
+                                                long long* total, long long* Ob, long long* Rb) {
     const int lane = threadIdx.x & 31;
     long long tot = 0, before = 0, rb = 0;
     for (int base = 0; base < p.B; base += 32) {
         const int bb = base + lane;
-        long long st = bb < p.B ? (long long)__ldcg(p.seq_rows + bb) : 0;
+        long long st = bb < p.B ? (long long)__ldcg(seq_rows + bb) : 0;
         long long pre = bb < b ? st : 0;
         long long me = bb == b ? st : 0;
 #pragma unroll
@@ -378,7 +378,7 @@ constexpr int kCombineThreads = 256;
 // COLS columns per CTA: 16 when (sequence, kv head, group) units are few (more
 // CTAs per unit, shorter chains), 128 (64 at head_dim 64) when they already
 // fill a wave of CTAs.
-template <int D, int GH, bool PAGED, int COLS>
+template <int D, int GH, bool PAGED, int COLS, int EXT = kExtNone>
 __global__ void __launch_bounds__(kCombineThreads) combine_streamk_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int C4 = COLS / 4;                   // float4 columns per chunk
     constexpr int PAIRS = GH * C4;                 // (head, float4) outputs of the chunk
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_streamk_kernel(const 
         // the decode kernel started, so before this grid launched)
         if (tid < 32) {
             long long R, Ob, Rb;
-            paged_partition(p, b, &R, &Ob, &Rb);
+            paged_partition(p, EXT == kExtSelect ? p.seq_rows + (long long)kvh * p.B : p.seq_rows, b, &R, &Ob, &Rb);
             const int2 fl = paged_seq_shares(Ob, Rb, R, paged_share_count(R, p.nsplit));
             if (tid == 0) {
                 s_fn[0] = fl.x + b;
@@ -489,6 +489,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_streamk_kernel(const 
         if (lane == 0) {
             s_M[warp] = M;
             s_L[warp] = L;
+            if (EXT == kExtWeigh && blockIdx.z == 0)
+                p.ml_out[(long long)b * p.Hq + qh0 + warp] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
         }
     }
     __syncthreads();
@@ -580,7 +582,8 @@ __device__ __noinline__ void append_token_warp(const DecodeParams& p, long long 
 // wholly below the sequence's start are not copied.  Paged bf16 batch of 64, 1008 MB of
 // attended rows, distance bias and starts: 166 us, 0.89 of the measured bandwidth;
 // 8 rings of 4096, cap: 27 us, 0.73 (31 replayed from a graph).
-template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE>
+// EXT: one of DecodeExt's additions to a paged decode.
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE, int EXT = kExtNone>
 // Two CTAs (ten warps) per SM: three warps share a sub-partition's 16K
 // registers, so a thread may hold at most 168.
 __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, READ, D))
@@ -590,6 +593,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
     static_assert(!(READ && Q8 && PAGED), "paged caches take no read-time RoPE");
     static_assert(!Q8 || D >= 128, "INT8 rows are whole 128-byte column blocks");
     static_assert(!(READ && SCORE), "modified scores: no read-time RoPE");
+    static_assert(EXT == kExtNone || (PAGED && !READ && !SCORE), "additions to plain paged decodes");
+    constexpr bool kPlace = SCORE || EXT == kExtWeigh;    // sub-tiles carry the position of their first row
     constexpr int NST = S::kStages, NSUB = S::kNsub, HALF = S::kHalf;
 
     extern __shared__ unsigned char smem_raw[];
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
             }
         }
     }
-    if constexpr (PAGED && !Q8) {
+    if constexpr (PAGED && !Q8 && EXT != kExtSelect) {
         // A paged batch: the same guess from the plan's per-sequence rows and
         // block directory as they stand (the plan kernel may be rewriting them,
         // for this call or the last), and the block table; every index is
@@ -1136,17 +1141,18 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
             }
             }
         } else {
-            const bool self = p.self_plan != 0;
+            const bool self = EXT != kExtSelect && p.self_plan != 0;
+            const int32_t* const seq_rows = EXT == kExtSelect ? p.seq_rows + (long long)kvh * p.B : p.seq_rows;
             // batch: the shares are cut here from each sequence's attended rows
             // (seq_rows, plan_rows_kernel) laid end to end, as the plan defines
             // them; rows of the first 64 sequences stay in registers
             long long Rt = 0;
             int rows0 = 0, rows1 = 0;
             if (!self) {
-                rows0 = lane < p.B ? __ldcg(p.seq_rows + lane) : 0;
-                rows1 = 32 + lane < p.B ? __ldcg(p.seq_rows + 32 + lane) : 0;
+                rows0 = lane < p.B ? __ldcg(seq_rows + lane) : 0;
+                rows1 = 32 + lane < p.B ? __ldcg(seq_rows + 32 + lane) : 0;
                 long long r = (long long)rows0 + rows1;
-                for (int base = 64; base < p.B; base += 32) r += base + lane < p.B ? __ldcg(p.seq_rows + base + lane) : 0;
+                for (int base = 64; base < p.B; base += 32) r += base + lane < p.B ? __ldcg(seq_rows + base + lane) : 0;
 #pragma unroll
                 for (int off = 16; off >= 1; off >>= 1) r += __shfl_xor_sync(0xffffffffu, r, off);
                 Rt = r;
@@ -1175,7 +1181,8 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
             // itv.w attended rows; inf = (t, first partial slot and slot count of
             // the sequence, physical block of itv.y or -2 when not known), `item`
             // its partial slot.
-            auto walk_item = [&](const int4 itv, const int4 inf, int item) {
+            // (kExtSelect: `total` rows of the list, whose entries are the logical blocks)
+            auto walk_item = [&](const int4 itv, const int4 inf, int item, int total) {
                 const int b = itv.x;
                 MmaSegment hdr;
                 hdr.b = b;
@@ -1185,8 +1192,10 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                 hdr.nparts = inf.z;
                 hdr.new_row = new_row;
                 if (!(ok = begin_segment(hdr))) return;
-                const int tt = clamp_paged_t(hdr.t, p.maxb, p.bs);
-                const int32_t* trow = p.table + (long long)b * p.maxb;
+                const int tt = EXT == kExtSelect ? total - 1 : clamp_paged_t(hdr.t, p.maxb, p.bs);
+                const int32_t* trow = EXT == kExtSelect ? p.list + ((long long)kvh * p.B + b) * p.list_k
+                                                        : p.table + (long long)b * p.maxb;
+                const uint32_t* const valid = EXT == kExtSelect ? nullptr : p.valid;
                 int lb = itv.y;
                 int rem = itv.w;
                 const int last_lb = tt < 0 ? -1 : tt / p.bs;
@@ -1211,7 +1220,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                             break;
                         }
                         const int n = min(take, 16 * room);
-                        emit_run(blk + row, n, SCORE ? lb * p.bs + row : 0, newrow_of(lb, row, n), true, evict_first);
+                        emit_run(blk + row, n, kPlace ? lb * p.bs + row : 0, newrow_of(lb, row, n), true, evict_first);
                         take -= n;
                         rem -= n;
                         row += n;
@@ -1225,7 +1234,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                     int my_phys = -1, my_rows = 0;
                     uint32_t my_refs = 1u;
                     if (my_lb <= last_lb)
-                        my_rows = paged_block_rows_refs(trow, p.valid, p.refs, p.err, my_lb, tt, p.bs, p.num_blocks,
+                        my_rows = paged_block_rows_refs(trow, valid, p.refs, p.err, my_lb, tt, p.bs, p.num_blocks,
                                                         &my_phys, &my_refs);
                     const bool my_ef = p.refs ? my_refs <= 1u : evict_first;
                     const int row0 = (my_lb == itv.y) ? itv.z : 0;
@@ -1250,7 +1259,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                         const bool mine = ((pending >> lane) & 1u) && rank < room;
                         const unsigned emitted = __ballot_sync(0xffffffffu, mine);
                         if (mine)
-                            emit_sub_lane(urow, take, rank, SCORE ? my_lb * p.bs + row0 : 0,
+                            emit_sub_lane(urow, take, rank, kPlace ? my_lb * p.bs + row0 : 0,
                                           newrow_of(my_lb, row0, take), my_ef);
                         __syncwarp();
                         fill += __popc(emitted);
@@ -1264,7 +1273,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                     int my_phys = -1, my_rows = 0;
                     uint32_t my_refs = 1u;
                     if (my_lb <= last_lb)
-                        my_rows = paged_block_rows_refs(trow, p.valid, p.refs, p.err, my_lb, tt, p.bs, p.num_blocks,
+                        my_rows = paged_block_rows_refs(trow, valid, p.refs, p.err, my_lb, tt, p.bs, p.num_blocks,
                                                         &my_phys, &my_refs);
                     const bool my_ef = p.refs ? my_refs <= 1u : evict_first;
                     unsigned mask = __ballot_sync(0xffffffffu, my_rows > 0);
@@ -1284,7 +1293,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                                 break;
                             }
                             const int n = min(take, 16 * room);
-                            emit_run(blk + row, n, SCORE ? (lb + src) * p.bs + row : 0, newrow_of(lb + src, row, n), true,
+                            emit_run(blk + row, n, kPlace ? (lb + src) * p.bs + row : 0, newrow_of(lb + src, row, n), true,
                                      bef);
                             take -= n;
                             rem -= n;
@@ -1300,6 +1309,11 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
             // group with fewer attended blocks before it than that rank holds it.
             auto first_block = [&](int b, int tb, long long s0, int* lb_out, int* row_out) -> bool {
                 const int kb = (int)(s0 / p.bs);
+                if constexpr (EXT == kExtSelect) {        // a list has no gaps
+                    *lb_out = kb;
+                    *row_out = (int)(s0 - (long long)kb * p.bs);
+                    return true;
+                }
                 const int tt = clamp_paged_t(tb, p.maxb, p.bs);
                 const int ng = tt < 0 ? 0 : (tt / p.bs) / 32 + 1;
                 const int2* drow = p.dir + (long long)b * p.dir_groups;
@@ -1333,7 +1347,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                 if (self) {
                     // one sequence: share x holds exactly its item x
                     walk_item(make_int4(0, s_plan.lb, s_plan.row, s_plan.rows), make_int4(s_plan.traw, 0, G, s_plan.phys),
-                              xs);
+                              xs, 0);
                     continue;
                 }
                 // the sequences that meet share xs, in order (b meets shares
@@ -1347,7 +1361,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                     if (run >= hi && hi < Rt) break;
                     const int bb = base + lane;
                     const int r = base == 0 ? rows0 : base == 32 ? rows1
-                                : (bb < p.B ? __ldcg(p.seq_rows + bb) : 0);
+                                : (bb < p.B ? __ldcg(seq_rows + bb) : 0);
                     long long incl = r;
 #pragma unroll
                     for (int off = 1; off < 32; off <<= 1) {
@@ -1378,7 +1392,7 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                             rows = (int)(s1 - s0);
                             if (!first_block(b, tb, s0, &lb, &row)) rows = 0;
                         }
-                        walk_item(make_int4(b, lb, row, rows), make_int4(tb, fl.x + b, fl.y - fl.x + 1, -2), xs + b);
+                        walk_item(make_int4(b, lb, row, rows), make_int4(tb, fl.x + b, fl.y - fl.x + 1, -2), xs + b, (int)Rb);
                     }
                     run += __shfl_sync(0xffffffffu, incl, 31);
                 }
@@ -2024,6 +2038,27 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
                     if (tk0 + off[e] < lo_rows) sv[e] = -INFINITY;
                 }
             }
+            if constexpr (EXT != kExtNone) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sv[e] *= p.score.scale2;
+            }
+            if constexpr (EXT == kExtWeigh) {
+                // the row's scores, where the weights are taken from them (written by one of the warps
+                // that share the sub-tile; pairs of positions together where they are aligned)
+                if (g < GH && hd == 0 && seg.b >= 0) {
+                    const int at = meta[s].ip0[tg] + tk0;
+                    float* dst = p.scores + ((long long)seg.b * p.Hq + kvh * p.G + z * GH + g) * p.scores_stride + at;
+                    if (!(at & 1) && tk0 + 9 < nrows) {
+                        *reinterpret_cast<float2*>(dst) = make_float2(sv[0], sv[1]);
+                        *reinterpret_cast<float2*>(dst + 8) = make_float2(sv[2], sv[3]);
+                    } else {
+                        if (tk0 < nrows) dst[0] = sv[0];
+                        if (tk0 + 1 < nrows) dst[1] = sv[1];
+                        if (tk0 + 8 < nrows) dst[8] = sv[2];
+                        if (tk0 + 9 < nrows) dst[9] = sv[3];
+                    }
+                }
+            }
             if (tk0 >= nrows) sv[0] = -INFINITY;
             if (tk0 + 1 >= nrows) sv[1] = -INFINITY;
             if (tk0 + 8 >= nrows) sv[2] = -INFINITY;
@@ -2126,21 +2161,21 @@ __global__ void __launch_bounds__(kDecodeThreads, decode_ctas_per_sm(Q8, PAGED, 
     }
 }
 
-template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false>
+template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE = false, int EXT = kExtNone>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream) {
     using SM = MmaSmem<D, GH, READ, Q8, PAGED>;
     // the resident CTAs per SM that __launch_bounds__ plans for must fit in
     // shared memory (228 KB per SM, 1 KB of it reserved per CTA)
     constexpr int kCtasPerSm = decode_ctas_per_sm(Q8, PAGED, READ, D);
     static_assert(kCtasPerSm * (SM::kTotal + 1024) <= 233472, "shared memory for the planned CTAs per SM");
-    auto kern = decode_mma_kernel<D, GH, PAGED, READ, Q8, SCORE>;
+    auto kern = decode_mma_kernel<D, GH, PAGED, READ, Q8, SCORE, EXT>;
     // few (sequence, kv head, group) units: narrow column chunks, more CTAs
     // each; many: 128 columns a CTA (measured: 64-column chunks 0.5 us slower
     // on the 64-sequence paged batch, 16-column ones 14 us)
     const long long units = (long long)p.B * p.Hkv * p.nsub;
     const bool narrow = units * (D / 16) <= 1216;
     constexpr int kWide = D >= 128 ? 128 : 64;
-    auto comb = narrow ? combine_streamk_kernel<D, GH, PAGED, 16> : combine_streamk_kernel<D, GH, PAGED, kWide>;
+    auto comb = narrow ? combine_streamk_kernel<D, GH, PAGED, 16, EXT> : combine_streamk_kernel<D, GH, PAGED, kWide, EXT>;
     static std::atomic<unsigned long long> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

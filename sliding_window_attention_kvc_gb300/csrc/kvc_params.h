@@ -125,7 +125,19 @@ struct DecodeParams {
     unsigned long long theta[kMaxHalfDim];   // RoPE frequencies as turns, fixed point: theta_i / (2 pi) * 2^64
     ScoreParams score;          // kvc_decode_attention_scored
     int no_combine;             // the caller joins the partials itself (kvc_decode_attention_shared)
+    const int32_t* list;        // kvc_decode_attention_selected: [Hkv][B][list_k] physical blocks of each kv
+    int list_k;                 // head; seq_rows is then [Hkv][B]
+    float* scores;              // kvc_decode_attention_weighed: [B][Hq][scores_stride] base-2 scores by position
+    long long scores_stride;
+    float2* ml_out;             // ... and [B][Hq] (M, 1 / L) of each softmax
 };
+
+// What a paged decode does besides (tensor-core kernel); q then enters the products
+// unscaled and fp32 scores are scaled, so that they are exact to fp32.
+//  kExtSelect  each kv head walks a list of blocks of its own: the list is its
+//              table, its rows are laid end to end, every block but the last is full;
+//  kExtWeigh   every row's score is kept.
+enum DecodeExt : int { kExtNone = 0, kExtSelect = 1, kExtWeigh = 2 };
 
 struct PlanParams {
     const int32_t* pos;
@@ -284,6 +296,9 @@ cudaError_t launch_decode(int dtype, int head_dim, int gh, bool paged, bool read
 // bf16 and INT8 (q8) caches: tensor-core kernel fed by TMA tensor copies through `maps`.
 cudaError_t launch_decode_mma(int head_dim, int gh, bool paged, bool read_rope, bool q8, bool scored,
                               const DecodeParams& p, const KvTensorMaps& maps, dim3 grid, cudaStream_t stream);
+// a paged decode with one of DecodeExt's additions
+cudaError_t launch_decode_ext(int head_dim, int gh, bool q8, int ext, const DecodeParams& p, const KvTensorMaps& maps,
+                              dim3 grid, cudaStream_t stream);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_plan_rows(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_append(int dtype, const AppendParams& p, cudaStream_t stream);

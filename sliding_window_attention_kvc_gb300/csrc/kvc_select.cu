@@ -1,0 +1,551 @@
+// Caches read in part: bounds of each block's keys, blocks chosen by what the
+// bounds allow a query's scores to be, and the lists that a decode over the
+// chosen blocks walks.
+//
+// For a block and kv head, hi_d and lo_d are the largest and smallest key
+// value of channel d.  For any key of the block
+//     q . k = sum q_d k_d <= sum max(q_d hi_d, q_d lo_d) = U,
+// so a block whose U is small holds no key that the query attends much.  hi and
+// lo are kept as 8-bit codes of one step s = max(|hi|, |lo|) / 127, hi rounded
+// up and lo down, so that the codes' bound is a bound still; q enters as codes
+// too (step max|q| / 127).  U is then s s_q u, u an integer below 127 127 256 <
+// 2^24: its products run four to an instruction (dp4a), and no order of the
+// sums, here or in any other program, gives another score.
+#include "kvc_decode.cuh"
+#include "kvc_select.h"
+
+namespace kvc {
+
+namespace {
+
+__device__ __forceinline__ void sl_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void sl_pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+cudaLaunchConfig_t sl_config(dim3 grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// ---------------------------------------------------------------------------
+// bounds
+// ---------------------------------------------------------------------------
+constexpr int kBoundsThreads = 128;
+
+// 16 bytes of a key row as floats.
+template <typename Elt>
+__device__ __forceinline__ void key_values(const uint4& w, float scale, float* f) {
+    if constexpr (sizeof(Elt) == 1) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = (float)(int8_t)(x[i >> 2] >> (8 * (i & 3))) * scale;
+    } else {
+        EltTraits<Elt>::unpack(w, f);
+    }
+}
+
+// One warp per (touched block, kv head) of a sequence.  A lane keeps the ends
+// of 16 bytes of the row (32 on rows of 1 KB); 512 / row bytes rows pass at
+// once.  The block is read whole from its first row, so that the result does not
+// depend on what was there before.
+template <typename Elt, int D>
+__global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __grid_constant__ BoundsParams p) {
+    constexpr int VPL = 16 / (int)sizeof(Elt);            // values of a chunk
+    constexpr int CPR = D / VPL;                          // chunks of a row
+    constexpr int LPR = CPR < 32 ? CPR : 32;              // lanes of a row
+    constexpr int NCH = CPR / LPR;                        // chunks of a lane
+    constexpr int RPW = 32 / LPR;                         // rows at once
+    constexpr int U = 4;                                  // loads in flight
+    sl_pdl_wait();
+    sl_pdl_launch();
+    const int lane = threadIdx.x & 31;
+    const int unit = blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+    const int slot = unit / p.Hkv, h = unit - slot * p.Hkv, b = blockIdx.y;
+    if (slot >= p.slots) return;
+    const long long t0 = p.pos[b];
+    int n = p.n_new;
+    if (p.n_tok) n = max(0, min(n, p.n_tok[b]));
+    const long long end = t0 + n, first = t0 > 0 ? t0 : 0;
+    const long long lb = first / p.bs + slot;
+    if (end <= first || lb * p.bs >= end) return;
+    if (lb >= p.maxb) {
+        if (lane == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
+        return;
+    }
+    const int phys = p.table[(long long)b * p.maxb + lb];
+    if (phys < 0 || phys >= p.num_blocks) {
+        if (lane == 0) set_error(p.err, phys < 0 ? 0x2u : 0x1u);
+        return;
+    }
+    const int rows = (int)min((long long)p.bs, end - lb * p.bs);
+    const long long row0 = ((long long)phys * p.Hkv + h) * p.bs;
+    const Elt* src = static_cast<const Elt*>(p.cache) + p.layer_off + row0 * D;
+    const float* sc = sizeof(Elt) == 1 ? p.scales + p.sc_layer_off + row0 : nullptr;
+    const int c = lane % LPR, r0 = lane / LPR;
+    float hi[NCH * VPL], lo[NCH * VPL];
+#pragma unroll
+    for (int i = 0; i < NCH * VPL; ++i) {
+        hi[i] = -INFINITY;
+        lo[i] = INFINITY;
+    }
+    for (int base = r0; base < rows; base += U * RPW) {
+        uint4 w[U][NCH];
+        float s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = min(base + u * RPW, rows - 1);  // (a row twice changes nothing)
+#pragma unroll
+            for (int k = 0; k < NCH; ++k)
+                w[u][k] = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * D + (k * LPR + c) * VPL));
+            s[u] = sizeof(Elt) == 1 ? __ldg(sc + r) : 1.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < NCH; ++k) {
+                float f[VPL];
+                key_values<Elt>(w[u][k], s[u], f);
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    hi[k * VPL + i] = fmaxf(hi[k * VPL + i], f[i]);
+                    lo[k * VPL + i] = fminf(lo[k * VPL + i], f[i]);
+                }
+            }
+    }
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH * VPL; ++i) {
+#pragma unroll
+        for (int off = LPR; off < 32; off <<= 1) {
+            hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
+            lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
+        }
+        a = fmaxf(a, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
+    }
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    const float step = __fdiv_rn(a, 127.f);
+    const long long at = (long long)phys * p.Hkv + h;
+    if (lane == 0) p.steps[at] = step;
+    if (lane < LPR) {
+        int8_t* dst = p.codes + at * 2 * D;
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t w[VPL / 4];
+#pragma unroll
+                for (int i = 0; i < VPL / 4; ++i) w[i] = 0u;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    int code = 0;
+                    if (step > 0.f) {
+                        const float x = __fdiv_rn(e ? lo[k * VPL + i] : hi[k * VPL + i], step);
+                        code = e ? (int)fmaxf(floorf(x), -127.f) : (int)fminf(ceilf(x), 127.f);
+                    }
+                    w[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
+                }
+                int8_t* d = dst + e * D + (k * LPR + c) * VPL;
+                if constexpr (VPL == 4)
+                    *reinterpret_cast<uint32_t*>(d) = w[0];
+                else if constexpr (VPL == 8)
+                    *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+                else
+                    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+    }
+}
+
+template <typename Elt, int D>
+cudaError_t launch_bounds_t(const BoundsParams& p, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const long long units = (long long)p.slots * p.Hkv;
+    constexpr int W = kBoundsThreads / 32;
+    const cudaLaunchConfig_t cfg =
+        sl_config(dim3((unsigned)((units + W - 1) / W), p.B), kBoundsThreads, 0, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, block_bounds_kernel<Elt, D>, p);
+}
+
+// ---------------------------------------------------------------------------
+// scores
+// ---------------------------------------------------------------------------
+constexpr int kScoreThreads = 128;
+
+// Order of floats as unsigned integers; -0 counts as 0, NaN as the least.
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (!(x == x)) x = -INFINITY;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// One CTA per (chunk of blocks, kv head, sequence).  The group's q heads as
+// codes in shared memory, positive and negative parts apart: hi meets the one
+// and lo the other.  D / 16 lanes hold a block's codes, 16 channels of each end a
+// lane; a warp takes 4 x 512 / D blocks at once.
+template <typename Act, int D>
+__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
+    constexpr int LPB = D / 16, BPW = 32 / LPB, U = 4, NP = D / 64;
+    extern __shared__ __align__(16) unsigned char s_q[];          // [G][2][D] codes, then [G] steps
+    int8_t* codes = reinterpret_cast<int8_t*>(s_q);
+    float* s_step = reinterpret_cast<float*>(s_q + (size_t)p.G * 2 * D);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.y, b = blockIdx.z;
+    sl_pdl_wait();
+    sl_pdl_launch();
+    const int traw = p.pos[b];
+    const int t = clamp_paged_t(traw, p.maxb, p.bs);
+    if ((traw < 0 || traw != t) && blockIdx.x == 0 && h == 0 && tid == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
+    const int nb = t < 0 ? 0 : t / p.bs + 1;
+    const int c0 = blockIdx.x * kScoreChunk, c1 = min(nb, c0 + kScoreChunk);
+    if (c0 >= c1) return;
+    for (int g = warp; g < p.G; g += kScoreThreads / 32) {
+        const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + g) * D;
+        float x[2 * NP], a = 0.f;
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int i = lane + 32 * m;
+            float x1 = EltTraits<Act>::to_f32(qr[i]), x2 = EltTraits<Act>::to_f32(qr[i + D / 2]);
+            if (p.rope != kRopeNone) {
+                float cs, sn;
+                rope_cos_sin((long long)t, p.theta[i], &cs, &sn);
+                const float y1 = x1 * cs - x2 * sn, y2 = x1 * sn + x2 * cs;
+                x1 = y1;
+                x2 = y2;
+            }
+            x[2 * m] = x1;
+            x[2 * m + 1] = x2;
+            a = fmaxf(a, fmaxf(fabsf(x1), fabsf(x2)));
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        const float step = __fdiv_rn(a, 127.f);
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int code = q8_code(x[2 * m + e], step);
+                int8_t* d = codes + (size_t)g * 2 * D + lane + 32 * m + e * (D / 2);
+                d[0] = (int8_t)max(code, 0);
+                d[D] = (int8_t)min(code, 0);
+            }
+        if (lane == 0) s_step[g] = step;
+    }
+    __syncthreads();
+    const int32_t* trow = p.table + (long long)b * p.maxb;
+    uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
+    const int ln = lane % LPB, sub = lane / LPB;
+    for (int base = c0 + warp * U * BPW; base < c1; base += (kScoreThreads / 32) * U * BPW) {
+        int lb[U], ok[U];
+        uint4 hi[U], lo[U];
+        float step[U], best[U];
+        int phys[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            lb[u] = base + u * BPW + sub;
+            phys[u] = lb[u] < c1 ? __ldg(trow + lb[u]) : -1;
+            if (phys[u] >= p.num_blocks) {
+                set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+                phys[u] = -1;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ok[u] = phys[u] >= 0;
+            if (ok[u] && p.valid) ok[u] = (__ldg(p.valid + (phys[u] >> 5)) >> (phys[u] & 31)) & 1u;
+            const long long at = (long long)max(phys[u], 0) * p.Hkv + h;
+            const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
+            hi[u] = __ldg(src + ln);
+            lo[u] = __ldg(src + LPB + ln);
+            step[u] = __ldg(p.steps + at);
+            best[u] = -INFINITY;
+        }
+        for (int g = 0; g < p.G; ++g) {
+            const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + 16 * ln);
+            const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + D + 16 * ln);
+            const float sq = s_step[g];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                int a = __dp4a((int)hi[u].x, (int)qp.x, 0);
+                int e = __dp4a((int)lo[u].x, (int)qn.x, 0);
+                a = __dp4a((int)hi[u].y, (int)qp.y, a);
+                e = __dp4a((int)lo[u].y, (int)qn.y, e);
+                a = __dp4a((int)hi[u].z, (int)qp.z, a);
+                e = __dp4a((int)lo[u].z, (int)qn.z, e);
+                a = __dp4a((int)hi[u].w, (int)qp.w, a);
+                e = __dp4a((int)lo[u].w, (int)qn.w, e);
+                a += e;
+#pragma unroll
+                for (int off = 1; off < LPB; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+                best[u] = fmaxf(best[u], __fmul_rn((float)a, __fmul_rn(sq, step[u])));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (ln == 0 && lb[u] < c1)
+                keys[lb[u]] = !ok[u] ? 0u
+                              : (lb[u] < p.first || lb[u] >= nb - p.recent) ? 0xffffffffu
+                                                                            : score_key(best[u]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// selection
+// ---------------------------------------------------------------------------
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
+
+// Sums over the CTA's threads before this one, of two counts at once; totals in *tot.
+__device__ __forceinline__ int2 pick_scan(int2 v, int2* s_w, int2* tot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int2 x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x.x, off), c = __shfl_up_sync(0xffffffffu, x.y, off);
+        if (lane >= off) {
+            x.x += a;
+            x.y += c;
+        }
+    }
+    if (lane == 31) s_w[warp] = x;
+    __syncthreads();
+    int2 before = make_int2(0, 0), all = before;
+    for (int w = 0; w < nw; ++w) {
+        const int2 s = s_w[w];
+        if (w < warp) {
+            before.x += s.x;
+            before.y += s.y;
+        }
+        all.x += s.x;
+        all.y += s.y;
+    }
+    __syncthreads();
+    *tot = all;
+    return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
+}
+
+// Counts key `key`'s digit among the warp's (one addition for lanes of one digit).
+__device__ __forceinline__ void pick_count(int* hist, bool in, uint32_t digit) {
+    const unsigned act = __ballot_sync(0xffffffffu, in);
+    if (in) {
+        const unsigned same = __match_any_sync(act, digit);
+        if ((threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+    }
+}
+
+// The digit that holds the want-th key (1-based) from the top (DOWN) or the
+// bottom; how many keys lie beyond it on that side goes to *beyond.  By warp 0.
+template <bool DOWN>
+__device__ __forceinline__ void pick_digit(const int* hist, int want, int* digit, int* beyond) {
+    const int lane = threadIdx.x & 31;
+    int c[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int d = lane * 8 + i;
+        c[i] = hist[DOWN ? 255 - d : d];
+        sum += c[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += a;
+    }
+    int run = incl - sum;
+    if (run < want && incl >= want) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (run < want && run + c[i] >= want) {
+                *digit = DOWN ? 255 - (lane * 8 + i) : lane * 8 + i;
+                *beyond = run;
+            }
+            run += c[i];
+        }
+    }
+}
+
+// One CTA per (kv head, sequence): the k largest keys, ties by the lowest index,
+// by a radix search of the k-th largest (four digits), then the kept indices in
+// ascending order.
+__global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ int s_hist[256];
+    __shared__ int2 s_w[kPickWarps];
+    __shared__ int s_digit, s_beyond;
+    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+    sl_pdl_wait();
+    sl_pdl_launch();
+    const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
+    const int nb = t < 0 ? 0 : t / p.bs + 1;
+    const uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
+    int32_t* out = p.blocks + ((long long)b * p.Hkv + h) * p.k;
+    // key >= low is kept whole but for the keys equal to it, of which the first `ties` are
+    uint32_t prefix = 0, mask = 0;
+    int want = p.k;
+    bool every = false;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kPickThreads) s_hist[i] = 0;
+        if (tid == 0) s_digit = -1;
+        __syncthreads();
+        for (int base = 0; base < nb; base += kPickThreads) {
+            const int i = base + tid;
+            const uint32_t key = i < nb ? __ldcg(keys + i) : 0u;
+            pick_count(s_hist, key != 0u && (key & mask) == prefix, (key >> shift) & 255u);
+        }
+        __syncthreads();
+        if (tid < 32) pick_digit<true>(s_hist, want, &s_digit, &s_beyond);
+        __syncthreads();
+        const int digit = s_digit;
+        if (digit < 0) {                  // fewer candidates than k (seen in the first pass)
+            every = true;
+            break;
+        }
+        want -= s_beyond;
+        prefix |= (uint32_t)digit << shift;
+        mask |= 255u << shift;
+        __syncthreads();
+    }
+    const uint32_t low = every ? 1u : prefix;
+    const int ties = every ? 0x7fffffff : want;
+    int2 run = make_int2(0, 0);           // keys above `low`, keys equal to it, before this pass
+    for (int base = 0; base < nb; base += kPickThreads) {
+        const int i = base + tid;
+        const uint32_t key = i < nb ? __ldcg(keys + i) : 0u;
+        const bool more = key > low, same = key == low;
+        int2 tot;
+        const int2 ex = pick_scan(make_int2(more, same), s_w, &tot);
+        const int above = run.x + ex.x, equal = run.y + ex.y;
+        if (more || (same && equal < ties)) {
+            const int at = above + min(equal, ties);
+            if (at < p.k)
+                out[at] = i;
+            else
+                index_fault(p.err, 40, at);
+        }
+        run.x += tot.x;
+        run.y += tot.y;
+    }
+    for (int i = run.x + min(run.y, ties) + tid; i < p.k; i += kPickThreads) out[i] = -1;
+}
+
+// ---------------------------------------------------------------------------
+// lists of a selected decode
+// ---------------------------------------------------------------------------
+constexpr int kListThreads = 256;
+
+// One CTA per (kv head, sequence): its blocks, checked, as physical ones without
+// gaps.  Entries ascend; one that does not lie above those before it (a block
+// named twice) or past the table is reported and left out, negative ones are no
+// entries.  Blocks that are unmapped, not resident or past the position are not
+// attended.
+__global__ void __launch_bounds__(kListThreads) select_list_kernel(const __grid_constant__ SelectPlanParams p) {
+    constexpr int NW = kListThreads / 32;
+    __shared__ int s_max[NW], s_cnt[NW], s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x, b = blockIdx.y;
+    sl_pdl_wait();
+    sl_pdl_launch();
+    const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
+    const int last = t < 0 ? -1 : t / p.bs;
+    const int32_t* src = p.blocks + ((long long)b * p.Hkv + h) * p.k;
+    const int32_t* trow = p.table + (long long)b * p.maxb;
+    int32_t* dst = p.list + ((long long)h * p.B + b) * p.k;
+    if (tid == 0) s_last = 0;
+    int top = -1, n = 0;                  // largest entry and attended blocks before this pass
+    for (int base = 0; base < p.k; base += kListThreads) {
+        const int i = base + tid;
+        int lb = i < p.k ? __ldcg(src + i) : -1;
+        if (lb >= p.maxb) {
+            set_error(p.err, 0x10u /* KVC_DEV_BAD_ENTRY */);
+            lb = -1;
+        }
+        int m = lb;                       // largest entry up to here
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, m, off);
+            if (lane >= off) m = max(m, a);
+        }
+        if (lane == 31) s_max[warp] = m;
+        int before = __shfl_up_sync(0xffffffffu, m, 1);
+        if (lane == 0) before = -1;
+        __syncthreads();
+        before = max(before, top);
+        int all = top;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before = max(before, s_max[w]);
+            all = max(all, s_max[w]);
+        }
+        top = all;
+        int phys = -1;
+        if (lb >= 0 && lb <= before) {
+            set_error(p.err, 0x10u);
+        } else if (lb >= 0 && lb <= last) {
+            phys = __ldg(trow + lb);
+            if (phys >= p.num_blocks) {
+                set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+                phys = -1;
+            }
+            if (phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
+        }
+        const unsigned have = __ballot_sync(0xffffffffu, phys >= 0);
+        if (lane == 0) s_cnt[warp] = __popc(have);
+        if (phys >= 0 && lb == last) s_last = 1;
+        __syncthreads();
+        int at = n + __popc(have & ((1u << lane) - 1u));
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) at += s_cnt[w];
+            n += s_cnt[w];
+        }
+        if (phys >= 0) dst[at] = phys;
+        __syncthreads();
+    }
+    // every attended block but the position's own holds bs rows
+    if (tid == 0) p.rows[h * p.B + b] = n * p.bs - (s_last ? p.bs - (t - last * p.bs + 1) : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_block_bounds(int dtype, int D, const BoundsParams& p, cudaStream_t s) {
+#define KVC_CASE(T, E, DD) \
+    if (dtype == T && D == DD) return launch_bounds_t<E, DD>(p, s);
+    KVC_CASE(0, float, 64) KVC_CASE(0, float, 128) KVC_CASE(0, float, 256)
+    KVC_CASE(1, __nv_bfloat16, 64) KVC_CASE(1, __nv_bfloat16, 128) KVC_CASE(1, __nv_bfloat16, 256)
+    KVC_CASE(2, int8_t, 128) KVC_CASE(2, int8_t, 256)
+#undef KVC_CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_select(int dtype, int D, const SelectParams& p, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    const int smem = p.G * (2 * D + 4);
+    cudaLaunchConfig_t cfg =
+        sl_config(dim3((p.maxb + kScoreChunk - 1) / kScoreChunk, p.Hkv, p.B), kScoreThreads, smem, s, &attr);
+    cudaError_t e = cudaErrorInvalidValue;
+    // (above 48 KB, groups of more than 93 heads of 256, a kernel asks for its shared memory)
+#define KVC_CASE(F, A, DD)                                                                                   \
+    if ((dtype == 0) == F && D == DD) {                                                                      \
+        e = smem > 48 * 1024 ? cudaFuncSetAttribute(block_score_kernel<A, DD>,                               \
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem)       \
+                             : cudaSuccess;                                                                  \
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, block_score_kernel<A, DD>, p);                    \
+    }
+    KVC_CASE(true, float, 64) KVC_CASE(true, float, 128) KVC_CASE(true, float, 256)
+    KVC_CASE(false, __nv_bfloat16, 64) KVC_CASE(false, __nv_bfloat16, 128) KVC_CASE(false, __nv_bfloat16, 256)
+#undef KVC_CASE
+    if (e != cudaSuccess) return e;
+    cfg = sl_config(dim3(p.Hkv, p.B), kPickThreads, 0, s, &attr);
+    return cudaLaunchKernelEx(&cfg, block_pick_kernel, p);
+}
+
+cudaError_t launch_select_plan(const SelectPlanParams& p, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = sl_config(dim3(p.Hkv, p.B), kListThreads, 0, s, &attr);
+    return cudaLaunchKernelEx(&cfg, select_list_kernel, p);
+}
+
+}  // namespace kvc
