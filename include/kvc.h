@@ -433,6 +433,39 @@ KVC_API int kvc_decode_attention_weighed(const kvc_desc* d, const void* cache, i
                                          float decay, float* weights, void* out, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
+/* Attention of a tree of drafted tokens over a cache, as speculative decoding
+ * verifies it: token i of sequence b continues token parent[b][i] of the draft
+ * (-1: the sequence's last cached token), stands at position pos0[b] + its depth
+ * (0 for a token whose parent is -1) and attends what a token there attends of the
+ * positions below pos0[b], read from the cache as it stands, the tokens above it
+ * in the draft and itself.  Nothing is appended (kvc_append_path does that for
+ * the path that is kept).
+ *   q            [batch, T, q_heads, head_dim] bf16, pre-RoPE.
+ *   k_new, v_new [batch, T, kv_heads, head_dim] bf16, pre-RoPE.
+ *   T            1 .. KVC_TREE_MAX (else KVC_ERR_ARG).
+ *   pos0         [batch] int32: tokens in the cache.  Below 0: idle, zeros.
+ *   parent       [batch, T] int32: -1 .. i - 1.  Below -1: no token (padding; its
+ *                rows may hold anything).  i or more sets KVC_DEV_BAD_ENTRY and
+ *                counts as no token.  What continues no token is none either; it
+ *                gets zeros.
+ *   block_table, valid_bits  PAGED as in kvc_decode_attention.
+ *   out          [batch, T, q_heads, head_dim] bf16.
+ *   workspace    kvc_tree_workspace_bytes(d, T) bytes (0 if refused), set up by
+ *                kvc_workspace_init; it serves the decode calls too.
+ * bf16 caches, rope NONE or BAKED, at most 128 q heads for each kv head; window
+ * layouts with T <= window, paged ones with blocks whose size is a multiple of 8
+ * and divides 64 or is a multiple of 64 (else KVC_ERR_UNSUPPORTED).  Cached rows
+ * below pos0[b] and the tokens' rows hold finite values.  PAGED positions past the
+ * table's end set KVC_DEV_BAD_POSITION; the table's are attended.  It runs on
+ * the tcgen05 tensor cores, one CTA per SM that holds its tensor memory while it
+ * runs. */
+#define KVC_TREE_MAX 64
+KVC_API size_t kvc_tree_workspace_bytes(const kvc_desc* d, int32_t T);
+KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t layer, const void* q, const void* k_new,
+                               const void* v_new, int32_t T, const int32_t* pos0, const int32_t* parent,
+                               const int32_t* block_table, const uint32_t* valid_bits, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* The accepted path of a tree of drafted tokens, appended: token path[b][j] of
  * the draft goes to position pos0[b] + j, for j < n_path[b], as kvc_append of
  * those tokens would put it (any layout, element type and rope).

@@ -28,6 +28,7 @@ KVC_ERR_NULL, KVC_ERR_DESC, KVC_ERR_UNSUPPORTED = -1, -2, -3
 KVC_ERR_ALIGN, KVC_ERR_WORKSPACE, KVC_ERR_ARG, KVC_ERR_CUDA = -4, -5, -6, -7
 KVC_ERR_TOO_LARGE = -8
 KVC_NOALLOC_SCRATCH_BYTES = 8 << 20
+KVC_TREE_MAX = 64
 KVC_DEV_BAD_BLOCK, KVC_DEV_UNMAPPED_APPEND, KVC_DEV_BAD_POSITION = 0x1, 0x2, 0x4
 KVC_DEV_TIMEOUT, KVC_DEV_BAD_ENTRY = 0x8, 0x10
 KVC_DEV_INTERNAL, KVC_DEV_NO_FREE_BLOCK = 0x20, 0x40
@@ -43,7 +44,7 @@ ABI_FUNCTIONS = (
     "kvc_shared_workspace_bytes", "kvc_decode_attention_shared",
     "kvc_bounds_bytes", "kvc_block_bounds", "kvc_select_workspace_bytes", "kvc_select_blocks",
     "kvc_decode_attention_selected", "kvc_weighed_workspace_bytes", "kvc_decode_attention_weighed",
-    "kvc_block_evict", "kvc_append_path",
+    "kvc_block_evict", "kvc_tree_workspace_bytes", "kvc_tree_attention", "kvc_append_path",
 )
 
 
@@ -145,13 +146,16 @@ def lib() -> ctypes.CDLL:
         L.kvc_weighed_workspace_bytes.restype = sz
         L.kvc_decode_attention_weighed.argtypes = [dp, vp, i32, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.kvc_block_evict.argtypes = [dp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.kvc_tree_workspace_bytes.argtypes = [dp, i32]
+        L.kvc_tree_workspace_bytes.restype = sz
+        L.kvc_tree_attention.argtypes = [dp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.kvc_append_path.argtypes = [dp, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp, sz, vp]
         L.kvc_strerror.argtypes = [ctypes.c_int]
         L.kvc_strerror.restype = ctypes.c_char_p
         for name in ABI_FUNCTIONS:
             if name not in ("kvc_cache_bytes", "kvc_workspace_bytes", "kvc_prefill_workspace_bytes", "kvc_strerror",
                             "kvc_shared_workspace_bytes", "kvc_bounds_bytes", "kvc_select_workspace_bytes",
-                            "kvc_weighed_workspace_bytes",
+                            "kvc_weighed_workspace_bytes", "kvc_tree_workspace_bytes",
                             "kvc_pager_create", "kvc_pager_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -702,6 +706,44 @@ def decode_attention_weighed(d: KvcDesc, cache: torch.Tensor, layer: int, q: tor
         _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         raise KvcError(rc, "kvc_decode_attention_weighed")
+    return out
+
+
+def tree_workspace_bytes(d: KvcDesc, T: int) -> int:
+    return int(lib().kvc_tree_workspace_bytes(ctypes.byref(d), int(T)))
+
+
+def alloc_tree_workspace(d: KvcDesc, T: int, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for kvc_tree_attention with drafts of T tokens (also a decode workspace)."""
+    n = tree_workspace_bytes(d, T)
+    if n == 0:
+        raise KvcError(KVC_ERR_DESC, "kvc_tree_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def tree_attention(d: KvcDesc, cache: torch.Tensor, layer: int, q: torch.Tensor, k_new: torch.Tensor,
+                   v_new: torch.Tensor, pos0: torch.Tensor, parent: torch.Tensor, workspace: torch.Tensor,
+                   block_table: torch.Tensor | None = None, valid_bits: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvc_tree_attention: q [batch, T, q_heads, D], k_new / v_new [batch, T, kv_heads, D] of the drafted tokens,
+    parent int32 [batch, T] (-1: the cache's last token, below: padding) -> out [batch, T, q_heads, D]."""
+    z, dev = _sizes_of(d), _device_of(q)
+    qp = _take(q, "q", z.act, None, dev)
+    T = q.numel() // z.q
+    if q.numel() != T * z.q:
+        raise ValueError("q must be [batch, T, q_heads, head_dim]")
+    if out is None:
+        out = torch.empty((z.B, T, z.H, z.D), dtype=z.act, device=q.device)
+    rc = lib().kvc_tree_attention(
+        ctypes.byref(d), _take_cache(z, cache, dev), layer, qp, _take(k_new, "k_new", z.act, z.kv * T, dev),
+        _take(v_new, "v_new", z.act, z.kv * T, dev), T, _take(pos0, "pos0", _INT32, z.B, dev),
+        _take(parent, "parent", _INT32, z.B * T, dev),
+        None if block_table is None else _take(block_table, "block_table", _INT32, z.table, dev),
+        None if valid_bits is None else _take(valid_bits, "valid_bits", _INT32, z.valid, dev),
+        _take(out, "out", z.act, z.q * T, dev), _take(workspace, "workspace", _UINT8, None, dev), workspace.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        raise KvcError(rc, "kvc_tree_attention")
     return out
 
 

@@ -1284,6 +1284,124 @@ KVC_API int kvc_block_evict(const kvc_desc* d, float* weights, const int32_t* po
     return launch_block_evict(p, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
+// What kvc_tree_attention takes of a descriptor and T.
+static int tree_desc(const kvc_desc* d, const Geo& g, int32_t T) {
+    if (d->dtype != KVC_BF16 || d->rope == KVC_ROPE_READ_INCACHE || g.G > 128) return KVC_ERR_UNSUPPORTED;
+    if (T < 1 || T > kTreeMax) return KVC_ERR_ARG;
+    // a window no shorter than the draft, so that a token attends all of its ancestors
+    if (d->layout != KVC_LAYOUT_PAGED && T > d->window) return KVC_ERR_UNSUPPORTED;
+    if (d->layout == KVC_LAYOUT_PAGED &&
+        (d->block_size % 8 || (d->block_size < 64 ? 64 % d->block_size : d->block_size % 64)))
+        return KVC_ERR_UNSUPPORTED;
+    if ((long long)d->batch * T * d->q_heads > 0x7fffffffLL) return KVC_ERR_UNSUPPORTED;
+    return KVC_OK;
+}
+
+// The columns of a draft of T tokens, and what kvc_tree_attention adds to the decode workspace, after it.
+struct TreeLayout {
+    int tq, mq, ncol, last_units, rows, alt_off;
+    size_t stage, part_ml, part_o, total;
+};
+static TreeLayout tree_layout(const kvc_desc* d, const Geo& g, int T) {
+    TreeLayout l{};
+    const int nq = tree_q_tiles(d->head_dim);
+    l.tq = 128 / g.G;
+    l.mq = l.tq * nq;
+    l.ncol = (T + l.mq - 1) / l.mq;
+    l.last_units = T - (l.ncol - 1) * l.mq <= l.tq ? 1 : nq;
+    const bool alt = nq == 2 && l.last_units == 1;
+    l.rows = l.ncol > 1 ? nq * 128 : (alt ? 2 : 1) * T * g.G;
+    l.alt_off = l.ncol > 1 ? 128 : T * g.G;
+    const size_t slots = (size_t)kTreeCtas + (size_t)d->batch * d->kv_heads * l.ncol;
+    l.stage = align_up(ws_layout(d, g).total, 256);
+    const size_t staged = d->rope == KVC_ROPE_BAKED ? (size_t)d->batch * T * d->kv_heads * d->head_dim * 2 : 0;
+    l.part_ml = align_up(l.stage + staged, 256);
+    l.part_o = align_up(l.part_ml + slots * l.rows * 8, 256);
+    l.total = align_up(l.part_o + slots * l.rows * d->head_dim * 4, 256);
+    return l;
+}
+
+KVC_API size_t kvc_tree_workspace_bytes(const kvc_desc* d, int32_t T) {
+    Geo g;
+    if (check_desc(d, &g) != KVC_OK || tree_desc(d, g, T) != KVC_OK) return 0;
+    return tree_layout(d, g, T).total;
+}
+
+KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t layer, const void* q, const void* k_new,
+                               const void* v_new, int32_t T, const int32_t* pos0, const int32_t* parent,
+                               const int32_t* block_table, const uint32_t* valid_bits, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    Geo g;
+    int rc = check_desc(d, &g);
+    if (rc) return rc;
+    if ((rc = tree_desc(d, g, T))) return rc;
+    if (!cache || !q || !k_new || !v_new || !pos0 || !parent || !out || !workspace) return KVC_ERR_NULL;
+    const bool paged = d->layout == KVC_LAYOUT_PAGED;
+    if (paged && !block_table) return KVC_ERR_NULL;
+    if (!aligned16(cache) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) ||
+        !aligned16(workspace) || (reinterpret_cast<uintptr_t>(parent) & 3u))
+        return KVC_ERR_ALIGN;
+    if (layer < 0 || layer >= d->layers) return KVC_ERR_ARG;
+    const TreeLayout l = tree_layout(d, g, T);
+    if (workspace_bytes < l.total) return KVC_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    TreeParams p{};
+    p.q = q;
+    p.k_new = k_new;
+    p.pos = pos0;
+    p.parent = parent;
+    p.table = block_table;
+    p.valid = valid_bits;
+    p.out = out;
+    p.stage = ws + l.stage;
+    p.err = reinterpret_cast<uint32_t*>(ws + ws_layout(d, g).err);
+    p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+    p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+    p.B = d->batch;
+    p.T = T;
+    p.Hq = d->q_heads;
+    p.Hkv = d->kv_heads;
+    p.G = g.G;
+    p.layer = layer;
+    p.layout = d->layout;
+    p.window = d->window;
+    p.sinks = d->layout == KVC_LAYOUT_SINK_RING ? d->sinks : 0;
+    p.capacity = g.C;
+    p.bs = d->block_size;
+    p.num_blocks = d->num_blocks;
+    p.maxb = d->max_blocks_per_seq;
+    p.tq = l.tq;
+    p.mq = l.mq;
+    p.ncol = l.ncol;
+    p.last_units = l.last_units;
+    p.col_units = (l.ncol - 1) * tree_q_tiles(d->head_dim) + l.last_units;
+    p.rows = l.rows;
+    p.alt_off = l.alt_off;
+    p.ctas = kTreeCtas;
+    p.rope = d->rope;
+    const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
+    p.scale2 = scale * 1.4426950408889634f;
+    const bool baked = d->rope == KVC_ROPE_BAKED;
+    if (baked) fill_theta(d->head_dim, d->rope_base, p.theta, nullptr);
+    // the maps, encoded before anything is launched
+    TreeMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (paged) {
+        if ((rc = encode_block_map(d, g, cache, &maps.cache))) return rc;
+    } else {
+        KvTensorMaps km;
+        if ((rc = kv_maps_for(d, g, cache, &km, &p.slot_whole))) return rc;
+        maps.cache = km.run[kRunMaps - 1];              // 64-row runs
+    }
+    if ((rc = encode_rows_map(d, baked ? p.stage : k_new, T, &maps.k)) || (rc = encode_rows_map(d, v_new, T, &maps.v)))
+        return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if ((baked && launch_tree_stage(d->head_dim, p, s) != cudaSuccess) ||
+        launch_tree(d->head_dim, p, maps, s) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    return KVC_OK;
+}
+
 KVC_API int kvc_append_path(const kvc_desc* d, void* cache, int32_t layer, const void* k_new, const void* v_new,
                             int32_t T, const int32_t* pos0, const int32_t* path, int32_t P, const int32_t* n_path,
                             const int32_t* block_table, void* workspace, size_t workspace_bytes, void* stream) {

@@ -1,0 +1,922 @@
+// kvc_tree_attention: attention of a tree of drafted tokens over a cache, as a
+// step of speculative decoding verifies it.  Token i of sequence b continues
+// token parent[i] (-1: the sequence itself); it stands at position
+// t = pos0 + its depth and attends what a token there attends in the cache, its
+// ancestors in the draft and itself.
+//
+// The (token, q head of the group) pairs of a kv head are the rows of one matrix
+// product with the keys of that head, so the cache is read once for the whole
+// draft.  A column is (sequence, kv head, up to NQ x 128 rows); its keys are cut
+// into tiles of 64, the last tile the draft's own rows under the mask of
+// ancestors.  A unit of work is a tile for one Q tile; all units of all columns,
+// laid end to end, are split into nearly equal contiguous shares, one per CTA (one
+// CTA per SM), so that one long sequence fills the GPU as a batch does.  The part of
+// a column in a share is a segment and leaves one partial (m, l, o) per row;
+// tree_combine_kernel joins them:  M = max m_i,
+// out = sum o_i 2^(m_i - M) / sum l_i 2^(m_i - M).
+//
+// Roles of a CTA's warps: 0 brings tiles in by TMA; 2 zeroes the V rows without a
+// key (they may hold anything); 1 and 3 issue the products of a Q tile each,
+// S = Q K^T a tile ahead of O += P V, accumulators in tensor memory; a warpgroup a
+// Q tile does the softmax, a thread a row.  A column of one Q tile gives both
+// warpgroups the same rows and alternate tiles, with sums of their own.
+// What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for
+// 4 x 64 x 128 x D flops a Q tile: bytes up to one Q tile, the softmax beyond.
+#include <atomic>
+
+#include "kvc_decode.cuh"
+#include "kvc_tc.cuh"
+#include "kvc_tree.h"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kTrSoftmax0 = 4;              // first softmax warp
+constexpr float kTrLazy = 8.f;              // the reference maximum moves when a tile's exceeds it by more
+
+__device__ __forceinline__ void tr_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void tr_pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <int D>
+struct TrShape {
+    static constexpr int NQ = tree_q_tiles(D);
+    static constexpr int STAGES = D == 64 ? 6 : (D == 128 ? 4 : 2);
+    static constexpr int CB = D / 64;                          // 64-column blocks of a row
+    static constexpr int QBytes = kWsRows * D * 2;             // one Q tile
+    static constexpr int KVBlock = 2 * kWsKeys * 128;          // one column block of K and V
+    static constexpr int StageBytes = CB * KVBlock;
+    static constexpr int OffQ = 0;
+    static constexpr int OffStage = OffQ + NQ * QBytes;
+    static constexpr int OffMeta = OffStage + STAGES * StageBytes;
+    static constexpr int TmemCols = 512;
+    static constexpr int SCol0 = NQ * D;                       // S buffers after the O tiles
+    static_assert(NQ * D + NQ * 2 * kWsKeys <= TmemCols, "TMEM columns");
+    static constexpr int Threads = 32 * (kTrSoftmax0 + 4 * NQ);
+};
+
+// kTileOpen: every key of the tile that is there is attended by every token;
+// kTileWindow: each row's window cuts it; kTileDraft: the draft's own rows.
+enum : int { kTileOpen = 0, kTileWindow = 1, kTileDraft = 2 };
+
+struct alignas(16) TrStageMeta {
+    unsigned long long present;     // rows of the tile that hold a key
+    int kind;
+    int slot0;                      // kTileWindow: slot of the tile's first row
+};
+
+struct TrBars {
+    uint64_t full[6], ready[6], empty[6];
+    uint64_t s_full[2][2], p_full[2], o_done[2], q_ready[2], fin[2];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int D>
+constexpr int tr_smem_bytes() {
+    using S = TrShape<D>;
+    return S::OffMeta + S::STAGES * (int)sizeof(TrStageMeta) + (int)sizeof(TrBars) + 1024;
+}
+
+// Cached rows of sequence b: live slots of a window layout, positions of a paged one.
+__device__ __forceinline__ int tr_cached(const TreeParams& p, int pos) {
+    if (pos <= 0) return 0;
+    if (p.layout != kPaged) return pos < p.capacity ? pos : p.capacity;
+    const long long lim = (long long)p.maxb * p.bs;
+    return pos < lim ? pos : (int)lim;
+}
+__device__ __forceinline__ int tr_tiles(const TreeParams& p, int pos) { return (tr_cached(p, pos) + kWsKeys - 1) / kWsKeys + 1; }
+__device__ __forceinline__ long long tr_seq_units(const TreeParams& p, int pos) {
+    return (long long)tr_tiles(p, pos) * p.col_units * p.Hkv;
+}
+
+// Units of all sequences, and of those before b (a whole warp's call).
+__device__ __forceinline__ void tr_partition(const TreeParams& p, int b, long long* total, long long* before) {
+    const int lane = threadIdx.x & 31;
+    long long tot = 0, pre = 0;
+    for (int base = 0; base < p.B; base += 32) {
+        const int o = base + lane;
+        const long long u = o < p.B ? tr_seq_units(p, __ldg(p.pos + o)) : 0;
+        tot += u;
+        if (o < b) pre += u;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        tot += __shfl_xor_sync(0xffffffffu, tot, off);
+        pre += __shfl_xor_sync(0xffffffffu, pre, off);
+    }
+    *total = tot;
+    *before = pre;
+}
+
+__device__ __forceinline__ int tr_shares(const TreeParams& p, long long units) {
+    const long long s = (units + kTreeMinTiles - 1) / kTreeMinTiles;
+    return (int)(s < p.ctas ? s : p.ctas);
+}
+
+// Where a share stands: the sequence and the units before it.
+struct TrWalk {
+    int b;
+    long long before;
+};
+// The sequence that holds unit u (a whole warp's call).
+__device__ __forceinline__ TrWalk tr_find(const TreeParams& p, long long u) {
+    const int lane = threadIdx.x & 31;
+    TrWalk w{0, 0};
+    long long run = 0;
+    for (int base = 0; base < p.B; base += 32) {
+        const int o = base + lane;
+        const long long n = o < p.B ? tr_seq_units(p, __ldg(p.pos + o)) : 0;
+        long long incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long a = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += a;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, o < p.B && run + incl > u);
+        if (in) {
+            const int src = __ffs(in) - 1;
+            w.b = base + src;
+            w.before = run + __shfl_sync(0xffffffffu, incl - n, src);
+            return w;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    w.b = p.B - 1;                                  // (not reached: u lies below the total)
+    return w;
+}
+
+// One segment: tiles tile0 .. tile0 + nt - 1 of a column.
+struct TrSegment {
+    int b, h, pos, n0, tokens;                 // sequence, kv head, its tokens in the cache; first token and tokens of the column
+    int kt;                                    // tiles of the column, the last of them the draft
+    int tile0, nt;                             // nt may be 0: one unit of a tile that begins in the share before
+    long long units;
+    int alt;                                   // one Q tile's rows: the warpgroups take alternate tiles
+    long long col;                             // index of the column
+    __device__ __forceinline__ int tiles(int i) const { return alt ? (nt + 1 - i) >> 1 : nt; }
+};
+
+// The segment that begins at unit u of a share ending at hi.
+template <int D>
+__device__ __forceinline__ TrSegment tr_segment(const TreeParams& p, TrWalk& w, long long u, long long hi) {
+    TrSegment s;
+    s.pos = __ldg(p.pos + w.b);
+    for (long long n = tr_seq_units(p, s.pos); u >= w.before + n && w.b < p.B - 1;) {
+        w.before += n;
+        s.pos = __ldg(p.pos + ++w.b);
+        n = tr_seq_units(p, s.pos);
+    }
+    s.b = w.b;
+    s.kt = tr_tiles(p, s.pos);
+    const long long hu = (long long)s.kt * p.col_units;
+    long long v = u - w.before;
+    s.h = (int)div_nonneg(v, hu);
+    v -= s.h * hu;
+    constexpr int NQ = TrShape<D>::NQ;
+    int m = (int)div_nonneg(v, (long long)s.kt * NQ);          // every column but a head's last has NQ Q tiles
+    if (m > p.ncol - 1) m = p.ncol - 1;
+    v -= (long long)m * s.kt * NQ;
+    s.n0 = m * p.mq;
+    s.tokens = min(p.mq, p.T - s.n0);
+    // units to tiles: a tile belongs to the share that holds its first unit
+    const int per = m < p.ncol - 1 ? NQ : p.last_units;
+    const long long take = min((long long)s.kt * per - v, hi - u);
+    s.units = take;
+    s.tile0 = (int)((v + per - 1) / per);
+    s.nt = (int)((v + take + per - 1) / per) - s.tile0;
+    s.alt = NQ == 2 && per == 1;
+    s.col = ((long long)s.b * p.Hkv + s.h) * p.ncol + m;
+    return s;
+}
+
+// The draft of sequence b, by a whole warp: lane l holds tokens l and l + 32, each
+// with the tokens it attends in the draft (itself and its ancestors; 0: not a
+// token, nor is what continues it).  Ancestors by doubling: after k rounds a token
+// knows those up to 2^k steps above it.
+struct TrDraft {
+    unsigned long long see[2];
+    __device__ __forceinline__ unsigned long long of(int t) const {
+        const unsigned long long a = __shfl_sync(0xffffffffu, see[0], t & 31), c = __shfl_sync(0xffffffffu, see[1], t & 31);
+        return t < 32 ? a : c;
+    }
+};
+__device__ __forceinline__ TrDraft tr_draft(const TreeParams& p, int b, int pos, bool report) {
+    const int lane = threadIdx.x & 31;
+    TrDraft d;
+    int up[2];                                  // the token above those in `see`; -1: the sequence, -2: none
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = lane + 32 * e;
+        int par = -2;
+        if (i < p.T && pos >= 0) {
+            par = __ldg(p.parent + (long long)b * p.T + i);
+            if (par >= i) {
+                if (report) set_error(p.err, 0x10u /* KVC_DEV_BAD_ENTRY */);
+                par = -2;
+            }
+            if (par < -2) par = -2;
+        }
+        up[e] = par;
+        d.see[e] = 1ull << i;
+    }
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+        unsigned long long more[2];
+        int next[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int src = up[e] & 31;
+            const unsigned long long a = __shfl_sync(0xffffffffu, d.see[0], src), c = __shfl_sync(0xffffffffu, d.see[1], src);
+            const int x = __shfl_sync(0xffffffffu, up[0], src), y = __shfl_sync(0xffffffffu, up[1], src);
+            more[e] = up[e] < 0 ? 0ull : (up[e] < 32 ? a : c);
+            next[e] = up[e] < 0 ? up[e] : (up[e] < 32 ? x : y);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            d.see[e] |= more[e];
+            up[e] = next[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (up[e] != -1) d.see[e] = 0ull;
+    return d;
+}
+
+// Bits lo .. hi of a word.
+__device__ __forceinline__ unsigned long long tr_bits(int lo, int hi) {
+    if (lo < 0) lo = 0;
+    if (hi > 63) hi = 63;
+    if (lo > hi) return 0ull;
+    return (~0ull >> (63 - hi)) & (~0ull << lo);
+}
+
+// Age of the newest position at ring slot s >= sinks when pos tokens are cached (0: the last of them).
+__device__ __forceinline__ int tr_age(const TreeParams& p, int pos, int s) {
+    const int a = (int)(((long long)pos - 1 - s) % p.window);
+    return a < 0 ? a + p.window : a;
+}
+
+// Keys of the tile of slots slot0 .. slot0 + 63 that the token at depth `depth`
+// attends: sinks, and ages up to window - 2 - depth.  Ages fall by one a slot and
+// go from 0 to window - 1 at one place.
+__device__ __forceinline__ unsigned long long tr_window(const TreeParams& p, int pos, int slot0, int depth) {
+    const int ks = max(0, p.sinks - slot0);
+    if (ks >= 64) return ~0ull;
+    const int a = tr_age(p, pos, slot0 + ks), lim = p.window - 2 - depth;
+    return tr_bits(0, ks - 1) | tr_bits(ks + max(0, a - lim), min((long long)ks + a, 63LL)) |
+           ((long long)ks + a + p.window - lim > 63 ? 0ull : tr_bits(ks + a + p.window - lim, 63));
+}
+
+// Eight rotation pairs (elements of lo with those of hi) of a bf16 row at `pos`.
+__device__ __forceinline__ void tr_rotate8(uint4& lo, uint4& hi, long long pos, const unsigned long long* turns) {
+    uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float y[2], z[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const float x1 = __uint_as_float(w ? a[e] & 0xffff0000u : a[e] << 16);
+            const float x2 = __uint_as_float(w ? b[e] & 0xffff0000u : b[e] << 16);
+            float cs, sn;
+            rope_cos_sin(pos, turns[2 * e + w], &cs, &sn);
+            y[w] = x1 * cs - x2 * sn;
+            z[w] = x1 * sn + x2 * cs;
+        }
+        a[e] = pack_bf16x2(y[0], y[1]);
+        b[e] = pack_bf16x2(z[0], z[1]);
+    }
+    lo = make_uint4(a[0], a[1], a[2], a[3]);
+    hi = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// BAKED: the draft's keys as the cache would store them, rotated at pos0 + depth.
+// One CTA per sequence.
+template <int D>
+__global__ void __launch_bounds__(256) tree_stage_kernel(const __grid_constant__ TreeParams p) {
+    __shared__ int s_depth[kTreeMax];
+    tr_pdl_wait();
+    tr_pdl_launch();
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int pos = __ldg(p.pos + b);
+    if (tid < 32) {
+        const TrDraft d = tr_draft(p, b, pos, false);
+        s_depth[lane] = __popcll(d.see[0]) - 1;
+        s_depth[lane + 32] = __popcll(d.see[1]) - 1;
+    }
+    __syncthreads();
+    constexpr int UPH = D / 16;
+    const int units = p.T * p.Hkv * UPH;
+    for (int u = tid; u < units; u += 256) {
+        const int c = (u % UPH) * 8, row = u / UPH, t = row / p.Hkv;
+        if (s_depth[t] < 0) continue;
+        const long long at = ((long long)b * p.T * p.Hkv + row) * D + c;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k_new) + at;
+        uint4 x = __ldg(reinterpret_cast<const uint4*>(src)), y = __ldg(reinterpret_cast<const uint4*>(src + D / 2));
+        tr_rotate8(x, y, (long long)pos + s_depth[t], p.theta + c);
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.stage) + at;
+        *reinterpret_cast<uint4*>(dst) = x;
+        *reinterpret_cast<uint4*>(dst + D / 2) = y;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TrShape<D>::Threads, 1)
+    tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
+    using S = TrShape<D>;
+    constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
+    extern __shared__ unsigned char tr_raw[];
+    const uint32_t raw_u = smem_u32(tr_raw);
+    unsigned char* sm = tr_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
+    const uint32_t sm_u = smem_u32(sm);
+    TrStageMeta* meta = reinterpret_cast<TrStageMeta*>(sm + S::OffMeta);
+    TrBars* bars = reinterpret_cast<TrBars*>(sm + S::OffMeta + NST * sizeof(TrStageMeta));
+    volatile int* abort = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->ready[s], 1);
+            mbar_init(&bars->empty[s], NQ);
+        }
+        for (int i = 0; i < 2; ++i) {
+            for (int u = 0; u < 2; ++u) mbar_init(&bars->s_full[i][u], 1);
+            mbar_init(&bars->p_full[i], 4);
+            mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->q_ready[i], 4);
+            mbar_init(&bars->fin[i], 1);
+        }
+        bars->abort = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&maps.cache);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
+    tr_pdl_wait();
+    tr_pdl_launch();
+    long long units, unused;
+    tr_partition(p, 0, &units, &unused);
+    const int shares = tr_shares(p, units), x = blockIdx.x;
+    if (x >= shares) return;                         // (uniform: before the tensor memory is taken)
+    const long long lo = div_nonneg((long long)x * units, shares), hi = div_nonneg((long long)(x + 1) * units, shares);
+    TrWalk walk = tr_find(p, lo);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem)),
+                     "r"(S::TmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    ws_fence_before();
+    __syncthreads();
+    ws_fence_after();
+    const uint32_t tmem = bars->tmem;
+    auto give_up = [&]() {
+        if (!*abort) {
+            bars->abort = 1;
+            set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+        }
+    };
+
+    if (warp == 0) {
+        // ============================ producer ==============================
+        int idx = 0;
+        bool ok = true;
+        const bool paged = p.layout == kPaged;
+        const int bs = p.bs;
+        const int box = !paged || bs > kWsKeys ? kWsKeys : bs;  // rows of one copy
+        const int per = kWsKeys / box;                          // copies of a tile
+        auto take_stage = [&](int s) -> bool {
+            if (idx < NST || ws_wait(&bars->empty[s], ((idx / NST) - 1) & 1, abort)) return true;
+            if (lane == 0) give_up();
+            return ok = false;
+        };
+        for (long long u = lo; u < hi && ok;) {
+            const TrSegment sg = tr_segment<D>(p, walk, u, hi);
+            const int n = tr_cached(p, sg.pos);
+            if (paged && n < sg.pos && lane == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
+            const int32_t* trow = p.table + (long long)sg.b * p.maxb;
+            const int ncopy = (n + box - 1) / box;
+            const int end = min(sg.tile0 + sg.nt, sg.kt - 1);   // past the segment's cached tiles
+            // 32 copies at a time, one per lane: 32 / per tiles
+            for (int t0 = sg.tile0; t0 < end && ok; t0 += 32 / per) {
+                const int cp = t0 * per + lane;                 // this lane's copy: rows cp * box ..
+                int row = -1;
+                if (cp < ncopy) {
+                    const int r0 = cp * box;
+                    if (paged) {
+                        const int lb = r0 / bs;
+                        const int phys = __ldg(trow + lb);
+                        bool att = phys >= 0;
+                        if (phys >= p.num_blocks) {
+                            set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+                            att = false;
+                        }
+                        if (att && p.valid) att = (__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u;
+                        if (att) row = (int)(((long long)phys * p.Hkv + sg.h) * bs + (r0 - lb * bs));
+                    } else {
+                        row = (int)(((long long)sg.b * p.Hkv + sg.h) * p.capacity + r0);
+                    }
+                }
+                const unsigned have = __ballot_sync(0xffffffffu, row >= 0);
+                for (int k = 0; k < 32 / per && t0 + k < end; ++k) {
+                    const int s = idx % NST;
+                    if (!take_stage(s)) break;
+                    const unsigned mine = (have >> (k * per)) & ((per == 32) ? 0xffffffffu : ((1u << per) - 1u));
+                    const int j = lane - k * per;
+                    if (j >= 0 && j < per && row >= 0) {
+                        mbar_expect_tx(&bars->full[s], (uint32_t)(box * D * 4));
+                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes + j * box * 128;
+                        if (paged) {
+#pragma unroll
+                            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                                for (int kv = 0; kv < 2; ++kv)
+                                    tma_load_4d(dst + cb * S::KVBlock + kv * kWsKeys * 128, &maps.cache, cb * 64, row, kv,
+                                                p.layer, &bars->full[s]);
+                        } else if (p.slot_whole) {
+                            tma_load_5d(dst, &maps.cache, 0, row, 0, p.layer, 0, &bars->full[s]);
+                        } else {
+#pragma unroll
+                            for (int cb = 0; cb < CB; ++cb)
+                                tma_load_4d(dst + cb * S::KVBlock, &maps.cache, cb * 64, row, 0, p.layer, &bars->full[s]);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int s0 = (t0 + k) * kWsKeys, live = min(n - s0, kWsKeys);
+                        unsigned long long present = 0;
+                        for (int c = 0; c < per; ++c)
+                            if ((mine >> c) & 1u) present |= (box == 64 ? ~0ull : ((1ull << box) - 1)) << (c * box);
+                        present &= tr_bits(0, live - 1);
+                        int kind = kTileOpen;
+                        if (!paged) {
+                            // open if even the deepest token's window holds the oldest of its rows
+                            const int ks = max(0, p.sinks - s0);
+                            if (ks < live) {
+                                const int a = tr_age(p, sg.pos, s0 + ks);
+                                if (a < live - 1 - ks || a > p.window - 1 - p.T) kind = kTileWindow;
+                            }
+                        }
+                        meta[s].present = present;
+                        meta[s].kind = kind;
+                        meta[s].slot0 = s0;
+                        mbar_arrive(&bars->full[s]);
+                    }
+                    ++idx;
+                }
+            }
+            if (ok && sg.nt > 0 && sg.tile0 + sg.nt == sg.kt) {
+                // the draft's own rows
+                const TrDraft d = tr_draft(p, sg.b, sg.pos, true);
+                const unsigned r0 = __ballot_sync(0xffffffffu, d.see[0] != 0ull), r1 = __ballot_sync(0xffffffffu, d.see[1] != 0ull);
+                const int s = idx % NST;
+                if (take_stage(s)) {
+                    if (lane == 0) {
+                        mbar_expect_tx(&bars->full[s], (uint32_t)S::StageBytes);
+                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes;
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) {
+                            tma_load_3d(dst + cb * S::KVBlock, &maps.k, cb * 64, sg.h, sg.b * p.T, &bars->full[s]);
+                            tma_load_3d(dst + cb * S::KVBlock + kWsKeys * 128, &maps.v, cb * 64, sg.h, sg.b * p.T,
+                                        &bars->full[s]);
+                        }
+                        meta[s].present = (unsigned long long)r0 | ((unsigned long long)r1 << 32);
+                        meta[s].kind = kTileDraft;
+                        meta[s].slot0 = 0;
+                        mbar_arrive(&bars->full[s]);
+                    }
+                    ++idx;
+                }
+                __syncwarp();
+            }
+            u += sg.units;
+        }
+        // never leave with copies landing in shared memory
+        if (!ok && lane == 0)
+            for (int k = (idx > NST ? idx - NST : 0); k < idx; ++k) mbar_wait(&bars->full[k % NST], (k / NST) & 1);
+    } else if (warp == 2) {
+        // ============================ fix-up ===============================
+        int j = 0;
+        bool ok = true;
+        for (long long u = lo; u < hi && ok;) {
+            const TrSegment sg = tr_segment<D>(p, walk, u, hi);
+            u += sg.units;
+            for (const int end = j + sg.nt; j < end; ++j) {
+                const int s = j % NST;
+                if (!ws_wait(&bars->full[s], (j / NST) & 1, abort)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const unsigned long long present = meta[s].present;
+                if (present != ~0ull) {
+#pragma unroll 1
+                    for (int r = lane; r < kWsKeys; r += 32) {
+                        if ((present >> r) & 1ull) continue;
+                        unsigned char* st = sm + S::OffStage + s * S::StageBytes + kWsKeys * 128 + r * 128;
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                            for (int ch = 0; ch < 8; ++ch)
+                                *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->ready[s]);
+            }
+        }
+    } else if (warp == 1 || (NQ == 2 && warp == 3)) {
+        // ========================== MMA issuers =============================
+        // One warp for each Q tile: S_i = Q_i K^T a tile ahead of O_i += P_i V.  The
+        // whole warp walks the tiles, its values stay uniform; lane 0 issues.
+        const int i = warp >> 1;
+        bool ok = true;
+        int idx0 = 0, base = 0, loads = 0;             // tiles of the segments before; of this Q tile; its loads
+        const uint64_t qd = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
+        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
+        const uint32_t s0 = tmem + S::SCol0 + (uint32_t)(i * 2 * kWsKeys), o_t = tmem + (uint32_t)(i * D);
+        for (long long u = lo; u < hi && ok;) {
+            const TrSegment sg = tr_segment<D>(p, walk, u, hi);
+            const int own = sg.tiles(i), others = sg.nt - own;
+            if (own > 0) {
+                ok = ws_wait(&bars->q_ready[i], loads & 1, abort);
+                ++loads;
+            }
+            int ns = 0, npv = 0, nother = 0;           // S issued, P V issued, the other Q tile's tiles passed
+            long long t0 = clock64();
+            while (ok && (npv < own || nother < others)) {
+                // (each barrier's phases are asked for in order)
+                if (ns < own && ns < npv + 2) {
+                    const int t = idx0 + (sg.alt ? 2 * ns + i : ns), s = t % NST;
+                    if (ws_test(&bars->ready[s], (t / NST) & 1)) {
+                        ws_fence_after();
+                        if (lane == 0) {
+                            ws_issue_s<D, kWsRows * 128, S::KVBlock>(s0 + (uint32_t)(((base + ns) & 1) * kWsKeys), qd,
+                                                                     kd0 + (uint64_t)((s * S::StageBytes) >> 4));
+                            ws_commit(&bars->s_full[i][(base + ns) & 1]);
+                        }
+                        __syncwarp();
+                        ++ns;
+                        t0 = clock64();
+                        continue;
+                    }
+                }
+                if (npv < ns && ws_test(&bars->p_full[i], (base + npv) & 1)) {
+                    ws_fence_after();
+                    const int t = idx0 + (sg.alt ? 2 * npv + i : npv), s = t % NST;
+                    if (lane == 0) {
+                        // P_i in the S buffer it came from (bf16 pairs)
+                        ws_issue_pv<D>(o_t, s0 + (uint32_t)(((base + npv) & 1) * kWsKeys),
+                                       vd0 + (uint64_t)((s * S::StageBytes) >> 4), npv > 0);
+                        ws_commit(&bars->o_done[i]);
+                        ws_commit(&bars->empty[s]);        // this Q tile is done with the tile's K and V
+                    }
+                    __syncwarp();
+                    ++npv;
+                    t0 = clock64();
+                    continue;
+                }
+                if (nother < others) {
+                    const int t = idx0 + 2 * nother + (i ^ 1), s = t % NST;
+                    if (ws_test(&bars->ready[s], (t / NST) & 1)) {
+                        if (lane == 0) mbar_arrive(&bars->empty[s]);
+                        __syncwarp();
+                        ++nother;
+                        t0 = clock64();
+                        continue;
+                    }
+                }
+                if (*abort || clock64() - t0 > kWaitCycles) ok = false;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok && lane == 0) give_up();
+            __syncwarp();
+            idx0 += sg.nt;
+            base += own;
+            u += sg.units;
+        }
+        if (lane == 0) {
+            // every product this thread issued is done before TMEM is freed
+            ws_commit(&bars->fin[i]);
+            if (!mbar_wait(&bars->fin[i], 0)) set_error(p.err, 0x8u /* KVC_DEV_TIMEOUT */);
+        }
+        __syncwarp();
+    } else if (warp >= kTrSoftmax0) {
+        // ============================ softmax ==============================
+        const int qi = (warp - kTrSoftmax0) >> 2;          // Q tile
+        const int r = tid - (kTrSoftmax0 + 4 * qi) * 32;   // row = TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
+        const int tl = r / p.G;
+        bool ok = true;
+        int idx0 = 0, base = 0, at_b = -1;
+        TrDraft draft{};
+        for (long long u = lo; u < hi && ok;) {
+            const TrSegment sg = tr_segment<D>(p, walk, u, hi);
+            if (sg.b != at_b) {
+                draft = tr_draft(p, sg.b, sg.pos, false);
+                at_b = sg.b;
+            }
+            const int c0 = sg.alt ? 0 : qi * p.tq;         // the Q tile's first token in the column
+            const bool row_ok = tl < p.tq && c0 + tl < sg.tokens;
+            const unsigned long long see = draft.of(row_ok ? sg.n0 + c0 + tl : 0);
+            const bool real = row_ok && see != 0ull;
+            const int depth = __popcll(see) - 1;
+            const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
+            // Q rows, rotated at their positions when BAKED, unscaled bf16
+            if (nt > 0) {
+                // (D / 16 lanes share a row: a load covers whole lines)
+                constexpr int LPR = D / 16, RPW = 32 / LPR;
+                const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
+#pragma unroll 4
+                for (int it = 0; it < 32 / RPW; ++it) {
+                    const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
+                    const int rtl = rr / p.G;
+                    const bool rok = rtl < p.tq && c0 + rtl < sg.tokens;
+                    const int t = sg.n0 + c0 + rtl;
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                    if (rok) {
+                        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
+                                                    (((long long)sg.b * p.T + t) * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
+                        a = __ldg(reinterpret_cast<const uint4*>(qrow + 8 * c));
+                        b = __ldg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
+                    }
+                    if (p.rope != kRopeNone) {
+                        const unsigned long long mine = draft.of(rok ? t : 0);
+                        if (rok) tr_rotate8(a, b, (long long)sg.pos + max(__popcll(mine) - 1, 0), p.theta + 8 * c);
+                    }
+                    // Q tile: [column block][128 rows][128 B], 128-byte swizzle
+                    const int c1 = c, c2 = c + D / 16;
+                    *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = a;
+                    *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->q_ready[qi]);
+            }
+            float m_run = -INFINITY, l_run = 0.f;          // m in base-2 units of the scaled scores
+            for (int lt = 0; lt < nt; ++lt) {
+                const int j = base + lt;
+                if (!ws_wait(&bars->s_full[qi][j & 1], (j >> 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                ws_fence_after();
+                float sv[kWsKeys];
+                const uint32_t scol = S::SCol0 + (uint32_t)((qi * 2 + (j & 1)) * kWsKeys);
+                ws_ld32(lane_base + scol, sv);
+                ws_ld32(lane_base + scol + 32, sv + 32);
+                ws_wait_ld();
+                const int gt = idx0 + (sg.alt ? 2 * lt + qi : lt);
+                if (!ws_wait(&bars->ready[gt % NST], (gt / NST) & 1, abort)) {    // the stage's meta
+                    ok = false;
+                    break;
+                }
+                const TrStageMeta mt = meta[gt % NST];
+                unsigned long long vis = mt.present;
+                if (mt.kind == kTileDraft)
+                    vis &= see;
+                else if (mt.kind == kTileWindow)
+                    vis &= tr_window(p, sg.pos, mt.slot0, depth);
+                if (__any_sync(0xffffffffu, vis != ~0ull)) {
+                    const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                    for (int k = 0; k < kWsKeys; ++k)
+                        sv[k] = (((k < 32 ? v0 : v1) >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
+                }
+                const float mx = ws_max64(sv) * p.scale2;
+                float mn = m_run, alpha = 1.f;
+                if (mx > m_run + kTrLazy) {
+                    mn = mx;
+                    alpha = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+                }
+                const float ls = ws_exp64(sv, p.scale2, mn == -INFINITY ? 0.f : -mn);
+                l_run = l_run * alpha + ls;
+                m_run = mn;
+                // P V of the previous tile is done: O is free
+                if (lt > 0 && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (lt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    ws_fence_after();
+#pragma unroll 1
+                    for (int c4 = 0; c4 < D / 32; ++c4) {
+                        float ov[32];
+                        ws_ld32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
+                        ws_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+                        ws_st32(lane_base + (uint32_t)(qi * D + 32 * c4), ov);
+                    }
+                    ws_wait_st();
+                }
+                {
+                    float pw[kWsKeys / 2];
+#pragma unroll
+                    for (int k2 = 0; k2 < kWsKeys / 2; ++k2)
+                        pw[k2] = __uint_as_float(pack_bf16x2(sv[2 * k2], sv[2 * k2 + 1]));
+                    ws_st32(lane_base + scol, pw);
+                }
+                ws_wait_st();
+                ws_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[qi]);
+            }
+            if (!ok) {
+                give_up();
+                break;
+            }
+            // the last P V, then the partial (m, l, o) of each row
+            if (nt > 0) {
+                if (!ws_wait(&bars->o_done[qi], (base + nt - 1) & 1, abort)) {
+                    give_up();
+                    break;
+                }
+                ws_fence_after();
+            }
+            const long long row_a = (x + sg.col) * p.rows + (sg.alt ? qi * p.alt_off : qi * p.tq * p.G);
+            if (row_ok) p.part_ml[row_a + r] = real ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
+            if (nt > 0) {
+                // through the Q tile's shared memory (its products are done), each row in the
+                // place of its own q (which this warp alone writes), CP columns at a time, so
+                // that whole lines go out
+                constexpr int CP = D == 64 ? 32 : 64, CPL = CP / 4;            // 16-byte chunks of a staged row
+                auto stg = [&](int row, int ch) {
+                    return reinterpret_cast<float4*>(Qs + (ch >> 3) * (kWsRows * 128) + row * 128 + (((ch ^ row) & 7) << 4));
+                };
+#pragma unroll 1
+                for (int c6 = 0; c6 < D / CP; ++c6) {
+#pragma unroll
+                    for (int hf = 0; hf < CP / 32; ++hf) {
+                        float ov[32];
+                        ws_ld32(lane_base + (uint32_t)(qi * D + CP * c6 + 32 * hf), ov);
+                        ws_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *stg(r, 8 * hf + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int it = 0; it < CPL; ++it) {
+                        const int rr = (warp & 3) * 32 + (32 / CPL) * it + lane / CPL, ch = lane % CPL;
+                        const int rtl = rr / p.G;
+                        if (rtl < p.tq && c0 + rtl < sg.tokens)
+                            *reinterpret_cast<float4*>(p.part_o + (row_a + rr) * D + CP * c6 + 4 * ch) = *stg(rr, ch);
+                    }
+                    __syncwarp();
+                }
+                // O is read: the next segment's first product may overwrite it
+                // (it waits for this warpgroup's next P)
+                ws_fence_before();
+            }
+            idx0 += sg.nt;
+            base += nt;
+            u += sg.units;
+        }
+    }
+
+    // the MMA thread has waited for all of its products (its last commit)
+    ws_fence_before();
+    __syncthreads();
+    ws_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TmemCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// combine
+// ---------------------------------------------------------------------------
+constexpr int kTrCombineWarps = 8;
+
+// One warp per (sequence, token, q head): lane l holds D / 32 columns.  The parts
+// are the shares of its column (two each when its warpgroups took alternate tiles).
+template <int D>
+__global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int NC = D / 32, NQ = TrShape<D>::NQ;
+    tr_pdl_launch();
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * kTrCombineWarps + (threadIdx.x >> 5);
+    const bool mine = w < (long long)p.B * p.T * p.Hq;
+    const int qh = (int)(w % p.Hq), t = (int)(w / p.Hq % p.T), b = mine ? (int)(w / p.Hq / p.T) : 0;
+    tr_pdl_wait();
+    if (!mine) return;
+    long long units, before;
+    tr_partition(p, b, &units, &before);
+    const int shares = tr_shares(p, units), kt = tr_tiles(p, __ldg(p.pos + b));
+    const int h = qh / p.G, m = t / p.mq, tc = t - m * p.mq;              // its column, and token of the column
+    const int per = m < p.ncol - 1 ? NQ : p.last_units;
+    const bool alt = NQ == 2 && per == 1;
+    const long long u0 = before + (long long)kt * p.col_units * h + (long long)m * kt * NQ;
+    const int fx = streamk_share_of(u0, units, shares);
+    const int np = (streamk_share_of(u0 + (long long)kt * per - 1, units, shares) - fx + 1) * (alt ? 2 : 1);
+    const long long slot0 = fx + ((long long)b * p.Hkv + h) * p.ncol + m;
+    const int row = tc * p.G + qh % p.G;                                  // (a Q tile has tq G rows)
+    auto part = [&](int k) -> long long {
+        return alt ? (slot0 + (k >> 1)) * p.rows + (k & 1) * p.alt_off + row : (slot0 + k) * p.rows + row;
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(p.part_ml + part(k)).x);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f, acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+    for (int base = 0; base < np; base += 32) {
+        float e = 0.f;
+        if (base + lane < np) {
+            const float2 v = __ldcg(p.part_ml + part(base + lane));
+            if (v.x != -INFINITY || v.y != v.y) {      // (NaN scores leave no maximum, but a sum of NaN)
+                e = exp2f(v.x - M);
+                L += v.y * e;
+            }
+        }
+        const int cnt = min(32, np - base);
+        // eight parts' loads in flight; an empty part's o may hold anything: not read
+        constexpr int U = NC == 8 ? 4 : 8;
+        for (int k0 = 0; k0 < cnt; k0 += U) {
+            float v[U][NC], ek[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                ek[u] = __shfl_sync(0xffffffffu, e, (k0 + u) & 31);
+                if (k0 + u >= cnt) ek[u] = 0.f;
+                const float* o = p.part_o + part(base + k0 + u) * D + lane * NC;
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) {
+                    float2 w2 = make_float2(0.f, 0.f);
+                    if (ek[u] != 0.f) w2 = __ldcg(reinterpret_cast<const float2*>(o + c));
+                    v[u][c] = w2.x;
+                    v[u][c + 1] = w2.y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[c] = fmaf(v[u][c], ek[u], acc[c]);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + w * D + lane * NC;
+#pragma unroll
+    for (int c = 0; c < NC; c += 2)
+        *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+}
+
+cudaLaunchConfig_t tr_config(dim3 grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int D>
+cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_t stream) {
+    constexpr int kSmem = tr_smem_bytes<D>();
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = tr_config(dim3(p.ctas), TrShape<D>::Threads, kSmem, stream, &attr);
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<D>, p, maps);
+    if (e != cudaSuccess) return e;
+    const long long warps = (long long)p.B * p.T * p.Hq;
+    cfg = tr_config(dim3((unsigned)((warps + kTrCombineWarps - 1) / kTrCombineWarps)), kTrCombineWarps * 32, 0, stream,
+                    &attr);
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tree(int D, const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
+    return D == 64 ? launch_tree_t<64>(p, maps, s) : (D == 128 ? launch_tree_t<128>(p, maps, s) : launch_tree_t<256>(p, maps, s));
+}
+
+cudaError_t launch_tree_stage(int D, const TreeParams& p, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = tr_config(dim3(p.B), 256, 0, s, &attr);
+    return D == 64    ? cudaLaunchKernelEx(&cfg, tree_stage_kernel<64>, p)
+           : D == 128 ? cudaLaunchKernelEx(&cfg, tree_stage_kernel<128>, p)
+                      : cudaLaunchKernelEx(&cfg, tree_stage_kernel<256>, p);
+}
+
+}  // namespace kvc

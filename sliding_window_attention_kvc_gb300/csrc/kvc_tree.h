@@ -25,6 +25,49 @@ struct PathParams {
     unsigned long long theta[kMaxHalfDim];
 };
 
+constexpr int kTreeMax = 64;                    // tokens of a draft: one tile of keys
+constexpr int kTreeCtas = 152;                  // one CTA per SM
+// Fewest units (a tile of 64 keys for a tile of 128 rows) of a share: each leaves partials to the combine.
+constexpr int kTreeMinTiles = 2;
+// Q tiles of 128 rows of one column: head_dim 256 leaves tensor memory for one.
+__host__ __device__ constexpr int tree_q_tiles(int D) { return D == 256 ? 1 : 2; }
+
+// Attention of a tree of drafted tokens (kvc_tree_attention).  A column is
+// (sequence, kv head, up to mq tokens); its keys are tiles of 64: the cached rows
+// (slots, or positions of a paged sequence), then the draft itself.
+struct TreeParams {
+    const void* q;              // [B, T, Hq, D]
+    const void* k_new;          // [B, T, Hkv, D]
+    const int32_t* pos;         // [B]: tokens in the cache (below 0: idle)
+    const int32_t* parent;      // [B, T]
+    const int32_t* table;
+    const uint32_t* valid;      // may be null
+    void* out;                  // [B, T, Hq, D]
+    void* stage;                // BAKED: the draft's rotated keys [B, T, Hkv, D]
+    uint32_t* err;
+    float2* part_ml;            // [slots][rows]: slot = share + column
+    float* part_o;
+    int B, T, Hq, Hkv, G, layer;
+    int layout, window, sinks, capacity, bs, num_blocks, maxb;
+    int tq, mq, ncol;           // tokens of a Q tile, of a column; columns of a (sequence, kv head)
+    int col_units;              // units a tile of all columns of a kv head
+    int last_units;             // units a tile of the last column: its Q tiles
+    int rows, alt_off;          // partial rows of a slot; to those of its second warpgroup
+    int slot_whole;             // window layouts: the map brings every column block in one copy
+    int ctas;
+    int rope;
+    float scale2;               // softmax scale * log2(e)
+    unsigned long long theta[kMaxHalfDim];
+};
+
+// cache: window layouts 64 slots of K and V (five or four dimensions), paged a
+// block; k, v: the draft's rows.
+struct TreeMaps {
+    CUtensorMap cache, k, v;
+};
+
+cudaError_t launch_tree(int head_dim, const TreeParams& p, const TreeMaps& maps, cudaStream_t stream);
+cudaError_t launch_tree_stage(int head_dim, const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_append_path(int dtype, int head_dim, const PathParams& p, cudaStream_t stream);
 
 }  // namespace kvc

@@ -167,3 +167,31 @@ def test_binding_checks(kvc):
         kvc.append_path(d, cache, 0, kv, kv, i, torch.zeros(3, 2, dtype=torch.int32), i, ws, table)
     with pytest.raises(ValueError, match="CUDA"):
         kvc.block_evict(d, kvc.BlockState(d, device="cpu"), w, i, 3, ws)
+
+
+def test_tree_refusals(kvc):
+    L = kvc.lib()
+
+    def call(base=PAGED, cache=A, layer=0, q=A, k=A, v=A, T=8, pos=A, parent=A, table=A, out=A, ws=A, short=0, **kw):
+        d = kvc.make_desc(**dict(base, **kw))
+        n = kvc.tree_workspace_bytes(d, T) - short if short else 1 << 40
+        return L.kvc_tree_attention(ctypes.byref(d), cache, layer, q, k, v, T, pos, parent, table, None, out, ws, n, None)
+
+    _all(call, kvc, ("cache", "q", "k", "v", "pos", "parent", "table", "out", "ws"), ("cache", "q", "k", "v", "out", "ws"),
+         ("parent",))
+    assert call(T=0) == kvc.KVC_ERR_ARG and call(T=kvc.KVC_TREE_MAX + 1) == kvc.KVC_ERR_ARG
+    assert call(short=1) == kvc.KVC_ERR_WORKSPACE
+    for kw in (dict(dtype="f32"), dict(dtype="i8"), dict(block_size=12), dict(block_size=48), dict(block_size=100),
+               dict(q_heads=258), dict(base=RING, rope="read_time"), dict(base=RING, window=7), dict(head_dim=96)):
+        assert call(**kw) == kvc.KVC_ERR_UNSUPPORTED, kw
+        kw = dict(kw)
+        assert kvc.tree_workspace_bytes(kvc.make_desc(**dict(kw.pop("base", PAGED), **kw)), 8) == 0
+    d = kvc.make_desc(**PAGED)
+    assert kvc.tree_workspace_bytes(d, 8) > kvc.workspace_bytes(d)
+    with pytest.raises(kvc.KvcError):
+        kvc.alloc_tree_workspace(d, 65)
+    q = torch.zeros(3, 5, 8, 128, dtype=torch.bfloat16)
+    kv = torch.zeros(3, 5, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvc.tree_attention(d, kv, 0, q, kv, kv, torch.zeros(3, dtype=torch.int32), torch.zeros(3, 5, dtype=torch.int32),
+                           torch.zeros(64, dtype=torch.uint8))
