@@ -1293,14 +1293,15 @@ static int tree_desc(const kvc_desc* d, const Geo& g, int32_t T) {
     if (d->layout == KVC_LAYOUT_PAGED &&
         (d->block_size % 8 || (d->block_size < 64 ? 64 % d->block_size : d->block_size % 64)))
         return KVC_ERR_UNSUPPORTED;
+    // rows and columns are counted in 32 bits
     if ((long long)d->batch * T * d->q_heads > 0x7fffffffLL) return KVC_ERR_UNSUPPORTED;
     return KVC_OK;
 }
 
 // The columns of a draft of T tokens, and what kvc_tree_attention adds to the decode workspace, after it.
 struct TreeLayout {
-    int tq, mq, ncol, last_units, rows, alt_off;
-    size_t stage, part_ml, part_o, total;
+    int tq, mq, ncol, last_units, rows;
+    size_t stage, cols, part_ml, part_o, total;
 };
 static TreeLayout tree_layout(const kvc_desc* d, const Geo& g, int T) {
     TreeLayout l{};
@@ -1309,13 +1310,12 @@ static TreeLayout tree_layout(const kvc_desc* d, const Geo& g, int T) {
     l.mq = l.tq * nq;
     l.ncol = (T + l.mq - 1) / l.mq;
     l.last_units = T - (l.ncol - 1) * l.mq <= l.tq ? 1 : nq;
-    const bool alt = nq == 2 && l.last_units == 1;
-    l.rows = l.ncol > 1 ? nq * 128 : (alt ? 2 : 1) * T * g.G;
-    l.alt_off = l.ncol > 1 ? 128 : T * g.G;
-    const size_t slots = (size_t)kTreeCtas + (size_t)d->batch * d->kv_heads * l.ncol;
+    l.rows = (l.ncol > 1 ? l.mq : T) * g.G;
+    const size_t cols = (size_t)d->batch * d->kv_heads * l.ncol, slots = (size_t)kTreeCtas + cols;
     l.stage = align_up(ws_layout(d, g).total, 256);
     const size_t staged = d->rope == KVC_ROPE_BAKED ? (size_t)d->batch * T * d->kv_heads * d->head_dim * 2 : 0;
-    l.part_ml = align_up(l.stage + staged, 256);
+    l.cols = align_up(l.stage + staged, 256);
+    l.part_ml = align_up(l.cols + cols * 8, 256);
     l.part_o = align_up(l.part_ml + slots * l.rows * 8, 256);
     l.total = align_up(l.part_o + slots * l.rows * d->head_dim * 4, 256);
     return l;
@@ -1355,6 +1355,7 @@ KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t lay
     p.out = out;
     p.stage = ws + l.stage;
     p.err = reinterpret_cast<uint32_t*>(ws + ws_layout(d, g).err);
+    p.col_shares = reinterpret_cast<int2*>(ws + l.cols);
     p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.B = d->batch;
@@ -1376,7 +1377,6 @@ KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t lay
     p.last_units = l.last_units;
     p.col_units = (l.ncol - 1) * tree_q_tiles(d->head_dim) + l.last_units;
     p.rows = l.rows;
-    p.alt_off = l.alt_off;
     p.ctas = kTreeCtas;
     p.rope = d->rope;
     const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);

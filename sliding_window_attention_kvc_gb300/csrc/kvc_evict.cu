@@ -1,5 +1,7 @@
 // Caches kept in part: how much attention weight each block received, and the
 // lightest blocks given back.
+#include <cooperative_groups.h>
+
 #include "kvc_decode.cuh"
 #include "kvc_select.h"
 
@@ -14,20 +16,25 @@ __device__ __forceinline__ void ev_pdl_launch() { asm volatile("griddepcontrol.l
 // weights of blocks
 // ---------------------------------------------------------------------------
 constexpr int kWeighThreads = 256;
+constexpr int kWeighRows = 256;                     // positions of a CTA, where a block has no more
+constexpr int kWeighParts = kWeighThreads / (kWeighRows / 4);   // head groups that share a position
 
-// One CTA per (`per` blocks, sequence), a thread a position: the weights
-// 2^(s - M) / L of its row over all q heads, added up in head order, then the
-// rows of each block in row order: the same sums whatever the decode's shares were.
+// One CTA per (`per` blocks, sequence).  A thread adds up the weights
+// 2^(s - M) / L of four positions (one 16-byte load a head) over a quarter of the q
+// heads, in head order; the quarters, then the rows of each block, are added in
+// order: the same sums whatever the decode's shares were.  What bounds it: 4 bytes a
+// row and head, which the decode has just left in L2, and an exponential for each.
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ WeighParams p) {
-    __shared__ float s_row[kWeighThreads];
+    __shared__ float4 s_part[kWeighThreads];
+    __shared__ float s_row[kWeighRows];
     __shared__ float s_warp[kWeighThreads / 32];
     constexpr int U = 8;                            // heads in flight
     const int tid = threadIdx.x, b = blockIdx.y;
     const int lb0 = blockIdx.x * p.per;
+    const int32_t* trow = p.table + (long long)b * p.maxb;
     ev_pdl_wait();
     ev_pdl_launch();
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
-    const int32_t* trow = p.table + (long long)b * p.maxb;
     const float* sc = p.scores + (long long)b * p.Hq * p.stride;
     const float2* ml = p.ml + (long long)b * p.Hq;
     float* wrow = p.weights + (long long)b * p.maxb;
@@ -35,29 +42,64 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         const int phys = __ldg(trow + lb);
         return phys >= 0 && phys < p.num_blocks && (!p.valid || ((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u));
     };
-    auto row_weight = [&](long long pos) {
-        float a = 0.f;
-        for (int h0 = 0; h0 < p.Hq; h0 += U) {
-            float s[U];
+    auto store = [&](int lb, float sum) { wrow[lb] = p.decay == 0.f ? sum : fmaf(p.decay, wrow[lb], sum); };
+    // weights of positions pos .. pos + 3 (pos a multiple of 4, within the row) over heads h0 .. h1 - 1; what lies
+    // behind the position, or in a block that is not attended, is whatever was there
+    auto weights4 = [&](long long pos, int h0, int h1) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int h = h0; h < h1; h += U) {
+            float4 s[U];
             float2 m[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = min(h0 + u, p.Hq - 1);
-                s[u] = __ldcg(sc + h * p.stride + pos);
-                m[u] = __ldcg(ml + h);
+                const int x = min(h + u, h1 - 1);
+                s[u] = __ldcg(reinterpret_cast<const float4*>(sc + x * p.stride + pos));
+                m[u] = __ldcg(ml + x);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (h0 + u < p.Hq) a = fmaf(exp2f(s[u] - m[u].x), m[u].y, a);
+                if (h + u < h1) {
+                    a.x = fmaf(exp2f(s[u].x - m[u].x), m[u].y, a.x);
+                    a.y = fmaf(exp2f(s[u].y - m[u].x), m[u].y, a.y);
+                    a.z = fmaf(exp2f(s[u].z - m[u].x), m[u].y, a.z);
+                    a.w = fmaf(exp2f(s[u].w - m[u].x), m[u].y, a.w);
+                }
         }
         return a;
     };
-    auto store = [&](int lb, float sum) { wrow[lb] = p.decay == 0.f ? sum : fmaf(p.decay, wrow[lb], sum); };
-    if (p.bs > kWeighThreads) {                     // one block, its rows in turn
+    // positions p0 .. p0 + kWeighRows - 1 (p0 a multiple of 4) into s_row
+    constexpr int QUADS = kWeighRows / 4;
+    const int quad = tid % QUADS, part = tid / QUADS;
+    const int h0 = (int)((long long)p.Hq * part / kWeighParts), h1 = (int)((long long)p.Hq * (part + 1) / kWeighParts);
+    auto rows = [&](long long p0) {
+        const long long pos = p0 + 4 * quad;
+        s_part[tid] = pos <= t ? weights4(pos, h0, h1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncthreads();
+        if (tid < QUADS) {
+            float4 a = s_part[tid];
+            for (int k = 1; k < kWeighParts; ++k) {
+                const float4 c = s_part[k * QUADS + tid];
+                a.x += c.x;
+                a.y += c.y;
+                a.z += c.z;
+                a.w += c.w;
+            }
+            *reinterpret_cast<float4*>(s_row + 4 * tid) = a;
+        }
+        __syncthreads();
+    };
+    const long long pos0 = (long long)lb0 * p.bs, lead = pos0 & 3;    // rows read in front of the first
+    if (p.per == 1) {                               // one block, its rows in turn
         float a = 0.f;
-        if ((long long)lb0 * p.bs <= t && attended(lb0))
-            for (long long r = tid; r < p.bs; r += kWeighThreads)
-                if (lb0 * (long long)p.bs + r <= t) a += row_weight(lb0 * (long long)p.bs + r);
+        if (pos0 <= t && attended(lb0)) {           // (uniform)
+            const long long end = min(pos0 + p.bs - 1, (long long)t);
+            for (long long r0 = pos0 - lead; r0 <= end; r0 += kWeighRows) {
+                rows(r0);
+                const long long r = r0 + tid;
+                if (r >= pos0 && r <= end) a += s_row[tid];
+                __syncthreads();
+            }
+        }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
         if ((tid & 31) == 0) s_warp[tid >> 5] = a;
@@ -68,15 +110,15 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         }
         return;
     }
-    const int i = tid / p.bs, lb = lb0 + i;         // block of this thread's position
-    const long long pos = (long long)lb0 * p.bs + tid;
-    float a = 0.f;
-    if (i < p.per && lb < p.maxb && pos <= t && attended(lb)) a = row_weight(pos);
-    s_row[tid] = a;
-    __syncthreads();
-    if (tid < p.per && lb0 + tid < p.maxb) {
+    const bool mine = tid < p.per && lb0 + tid < p.maxb;
+    const bool on = mine && pos0 + (long long)tid * p.bs <= t && attended(lb0 + tid);
+    if (pos0 <= t) rows(pos0 - lead);               // (uniform)
+    if (mine) {
         float sum = 0.f;
-        for (int r = 0; r < p.bs; ++r) sum += s_row[tid * p.bs + r];
+        if (on) {
+            const int end = (int)min((long long)p.bs - 1, t - (pos0 + (long long)tid * p.bs));
+            for (int r = 0; r <= end; ++r) sum += s_row[(int)lead + tid * p.bs + r];
+        }
         store(lb0 + tid, sum);
     }
 }
@@ -89,7 +131,7 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 
 // Order of weights as unsigned integers: -0 counts as 0, NaN as the heaviest.
 __device__ __forceinline__ uint32_t weight_key(float x) {
-    if (!(x == x)) return 0xffffffffu;
+    if (!(x == x)) return 0xfffffffeu;
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -121,58 +163,109 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
     return ex;
 }
 
-// One CTA per sequence: the excess over `keep` of its mapped blocks, lightest
-// first, ties by the lowest index, from a radix search of the excess-th lightest
-// (four digits).  Blocks whose count reaches zero are marked; the last CTA to
-// finish (an atomic ticket, no waiting) puts the marked ones on the free list in
-// ascending order and clears their resident bits.
+// A cluster of CTAs per sequence, a contiguous part of its blocks each: the excess
+// over `keep` of its mapped blocks, lightest first, ties by the lowest index, from a
+// radix search of the excess-th lightest (four digits; every CTA counts its own
+// keys, kept in shared memory, and adds up the cluster's counts).  Blocks whose
+// count reaches zero are marked; the last CTA to finish (an atomic ticket, no
+// waiting) puts the marked ones on the free list in ascending order and clears
+// their resident bits.
+// What bounds it: a few dependent trips to L2 and as many cluster barriers, whatever
+// the length (a single CTA took 309 us for two sequences of up to 62,500 blocks).
+constexpr int kEvictKeys = 8192;                // keys a CTA keeps
+constexpr uint32_t kKeyStays = 0xffffffffu;     // not among the blocks that may go
+
 __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int s_hist[256];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    __shared__ int s_hist[4][256];
     __shared__ int s_w[kEvictWarps];
+    __shared__ int s_count[2];                  // mapped, and those that may go
     __shared__ int s_digit, s_beyond, s_last;
-    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
+    __shared__ uint32_t s_key[kEvictKeys];
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x / CL;
+    for (int i = tid; i < 4 * 256; i += kEvictThreads) s_hist[0][i] = 0;
+    if (tid < 2) s_count[tid] = 0;
     ev_pdl_wait();
     ev_pdl_launch();
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
     int32_t* trow = p.table + (long long)b * p.maxb;
     float* wrow = p.weights + (long long)b * p.maxb;
-    const int hi = nb - p.recent;                   // blocks first .. hi - 1 may go
+    const int hi = nb - p.recent;               // blocks first .. hi - 1 may go
+    const int lo_i = (int)((long long)nb * rank / CL), hi_i = (int)((long long)nb * (rank + 1) / CL);
+    const bool kept = hi_i - lo_i <= kEvictKeys;
+    auto key_of = [&](int i) -> uint32_t {
+        return i >= p.first && i < hi && trow[i] >= 0 ? weight_key(wrow[i]) : kKeyStays;
+    };
+    __syncthreads();
     int live = 0, loose = 0;
-    for (int i = tid; i < nb; i += kEvictThreads) {
-        const int on = trow[i] >= 0;
-        live += on;
-        loose += on && i >= p.first && i < hi;
+    for (int base = lo_i; base < hi_i; base += 4 * kEvictThreads) {
+        int e[4];
+        float w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = base + u * kEvictThreads + tid;
+            e[u] = i < hi_i ? trow[i] : -1;
+            w[u] = i < hi_i ? wrow[i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = base + u * kEvictThreads + tid;
+            const bool may = e[u] >= 0 && i >= p.first && i < hi;
+            live += e[u] >= 0;
+            loose += may;
+            if (kept && i < hi_i) s_key[i - lo_i] = may ? weight_key(w[u]) : kKeyStays;
+        }
     }
-    int nlive, nloose;
-    evict_scan(live, s_w, &nlive);
-    evict_scan(loose, s_w, &nloose);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        live += __shfl_xor_sync(0xffffffffu, live, off);
+        loose += __shfl_xor_sync(0xffffffffu, loose, off);
+    }
+    if (lane == 0) {
+        atomicAdd(&s_count[0], live);
+        atomicAdd(&s_count[1], loose);
+    }
+    cluster.sync();
+    int nlive = 0, nloose = 0;
+    for (int c = 0; c < CL; ++c) {
+        const int* o = cluster.map_shared_rank(s_count, c);
+        nlive += o[0];
+        nloose += o[1];
+    }
     int want = min(nlive - p.keep, nloose);
-    if (want > 0) {
-        uint32_t prefix = 0, mask = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kEvictThreads) s_hist[i] = 0;
-            __syncthreads();
-            for (int base = p.first; base < hi; base += kEvictThreads) {
+    const bool some = want > 0;                 // (the same in every CTA of the cluster)
+    uint32_t prefix = 0, mask = 0;
+    int digit = 0;
+    if (some) {
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            for (int base = lo_i; base < hi_i; base += kEvictThreads) {
                 const int i = base + tid;
-                const bool in0 = i < hi && trow[i] >= 0;
-                const uint32_t key = in0 ? weight_key(wrow[i]) : 0u;
-                const bool in = in0 && (key & mask) == prefix;
-                const uint32_t digit = (key >> shift) & 255u;
+                const uint32_t key = i < hi_i ? (kept ? s_key[i - lo_i] : key_of(i)) : kKeyStays;
+                const bool in = key != kKeyStays && (key & mask) == prefix;
+                const uint32_t d = (key >> shift) & 255u;
                 const unsigned act = __ballot_sync(0xffffffffu, in);
                 if (in) {
-                    const unsigned same = __match_any_sync(act, digit);
-                    if (lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], __popc(same));
+                    const unsigned same = __match_any_sync(act, d);
+                    if (lane == __ffs(same) - 1) atomicAdd(&s_hist[pass][d], __popc(same));
                 }
             }
-            __syncthreads();
+            cluster.sync();
             if (tid < 32) {
                 int c[8], sum = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    c[k] = s_hist[lane * 8 + k];
-                    sum += c[k];
+                for (int k = 0; k < 8; ++k) c[k] = 0;
+                for (int o = 0; o < CL; ++o) {
+                    const int4* h = reinterpret_cast<const int4*>(cluster.map_shared_rank(&s_hist[pass][0], o)) + lane * 2;
+                    const int4 x = h[0], y = h[1];
+                    c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
+                    c[4] += y.x; c[5] += y.y; c[6] += y.z; c[7] += y.w;
                 }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += c[k];
                 int incl = sum;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -192,20 +285,32 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
                 }
             }
             __syncthreads();
+            digit = s_digit;
             want -= s_beyond;
-            prefix |= (uint32_t)s_digit << shift;
+            prefix |= (uint32_t)digit << shift;
             mask |= 255u << shift;
             __syncthreads();
         }
-        int run = 0;                                // equal keys before this pass
-        for (int base = p.first; base < hi; base += kEvictThreads) {
+        // keys below `prefix` go, and the first `want` of those equal to it: so many lie in the CTAs before
+        int before = 0;
+        for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&s_hist[3][digit], c);
+        const int mine = s_hist[3][digit];
+        const int take = before >= want ? 0 : min(mine, want - before);      // of this CTA's
+        int run = 0;                            // equal keys before this pass
+        for (int base = lo_i; base < hi_i; base += kEvictThreads) {
             const int i = base + tid;
-            const int phys = i < hi ? trow[i] : -1;
-            const uint32_t key = phys >= 0 ? weight_key(wrow[i]) : 0xffffffffu;
-            const int same = phys >= 0 && key == prefix;
-            int tot;
-            const int ex = evict_scan(same, s_w, &tot);
-            if (phys >= 0 && (key < prefix || (same && run + ex < want))) {
+            const uint32_t key = i < hi_i ? (kept ? s_key[i - lo_i] : key_of(i)) : kKeyStays;
+            bool goes = key < prefix;
+            if (take == mine) {
+                goes = goes || (take > 0 && key == prefix);
+            } else if (take > 0) {              // (uniform)
+                int tot;
+                const int same = key == prefix, ex = evict_scan(same, s_w, &tot);
+                goes = goes || (same && run + ex < take);
+                run += tot;
+            }
+            if (goes) {
+                const int phys = trow[i];
                 trow[i] = -1;
                 wrow[i] = 0.f;
                 if (phys >= p.num_blocks)
@@ -213,11 +318,10 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
                 else if (atomicSub(&p.refcount[phys], 1) == 1)
                     atomicOr(&p.back[phys >> 5], 1u << (phys & 31));
             }
-            run += tot;
         }
     }
     __threadfence();
-    __syncthreads();
+    cluster.sync();                             // no CTA leaves while its counts are read
     if (tid == 0) s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
@@ -246,7 +350,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     }
     if (tid == 0) {
         *p.free_count = min(at, p.num_blocks);
-        *p.ticket = 0u;                             // ready for the next call
+        *p.ticket = 0u;                         // ready for the next call
     }
 }
 
@@ -266,15 +370,24 @@ cudaLaunchConfig_t ev_config(dim3 grid, int threads, cudaStream_t stream, cudaLa
 
 cudaError_t launch_weigh(const WeighParams& p, cudaStream_t s) {
     WeighParams q = p;
-    q.per = p.bs > kWeighThreads ? 1 : kWeighThreads / p.bs;
+    // blocks of a CTA: their rows, and up to 3 in front of them, at most kWeighRows
+    q.per = p.bs > kWeighRows / 2 ? 1 : (p.bs % 4 ? kWeighRows - 3 : kWeighRows) / p.bs;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = ev_config(dim3((p.maxb + q.per - 1) / q.per, p.B), kWeighThreads, s, &attr);
     return cudaLaunchKernelEx(&cfg, weigh_kernel, q);
 }
 
 cudaError_t launch_block_evict(const EvictParams& p, cudaStream_t s) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = ev_config(dim3(p.B), kEvictThreads, s, &attr);
+    // up to four keys a thread, as far as eight CTAs go (a cluster of eight runs on every GPU)
+    int cl = 1;
+    while (cl < 8 && (long long)cl * 4 * kEvictThreads < p.maxb) cl *= 2;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = ev_config(dim3((unsigned)(p.B * cl)), kEvictThreads, s, attr);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cl;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, block_evict_kernel, p);
 }
 

@@ -38,6 +38,7 @@ cudaLaunchConfig_t sl_config(dim3 grid, int threads, int smem, cudaStream_t stre
 // bounds
 // ---------------------------------------------------------------------------
 constexpr int kBoundsThreads = 128;
+constexpr int kBoundsWarps = 152 * 24;         // warps that fill the GPU
 
 // 16 bytes of a key row as floats.
 template <typename Elt>
@@ -51,8 +52,8 @@ __device__ __forceinline__ void key_values(const uint4& w, float scale, float* f
     }
 }
 
-// One warp per (touched block, kv head) of a sequence.  A lane keeps the ends
-// of 16 bytes of the row (32 on rows of 1 KB); 512 / row bytes rows pass at
+// One warp per touched block of a sequence and `heads` kv heads.  A lane keeps the
+// ends of 16 bytes of the row (32 on rows of 1 KB); 512 / row bytes rows pass at
 // once.  The block is read whole from its first row, so that the result does not
 // depend on what was there before.
 template <typename Elt, int D>
@@ -62,12 +63,12 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __gr
     constexpr int LPR = CPR < 32 ? CPR : 32;              // lanes of a row
     constexpr int NCH = CPR / LPR;                        // chunks of a lane
     constexpr int RPW = 32 / LPR;                         // rows at once
-    constexpr int U = 4;                                  // loads in flight
+    constexpr int U = NCH > 1 ? 4 : 8;                    // loads in flight
     sl_pdl_wait();
     sl_pdl_launch();
     const int lane = threadIdx.x & 31;
     const int unit = blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
-    const int slot = unit / p.Hkv, h = unit - slot * p.Hkv, b = blockIdx.y;
+    const int slot = unit / p.parts, h0 = (unit - slot * p.parts) * p.heads, b = blockIdx.y;
     if (slot >= p.slots) return;
     const long long t0 = p.pos[b];
     int n = p.n_new;
@@ -85,92 +86,101 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __gr
         return;
     }
     const int rows = (int)min((long long)p.bs, end - lb * p.bs);
-    const long long row0 = ((long long)phys * p.Hkv + h) * p.bs;
-    const Elt* src = static_cast<const Elt*>(p.cache) + p.layer_off + row0 * D;
-    const float* sc = sizeof(Elt) == 1 ? p.scales + p.sc_layer_off + row0 : nullptr;
     const int c = lane % LPR, r0 = lane / LPR;
-    float hi[NCH * VPL], lo[NCH * VPL];
+    for (int h = h0; h < min(h0 + p.heads, p.Hkv); ++h) {
+        const long long row0 = ((long long)phys * p.Hkv + h) * p.bs;
+        const Elt* src = static_cast<const Elt*>(p.cache) + p.layer_off + row0 * D;
+        const float* sc = sizeof(Elt) == 1 ? p.scales + p.sc_layer_off + row0 : nullptr;
+        float hi[NCH * VPL], lo[NCH * VPL];
 #pragma unroll
-    for (int i = 0; i < NCH * VPL; ++i) {
-        hi[i] = -INFINITY;
-        lo[i] = INFINITY;
-    }
-    for (int base = r0; base < rows; base += U * RPW) {
-        uint4 w[U][NCH];
-        float s[U];
+        for (int i = 0; i < NCH * VPL; ++i) {
+            hi[i] = -INFINITY;
+            lo[i] = INFINITY;
+        }
+        for (int base = r0; base < rows; base += U * RPW) {
+            uint4 w[U][NCH];
+            float s[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = min(base + u * RPW, rows - 1);  // (a row twice changes nothing)
+            for (int u = 0; u < U; ++u) {
+                const int r = min(base + u * RPW, rows - 1);  // (a row twice changes nothing)
+#pragma unroll
+                for (int k = 0; k < NCH; ++k)
+                    w[u][k] = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * D + (k * LPR + c) * VPL));
+                s[u] = sizeof(Elt) == 1 ? __ldg(sc + r) : 1.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < NCH; ++k) {
+                    float f[VPL];
+                    key_values<Elt>(w[u][k], s[u], f);
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) {
+                        hi[k * VPL + i] = fmaxf(hi[k * VPL + i], f[i]);
+                        lo[k * VPL + i] = fminf(lo[k * VPL + i], f[i]);
+                    }
+                }
+        }
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < NCH * VPL; ++i) {
+#pragma unroll
+            for (int off = LPR; off < 32; off <<= 1) {
+                hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
+                lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
+            }
+            a = fmaxf(a, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
+        }
+#pragma unroll
+        for (int off = 1; off < LPR; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        const float step = __fdiv_rn(a, 127.f);
+        const long long at = (long long)phys * p.Hkv + h;
+        if (lane == 0) p.steps[at] = step;
+        if (lane < LPR) {
+            int8_t* dst = p.codes + at * 2 * D;
 #pragma unroll
             for (int k = 0; k < NCH; ++k)
-                w[u][k] = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * D + (k * LPR + c) * VPL));
-            s[u] = sizeof(Elt) == 1 ? __ldg(sc + r) : 1.f;
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t w[VPL / 4];
 #pragma unroll
-            for (int k = 0; k < NCH; ++k) {
-                float f[VPL];
-                key_values<Elt>(w[u][k], s[u], f);
+                    for (int i = 0; i < VPL / 4; ++i) w[i] = 0u;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    hi[k * VPL + i] = fmaxf(hi[k * VPL + i], f[i]);
-                    lo[k * VPL + i] = fminf(lo[k * VPL + i], f[i]);
-                }
-            }
-    }
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < NCH * VPL; ++i) {
-#pragma unroll
-        for (int off = LPR; off < 32; off <<= 1) {
-            hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
-            lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
-        }
-        a = fmaxf(a, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
-    }
-#pragma unroll
-    for (int off = 1; off < LPR; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const float step = __fdiv_rn(a, 127.f);
-    const long long at = (long long)phys * p.Hkv + h;
-    if (lane == 0) p.steps[at] = step;
-    if (lane < LPR) {
-        int8_t* dst = p.codes + at * 2 * D;
-#pragma unroll
-        for (int k = 0; k < NCH; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t w[VPL / 4];
-#pragma unroll
-                for (int i = 0; i < VPL / 4; ++i) w[i] = 0u;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    int code = 0;
-                    if (step > 0.f) {
-                        const float x = __fdiv_rn(e ? lo[k * VPL + i] : hi[k * VPL + i], step);
-                        code = e ? (int)fmaxf(floorf(x), -127.f) : (int)fminf(ceilf(x), 127.f);
+                    for (int i = 0; i < VPL; ++i) {
+                        int code = 0;
+                        if (step > 0.f) {
+                            const float x = __fdiv_rn(e ? lo[k * VPL + i] : hi[k * VPL + i], step);
+                            code = e ? (int)fmaxf(floorf(x), -127.f) : (int)fminf(ceilf(x), 127.f);
+                        }
+                        w[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
                     }
-                    w[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
+                    int8_t* d = dst + e * D + (k * LPR + c) * VPL;
+                    if constexpr (VPL == 4)
+                        *reinterpret_cast<uint32_t*>(d) = w[0];
+                    else if constexpr (VPL == 8)
+                        *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+                    else
+                        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                int8_t* d = dst + e * D + (k * LPR + c) * VPL;
-                if constexpr (VPL == 4)
-                    *reinterpret_cast<uint32_t*>(d) = w[0];
-                else if constexpr (VPL == 8)
-                    *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
-                else
-                    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+        }
     }
 }
 
 template <typename Elt, int D>
 cudaError_t launch_bounds_t(const BoundsParams& p, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const long long units = (long long)p.slots * p.Hkv;
+    BoundsParams q = p;
+    // a warp walks several heads of its block where there are more than enough warps: the
+    // way to the block (position, table) is paid once
+    q.heads = 1;
+    while (q.heads < 8 && 2 * q.heads <= p.Hkv && (long long)p.B * p.slots * p.Hkv / (2 * q.heads) >= kBoundsWarps)
+        q.heads *= 2;
+    q.parts = (p.Hkv + q.heads - 1) / q.heads;
+    const long long units = (long long)p.slots * q.parts;
     constexpr int W = kBoundsThreads / 32;
     const cudaLaunchConfig_t cfg =
         sl_config(dim3((unsigned)((units + W - 1) / W), p.B), kBoundsThreads, 0, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, block_bounds_kernel<Elt, D>, p);
+    return cudaLaunchKernelEx(&cfg, block_bounds_kernel<Elt, D>, q);
 }
 
 // ---------------------------------------------------------------------------
@@ -187,8 +197,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 
 // One CTA per (chunk of blocks, kv head, sequence).  The group's q heads as
 // codes in shared memory, positive and negative parts apart: hi meets the one
-// and lo the other.  D / 16 lanes hold a block's codes, 16 channels of each end a
-// lane; a warp takes 4 x 512 / D blocks at once.
+// and lo the other.  A warp scores 32 blocks, a lane keeping track of each; D / 16
+// lanes hold a block's codes, 16 channels of each end a lane, 4 x 512 / D blocks at
+// once; the first ones are on their way while the queries are made codes.
 template <typename Act, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
     constexpr int LPB = D / 16, BPW = 32 / LPB, U = 4, NP = D / 64;
@@ -199,12 +210,44 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     const int h = blockIdx.y, b = blockIdx.z;
     sl_pdl_wait();
     sl_pdl_launch();
+    const int c0 = blockIdx.x * kScoreChunk;
+    // a warp's blocks, one a lane: their table entries while the queries are read
+    constexpr int PW = kScoreChunk / (kScoreThreads / 32);            // blocks of a warp
+    static_assert(PW == 32, "a lane a block");
+    const int w0 = c0 + warp * PW;
+    const int32_t* trow = p.table + (long long)b * p.maxb;
+    int my_phys = w0 + lane < p.maxb ? __ldg(trow + w0 + lane) : -1;
     const int traw = p.pos[b];
     const int t = clamp_paged_t(traw, p.maxb, p.bs);
     if ((traw < 0 || traw != t) && blockIdx.x == 0 && h == 0 && tid == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
-    const int c0 = blockIdx.x * kScoreChunk, c1 = min(nb, c0 + kScoreChunk);
+    const int c1 = min(nb, c0 + kScoreChunk);
     if (c0 >= c1) return;
+    if (w0 + lane >= c1) my_phys = -1;
+    if (my_phys >= p.num_blocks) {
+        set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+        my_phys = -1;
+    }
+    if (my_phys >= 0 && p.valid && !((__ldg(p.valid + (my_phys >> 5)) >> (my_phys & 31)) & 1u)) my_phys = -1;
+    const int ln = lane % LPB, sub = lane / LPB;
+    uint4 hi[U], lo[U];
+    float step[U];
+    auto load = [&](int it) {                                         // the ends of U BPW blocks of the warp
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int phys = __shfl_sync(0xffffffffu, my_phys, (it * U + u) * BPW + sub);
+            const long long at = (long long)max(phys, 0) * p.Hkv + h;
+            const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
+            hi[u] = lo[u] = make_uint4(0u, 0u, 0u, 0u);
+            step[u] = 0.f;
+            if (phys >= 0) {
+                hi[u] = __ldg(src + ln);
+                lo[u] = __ldg(src + LPB + ln);
+                step[u] = __ldg(p.steps + at);
+            }
+        }
+    };
+    load(0);
     for (int g = warp; g < p.G; g += kScoreThreads / 32) {
         const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + g) * D;
         float x[2 * NP], a = 0.f;
@@ -238,34 +281,14 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         if (lane == 0) s_step[g] = step;
     }
     __syncthreads();
-    const int32_t* trow = p.table + (long long)b * p.maxb;
     uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
-    const int ln = lane % LPB, sub = lane / LPB;
-    for (int base = c0 + warp * U * BPW; base < c1; base += (kScoreThreads / 32) * U * BPW) {
-        int lb[U], ok[U];
-        uint4 hi[U], lo[U];
-        float step[U], best[U];
-        int phys[U];
+    constexpr int IT = PW / (U * BPW);
+    float score = -INFINITY;                                          // of this lane's own block
+#pragma unroll 1
+    for (int it = 0; it < IT; ++it) {
+        float best[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            lb[u] = base + u * BPW + sub;
-            phys[u] = lb[u] < c1 ? __ldg(trow + lb[u]) : -1;
-            if (phys[u] >= p.num_blocks) {
-                set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
-                phys[u] = -1;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            ok[u] = phys[u] >= 0;
-            if (ok[u] && p.valid) ok[u] = (__ldg(p.valid + (phys[u] >> 5)) >> (phys[u] & 31)) & 1u;
-            const long long at = (long long)max(phys[u], 0) * p.Hkv + h;
-            const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
-            hi[u] = __ldg(src + ln);
-            lo[u] = __ldg(src + LPB + ln);
-            step[u] = __ldg(p.steps + at);
-            best[u] = -INFINITY;
-        }
+        for (int u = 0; u < U; ++u) best[u] = -INFINITY;
         for (int g = 0; g < p.G; ++g) {
             const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + 16 * ln);
             const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + D + 16 * ln);
@@ -286,13 +309,18 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
                 best[u] = fmaxf(best[u], __fmul_rn((float)a, __fmul_rn(sq, step[u])));
             }
         }
+        if (it + 1 < IT) load(it + 1);
+        // the lane of each block takes its score
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (ln == 0 && lb[u] < c1)
-                keys[lb[u]] = !ok[u] ? 0u
-                              : (lb[u] < p.first || lb[u] >= nb - p.recent) ? 0xffffffffu
-                                                                            : score_key(best[u]);
+        for (int u = 0; u < U; ++u) {
+            const int j = lane - (it * U + u) * BPW;                  // this lane's block among these BPW
+            const float x = __shfl_sync(0xffffffffu, best[u], (j & (BPW - 1)) * LPB);
+            if (j >= 0 && j < BPW) score = x;
+        }
     }
+    const int lb = w0 + lane;
+    if (lb < c1)
+        keys[lb] = my_phys < 0 ? 0u : (lb < p.first || lb >= nb - p.recent) ? 0xffffffffu : score_key(score);
 }
 
 // ---------------------------------------------------------------------------
@@ -371,52 +399,70 @@ __device__ __forceinline__ void pick_digit(const int* hist, int want, int* digit
 }
 
 // One CTA per (kv head, sequence): the k largest keys, ties by the lowest index,
-// by a radix search of the k-th largest (four digits), then the kept indices in
-// ascending order.
+// by a radix search of the k-th largest (four digits at most: it ends where a digit
+// takes all of its keys), then the kept indices in ascending order.  A thread keeps
+// the first kPickKeys of its keys in registers; longer tables are read again.
+// What bounds it: one trip to the keys, then barriers.
+constexpr int kPickKeys = 4;
+
 __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ int s_hist[256];
+    __shared__ int s_hist[4][256];
     __shared__ int2 s_w[kPickWarps];
-    __shared__ int s_digit, s_beyond;
+    __shared__ int s_digit[4], s_beyond[4];
     const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+    for (int i = tid; i < 4 * 256; i += kPickThreads) s_hist[0][i] = 0;
+    if (tid < 4) s_digit[tid] = -1;
     sl_pdl_wait();
     sl_pdl_launch();
+    const uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
-    const uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
     int32_t* out = p.blocks + ((long long)b * p.Hkv + h) * p.k;
-    // key >= low is kept whole but for the keys equal to it, of which the first `ties` are
-    uint32_t prefix = 0, mask = 0;
-    int want = p.k;
-    bool every = false;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kPickThreads) s_hist[i] = 0;
-        if (tid == 0) s_digit = -1;
-        __syncthreads();
-        for (int base = 0; base < nb; base += kPickThreads) {
-            const int i = base + tid;
-            const uint32_t key = i < nb ? __ldcg(keys + i) : 0u;
-            pick_count(s_hist, key != 0u && (key & mask) == prefix, (key >> shift) & 255u);
+    uint32_t mine[kPickKeys];
+#pragma unroll
+    for (int u = 0; u < kPickKeys; ++u) {
+        const int i = u * kPickThreads + tid;
+        mine[u] = i < nb ? __ldcg(keys + i) : 0u;
+    }
+    const int tail = kPickKeys * kPickThreads;
+    __syncthreads();
+    // keys above `low` are kept, and the first `ties` of those equal to it
+    uint32_t prefix = 0, mask = 0, low = 0;
+    int want = p.k, ties = 0x7fffffff;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+#pragma unroll
+        for (int u = 0; u < kPickKeys; ++u)
+            if (u * kPickThreads < nb)         // (uniform)
+                pick_count(s_hist[pass], mine[u] != 0u && (mine[u] & mask) == prefix, (mine[u] >> shift) & 255u);
+        for (int base = tail; base < nb; base += kPickThreads) {
+            const uint32_t key = base + tid < nb ? __ldcg(keys + base + tid) : 0u;
+            pick_count(s_hist[pass], key != 0u && (key & mask) == prefix, (key >> shift) & 255u);
         }
         __syncthreads();
-        if (tid < 32) pick_digit<true>(s_hist, want, &s_digit, &s_beyond);
+        if (tid < 32) pick_digit<true>(s_hist[pass], want, &s_digit[pass], &s_beyond[pass]);
         __syncthreads();
-        const int digit = s_digit;
-        if (digit < 0) {                  // fewer candidates than k (seen in the first pass)
-            every = true;
+        const int digit = s_digit[pass];
+        if (digit < 0) {                       // fewer candidates than k (seen in the first pass): all of them
+            low = 0u;
+            ties = 0;
             break;
         }
-        want -= s_beyond;
+        want -= s_beyond[pass];
         prefix |= (uint32_t)digit << shift;
         mask |= 255u << shift;
-        __syncthreads();
+        if (s_hist[pass][digit] == want) {     // all that begin with these digits
+            low = prefix ? prefix - 1u : 0u;   // (candidates' keys are above 0)
+            ties = 0;
+            break;
+        }
+        low = prefix;
+        ties = want;
     }
-    const uint32_t low = every ? 1u : prefix;
-    const int ties = every ? 0x7fffffff : want;
-    int2 run = make_int2(0, 0);           // keys above `low`, keys equal to it, before this pass
-    for (int base = 0; base < nb; base += kPickThreads) {
-        const int i = base + tid;
-        const uint32_t key = i < nb ? __ldcg(keys + i) : 0u;
-        const bool more = key > low, same = key == low;
+    int2 run = make_int2(0, 0);                // keys above `low`, keys equal to it, before this pass
+    auto emit = [&](int i, uint32_t key) {
+        const bool more = key > low, same = key == low && key != 0u;
         int2 tot;
         const int2 ex = pick_scan(make_int2(more, same), s_w, &tot);
         const int above = run.x + ex.x, equal = run.y + ex.y;
@@ -429,7 +475,12 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_c
         }
         run.x += tot.x;
         run.y += tot.y;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kPickKeys; ++u)
+        if (u * kPickThreads < nb) emit(u * kPickThreads + tid, mine[u]);
+    for (int base = tail; base < nb; base += kPickThreads)
+        emit(base + tid, base + tid < nb ? __ldcg(keys + base + tid) : 0u);
     for (int i = run.x + min(run.y, ties) + tid; i < p.k; i += kPickThreads) out[i] = -1;
 }
 

@@ -23,6 +23,7 @@ struct BoundsParams {
     long long layer_off;        // elements to this layer's K half
     long long sc_layer_off;     // scales to this layer's K half
     int B, Hkv, bs, num_blocks, maxb, n_new, slots;
+    int heads, parts;           // kv heads of a warp; warps of a block
 };
 
 // Selection (kvc_select_blocks).

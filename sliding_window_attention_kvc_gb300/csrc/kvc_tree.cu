@@ -19,7 +19,8 @@
 // key (they may hold anything); 1 and 3 issue the products of a Q tile each,
 // S = Q K^T a tile ahead of O += P V, accumulators in tensor memory; a warpgroup a
 // Q tile does the softmax, a thread a row.  A column of one Q tile gives both
-// warpgroups the same rows and alternate tiles, with sums of their own.
+// warpgroups the same rows and alternate tiles, with sums of their own, which they join
+// at the segment's end, half of the columns each.
 // What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for
 // 4 x 64 x 128 x D flops a Q tile: bytes up to one Q tile, the softmax beyond.
 #include <atomic>
@@ -68,8 +69,10 @@ struct alignas(16) TrStageMeta {
 struct TrBars {
     uint64_t full[6], ready[6], empty[6];
     uint64_t s_full[2][2], p_full[2], o_done[2], q_ready[2], fin[2];
+    uint64_t both[2];               // alternate tiles: both warpgroups' sums are there; both have read them
     uint32_t tmem;
     int abort;
+    float2 ml[2][kWsRows];          // ... and their (m, l)
 };
 
 template <int D>
@@ -90,37 +93,54 @@ __device__ __forceinline__ long long tr_seq_units(const TreeParams& p, int pos) 
     return (long long)tr_tiles(p, pos) * p.col_units * p.Hkv;
 }
 
-// Units of all sequences, and of those before b (a whole warp's call).
-__device__ __forceinline__ void tr_partition(const TreeParams& p, int b, long long* total, long long* before) {
-    const int lane = threadIdx.x & 31;
-    long long tot = 0, pre = 0;
-    for (int base = 0; base < p.B; base += 32) {
-        const int o = base + lane;
-        const long long u = o < p.B ? tr_seq_units(p, __ldg(p.pos + o)) : 0;
-        tot += u;
-        if (o < b) pre += u;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        tot += __shfl_xor_sync(0xffffffffu, tot, off);
-        pre += __shfl_xor_sync(0xffffffffu, pre, off);
-    }
-    *total = tot;
-    *before = pre;
-}
-
-__device__ __forceinline__ int tr_shares(const TreeParams& p, long long units) {
-    const long long s = (units + kTreeMinTiles - 1) / kTreeMinTiles;
-    return (int)(s < p.ctas ? s : p.ctas);
-}
+// What runs once a segment or once a kernel is kept short and out of line, one copy for
+// all roles: it comes out of a cold instruction cache, a line of eight instructions at a
+// time (inlined and unrolled, the way to a CTA's first product took 20 us, most of it the
+// draft's ancestors).
 
 // Where a share stands: the sequence and the units before it.
 struct TrWalk {
     int b;
     long long before;
 };
+// Units of all sequences, and the shares they are cut into (a whole warp's call): one a
+// CTA; fewer where the columns are alike and fewer than the CTAs: then each is cut into
+// the same whole number of shares, and no CTA begins a second segment (its way to the
+// first product, and a partial, cost 6 us; bandwidth is reached with 100 CTAs and more).
+struct TrParts {
+    long long units;
+    int shares;
+};
+__device__ __noinline__ TrParts tr_partition(const TreeParams& p) {
+    const int lane = threadIdx.x & 31;
+    long long tot = 0;
+    int lo = 0x7fffffff, hi = 0;                    // tiles of the shortest and of the longest column
+    for (int base = 0; base < p.B; base += 32) {
+        const int o = base + lane;
+        if (o < p.B) {
+            const int kt = tr_tiles(p, __ldg(p.pos + o));
+            tot += (long long)kt * p.col_units * p.Hkv;
+            lo = min(lo, kt);
+            hi = max(hi, kt);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        tot += __shfl_xor_sync(0xffffffffu, tot, off);
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
+    TrParts r;
+    r.units = tot;
+    const long long s = (tot + kTreeMinTiles - 1) / kTreeMinTiles, cols = (long long)p.B * p.Hkv * p.ncol;
+    r.shares = s < p.ctas ? (int)s : p.ctas;
+    if (lo == hi && p.last_units * p.ncol == p.col_units && cols <= r.shares)
+        r.shares = (int)cols * (r.shares / (int)cols);
+    return r;
+}
+
 // The sequence that holds unit u (a whole warp's call).
-__device__ __forceinline__ TrWalk tr_find(const TreeParams& p, long long u) {
+__device__ __noinline__ TrWalk tr_find(const TreeParams& p, long long u) {
     const int lane = threadIdx.x & 31;
     TrWalk w{0, 0};
     long long run = 0;
@@ -151,7 +171,8 @@ struct TrSegment {
     int b, h, pos, n0, tokens;                 // sequence, kv head, its tokens in the cache; first token and tokens of the column
     int kt;                                    // tiles of the column, the last of them the draft
     int tile0, nt;                             // nt may be 0: one unit of a tile that begins in the share before
-    long long units;
+    int units;
+    int first, last;                           // the column's first and last unit lie in this share
     int alt;                                   // one Q tile's rows: the warpgroups take alternate tiles
     long long col;                             // index of the column
     __device__ __forceinline__ int tiles(int i) const { return alt ? (nt + 1 - i) >> 1 : nt; }
@@ -159,7 +180,7 @@ struct TrSegment {
 
 // The segment that begins at unit u of a share ending at hi.
 template <int D>
-__device__ __forceinline__ TrSegment tr_segment(const TreeParams& p, TrWalk& w, long long u, long long hi) {
+__device__ __noinline__ TrSegment tr_segment(const TreeParams& p, TrWalk& w, long long u, long long hi) {
     TrSegment s;
     s.pos = __ldg(p.pos + w.b);
     for (long long n = tr_seq_units(p, s.pos); u >= w.before + n && w.b < p.B - 1;) {
@@ -181,11 +202,14 @@ __device__ __forceinline__ TrSegment tr_segment(const TreeParams& p, TrWalk& w, 
     s.tokens = min(p.mq, p.T - s.n0);
     // units to tiles: a tile belongs to the share that holds its first unit
     const int per = m < p.ncol - 1 ? NQ : p.last_units;
-    const long long take = min((long long)s.kt * per - v, hi - u);
+    const int v0 = (int)v;                                     // (tiles of a column, times two at most)
+    const int take = (int)min((long long)(s.kt * per - v0), hi - u);
     s.units = take;
-    s.tile0 = (int)((v + per - 1) / per);
-    s.nt = (int)((v + take + per - 1) / per) - s.tile0;
+    s.tile0 = per == 2 ? (v0 + 1) >> 1 : v0;
+    s.nt = (per == 2 ? (v0 + take + 1) >> 1 : v0 + take) - s.tile0;
     s.alt = NQ == 2 && per == 1;
+    s.first = v0 == 0;
+    s.last = v0 + take == s.kt * per;
     s.col = ((long long)s.b * p.Hkv + s.h) * p.ncol + m;
     return s;
 }
@@ -201,7 +225,7 @@ struct TrDraft {
         return t < 32 ? a : c;
     }
 };
-__device__ __forceinline__ TrDraft tr_draft(const TreeParams& p, int b, int pos, bool report) {
+__device__ __noinline__ TrDraft tr_draft(const TreeParams& p, int b, int pos, bool report) {
     const int lane = threadIdx.x & 31;
     TrDraft d;
     int up[2];                                  // the token above those in `see`; -1: the sequence, -2: none
@@ -220,8 +244,8 @@ __device__ __forceinline__ TrDraft tr_draft(const TreeParams& p, int b, int pos,
         up[e] = par;
         d.see[e] = 1ull << i;
     }
-#pragma unroll
-    for (int k = 0; k < 6; ++k) {
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {      // (parents lie below: at most six rounds)
         unsigned long long more[2];
         int next[2];
 #pragma unroll
@@ -270,9 +294,9 @@ __device__ __forceinline__ unsigned long long tr_window(const TreeParams& p, int
 }
 
 // Eight rotation pairs (elements of lo with those of hi) of a bf16 row at `pos`.
-__device__ __forceinline__ void tr_rotate8(uint4& lo, uint4& hi, long long pos, const unsigned long long* turns) {
+__device__ __noinline__ void tr_rotate8(uint4& lo, uint4& hi, long long pos, const unsigned long long* turns) {
     uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < 4; ++e) {
         float y[2], z[2];
 #pragma unroll
@@ -347,6 +371,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             mbar_init(&bars->o_done[i], 1);
             mbar_init(&bars->q_ready[i], 4);
             mbar_init(&bars->fin[i], 1);
+            mbar_init(&bars->both[i], 4 * NQ);
         }
         bars->abort = 0;
         mbar_fence_init();
@@ -356,9 +381,9 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
     }
     tr_pdl_wait();
     tr_pdl_launch();
-    long long units, unused;
-    tr_partition(p, 0, &units, &unused);
-    const int shares = tr_shares(p, units), x = blockIdx.x;
+    const TrParts parts = tr_partition(p);
+    const long long units = parts.units;
+    const int shares = parts.shares, x = blockIdx.x;
     if (x >= shares) return;                         // (uniform: before the tensor memory is taken)
     const long long lo = div_nonneg((long long)x * units, shares), hi = div_nonneg((long long)(x + 1) * units, shares);
     TrWalk walk = tr_find(p, lo);
@@ -394,6 +419,10 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         };
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
+            if (lane == 0) {                                    // for the combine: the column's first and last share
+                if (sg.first) p.col_shares[sg.col].x = x;
+                if (sg.last) p.col_shares[sg.col].y = x;
+            }
             const int n = tr_cached(p, sg.pos);
             if (paged && n < sg.pos && lane == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
             const int32_t* trow = p.table + (long long)sg.b * p.maxb;
@@ -613,7 +642,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
         const int tl = r / p.G;
         bool ok = true;
-        int idx0 = 0, base = 0, at_b = -1;
+        int idx0 = 0, base = 0, at_b = -1, joins = 0;
         TrDraft draft{};
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
@@ -629,30 +658,47 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
             // Q rows, rotated at their positions when BAKED, unscaled bf16
             if (nt > 0) {
-                // (D / 16 lanes share a row: a load covers whole lines)
-                constexpr int LPR = D / 16, RPW = 32 / LPR;
+                // (D / 16 lanes share a row: a load covers whole lines; a batch is in flight at once)
+                constexpr int LPR = D / 16, RPW = 32 / LPR, NB = 32 / RPW < 8 ? 32 / RPW : 8;
                 const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
-#pragma unroll 4
-                for (int it = 0; it < 32 / RPW; ++it) {
-                    const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
-                    const int rtl = rr / p.G;
-                    const bool rok = rtl < p.tq && c0 + rtl < sg.tokens;
-                    const int t = sg.n0 + c0 + rtl;
-                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                    if (rok) {
-                        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
-                                                    (((long long)sg.b * p.T + t) * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
-                        a = __ldg(reinterpret_cast<const uint4*>(qrow + 8 * c));
-                        b = __ldg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
+#pragma unroll 1
+                for (int it0 = 0; it0 < 32 / RPW; it0 += NB) {
+                    uint4 a[NB], e[NB];
+#pragma unroll
+                    for (int it = 0; it < NB; ++it) {
+                        const int rr = (warp & 3) * 32 + (it0 + it) * RPW + lane / LPR;
+                        const int rtl = rr / p.G;
+                        a[it] = e[it] = make_uint4(0u, 0u, 0u, 0u);
+                        if (rtl < p.tq && c0 + rtl < sg.tokens) {
+                            const __nv_bfloat16* qrow =
+                                static_cast<const __nv_bfloat16*>(p.q) +
+                                (((long long)sg.b * p.T + sg.n0 + c0 + rtl) * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
+                            a[it] = __ldg(reinterpret_cast<const uint4*>(qrow + 8 * c));
+                            e[it] = __ldg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
+                        }
                     }
-                    if (p.rope != kRopeNone) {
-                        const unsigned long long mine = draft.of(rok ? t : 0);
-                        if (rok) tr_rotate8(a, b, (long long)sg.pos + max(__popcll(mine) - 1, 0), p.theta + 8 * c);
+#pragma unroll
+                    for (int it = 0; it < NB; ++it) {
+                        // Q tile: [column block][128 rows][128 B], 128-byte swizzle
+                        const int rr = (warp & 3) * 32 + (it0 + it) * RPW + lane / LPR;
+                        const int c1 = c, c2 = c + D / 16;
+                        *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = a[it];
+                        *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = e[it];
                     }
-                    // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-                    const int c1 = c, c2 = c + D / 16;
-                    *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = a;
-                    *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = b;
+                }
+                if (p.rope != kRopeNone) {
+                    // each lane's own chunks, in place
+#pragma unroll 1
+                    for (int it = 0; it < 32 / RPW; ++it) {
+                        const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
+                        const int rtl = rr / p.G;
+                        const bool rok = rtl < p.tq && c0 + rtl < sg.tokens;
+                        const unsigned long long mine = draft.of(rok ? sg.n0 + c0 + rtl : 0);
+                        const int c1 = c, c2 = c + D / 16;
+                        uint4* x = reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4));
+                        uint4* y = reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4));
+                        if (rok) tr_rotate8(*x, *y, (long long)sg.pos + max(__popcll(mine) - 1, 0), p.theta + 8 * c);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -697,12 +743,14 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 const float ls = ws_exp64(sv, p.scale2, mn == -INFINITY ? 0.f : -mn);
                 l_run = l_run * alpha + ls;
                 m_run = mn;
-                // P V of the previous tile is done: O is free
-                if (lt > 0 && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
-                    ok = false;
-                    break;
-                }
-                if (lt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                // O is touched only once P V of the previous tile is done; where nothing is
+                // rescaled, that is asked for after this tile's weights have been handed over
+                const bool rescale = lt > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+                if (rescale) {
+                    if (!ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
                     ws_fence_after();
 #pragma unroll 1
                     for (int c4 = 0; c4 < D / 32; ++c4) {
@@ -726,6 +774,10 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 ws_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_full[qi]);
+                if (lt > 0 && !rescale && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
             }
             if (!ok) {
                 give_up();
@@ -739,9 +791,41 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 }
                 ws_fence_after();
             }
-            const long long row_a = (x + sg.col) * p.rows + (sg.alt ? qi * p.alt_off : qi * p.tq * p.G);
-            if (row_ok) p.part_ml[row_a + r] = real ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
-            if (nt > 0) {
+            // Alternate tiles: the two warpgroups' sums of a row become one, each warpgroup
+            // joining half of the columns.  (f: what this row's sums enter with.)
+            float f[2] = {1.f, 0.f};
+            int cols = D, col0 = 0, o0 = qi * D;               // columns to write; O's column in tensor memory
+            const bool other = sg.alt && sg.nt > 1;            // (the second warpgroup had a tile)
+            if (sg.alt) {
+                bars->ml[qi][r] = make_float2(m_run, l_run);
+                ws_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->both[0]);
+                if (!ws_wait(&bars->both[0], joins & 1, abort)) {
+                    ok = false;
+                    give_up();
+                    break;
+                }
+                ws_fence_after();
+                const float2 a = bars->ml[0][r], e = bars->ml[1][r];
+                m_run = fmaxf(a.x, e.x);
+                f[0] = a.x == -INFINITY && a.y == a.y ? 0.f : exp2f(a.x - m_run);
+                f[1] = e.x == -INFINITY && e.y == e.y ? 0.f : exp2f(e.x - m_run);
+                l_run = a.y * f[0] + e.y * f[1];
+                cols = D / 2;
+                col0 = qi * (D / 2);
+                o0 = col0;
+            }
+            // a column in one piece goes to the output, others leave a partial of each row
+            const bool whole = sg.first && sg.last;
+            if (!real) {
+                m_run = -INFINITY;
+                l_run = 0.f;
+            }
+            const float inv = !whole ? 1.f : (l_run == 0.f ? 0.f : 1.f / l_run);
+            const long long row_a = (x + sg.col) * p.rows + (sg.alt ? 0 : qi * p.tq * p.G);
+            if (!whole && row_ok && (!sg.alt || qi == 0)) p.part_ml[row_a + r] = make_float2(m_run, l_run);
+            if (nt > 0 || sg.alt) {
                 // through the Q tile's shared memory (its products are done), each row in the
                 // place of its own q (which this warp alone writes), CP columns at a time, so
                 // that whole lines go out
@@ -750,12 +834,27 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     return reinterpret_cast<float4*>(Qs + (ch >> 3) * (kWsRows * 128) + row * 128 + (((ch ^ row) & 7) << 4));
                 };
 #pragma unroll 1
-                for (int c6 = 0; c6 < D / CP; ++c6) {
-#pragma unroll
+                for (int c6 = 0; c6 < cols; c6 += CP) {
+#pragma unroll 1
                     for (int hf = 0; hf < CP / 32; ++hf) {
                         float ov[32];
-                        ws_ld32(lane_base + (uint32_t)(qi * D + CP * c6 + 32 * hf), ov);
+                        ws_ld32(lane_base + (uint32_t)(o0 + c6 + 32 * hf), ov);
                         ws_wait_ld();
+                        if (sg.alt) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) ov[k] = f[0] == 0.f ? 0.f : ov[k] * f[0];
+                            if (other) {
+                                float ow[32];
+                                ws_ld32(lane_base + (uint32_t)(D + o0 + c6 + 32 * hf), ow);
+                                ws_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) ov[k] = f[1] == 0.f ? ov[k] : fmaf(ow[k], f[1], ov[k]);
+                            }
+                        }
+                        if (whole) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) ov[k] = real ? ov[k] * inv : 0.f;
+                        }
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             *stg(r, 8 * hf + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
@@ -765,14 +864,33 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     for (int it = 0; it < CPL; ++it) {
                         const int rr = (warp & 3) * 32 + (32 / CPL) * it + lane / CPL, ch = lane % CPL;
                         const int rtl = rr / p.G;
-                        if (rtl < p.tq && c0 + rtl < sg.tokens)
-                            *reinterpret_cast<float4*>(p.part_o + (row_a + rr) * D + CP * c6 + 4 * ch) = *stg(rr, ch);
+                        if (rtl < p.tq && c0 + rtl < sg.tokens) {
+                            const float4 w = *stg(rr, ch);
+                            if (whole) {
+                                const long long row =
+                                    ((long long)sg.b * p.T + sg.n0 + c0 + rtl) * p.Hq + sg.h * p.G + (rr - rtl * p.G);
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + col0 + c6 + 4 * ch) =
+                                    make_uint2(pack_bf16x2(w.x, w.y), pack_bf16x2(w.z, w.w));
+                            } else {
+                                *reinterpret_cast<float4*>(p.part_o + (row_a + rr) * D + col0 + c6 + 4 * ch) = w;
+                            }
+                        }
                     }
                     __syncwarp();
                 }
                 // O is read: the next segment's first product may overwrite it
                 // (it waits for this warpgroup's next P)
                 ws_fence_before();
+            }
+            if (sg.alt) {
+                // ... and for the other's reading of it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->both[1]);
+                if (!ws_wait(&bars->both[1], joins & 1, abort)) {
+                    give_up();
+                    break;
+                }
+                ++joins;
             }
             idx0 += sg.nt;
             base += nt;
@@ -791,81 +909,81 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
 // ---------------------------------------------------------------------------
 // combine
 // ---------------------------------------------------------------------------
-constexpr int kTrCombineWarps = 8;
+constexpr int kTrCombineThreads = 256;
 
-// One warp per (sequence, token, q head): lane l holds D / 32 columns.  The parts
-// are the shares of its column (two each when its warpgroups took alternate tiles).
+// One CTA per (column, p.comb_rows of its rows); columns that one share held whole are
+// done already.  D / 4 lanes a row, 16 bytes each; a batch of eight parts is in flight at
+// once, joined to those before by the running maximum.
 template <int D>
-__global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int NC = D / 32, NQ = TrShape<D>::NQ;
+__global__ void __launch_bounds__(kTrCombineThreads) tree_combine_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int LPR = D / 4 < 32 ? D / 4 : 32, NC = D / 4 / LPR;        // lanes of a row; 16-byte chunks of a lane
+    constexpr int U = NC == 1 ? 8 : 4;
     tr_pdl_launch();
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * kTrCombineWarps + (threadIdx.x >> 5);
-    const bool mine = w < (long long)p.B * p.T * p.Hq;
-    const int qh = (int)(w % p.Hq), t = (int)(w / p.Hq % p.T), b = mine ? (int)(w / p.Hq / p.T) : 0;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int col = blockIdx.x, bh = col / p.ncol, m = col - bh * p.ncol, b = bh / p.Hkv, h = bh - b * p.Hkv;
+    const int tokens = min(p.mq, p.T - m * p.mq);
     tr_pdl_wait();
-    if (!mine) return;
-    long long units, before;
-    tr_partition(p, b, &units, &before);
-    const int shares = tr_shares(p, units), kt = tr_tiles(p, __ldg(p.pos + b));
-    const int h = qh / p.G, m = t / p.mq, tc = t - m * p.mq;              // its column, and token of the column
-    const int per = m < p.ncol - 1 ? NQ : p.last_units;
-    const bool alt = NQ == 2 && per == 1;
-    const long long u0 = before + (long long)kt * p.col_units * h + (long long)m * kt * NQ;
-    const int fx = streamk_share_of(u0, units, shares);
-    const int np = (streamk_share_of(u0 + (long long)kt * per - 1, units, shares) - fx + 1) * (alt ? 2 : 1);
-    const long long slot0 = fx + ((long long)b * p.Hkv + h) * p.ncol + m;
-    const int row = tc * p.G + qh % p.G;                                  // (a Q tile has tq G rows)
-    auto part = [&](int k) -> long long {
-        return alt ? (slot0 + (k >> 1)) * p.rows + (k & 1) * p.alt_off + row : (slot0 + k) * p.rows + row;
-    };
-    float M = -INFINITY;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(p.part_ml + part(k)).x);
+    const int2 sh = __ldcg(p.col_shares + col);
+    const int np = sh.y - sh.x + 1;
+    if (np <= 1) return;                                                  // one share: written whole
+    const long long slot = (long long)sh.x + col;
+    const int c = lane % LPR;
+#pragma unroll 1
+    for (int row = blockIdx.y * p.comb_rows + tid / LPR; row < min(tokens * p.G, (int)(blockIdx.y + 1) * p.comb_rows);
+         row += kTrCombineThreads / LPR) {
+        float M = -INFINITY, L = 0.f;
+        float4 acc[NC];
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f, acc[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) acc[c] = 0.f;
-    for (int base = 0; base < np; base += 32) {
-        float e = 0.f;
-        if (base + lane < np) {
-            const float2 v = __ldcg(p.part_ml + part(base + lane));
-            if (v.x != -INFINITY || v.y != v.y) {      // (NaN scores leave no maximum, but a sum of NaN)
-                e = exp2f(v.x - M);
-                L += v.y * e;
-            }
-        }
-        const int cnt = min(32, np - base);
-        // eight parts' loads in flight; an empty part's o may hold anything: not read
-        constexpr int U = NC == 8 ? 4 : 8;
-        for (int k0 = 0; k0 < cnt; k0 += U) {
-            float v[U][NC], ek[U];
+        for (int k = 0; k < NC; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = 0; k0 < np; k0 += U) {
+            float2 ml[U];
+            float4 o[U][NC];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                ek[u] = __shfl_sync(0xffffffffu, e, (k0 + u) & 31);
-                if (k0 + u >= cnt) ek[u] = 0.f;
-                const float* o = p.part_o + part(base + k0 + u) * D + lane * NC;
+                const long long at = (slot + min(k0 + u, np - 1)) * p.rows + row;
+                ml[u] = k0 + u < np ? __ldcg(p.part_ml + at) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                for (int c = 0; c < NC; c += 2) {
-                    float2 w2 = make_float2(0.f, 0.f);
-                    if (ek[u] != 0.f) w2 = __ldcg(reinterpret_cast<const float2*>(o + c));
-                    v[u][c] = w2.x;
-                    v[u][c + 1] = w2.y;
+                for (int k = 0; k < NC; ++k)
+                    o[u][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + k * LPR + c);
+            }
+            float mn = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+            const float a = M == -INFINITY ? 1.f : exp2f(M - mn);         // (nothing yet, or a sum of NaN)
+            L *= a;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                acc[k].x *= a;
+                acc[k].y *= a;
+                acc[k].z *= a;
+                acc[k].w *= a;
+            }
+            M = mn;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // (an empty part's o may hold anything; NaN scores leave no maximum, but a sum of NaN)
+                if (ml[u].x == -INFINITY && ml[u].y == ml[u].y) continue;
+                const float e = exp2f(ml[u].x - mn);
+                L = fmaf(ml[u].y, e, L);
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    acc[k].x = fmaf(o[u][k].x, e, acc[k].x);
+                    acc[k].y = fmaf(o[u][k].y, e, acc[k].y);
+                    acc[k].z = fmaf(o[u][k].z, e, acc[k].z);
+                    acc[k].w = fmaf(o[u][k].w, e, acc[k].w);
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int c = 0; c < NC; ++c) acc[c] = fmaf(v[u][c], ek[u], acc[c]);
         }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int t = row / p.G;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                             (((long long)b * p.T + m * p.mq + t) * p.Hq + h * p.G + (row - t * p.G)) * D;
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+            *reinterpret_cast<uint2*>(dst + 4 * (k * LPR + c)) =
+                make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + w * D + lane * NC;
-#pragma unroll
-    for (int c = 0; c < NC; c += 2)
-        *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
 }
 
 cudaLaunchConfig_t tr_config(dim3 grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -899,10 +1017,14 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
     cudaLaunchConfig_t cfg = tr_config(dim3(p.ctas), TrShape<D>::Threads, kSmem, stream, &attr);
     e = cudaLaunchKernelEx(&cfg, tree_kernel<D>, p, maps);
     if (e != cudaSuccess) return e;
-    const long long warps = (long long)p.B * p.T * p.Hq;
-    cfg = tr_config(dim3((unsigned)((warps + kTrCombineWarps - 1) / kTrCombineWarps)), kTrCombineWarps * 32, 0, stream,
-                    &attr);
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
+    // few columns, each of many shares: a row a warp; many: four, so that a CTA's way to its
+    // parts is paid once for them
+    TreeParams c = p;
+    const long long cols = (long long)p.B * p.Hkv * p.ncol;
+    const int rows = (p.T < p.mq ? p.T : p.mq) * p.G, pass = kTrCombineThreads / (D / 4 < 32 ? D / 4 : 32);
+    c.comb_rows = cols * rows <= 152LL * 8 * pass ? pass : 4 * pass;
+    cfg = tr_config(dim3((unsigned)cols, (rows + c.comb_rows - 1) / c.comb_rows), kTrCombineThreads, 0, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, c);
 }
 
 }  // namespace

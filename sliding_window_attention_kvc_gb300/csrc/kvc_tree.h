@@ -47,14 +47,16 @@ struct TreeParams {
     uint32_t* err;
     float2* part_ml;            // [slots][rows]: slot = share + column
     float* part_o;
+    int2* col_shares;           // [columns]: the first and the last share of each
     int B, T, Hq, Hkv, G, layer;
     int layout, window, sinks, capacity, bs, num_blocks, maxb;
     int tq, mq, ncol;           // tokens of a Q tile, of a column; columns of a (sequence, kv head)
     int col_units;              // units a tile of all columns of a kv head
     int last_units;             // units a tile of the last column: its Q tiles
-    int rows, alt_off;          // partial rows of a slot; to those of its second warpgroup
+    int rows;                   // partial rows of a slot
     int slot_whole;             // window layouts: the map brings every column block in one copy
     int ctas;
+    int comb_rows;              // rows of a combine CTA
     int rope;
     float scale2;               // softmax scale * log2(e)
     unsigned long long theta[kMaxHalfDim];
