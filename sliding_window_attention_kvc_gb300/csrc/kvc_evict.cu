@@ -24,15 +24,16 @@ constexpr int kWeighParts = kWeighThreads / (kWeighRows / 4);   // head groups t
 // heads, in head order; the quarters, then the rows of each block, are added in
 // order: the same sums whatever the decode's shares were.  What bounds it: 4 bytes a
 // row and head, which the decode has just left in L2, and an exponential for each.
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ WeighParams p) {
+__global__ void __launch_bounds__(kWeighThreads, 6) weigh_kernel(const __grid_constant__ WeighParams p) {
     __shared__ float4 s_part[kWeighThreads];
     __shared__ float s_row[kWeighRows];
     __shared__ float s_warp[kWeighThreads / 32];
-    constexpr int U = 8;                            // heads in flight
+    constexpr int U = 4;                            // heads in flight
     const int tid = threadIdx.x, b = blockIdx.y;
     const int lb0 = blockIdx.x * p.per;
     const int32_t* trow = p.table + (long long)b * p.maxb;
-    ev_pdl_wait();
+    // (positions, table and valid bits were final before the decode could start the kernels
+    // behind it: they are read while it runs)
     ev_pdl_launch();
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
     const float* sc = p.scores + (long long)b * p.Hq * p.stride;
@@ -91,7 +92,9 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     const long long pos0 = (long long)lb0 * p.bs, lead = pos0 & 3;    // rows read in front of the first
     if (p.per == 1) {                               // one block, its rows in turn
         float a = 0.f;
-        if (pos0 <= t && attended(lb0)) {           // (uniform)
+        const bool on = pos0 <= t && attended(lb0); // (uniform)
+        ev_pdl_wait();
+        if (on) {
             const long long end = min(pos0 + p.bs - 1, (long long)t);
             for (long long r0 = pos0 - lead; r0 <= end; r0 += kWeighRows) {
                 rows(r0);
@@ -112,6 +115,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     }
     const bool mine = tid < p.per && lb0 + tid < p.maxb;
     const bool on = mine && pos0 + (long long)tid * p.bs <= t && attended(lb0 + tid);
+    ev_pdl_wait();
     if (pos0 <= t) rows(pos0 - lead);               // (uniform)
     if (mine) {
         float sum = 0.f;
@@ -165,13 +169,15 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
 
 // A cluster of CTAs per sequence, a contiguous part of its blocks each: the excess
 // over `keep` of its mapped blocks, lightest first, ties by the lowest index, from a
-// radix search of the excess-th lightest (four digits; every CTA counts its own
-// keys, kept in shared memory, and adds up the cluster's counts).  Blocks whose
-// count reaches zero are marked; the last CTA to finish (an atomic ticket, no
-// waiting) puts the marked ones on the free list in ascending order and clears
-// their resident bits.
-// What bounds it: a few dependent trips to L2 and as many cluster barriers, whatever
-// the length (a single CTA took 309 us for two sequences of up to 62,500 blocks).
+// radix search of the excess-th lightest (four digits at most: it ends where a digit
+// takes all of its keys; every CTA counts its own keys, kept in shared memory, and
+// adds up the cluster's counts).  Blocks whose count reaches zero are marked; the
+// last CTA to finish (an atomic ticket, no waiting) puts the marked ones on the
+// free list in ascending order and clears their resident bits.
+// What bounds it: a dozen dependent trips to L2, barriers and a cold instruction
+// cache, whatever the length (a single CTA a sequence took 309 us for two of up to
+// 62,500 blocks; the free list written a word of 32 marks a thread, 32 lines a store,
+// held it at 83).
 constexpr int kEvictKeys = 8192;                // keys a CTA keeps
 constexpr uint32_t kKeyStays = 0xffffffffu;     // not among the blocks that may go
 
@@ -182,11 +188,18 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     __shared__ int s_hist[4][256];
     __shared__ int s_w[kEvictWarps];
     __shared__ int s_count[2];                  // mapped, and those that may go
-    __shared__ int s_digit, s_beyond, s_last;
+    __shared__ int s_digit, s_beyond, s_in, s_last;
     __shared__ uint32_t s_key[kEvictKeys];
-    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x / CL;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x / CL;
+    auto sync_all = [&]() {
+        if (CL > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     for (int i = tid; i < 4 * 256; i += kEvictThreads) s_hist[0][i] = 0;
     if (tid < 2) s_count[tid] = 0;
+    __syncthreads();
     ev_pdl_wait();
     ev_pdl_launch();
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
@@ -196,11 +209,8 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     const int hi = nb - p.recent;               // blocks first .. hi - 1 may go
     const int lo_i = (int)((long long)nb * rank / CL), hi_i = (int)((long long)nb * (rank + 1) / CL);
     const bool kept = hi_i - lo_i <= kEvictKeys;
-    auto key_of = [&](int i) -> uint32_t {
-        return i >= p.first && i < hi && trow[i] >= 0 ? weight_key(wrow[i]) : kKeyStays;
-    };
-    __syncthreads();
     int live = 0, loose = 0;
+#pragma unroll 1
     for (int base = lo_i; base < hi_i; base += 4 * kEvictThreads) {
         int e[4];
         float w[4];
@@ -219,32 +229,36 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
             if (kept && i < hi_i) s_key[i - lo_i] = may ? weight_key(w[u]) : kKeyStays;
         }
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        live += __shfl_xor_sync(0xffffffffu, live, off);
-        loose += __shfl_xor_sync(0xffffffffu, loose, off);
-    }
+    live = __reduce_add_sync(0xffffffffu, live);
+    loose = __reduce_add_sync(0xffffffffu, loose);
     if (lane == 0) {
         atomicAdd(&s_count[0], live);
         atomicAdd(&s_count[1], loose);
     }
-    cluster.sync();
+    sync_all();
     int nlive = 0, nloose = 0;
+#pragma unroll 1
     for (int c = 0; c < CL; ++c) {
         const int* o = cluster.map_shared_rank(s_count, c);
         nlive += o[0];
         nloose += o[1];
     }
+    // this thread's key of index i (a long table's keys are worked out again)
+    auto key_of = [&](int i) -> uint32_t {
+        if (i >= hi_i) return kKeyStays;
+        if (kept) return s_key[i - lo_i];
+        return i >= p.first && i < hi && trow[i] >= 0 ? weight_key(wrow[i]) : kKeyStays;
+    };
     int want = min(nlive - p.keep, nloose);
-    const bool some = want > 0;                 // (the same in every CTA of the cluster)
-    uint32_t prefix = 0, mask = 0;
-    int digit = 0;
-    if (some) {
-        for (int pass = 0; pass < 4; ++pass) {
+    if (want > 0) {                             // (the same in every CTA of the cluster)
+        uint32_t prefix = 0, mask = 0;
+        int digit = 0, pass = 0;
+#pragma unroll 1
+        for (;; ++pass) {
             const int shift = 24 - 8 * pass;
+#pragma unroll 1
             for (int base = lo_i; base < hi_i; base += kEvictThreads) {
-                const int i = base + tid;
-                const uint32_t key = i < hi_i ? (kept ? s_key[i - lo_i] : key_of(i)) : kKeyStays;
+                const uint32_t key = key_of(base + tid);
                 const bool in = key != kKeyStays && (key & mask) == prefix;
                 const uint32_t d = (key >> shift) & 255u;
                 const unsigned act = __ballot_sync(0xffffffffu, in);
@@ -253,35 +267,27 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
                     if (lane == __ffs(same) - 1) atomicAdd(&s_hist[pass][d], __popc(same));
                 }
             }
-            cluster.sync();
-            if (tid < 32) {
-                int c[8], sum = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) c[k] = 0;
-                for (int o = 0; o < CL; ++o) {
-                    const int4* h = reinterpret_cast<const int4*>(cluster.map_shared_rank(&s_hist[pass][0], o)) + lane * 2;
-                    const int4 x = h[0], y = h[1];
-                    c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
-                    c[4] += y.x; c[5] += y.y; c[6] += y.z; c[7] += y.w;
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum += c[k];
-                int incl = sum;
+            sync_all();
+            // a thread a digit: its keys in the cluster, and those of smaller digits
+            int mine = 0, incl = 0;
+            if (tid < 256) {
+#pragma unroll 1
+                for (int o = 0; o < CL; ++o) mine += *cluster.map_shared_rank(&s_hist[pass][tid], o);
+                incl = mine;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const int a = __shfl_up_sync(0xffffffffu, incl, off);
                     if (lane >= off) incl += a;
                 }
-                int run = incl - sum;
-                if (run < want && incl >= want) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (run < want && run + c[k] >= want) {
-                            s_digit = lane * 8 + k;
-                            s_beyond = run;
-                        }
-                        run += c[k];
-                    }
+                if (lane == 31) s_w[warp] = incl;
+            }
+            __syncthreads();
+            if (tid < 256) {
+                for (int w = 0; w < warp; ++w) incl += s_w[w];
+                if (incl >= want && incl - mine < want) {
+                    s_digit = tid;
+                    s_beyond = incl - mine;
+                    s_in = mine;
                 }
             }
             __syncthreads();
@@ -289,62 +295,87 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
             want -= s_beyond;
             prefix |= (uint32_t)digit << shift;
             mask |= 255u << shift;
+            if (pass == 3 || s_in == want) break;       // all that begin with these digits go, or all four are known
             __syncthreads();
         }
-        // keys below `prefix` go, and the first `want` of those equal to it: so many lie in the CTAs before
+        // keys whose digits lie below `prefix` go, and the first `want` of those that begin with it: so many of
+        // them lie in the CTAs before
         int before = 0;
-        for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&s_hist[3][digit], c);
-        const int mine = s_hist[3][digit];
-        const int take = before >= want ? 0 : min(mine, want - before);      // of this CTA's
-        int run = 0;                            // equal keys before this pass
-        for (int base = lo_i; base < hi_i; base += kEvictThreads) {
-            const int i = base + tid;
-            const uint32_t key = i < hi_i ? (kept ? s_key[i - lo_i] : key_of(i)) : kKeyStays;
-            bool goes = key < prefix;
-            if (take == mine) {
-                goes = goes || (take > 0 && key == prefix);
-            } else if (take > 0) {              // (uniform)
-                int tot;
-                const int same = key == prefix, ex = evict_scan(same, s_w, &tot);
-                goes = goes || (same && run + ex < take);
-                run += tot;
+#pragma unroll 1
+        for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&s_hist[pass][digit], c);
+        const int own = s_hist[pass][digit];
+        const int take = before >= want ? 0 : min(own, want - before);      // of this CTA's
+        int run = 0;                            // such keys before this pass
+#pragma unroll 1
+        for (int base = lo_i; base < hi_i; base += 4 * kEvictThreads) {
+            int phys[4], old[4];
+            unsigned goes = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = base + u * kEvictThreads + tid;
+                const uint32_t key = key_of(i), top = key & mask;
+                bool g = key != kKeyStays && top < prefix;
+                const bool same = key != kKeyStays && top == prefix;
+                if (take == own) {
+                    g = g || same;
+                } else if (take > 0) {          // (uniform)
+                    int tot;
+                    const int ex = evict_scan(same, s_w, &tot);
+                    g = g || (same && run + ex < take);
+                    run += tot;
+                }
+                goes |= (unsigned)g << u;
+                phys[u] = g ? trow[i] : 0;
             }
-            if (goes) {
-                const int phys = trow[i];
-                trow[i] = -1;
-                wrow[i] = 0.f;
-                if (phys >= p.num_blocks)
-                    set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
-                else if (atomicSub(&p.refcount[phys], 1) == 1)
-                    atomicOr(&p.back[phys >> 5], 1u << (phys & 31));
-            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if ((goes >> u) & 1u) {
+                    const int i = base + u * kEvictThreads + tid;
+                    trow[i] = -1;
+                    wrow[i] = 0.f;
+                    old[u] = 0;
+                    if (phys[u] >= p.num_blocks)
+                        set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+                    else
+                        old[u] = atomicSub(&p.refcount[phys[u]], 1);
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (((goes >> u) & 1u) && old[u] == 1) atomicOr(&p.back[phys[u] >> 5], 1u << (phys[u] & 31));
         }
     }
     __threadfence();
-    cluster.sync();                             // no CTA leaves while its counts are read
+    sync_all();                                 // no CTA leaves while its counts are read
     if (tid == 0) s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
     const int words = (p.num_blocks + 31) / 32;
     int at = *p.free_count;
+#pragma unroll 1
     for (int base = 0; base < words; base += kEvictThreads) {
         const int i = base + tid;
-        uint32_t w = i < words ? __ldcg(p.back + i) : 0u;
+        const uint32_t w = i < words ? __ldcg(p.back + i) : 0u;
         int tot;
-        int k = at + evict_scan(__popc(w), s_w, &tot);
+        const int k = at + evict_scan(__popc(w), s_w, &tot);
         if (w) {
             p.back[i] = 0u;
             if (p.valid) p.valid[i] &= ~w;
         }
-        while (w) {
-            const int f = i * 32 + __ffs(w) - 1;
-            w &= w - 1u;
-            if (k >= 0 && k < p.num_blocks)
-                p.free_list[k] = f;
-            else
-                index_fault(p.err, 41, k);
-            ++k;
+        // the warp's words one after the other, a lane a mark: neighbours on the list are written together
+        unsigned some = __ballot_sync(0xffffffffu, w != 0u);
+#pragma unroll 1
+        while (some) {
+            const int src = __ffs(some) - 1;
+            some &= some - 1u;
+            const uint32_t v = __shfl_sync(0xffffffffu, w, src);
+            const int to = __shfl_sync(0xffffffffu, k, src) + __popc(v & ((1u << lane) - 1u));
+            if ((v >> lane) & 1u) {
+                if (to >= 0 && to < p.num_blocks)
+                    p.free_list[to] = (i - lane + src) * 32 + lane;
+                else
+                    index_fault(p.err, 41, to);
+            }
         }
         at += tot;
     }

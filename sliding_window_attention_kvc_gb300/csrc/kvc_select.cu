@@ -38,7 +38,7 @@ cudaLaunchConfig_t sl_config(dim3 grid, int threads, int smem, cudaStream_t stre
 // bounds
 // ---------------------------------------------------------------------------
 constexpr int kBoundsThreads = 128;
-constexpr int kBoundsWarps = 152 * 24;         // warps that fill the GPU
+constexpr int kBoundsWarps = 152 * 48;         // warps that keep the GPU full
 
 // 16 bytes of a key row as floats.
 template <typename Elt>
@@ -52,10 +52,67 @@ __device__ __forceinline__ void key_values(const uint4& w, float scale, float* f
     }
 }
 
+// The larger and the smaller of 16 bytes of values, kept as they come (bf16 pairs) or as floats.
+template <typename Elt>
+struct Ends {
+    static constexpr int VPL = 16 / (int)sizeof(Elt);
+    static constexpr bool kPacked = sizeof(Elt) == 2;
+    static constexpr int N = kPacked ? VPL / 2 : VPL;
+    float f[kPacked ? 1 : N];
+    uint32_t w[kPacked ? N : 1];
+    __device__ __forceinline__ void init(float x) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if constexpr (kPacked)
+                w[i] = pack_bf16x2(x, x);
+            else
+                f[i] = x;
+    }
+    template <bool MAX>
+    static __device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a), y = *reinterpret_cast<const __nv_bfloat162*>(&b);
+        const __nv_bfloat162 z = MAX ? __hmax2(x, y) : __hmin2(x, y);
+        return *reinterpret_cast<const uint32_t*>(&z);
+    }
+    template <bool MAX>
+    __device__ __forceinline__ void join(const uint4& v, float scale) {
+        if constexpr (kPacked) {
+            w[0] = pair<MAX>(w[0], v.x);
+            w[1] = pair<MAX>(w[1], v.y);
+            w[2] = pair<MAX>(w[2], v.z);
+            w[3] = pair<MAX>(w[3], v.w);
+        } else {
+            float x[VPL];
+            key_values<Elt>(v, scale, x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = MAX ? fmaxf(f[i], x[i]) : fminf(f[i], x[i]);
+        }
+    }
+    // joined with what lane ^ off has
+    template <bool MAX>
+    __device__ __forceinline__ void exchange(int off) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if constexpr (kPacked) {
+                w[i] = pair<MAX>(w[i], __shfl_xor_sync(0xffffffffu, w[i], off));
+            } else {
+                const float o = __shfl_xor_sync(0xffffffffu, f[i], off);
+                f[i] = MAX ? fmaxf(f[i], o) : fminf(f[i], o);
+            }
+    }
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (kPacked)
+            return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        else
+            return f[i];
+    }
+};
+
 // One warp per touched block of a sequence and `heads` kv heads.  A lane keeps the
 // ends of 16 bytes of the row (32 on rows of 1 KB); 512 / row bytes rows pass at
 // once.  The block is read whole from its first row, so that the result does not
-// depend on what was there before.
+// depend on what was there before.  Where lanes are left over, one group of them
+// makes the codes of the largest values and the next those of the smallest.
 template <typename Elt, int D>
 __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int VPL = 16 / (int)sizeof(Elt);            // values of a chunk
@@ -87,16 +144,18 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __gr
     }
     const int rows = (int)min((long long)p.bs, end - lb * p.bs);
     const int c = lane % LPR, r0 = lane / LPR;
+#pragma unroll 1
     for (int h = h0; h < min(h0 + p.heads, p.Hkv); ++h) {
         const long long row0 = ((long long)phys * p.Hkv + h) * p.bs;
         const Elt* src = static_cast<const Elt*>(p.cache) + p.layer_off + row0 * D;
         const float* sc = sizeof(Elt) == 1 ? p.scales + p.sc_layer_off + row0 : nullptr;
-        float hi[NCH * VPL], lo[NCH * VPL];
+        Ends<Elt> hi[NCH], lo[NCH];
 #pragma unroll
-        for (int i = 0; i < NCH * VPL; ++i) {
-            hi[i] = -INFINITY;
-            lo[i] = INFINITY;
+        for (int k = 0; k < NCH; ++k) {
+            hi[k].init(-INFINITY);
+            lo[k].init(INFINITY);
         }
+#pragma unroll 1
         for (int base = r0; base < rows; base += U * RPW) {
             uint4 w[U][NCH];
             float s[U];
@@ -112,49 +171,44 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __gr
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < NCH; ++k) {
-                    float f[VPL];
-                    key_values<Elt>(w[u][k], s[u], f);
-#pragma unroll
-                    for (int i = 0; i < VPL; ++i) {
-                        hi[k * VPL + i] = fmaxf(hi[k * VPL + i], f[i]);
-                        lo[k * VPL + i] = fminf(lo[k * VPL + i], f[i]);
-                    }
+                    hi[k].template join<true>(w[u][k], s[u]);
+                    lo[k].template join<false>(w[u][k], s[u]);
                 }
         }
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < NCH * VPL; ++i) {
+        for (int k = 0; k < NCH; ++k) {
 #pragma unroll
             for (int off = LPR; off < 32; off <<= 1) {
-                hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
-                lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
+                hi[k].template exchange<true>(off);
+                lo[k].template exchange<false>(off);
             }
-            a = fmaxf(a, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) a = fmaxf(a, fmaxf(fabsf(hi[k].value(i)), fabsf(lo[k].value(i))));
         }
 #pragma unroll
         for (int off = 1; off < LPR; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
         const float step = __fdiv_rn(a, 127.f);
         const long long at = (long long)phys * p.Hkv + h;
         if (lane == 0) p.steps[at] = step;
-        if (lane < LPR) {
-            int8_t* dst = p.codes + at * 2 * D;
+        // codes: lanes below LPR the largest, the next LPR the smallest (where a row takes the whole warp, both)
+        constexpr int BOTH = RPW == 1 ? 2 : 1;
+        if (r0 < 2) {
 #pragma unroll
             for (int k = 0; k < NCH; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int q = 0; q < BOTH; ++q) {
+                    const int e = BOTH == 2 ? q : r0;
                     uint32_t w[VPL / 4];
 #pragma unroll
                     for (int i = 0; i < VPL / 4; ++i) w[i] = 0u;
 #pragma unroll
                     for (int i = 0; i < VPL; ++i) {
-                        int code = 0;
-                        if (step > 0.f) {
-                            const float x = __fdiv_rn(e ? lo[k * VPL + i] : hi[k * VPL + i], step);
-                            code = e ? (int)fmaxf(floorf(x), -127.f) : (int)fminf(ceilf(x), 127.f);
-                        }
+                        const float x = step > 0.f ? __fdiv_rn(e ? lo[k].value(i) : hi[k].value(i), step) : 0.f;
+                        const int code = e ? (int)fmaxf(floorf(x), -127.f) : (int)fminf(ceilf(x), 127.f);
                         w[i >> 2] |= (uint32_t)(code & 0xff) << (8 * (i & 3));
                     }
-                    int8_t* d = dst + e * D + (k * LPR + c) * VPL;
+                    int8_t* d = p.codes + at * 2 * D + e * D + (k * LPR + c) * VPL;
                     if constexpr (VPL == 4)
                         *reinterpret_cast<uint32_t*>(d) = w[0];
                     else if constexpr (VPL == 8)
@@ -187,6 +241,7 @@ cudaError_t launch_bounds_t(const BoundsParams& p, cudaStream_t stream) {
 // scores
 // ---------------------------------------------------------------------------
 constexpr int kScoreThreads = 128;
+constexpr int kScoreCtas = 152 * 8;            // CTAs that keep the GPU full
 
 // Order of floats as unsigned integers; -0 counts as 0, NaN as the least.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -197,50 +252,54 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 
 // One CTA per (chunk of blocks, kv head, sequence).  The group's q heads as
 // codes in shared memory, positive and negative parts apart: hi meets the one
-// and lo the other.  A warp scores 32 blocks, a lane keeping track of each; D / 16
-// lanes hold a block's codes, 16 channels of each end a lane, 4 x 512 / D blocks at
-// once; the first ones are on their way while the queries are made codes.
+// and lo the other.  A warp scores groups of 32 blocks, a lane keeping track of
+// each; D / 16 lanes hold a block's codes, 16 channels of each end a lane, U x 512 / D
+// blocks at once, and the next ones (the first while the queries are made codes)
+// are on their way meanwhile.
 template <typename Act, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int LPB = D / 16, BPW = 32 / LPB, U = 4, NP = D / 64;
-    extern __shared__ __align__(16) unsigned char s_q[];          // [G][2][D] codes, then [G] steps
+    constexpr int LPB = D / 16, BPW = 32 / LPB, U = D == 64 ? 2 : 4, NP = D / 64, W = kScoreThreads / 32;
+    constexpr int IT = 32 / (U * BPW);                                // steps of a group
+    extern __shared__ __align__(16) unsigned char s_q[];              // [G][2][D] codes, then [G] steps
     int8_t* codes = reinterpret_cast<int8_t*>(s_q);
     float* s_step = reinterpret_cast<float*>(s_q + (size_t)p.G * 2 * D);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, b = blockIdx.z;
     sl_pdl_wait();
     sl_pdl_launch();
-    const int c0 = blockIdx.x * kScoreChunk;
-    // a warp's blocks, one a lane: their table entries while the queries are read
-    constexpr int PW = kScoreChunk / (kScoreThreads / 32);            // blocks of a warp
-    static_assert(PW == 32, "a lane a block");
-    const int w0 = c0 + warp * PW;
+    const int c0 = blockIdx.x * kScoreChunk * p.groups;
     const int32_t* trow = p.table + (long long)b * p.maxb;
-    int my_phys = w0 + lane < p.maxb ? __ldg(trow + w0 + lane) : -1;
+    // this lane's block of a group: its entry as it stands
+    auto entry = [&](int lb) { return lb < p.maxb ? __ldg(trow + lb) : -1; };
+    int raw = entry(c0 + warp * 32 + lane);
     const int traw = p.pos[b];
     const int t = clamp_paged_t(traw, p.maxb, p.bs);
     if ((traw < 0 || traw != t) && blockIdx.x == 0 && h == 0 && tid == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
-    const int c1 = min(nb, c0 + kScoreChunk);
+    const int c1 = min(nb, c0 + kScoreChunk * p.groups);
     if (c0 >= c1) return;
-    if (w0 + lane >= c1) my_phys = -1;
-    if (my_phys >= p.num_blocks) {
-        set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
-        my_phys = -1;
-    }
-    if (my_phys >= 0 && p.valid && !((__ldg(p.valid + (my_phys >> 5)) >> (my_phys & 31)) & 1u)) my_phys = -1;
+    auto resident = [&](int lb, int phys) -> int {
+        if (lb >= c1) return -1;
+        if (phys >= p.num_blocks) {
+            set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+            return -1;
+        }
+        return phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u) ? -1 : phys;
+    };
+    int lb = c0 + warp * 32 + lane;
+    int phys = resident(lb, raw);
     const int ln = lane % LPB, sub = lane / LPB;
     uint4 hi[U], lo[U];
     float step[U];
-    auto load = [&](int it) {                                         // the ends of U BPW blocks of the warp
+    auto load = [&](int it) {                                         // the ends of U BPW blocks of the group
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int phys = __shfl_sync(0xffffffffu, my_phys, (it * U + u) * BPW + sub);
-            const long long at = (long long)max(phys, 0) * p.Hkv + h;
+            const int ph = __shfl_sync(0xffffffffu, phys, (it * U + u) * BPW + sub);
+            const long long at = (long long)max(ph, 0) * p.Hkv + h;
             const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
             hi[u] = lo[u] = make_uint4(0u, 0u, 0u, 0u);
             step[u] = 0.f;
-            if (phys >= 0) {
+            if (ph >= 0) {
                 hi[u] = __ldg(src + ln);
                 lo[u] = __ldg(src + LPB + ln);
                 step[u] = __ldg(p.steps + at);
@@ -248,85 +307,100 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         }
     };
     load(0);
-    for (int g = warp; g < p.G; g += kScoreThreads / 32) {
+#pragma unroll 1
+    for (int g = warp; g < p.G; g += W) {
         const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + g) * D;
         float x[2 * NP], a = 0.f;
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
             const int i = lane + 32 * m;
-            float x1 = EltTraits<Act>::to_f32(qr[i]), x2 = EltTraits<Act>::to_f32(qr[i + D / 2]);
-            if (p.rope != kRopeNone) {
+            x[2 * m] = EltTraits<Act>::to_f32(qr[i]);
+            x[2 * m + 1] = EltTraits<Act>::to_f32(qr[i + D / 2]);
+        }
+        if (p.rope != kRopeNone) {
+#pragma unroll
+            for (int m = 0; m < NP; ++m) {
                 float cs, sn;
-                rope_cos_sin((long long)t, p.theta[i], &cs, &sn);
-                const float y1 = x1 * cs - x2 * sn, y2 = x1 * sn + x2 * cs;
-                x1 = y1;
-                x2 = y2;
+                rope_cos_sin((long long)t, p.theta[lane + 32 * m], &cs, &sn);
+                const float x1 = x[2 * m], x2 = x[2 * m + 1];
+                x[2 * m] = x1 * cs - x2 * sn;
+                x[2 * m + 1] = x1 * sn + x2 * cs;
             }
-            x[2 * m] = x1;
-            x[2 * m + 1] = x2;
-            a = fmaxf(a, fmaxf(fabsf(x1), fabsf(x2)));
         }
 #pragma unroll
+        for (int m = 0; m < 2 * NP; ++m) a = fmaxf(a, fabsf(x[m]));
+#pragma unroll
         for (int off = 16; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        const float step = __fdiv_rn(a, 127.f);
+        const float sq = __fdiv_rn(a, 127.f);
 #pragma unroll
-        for (int m = 0; m < NP; ++m)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int code = q8_code(x[2 * m + e], step);
-                int8_t* d = codes + (size_t)g * 2 * D + lane + 32 * m + e * (D / 2);
-                d[0] = (int8_t)max(code, 0);
-                d[D] = (int8_t)min(code, 0);
-            }
-        if (lane == 0) s_step[g] = step;
+        for (int m = 0; m < 2 * NP; ++m) {
+            const int code = q8_code(x[m], sq);
+            int8_t* d = codes + (size_t)g * 2 * D + lane + 32 * (m >> 1) + (m & 1) * (D / 2);
+            d[0] = (int8_t)max(code, 0);
+            d[D] = (int8_t)min(code, 0);
+        }
+        if (lane == 0) s_step[g] = sq;
     }
     __syncthreads();
     uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
-    constexpr int IT = PW / (U * BPW);
-    float score = -INFINITY;                                          // of this lane's own block
 #pragma unroll 1
-    for (int it = 0; it < IT; ++it) {
-        float best[U];
+    for (;;) {
+        const int next = lb + W * 32, next_raw = next - lane < c1 ? entry(next) : -1;
+        const int cur = phys;
+        float score = -INFINITY;                                      // of this lane's own block
 #pragma unroll
-        for (int u = 0; u < U; ++u) best[u] = -INFINITY;
-        for (int g = 0; g < p.G; ++g) {
-            const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + 16 * ln);
-            const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + D + 16 * ln);
-            const float sq = s_step[g];
+        for (int it = 0; it < IT; ++it) {
+            uint4 h4[U], l4[U];
+            float st[U], best[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                int a = __dp4a((int)hi[u].x, (int)qp.x, 0);
-                int e = __dp4a((int)lo[u].x, (int)qn.x, 0);
-                a = __dp4a((int)hi[u].y, (int)qp.y, a);
-                e = __dp4a((int)lo[u].y, (int)qn.y, e);
-                a = __dp4a((int)hi[u].z, (int)qp.z, a);
-                e = __dp4a((int)lo[u].z, (int)qn.z, e);
-                a = __dp4a((int)hi[u].w, (int)qp.w, a);
-                e = __dp4a((int)lo[u].w, (int)qn.w, e);
-                a += e;
+                h4[u] = hi[u];
+                l4[u] = lo[u];
+                st[u] = step[u];
+                best[u] = -INFINITY;
+            }
+            if (it == IT - 1) phys = resident(next, next_raw);
+            if (it < IT - 1 || next - lane < c1) load(it < IT - 1 ? it + 1 : 0);
+#pragma unroll 1
+            for (int g = 0; g < p.G; ++g) {
+                const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + 16 * ln);
+                const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + D + 16 * ln);
+                const float sq = s_step[g];
 #pragma unroll
-                for (int off = 1; off < LPB; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                best[u] = fmaxf(best[u], __fmul_rn((float)a, __fmul_rn(sq, step[u])));
+                for (int u = 0; u < U; ++u) {
+                    int a = __dp4a((int)h4[u].x, (int)qp.x, 0);
+                    int e = __dp4a((int)l4[u].x, (int)qn.x, 0);
+                    a = __dp4a((int)h4[u].y, (int)qp.y, a);
+                    e = __dp4a((int)l4[u].y, (int)qn.y, e);
+                    a = __dp4a((int)h4[u].z, (int)qp.z, a);
+                    e = __dp4a((int)l4[u].z, (int)qn.z, e);
+                    a = __dp4a((int)h4[u].w, (int)qp.w, a);
+                    e = __dp4a((int)l4[u].w, (int)qn.w, e);
+                    a += e;
+#pragma unroll
+                    for (int off = 1; off < LPB; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+                    best[u] = fmaxf(best[u], __fmul_rn((float)a, __fmul_rn(sq, st[u])));
+                }
+            }
+            // the lane of each block takes its score
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = lane - (it * U + u) * BPW;              // this lane's block among these BPW
+                const float x = __shfl_sync(0xffffffffu, best[u], (j & (BPW - 1)) * LPB);
+                if (j >= 0 && j < BPW) score = x;
             }
         }
-        if (it + 1 < IT) load(it + 1);
-        // the lane of each block takes its score
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = lane - (it * U + u) * BPW;                  // this lane's block among these BPW
-            const float x = __shfl_sync(0xffffffffu, best[u], (j & (BPW - 1)) * LPB);
-            if (j >= 0 && j < BPW) score = x;
-        }
+        if (lb < c1)
+            keys[lb] = cur < 0 ? 0u : (lb < p.first || lb >= nb - p.recent) ? 0xffffffffu : score_key(score);
+        if (next - lane >= c1) break;                                 // (uniform in the warp)
+        lb = next;
     }
-    const int lb = w0 + lane;
-    if (lb < c1)
-        keys[lb] = my_phys < 0 ? 0u : (lb < p.first || lb >= nb - p.recent) ? 0xffffffffu : score_key(score);
 }
 
 // ---------------------------------------------------------------------------
 // selection
 // ---------------------------------------------------------------------------
-constexpr int kPickThreads = 512;
+constexpr int kPickThreads = 256;
 constexpr int kPickWarps = kPickThreads / 32;
 
 // Sums over the CTA's threads before this one, of two counts at once; totals in *tot.
@@ -574,8 +648,13 @@ cudaError_t launch_block_bounds(int dtype, int D, const BoundsParams& p, cudaStr
 cudaError_t launch_select(int dtype, int D, const SelectParams& p, cudaStream_t s) {
     cudaLaunchAttribute attr;
     const int smem = p.G * (2 * D + 4);
-    cudaLaunchConfig_t cfg =
-        sl_config(dim3((p.maxb + kScoreChunk - 1) / kScoreChunk, p.Hkv, p.B), kScoreThreads, smem, s, &attr);
+    // a CTA walks several chunks where there are more than enough of them
+    SelectParams sp = p;
+    const long long chunks = (p.maxb + kScoreChunk - 1) / kScoreChunk, units = chunks * p.Hkv * p.B;
+    sp.groups = 1;
+    while (sp.groups < 8 && units / (2 * sp.groups) >= kScoreCtas) sp.groups *= 2;
+    cudaLaunchConfig_t cfg = sl_config(dim3((unsigned)((chunks + sp.groups - 1) / sp.groups), p.Hkv, p.B), kScoreThreads,
+                                       smem, s, &attr);
     cudaError_t e = cudaErrorInvalidValue;
     // (above 48 KB, groups of more than 93 heads of 256, a kernel asks for its shared memory)
 #define KVC_CASE(F, A, DD)                                                                                   \
@@ -583,14 +662,14 @@ cudaError_t launch_select(int dtype, int D, const SelectParams& p, cudaStream_t 
         e = smem > 48 * 1024 ? cudaFuncSetAttribute(block_score_kernel<A, DD>,                               \
                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem)       \
                              : cudaSuccess;                                                                  \
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, block_score_kernel<A, DD>, p);                    \
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, block_score_kernel<A, DD>, sp);                    \
     }
     KVC_CASE(true, float, 64) KVC_CASE(true, float, 128) KVC_CASE(true, float, 256)
     KVC_CASE(false, __nv_bfloat16, 64) KVC_CASE(false, __nv_bfloat16, 128) KVC_CASE(false, __nv_bfloat16, 256)
 #undef KVC_CASE
     if (e != cudaSuccess) return e;
     cfg = sl_config(dim3(p.Hkv, p.B), kPickThreads, 0, s, &attr);
-    return cudaLaunchKernelEx(&cfg, block_pick_kernel, p);
+    return cudaLaunchKernelEx(&cfg, block_pick_kernel, sp);
 }
 
 cudaError_t launch_select_plan(const SelectPlanParams& p, cudaStream_t s) {

@@ -7,7 +7,7 @@
 
 namespace kvc {
 
-constexpr int kScoreChunk = 128;       // logical blocks of a sequence that one CTA scores
+constexpr int kScoreChunk = 128;       // logical blocks that the warps of a CTA score at once, 32 each
 
 // Bounds of blocks (kvc_block_bounds): codes [layers][num_blocks][Hkv][2][D]
 // (largest, smallest), then their steps [layers][num_blocks][Hkv].
@@ -39,6 +39,7 @@ struct SelectParams {
     int32_t* blocks;            // [B][Hkv][k]
     int B, Hq, Hkv, G, bs, num_blocks, maxb;
     int k, first, recent;
+    int groups;                 // chunks of a CTA
     int rope;
     unsigned long long theta[kMaxHalfDim];
 };
