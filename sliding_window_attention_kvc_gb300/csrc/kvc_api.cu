@@ -339,12 +339,14 @@ static SharedLayout shared_layout(const kvc_desc* d, const Geo& g) {
 // kvc_select_blocks and kvc_decode_attention_selected: what they add to the decode workspace, after it.
 struct SelectLayout {
     size_t keys, list, rows, total;
+    int key_stride;
 };
 static SelectLayout select_layout(const kvc_desc* d, const Geo& g, int k) {
     SelectLayout l{};
     const size_t units = (size_t)d->batch * d->kv_heads;
+    l.key_stride = (int)align_up((size_t)d->max_blocks_per_seq, 4);
     l.keys = align_up(ws_layout(d, g).total, 256);
-    l.list = align_up(l.keys + units * d->max_blocks_per_seq * 4, 256);
+    l.list = align_up(l.keys + units * l.key_stride * 4, 256);
     l.rows = align_up(l.list + units * k * 4, 256);
     l.total = align_up(l.rows + units * 4, 256);
     return l;
@@ -1187,6 +1189,7 @@ KVC_API int kvc_select_blocks(const kvc_desc* d, const void* bounds, int32_t lay
     p.valid = valid_bits;
     p.err = reinterpret_cast<uint32_t*>(ws + ws_layout(d, g).err);
     p.keys = reinterpret_cast<uint32_t*>(ws + l.keys);
+    p.key_stride = l.key_stride;
     p.blocks = blocks;
     p.B = d->batch;
     p.Hq = d->q_heads;

@@ -172,7 +172,7 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
 // radix search of the excess-th lightest (four digits at most: it ends where a digit
 // takes all of its keys; every CTA counts its own keys, kept in shared memory, and
 // adds up the cluster's counts).  Blocks whose count reaches zero are marked; the
-// last CTA to finish (an atomic ticket, no waiting) puts the marked ones on the
+// last cluster to finish (an atomic ticket, no waiting) puts the marked ones on the
 // free list in ascending order and clears their resident bits.
 // What bounds it: a dozen dependent trips to L2, barriers and a cold instruction
 // cache, whatever the length (a single CTA a sequence took 309 us for two of up to
@@ -262,9 +262,12 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
                 const bool in = key != kKeyStays && (key & mask) == prefix;
                 const uint32_t d = (key >> shift) & 255u;
                 const unsigned act = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    const unsigned same = __match_any_sync(act, d);
-                    if (lane == __ffs(same) - 1) atomicAdd(&s_hist[pass][d], __popc(same));
+                const int lead = __ffs(act) - 1;
+                const uint32_t d0 = __shfl_sync(0xffffffffu, d, max(lead, 0));
+                if (__all_sync(0xffffffffu, !in || d == d0)) {      // one addition where all have the same
+                    if (lane == lead) atomicAdd(&s_hist[pass][d0], __popc(act));
+                } else if (in) {
+                    atomicAdd(&s_hist[pass][d], 1);
                 }
             }
             sync_all();
@@ -345,42 +348,63 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         }
     }
     __threadfence();
-    sync_all();                                 // no CTA leaves while its counts are read
-    if (tid == 0) s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!s_last) return;
+    sync_all();                                 // the cluster's marks are made, its counts read
+    if (rank == 0 && tid == 0) s_last = atomicAdd(p.ticket, 1u) == (unsigned)(gridDim.x / CL) - 1u;
+    sync_all();
+    if (!*cluster.map_shared_rank(&s_last, 0)) {
+        sync_all();                             // (no CTA leaves while it is read)
+        return;
+    }
+    // the last cluster: its CTAs share the words of marks
     __threadfence();
     const int words = (p.num_blocks + 31) / 32;
-    int at = *p.free_count;
+    const int w0 = (int)((long long)words * rank / CL), w1 = (int)((long long)words * (rank + 1) / CL);
+    const int free0 = *p.free_count;
+    int mine = 0;
 #pragma unroll 1
-    for (int base = 0; base < words; base += kEvictThreads) {
-        const int i = base + tid;
-        const uint32_t w = i < words ? __ldcg(p.back + i) : 0u;
+    for (int i = w0 + tid; i < w1; i += kEvictThreads) mine += __popc(__ldcg(p.back + i));
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (tid == 0) s_count[0] = 0;
+    __syncthreads();
+    if (lane == 0 && mine) atomicAdd(&s_count[0], mine);
+    sync_all();
+    int at = free0, all = free0;                // list entries before this CTA's, and in the end
+#pragma unroll 1
+    for (int c = 0; c < CL; ++c) {
+        const int n = cluster.map_shared_rank(s_count, c)[0];
+        at += c < rank ? n : 0;
+        all += n;
+    }
+    // a quarter of a word a thread: the marked blocks in order into shared memory, and out in whole lines
+    static_assert(kEvictKeys >= 8 * kEvictThreads, "every block of a pass may be marked");
+#pragma unroll 1
+    for (int base = w0; base < w1; base += kEvictThreads / 4) {
+        const int i = base + (tid >> 2), part = tid & 3;
+        const uint32_t w = i < w1 ? __ldcg(p.back + i) : 0u;
+        uint32_t byte = (w >> (8 * part)) & 255u;
         int tot;
-        const int k = at + evict_scan(__popc(w), s_w, &tot);
-        if (w) {
+        int k = evict_scan(__popc(byte), s_w, &tot);
+        while (byte) {
+            s_key[k++] = (uint32_t)(i * 32 + 8 * part + __ffs(byte) - 1);
+            byte &= byte - 1u;
+        }
+        __syncthreads();                        // (and the word has been read by its four threads)
+        if (w && part == 0) {
             p.back[i] = 0u;
             if (p.valid) p.valid[i] &= ~w;
         }
-        // the warp's words one after the other, a lane a mark: neighbours on the list are written together
-        unsigned some = __ballot_sync(0xffffffffu, w != 0u);
-#pragma unroll 1
-        while (some) {
-            const int src = __ffs(some) - 1;
-            some &= some - 1u;
-            const uint32_t v = __shfl_sync(0xffffffffu, w, src);
-            const int to = __shfl_sync(0xffffffffu, k, src) + __popc(v & ((1u << lane) - 1u));
-            if ((v >> lane) & 1u) {
-                if (to >= 0 && to < p.num_blocks)
-                    p.free_list[to] = (i - lane + src) * 32 + lane;
-                else
-                    index_fault(p.err, 41, to);
-            }
+        for (int j = tid; j < tot; j += kEvictThreads) {
+            if (at + j >= 0 && at + j < p.num_blocks)
+                p.free_list[at + j] = (int)s_key[j];
+            else
+                index_fault(p.err, 41, at + j);
         }
         at += tot;
+        __syncthreads();
     }
-    if (tid == 0) {
-        *p.free_count = min(at, p.num_blocks);
+    sync_all();                                 // (the counts have been read)
+    if (rank == 0 && tid == 0) {
+        *p.free_count = min(all, p.num_blocks);
         *p.ticket = 0u;                         // ready for the next call
     }
 }

@@ -240,8 +240,7 @@ cudaError_t launch_bounds_t(const BoundsParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // scores
 // ---------------------------------------------------------------------------
-constexpr int kScoreThreads = 128;
-constexpr int kScoreCtas = 152 * 8;            // CTAs that keep the GPU full
+constexpr int kScoreThreads = 128;             // a block of the cache a thread
 
 // Order of floats as unsigned integers; -0 counts as 0, NaN as the least.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -250,66 +249,86 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (chunk of blocks, kv head, sequence).  The group's q heads as
-// codes in shared memory, positive and negative parts apart: hi meets the one
-// and lo the other.  A warp scores groups of 32 blocks, a lane keeping track of
-// each; D / 16 lanes hold a block's codes, 16 channels of each end a lane, U x 512 / D
-// blocks at once, and the next ones (the first while the queries are made codes)
-// are on their way meanwhile.
+// Sums of N values over the W lanes that share them, in log2(W) steps of which each
+// halves the values that a lane still holds (N = 8, W = 8: 7 exchanges against 24 of a
+// sum at a time): lane bit `off` keeps the upper half where it is set.  Afterwards a lane
+// holds v[0 .. max(1, N / W) - 1] of the values whose index begins with its bits, from
+// the highest down; lanes beyond N hold the same.
+template <int N, int W>
+__device__ __forceinline__ void spread_sum(int (&v)[N], int lane) {
+    int n = N;
+#pragma unroll
+    for (int off = W / 2; off >= 1; off >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const bool up = lane & off;
+                    const int send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+        }
+    }
+}
+
+// One CTA per (128 blocks, kv head, sequence): a warp scores 32 blocks, a lane keeping
+// track of each.  The group's q heads are codes in shared memory, positive and negative
+// parts apart: hi meets the one and lo the other.  D / 16 lanes hold a block's codes, 16
+// channels of each end a lane, two blocks at a time; the next ones (the first while
+// the queries are made codes) are on their way meanwhile, and four q heads share their
+// sums' shuffles.
+// What bounds it: 2 D + 4 bytes a block and kv head from DRAM against 2 D / 4 products of
+// four for each q head and what surrounds them: at four heads a group the instructions,
+// so that addresses are one product and absent blocks are read like others (block 0) and
+// left out at the end.
 template <typename Act, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int LPB = D / 16, BPW = 32 / LPB, U = D == 64 ? 2 : 4, NP = D / 64, W = kScoreThreads / 32;
-    constexpr int IT = 32 / (U * BPW);                                // steps of a group
-    extern __shared__ __align__(16) unsigned char s_q[];              // [G][2][D] codes, then [G] steps
+    constexpr int LPB = D / 16, BPW = 32 / LPB, U = 2, NP = D / 64, W = kScoreThreads / 32;
+    constexpr int IT = 32 / (U * BPW);                                // steps of a warp
+    constexpr int HB = LPB / 4;                                       // lanes of a q head after the sums
+    extern __shared__ __align__(16) unsigned char s_q[];              // [G4][2][D] codes, then [G4] steps; G4: G in fours
+    const int G4 = (p.G + 3) & ~3;
     int8_t* codes = reinterpret_cast<int8_t*>(s_q);
-    float* s_step = reinterpret_cast<float*>(s_q + (size_t)p.G * 2 * D);
+    float* s_step = reinterpret_cast<float*>(s_q + (size_t)G4 * 2 * D);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, b = blockIdx.z;
     sl_pdl_wait();
     sl_pdl_launch();
-    const int c0 = blockIdx.x * kScoreChunk * p.groups;
-    const int32_t* trow = p.table + (long long)b * p.maxb;
-    // this lane's block of a group: its entry as it stands
-    auto entry = [&](int lb) { return lb < p.maxb ? __ldg(trow + lb) : -1; };
-    int raw = entry(c0 + warp * 32 + lane);
+    const int lb0 = (blockIdx.x * W + warp) * 32;                     // this warp's blocks
+    int phys = lb0 + lane < p.maxb ? __ldg(p.table + (long long)b * p.maxb + lb0 + lane) : -1;
     const int traw = p.pos[b];
     const int t = clamp_paged_t(traw, p.maxb, p.bs);
     if ((traw < 0 || traw != t) && blockIdx.x == 0 && h == 0 && tid == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
-    const int c1 = min(nb, c0 + kScoreChunk * p.groups);
-    if (c0 >= c1) return;
-    auto resident = [&](int lb, int phys) -> int {
-        if (lb >= c1) return -1;
-        if (phys >= p.num_blocks) {
-            set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
-            return -1;
-        }
-        return phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u) ? -1 : phys;
-    };
-    int lb = c0 + warp * 32 + lane;
-    int phys = resident(lb, raw);
+    if ((int)blockIdx.x * W * 32 >= nb) return;                       // (uniform)
+    if (lb0 + lane >= nb) phys = -1;
+    if (phys >= p.num_blocks) {
+        set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
+        phys = -1;
+    }
+    if (phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
+    const unsigned have = __ballot_sync(0xffffffffu, phys >= 0);
     const int ln = lane % LPB, sub = lane / LPB;
-    uint4 hi[U], lo[U];
-    float step[U];
-    auto load = [&](int it) {                                         // the ends of U BPW blocks of the group
+    const uint32_t unit = (uint32_t)max(phys, 0) * (uint32_t)p.Hkv + (uint32_t)h;      // (fits: the steps are an array of them)
+    const float step = have ? __ldg(p.steps + unit) : 0.f;
+    const uint4* src = reinterpret_cast<const uint4*>(p.codes) + ln;
+    uint4 hi[2][U], lo[2][U];
+    auto load = [&](int it) {                                         // the ends of U BPW blocks
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int ph = __shfl_sync(0xffffffffu, phys, (it * U + u) * BPW + sub);
-            const long long at = (long long)max(ph, 0) * p.Hkv + h;
-            const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D);
-            hi[u] = lo[u] = make_uint4(0u, 0u, 0u, 0u);
-            step[u] = 0.f;
-            if (ph >= 0) {
-                hi[u] = __ldg(src + ln);
-                lo[u] = __ldg(src + LPB + ln);
-                step[u] = __ldg(p.steps + at);
-            }
+            const uint4* at = src + (size_t)__shfl_sync(0xffffffffu, unit, (it * U + u) * BPW + sub) * (2 * LPB);
+            hi[it & 1][u] = __ldg(at);
+            lo[it & 1][u] = __ldg(at + LPB);
         }
     };
-    load(0);
+    if (have) load(0);
 #pragma unroll 1
-    for (int g = warp; g < p.G; g += W) {
-        const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + g) * D;
+    for (int g = warp; g < G4; g += W) {
+        // (behind the last head it stands again: the largest of the scores is what counts)
+        const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + min(g, p.G - 1)) * D;
         float x[2 * NP], a = 0.f;
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
@@ -342,65 +361,71 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         if (lane == 0) s_step[g] = sq;
     }
     __syncthreads();
-    uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
-#pragma unroll 1
-    for (;;) {
-        const int next = lb + W * 32, next_raw = next - lane < c1 ? entry(next) : -1;
-        const int cur = phys;
-        float score = -INFINITY;                                      // of this lane's own block
+    if (lb0 >= nb) return;
+    uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.key_stride + lb0;
+    if (!have) {
+        if (lb0 + lane < nb) keys[lane] = 0u;
+        return;
+    }
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            uint4 h4[U], l4[U];
-            float st[U], best[U];
+    for (int it = 0; it < IT; ++it) {
+        if (it + 1 < IT) load(it + 1);
+        float best[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                h4[u] = hi[u];
-                l4[u] = lo[u];
-                st[u] = step[u];
-                best[u] = -INFINITY;
-            }
-            if (it == IT - 1) phys = resident(next, next_raw);
-            if (it < IT - 1 || next - lane < c1) load(it < IT - 1 ? it + 1 : 0);
+        for (int u = 0; u < U; ++u) best[u] = -INFINITY;
+        // the step of this lane's block after the sums (LPB == 4: of both)
+        float st[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            st[u] = LPB == 4 || u == 0
+                        ? __shfl_sync(0xffffffffu, step,
+                                      (it * U + (LPB == 4 ? u : (ln & (HB / 2)) != 0)) * BPW + sub)
+                        : 0.f;
 #pragma unroll 1
-            for (int g = 0; g < p.G; ++g) {
-                const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + 16 * ln);
-                const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)g * 2 * D + D + 16 * ln);
-                const float sq = s_step[g];
+        for (int g = 0; g < G4; g += 4) {
+            int v[4 * U];                                             // [head][block]
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint4 qp = *reinterpret_cast<const uint4*>(codes + (size_t)(g + y) * 2 * D + 16 * ln);
+                const uint4 qn = *reinterpret_cast<const uint4*>(codes + (size_t)(g + y) * 2 * D + D + 16 * ln);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    int a = __dp4a((int)h4[u].x, (int)qp.x, 0);
-                    int e = __dp4a((int)l4[u].x, (int)qn.x, 0);
-                    a = __dp4a((int)h4[u].y, (int)qp.y, a);
-                    e = __dp4a((int)l4[u].y, (int)qn.y, e);
-                    a = __dp4a((int)h4[u].z, (int)qp.z, a);
-                    e = __dp4a((int)l4[u].z, (int)qn.z, e);
-                    a = __dp4a((int)h4[u].w, (int)qp.w, a);
-                    e = __dp4a((int)l4[u].w, (int)qn.w, e);
-                    a += e;
-#pragma unroll
-                    for (int off = 1; off < LPB; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-                    best[u] = fmaxf(best[u], __fmul_rn((float)a, __fmul_rn(sq, st[u])));
+                    const uint4 a4 = hi[it & 1][u], b4 = lo[it & 1][u];
+                    int a = __dp4a((int)a4.x, (int)qp.x, 0);
+                    a = __dp4a((int)b4.x, (int)qn.x, a);
+                    a = __dp4a((int)a4.y, (int)qp.y, a);
+                    a = __dp4a((int)b4.y, (int)qn.y, a);
+                    a = __dp4a((int)a4.z, (int)qp.z, a);
+                    a = __dp4a((int)b4.z, (int)qn.z, a);
+                    a = __dp4a((int)a4.w, (int)qp.w, a);
+                    a = __dp4a((int)b4.w, (int)qn.w, a);
+                    v[y * U + u] = a;
                 }
             }
-            // the lane of each block takes its score
+            spread_sum<4 * U, LPB>(v, lane);
+            // this lane's head of the four: its upper two bits among the LPB; block: the next one, or both
+            const float sq = s_step[g + (ln / HB & 3)];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = lane - (it * U + u) * BPW;              // this lane's block among these BPW
-                const float x = __shfl_sync(0xffffffffu, best[u], (j & (BPW - 1)) * LPB);
-                if (j >= 0 && j < BPW) score = x;
-            }
+            for (int u = 0; u < (LPB == 4 ? U : 1); ++u) best[u] = fmaxf(best[u], __fmul_rn((float)v[u], __fmul_rn(sq, st[u])));
         }
-        if (lb < c1)
-            keys[lb] = cur < 0 ? 0u : (lb < p.first || lb >= nb - p.recent) ? 0xffffffffu : score_key(score);
-        if (next - lane >= c1) break;                                 // (uniform in the warp)
-        lb = next;
+        // the largest over the heads; a lane of each block stores its key
+#pragma unroll
+        for (int u = 0; u < (LPB == 4 ? U : 1); ++u) {
+            best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], HB));
+            best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], 2 * HB));
+            const int j = (it * U + (LPB == 4 ? u : (ln & (HB / 2)) != 0)) * BPW + sub, lb = lb0 + j;
+            if ((LPB == 4 ? ln == 0 : (ln & ~(HB / 2)) == 0) && lb < nb)
+                keys[j] = !((have >> j) & 1u)                     ? 0u
+                          : (lb < p.first || lb >= nb - p.recent) ? 0xffffffffu
+                                                                  : score_key(best[u]);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
 // selection
 // ---------------------------------------------------------------------------
-constexpr int kPickThreads = 256;
+constexpr int kPickThreads = 1024;             // at most
 constexpr int kPickWarps = kPickThreads / 32;
 
 // Sums over the CTA's threads before this one, of two counts at once; totals in *tot.
@@ -432,12 +457,17 @@ __device__ __forceinline__ int2 pick_scan(int2 v, int2* s_w, int2* tot) {
     return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
-// Counts key `key`'s digit among the warp's (one addition for lanes of one digit).
+// Counts the digits of the warp's keys (one addition where all lanes have the same).
 __device__ __forceinline__ void pick_count(int* hist, bool in, uint32_t digit) {
     const unsigned act = __ballot_sync(0xffffffffu, in);
-    if (in) {
-        const unsigned same = __match_any_sync(act, digit);
-        if ((threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+    if (!act) return;
+    const int lead = __ffs(act) - 1;
+    const uint32_t d0 = __shfl_sync(0xffffffffu, digit, lead);
+    const bool alike = __all_sync(0xffffffffu, !in || digit == d0);
+    if (alike) {
+        if ((int)(threadIdx.x & 31) == lead) atomicAdd(&hist[d0], __popc(act));
+    } else if (in) {
+        atomicAdd(&hist[digit], 1);
     }
 }
 
@@ -475,30 +505,31 @@ __device__ __forceinline__ void pick_digit(const int* hist, int want, int* digit
 // One CTA per (kv head, sequence): the k largest keys, ties by the lowest index,
 // by a radix search of the k-th largest (four digits at most: it ends where a digit
 // takes all of its keys), then the kept indices in ascending order.  A thread keeps
-// the first kPickKeys of its keys in registers; longer tables are read again.
+// four neighbouring keys in registers; what is behind those is read again.
 // What bounds it: one trip to the keys, then barriers.
-constexpr int kPickKeys = 4;
-
 __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_constant__ SelectParams p) {
     __shared__ int s_hist[4][256];
     __shared__ int2 s_w[kPickWarps];
     __shared__ int s_digit[4], s_beyond[4];
-    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
-    for (int i = tid; i < 4 * 256; i += kPickThreads) s_hist[0][i] = 0;
+    const int tid = threadIdx.x, nt = blockDim.x, h = blockIdx.x, b = blockIdx.y;
+    for (int i = tid; i < 4 * 256; i += nt) s_hist[0][i] = 0;
     if (tid < 4) s_digit[tid] = -1;
     sl_pdl_wait();
     sl_pdl_launch();
-    const uint32_t* keys = p.keys + ((long long)b * p.Hkv + h) * p.maxb;
+    const uint4* keys = reinterpret_cast<const uint4*>(p.keys + ((long long)b * p.Hkv + h) * p.key_stride);
     const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
     const int nb = t < 0 ? 0 : t / p.bs + 1;
     int32_t* out = p.blocks + ((long long)b * p.Hkv + h) * p.k;
-    uint32_t mine[kPickKeys];
-#pragma unroll
-    for (int u = 0; u < kPickKeys; ++u) {
-        const int i = u * kPickThreads + tid;
-        mine[u] = i < nb ? __ldcg(keys + i) : 0u;
-    }
-    const int tail = kPickKeys * kPickThreads;
+    // four keys from index i on (0 behind the last)
+    auto four = [&](int i, uint32_t (&k)[4]) {
+        const uint4 w = i < nb ? __ldcg(keys + (i >> 2)) : make_uint4(0u, 0u, 0u, 0u);
+        k[0] = w.x;
+        k[1] = i + 1 < nb ? w.y : 0u;
+        k[2] = i + 2 < nb ? w.z : 0u;
+        k[3] = i + 3 < nb ? w.w : 0u;
+    };
+    uint32_t mine[4];
+    four(4 * tid, mine);
     __syncthreads();
     // keys above `low` are kept, and the first `ties` of those equal to it
     uint32_t prefix = 0, mask = 0, low = 0;
@@ -506,13 +537,12 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_c
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
+#pragma unroll 1
+        for (int base = 0; base < nb; base += 4 * nt) {
+            uint32_t k[4] = {mine[0], mine[1], mine[2], mine[3]};
+            if (base > 0) four(base + 4 * tid, k);
 #pragma unroll
-        for (int u = 0; u < kPickKeys; ++u)
-            if (u * kPickThreads < nb)         // (uniform)
-                pick_count(s_hist[pass], mine[u] != 0u && (mine[u] & mask) == prefix, (mine[u] >> shift) & 255u);
-        for (int base = tail; base < nb; base += kPickThreads) {
-            const uint32_t key = base + tid < nb ? __ldcg(keys + base + tid) : 0u;
-            pick_count(s_hist[pass], key != 0u && (key & mask) == prefix, (key >> shift) & 255u);
+            for (int u = 0; u < 4; ++u) pick_count(s_hist[pass], k[u] != 0u && (k[u] & mask) == prefix, (k[u] >> shift) & 255u);
         }
         __syncthreads();
         if (tid < 32) pick_digit<true>(s_hist[pass], want, &s_digit[pass], &s_beyond[pass]);
@@ -535,27 +565,36 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_c
         ties = want;
     }
     int2 run = make_int2(0, 0);                // keys above `low`, keys equal to it, before this pass
-    auto emit = [&](int i, uint32_t key) {
-        const bool more = key > low, same = key == low && key != 0u;
+#pragma unroll 1
+    for (int base = 0; base < nb; base += 4 * nt) {
+        uint32_t k[4] = {mine[0], mine[1], mine[2], mine[3]};
+        if (base > 0) four(base + 4 * tid, k);
+        int2 n = make_int2(0, 0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            n.x += k[u] > low;
+            n.y += k[u] == low && k[u] != 0u;
+        }
         int2 tot;
-        const int2 ex = pick_scan(make_int2(more, same), s_w, &tot);
-        const int above = run.x + ex.x, equal = run.y + ex.y;
-        if (more || (same && equal < ties)) {
-            const int at = above + min(equal, ties);
-            if (at < p.k)
-                out[at] = i;
-            else
-                index_fault(p.err, 40, at);
+        const int2 ex = pick_scan(n, s_w, &tot);
+        int above = run.x + ex.x, equal = run.y + ex.y;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool more = k[u] > low, same = k[u] == low && k[u] != 0u;
+            if (more || (same && equal < ties)) {
+                const int at = above + min(equal, ties);
+                if (at < p.k)
+                    out[at] = base + 4 * tid + u;
+                else
+                    index_fault(p.err, 40, at);
+            }
+            above += more;
+            equal += same;
         }
         run.x += tot.x;
         run.y += tot.y;
-    };
-#pragma unroll
-    for (int u = 0; u < kPickKeys; ++u)
-        if (u * kPickThreads < nb) emit(u * kPickThreads + tid, mine[u]);
-    for (int base = tail; base < nb; base += kPickThreads)
-        emit(base + tid, base + tid < nb ? __ldcg(keys + base + tid) : 0u);
-    for (int i = run.x + min(run.y, ties) + tid; i < p.k; i += kPickThreads) out[i] = -1;
+    }
+    for (int i = run.x + min(run.y, ties) + tid; i < p.k; i += nt) out[i] = -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -645,31 +684,34 @@ cudaError_t launch_block_bounds(int dtype, int D, const BoundsParams& p, cudaStr
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_select(int dtype, int D, const SelectParams& p, cudaStream_t s) {
-    cudaLaunchAttribute attr;
-    const int smem = p.G * (2 * D + 4);
-    // a CTA walks several chunks where there are more than enough of them
-    SelectParams sp = p;
-    const long long chunks = (p.maxb + kScoreChunk - 1) / kScoreChunk, units = chunks * p.Hkv * p.B;
-    sp.groups = 1;
-    while (sp.groups < 8 && units / (2 * sp.groups) >= kScoreCtas) sp.groups *= 2;
-    cudaLaunchConfig_t cfg = sl_config(dim3((unsigned)((chunks + sp.groups - 1) / sp.groups), p.Hkv, p.B), kScoreThreads,
-                                       smem, s, &attr);
-    cudaError_t e = cudaErrorInvalidValue;
-    // (above 48 KB, groups of more than 93 heads of 256, a kernel asks for its shared memory)
-#define KVC_CASE(F, A, DD)                                                                                   \
-    if ((dtype == 0) == F && D == DD) {                                                                      \
-        e = smem > 48 * 1024 ? cudaFuncSetAttribute(block_score_kernel<A, DD>,                               \
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem)       \
-                             : cudaSuccess;                                                                  \
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, block_score_kernel<A, DD>, sp);                    \
+template <typename Act, int D>
+cudaError_t launch_score_t(const SelectParams& p, cudaStream_t s) {
+    const int smem = ((p.G + 3) & ~3) * (2 * D + 4);
+    // (above 48 KB, groups of more than 92 heads of 256, a kernel asks for its shared memory)
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(block_score_kernel<Act, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
     }
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg =
+        sl_config(dim3((unsigned)((p.maxb + kScoreThreads - 1) / kScoreThreads), p.Hkv, p.B), kScoreThreads, smem, s, &attr);
+    return cudaLaunchKernelEx(&cfg, block_score_kernel<Act, D>, p);
+}
+
+cudaError_t launch_select(int dtype, int D, const SelectParams& p, cudaStream_t s) {
+    cudaError_t e = cudaErrorInvalidValue;
+#define KVC_CASE(F, A, DD) \
+    if ((dtype == 0) == F && D == DD) e = launch_score_t<A, DD>(p, s);
     KVC_CASE(true, float, 64) KVC_CASE(true, float, 128) KVC_CASE(true, float, 256)
     KVC_CASE(false, __nv_bfloat16, 64) KVC_CASE(false, __nv_bfloat16, 128) KVC_CASE(false, __nv_bfloat16, 256)
 #undef KVC_CASE
     if (e != cudaSuccess) return e;
-    cfg = sl_config(dim3(p.Hkv, p.B), kPickThreads, 0, s, &attr);
-    return cudaLaunchKernelEx(&cfg, block_pick_kernel, sp);
+    // four keys a thread, as far as a CTA goes
+    int threads = 128;
+    while (threads < kPickThreads && 4 * threads < p.maxb) threads *= 2;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = sl_config(dim3(p.Hkv, p.B), threads, 0, s, &attr);
+    return cudaLaunchKernelEx(&cfg, block_pick_kernel, p);
 }
 
 cudaError_t launch_select_plan(const SelectPlanParams& p, cudaStream_t s) {

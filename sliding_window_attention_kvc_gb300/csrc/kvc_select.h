@@ -7,8 +7,6 @@
 
 namespace kvc {
 
-constexpr int kScoreChunk = 128;       // logical blocks that the warps of a CTA score at once, 32 each
-
 // Bounds of blocks (kvc_block_bounds): codes [layers][num_blocks][Hkv][2][D]
 // (largest, smallest), then their steps [layers][num_blocks][Hkv].
 struct BoundsParams {
@@ -35,11 +33,11 @@ struct SelectParams {
     const int32_t* table;
     const uint32_t* valid;      // may be null
     uint32_t* err;
-    uint32_t* keys;             // [B][Hkv][maxb]: 0 no candidate, 0xffffffff always in, else the ordered score
+    uint32_t* keys;             // [B][Hkv][key_stride]: 0 no candidate, 0xffffffff always in, else the ordered score
     int32_t* blocks;            // [B][Hkv][k]
     int B, Hq, Hkv, G, bs, num_blocks, maxb;
     int k, first, recent;
-    int groups;                 // chunks of a CTA
+    int key_stride;             // maxb in whole fours
     int rope;
     unsigned long long theta[kMaxHalfDim];
 };
