@@ -246,6 +246,42 @@ int encode_rows_map(const kvc_desc* d, const void* rows, long long T, CUtensorMa
                : KVC_ERR_CUDA;
 }
 
+// The maps of kvc_tree_attention (kvc_tree.h): the cached rows of one layer ...
+int encode_tree_cache_map(const kvc_desc* d, const Geo& g, const void* cache, int layer, bool grouped, int box_rows,
+                          CUtensorMap* map) {
+    const unsigned long long half_rows = (unsigned long long)g.half_elems / d->head_dim;
+    if (half_rows >= (1ull << 31)) return KVC_ERR_UNSUPPORTED;
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KVC_ERR_CUDA;
+    const cuuint64_t row = (cuuint64_t)d->head_dim * 2, half = half_rows * row, blocks = (cuuint64_t)d->head_dim / 64;
+    void* base = const_cast<char*>(static_cast<const char*>(cache) + (size_t)layer * 2 * half);
+    const cuuint64_t dims[5] = {64, grouped ? 8 : half_rows, blocks, 2, half_rows / 8};
+    const cuuint64_t strides[4] = {row, 128, half, 8 * row};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)blocks, 2, (cuuint32_t)(box_rows / 8)};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, grouped ? 5 : 4, base, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
+// ... and the draft's keys or values [batch][T][kv head][D].
+int encode_tree_rows_map(const kvc_desc* d, const void* rows, long long T, CUtensorMap* map) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KVC_ERR_CUDA;
+    const cuuint64_t D = (cuuint64_t)d->head_dim;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)(d->batch * T), D / 64, (cuuint64_t)d->kv_heads};
+    const cuuint64_t strides[3] = {(cuuint64_t)d->kv_heads * D * 2, 128, D * 2};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
 // The chunk's staged rows, K [batch][T][kv head][D] then V at kv_bytes past
 // it: {64 columns, kv head, batch * T, K|V, column block}, boxes of 64 tokens
 // of one kv head, K and V, every column.
@@ -1389,14 +1425,11 @@ KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t lay
     // the maps, encoded before anything is launched
     TreeMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (paged) {
-        if ((rc = encode_block_map(d, g, cache, &maps.cache))) return rc;
-    } else {
-        KvTensorMaps km;
-        if ((rc = kv_maps_for(d, g, cache, &km, &p.slot_whole))) return rc;
-        maps.cache = km.run[kRunMaps - 1];              // 64-row runs
-    }
-    if ((rc = encode_rows_map(d, baked ? p.stage : k_new, T, &maps.k)) || (rc = encode_rows_map(d, v_new, T, &maps.v)))
+    p.grouped = paged || g.C % 8 == 0;
+    p.box = !p.grouped ? 8 : (paged && d->block_size < 64 ? d->block_size : 64);
+    if ((rc = encode_tree_cache_map(d, g, cache, layer, p.grouped, p.box, &maps.cache)) ||
+        (rc = encode_tree_rows_map(d, baked ? p.stage : k_new, T, &maps.k)) ||
+        (rc = encode_tree_rows_map(d, v_new, T, &maps.v)))
         return rc;
     cudaStream_t s = (cudaStream_t)stream;
     if ((baked && launch_tree_stage(d->head_dim, p, s) != cudaSuccess) ||

@@ -274,6 +274,12 @@ __device__ __forceinline__ void spread_sum(int (&v)[N], int lane) {
     }
 }
 
+__device__ __noinline__ float2 score_angle(int t, unsigned long long turns) {
+    float2 r;
+    rope_cos_sin((long long)t, turns, &r.x, &r.y);
+    return r;
+}
+
 // One CTA per (128 blocks, kv head, sequence): a warp scores 32 blocks, a lane keeping
 // track of each.  The group's q heads are codes in shared memory, positive and negative
 // parts apart: hi meets the one and lo the other.  D / 16 lanes hold a block's codes, 16
@@ -286,7 +292,7 @@ __device__ __forceinline__ void spread_sum(int (&v)[N], int lane) {
 // left out at the end.
 template <typename Act, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int LPB = D / 16, BPW = 32 / LPB, U = 2, NP = D / 64, W = kScoreThreads / 32;
+    constexpr int LPB = D / 16, BPW = 32 / LPB, U = 2, W = kScoreThreads / 32;
     constexpr int IT = 32 / (U * BPW);                                // steps of a warp
     constexpr int HB = LPB / 4;                                       // lanes of a q head after the sums
     extern __shared__ __align__(16) unsigned char s_q[];              // [G4][2][D] codes, then [G4] steps; G4: G in fours
@@ -325,40 +331,48 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         }
     };
     if (have) load(0);
+    // q heads as codes: D / 16 lanes a row, 8 channels of each half a lane
 #pragma unroll 1
-    for (int g = warp; g < G4; g += W) {
+    for (int g = warp * BPW; g < G4; g += W * BPW) {
         // (behind the last head it stands again: the largest of the scores is what counts)
-        const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + min(g, p.G - 1)) * D;
-        float x[2 * NP], a = 0.f;
+        const Act* qr = static_cast<const Act*>(p.q) + ((long long)b * p.Hq + h * p.G + min(g + sub, p.G - 1)) * D + 8 * ln;
+        constexpr int CH = 8 * (int)sizeof(Act) / 16, V = 16 / (int)sizeof(Act);
+        float x[2][8], a = 0.f;                                       // halves of the head
 #pragma unroll
-        for (int m = 0; m < NP; ++m) {
-            const int i = lane + 32 * m;
-            x[2 * m] = EltTraits<Act>::to_f32(qr[i]);
-            x[2 * m + 1] = EltTraits<Act>::to_f32(qr[i + D / 2]);
-        }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                EltTraits<Act>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + e * (D / 2)) + c), x[e] + c * V);
         if (p.rope != kRopeNone) {
 #pragma unroll
-            for (int m = 0; m < NP; ++m) {
-                float cs, sn;
-                rope_cos_sin((long long)t, p.theta[lane + 32 * m], &cs, &sn);
-                const float x1 = x[2 * m], x2 = x[2 * m + 1];
-                x[2 * m] = x1 * cs - x2 * sn;
-                x[2 * m + 1] = x1 * sn + x2 * cs;
+            for (int i = 0; i < 8; ++i) {
+                const float2 cs = score_angle(t, p.theta[8 * ln + i]);
+                const float x1 = x[0][i], x2 = x[1][i];
+                x[0][i] = x1 * cs.x - x2 * cs.y;
+                x[1][i] = x1 * cs.y + x2 * cs.x;
             }
         }
 #pragma unroll
-        for (int m = 0; m < 2 * NP; ++m) a = fmaxf(a, fabsf(x[m]));
+        for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(x[0][i]), fabsf(x[1][i])));
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        for (int off = 1; off < LPB; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
         const float sq = __fdiv_rn(a, 127.f);
+        if (g + sub < G4) {
+            int8_t* d = codes + (size_t)(g + sub) * 2 * D + 8 * ln;
 #pragma unroll
-        for (int m = 0; m < 2 * NP; ++m) {
-            const int code = q8_code(x[m], sq);
-            int8_t* d = codes + (size_t)g * 2 * D + lane + 32 * (m >> 1) + (m & 1) * (D / 2);
-            d[0] = (int8_t)max(code, 0);
-            d[D] = (int8_t)min(code, 0);
+            for (int e = 0; e < 2; ++e) {
+                uint32_t up[2] = {0u, 0u}, down[2] = {0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int code = q8_code(x[e][i], sq);
+                    up[i >> 2] |= (uint32_t)max(code, 0) << (8 * (i & 3));
+                    down[i >> 2] |= (uint32_t)(min(code, 0) & 0xff) << (8 * (i & 3));
+                }
+                *reinterpret_cast<uint2*>(d + e * (D / 2)) = make_uint2(up[0], up[1]);
+                *reinterpret_cast<uint2*>(d + D + e * (D / 2)) = make_uint2(down[0], down[1]);
+            }
+            if (ln == 0) s_step[g + sub] = sq;
         }
-        if (lane == 0) s_step[g] = sq;
     }
     __syncthreads();
     if (lb0 >= nb) return;

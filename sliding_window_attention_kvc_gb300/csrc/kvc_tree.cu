@@ -45,8 +45,11 @@ struct TrShape {
     static constexpr int STAGES = D == 64 ? 6 : (D == 128 ? 4 : 2);
     static constexpr int CB = D / 64;                          // 64-column blocks of a row
     static constexpr int QBytes = kWsRows * D * 2;             // one Q tile
-    static constexpr int KVBlock = 2 * kWsKeys * 128;          // one column block of K and V
-    static constexpr int StageBytes = CB * KVBlock;
+    // a stage: [8 rows of the tile][K|V][column block][8 rows x 128 bytes], so that one copy brings any
+    // number of whole groups of 8 rows
+    static constexpr int VOff = CB * 1024;
+    static constexpr int Group = 2 * VOff;
+    static constexpr int StageBytes = (kWsKeys / 8) * Group;
     static constexpr int OffQ = 0;
     static constexpr int OffStage = OffQ + NQ * QBytes;
     static constexpr int OffMeta = OffStage + STAGES * StageBytes;
@@ -293,6 +296,12 @@ __device__ __forceinline__ unsigned long long tr_window(const TreeParams& p, int
            ((long long)ks + a + p.window - lim > 63 ? 0ull : tr_bits(ks + a + p.window - lim, 63));
 }
 
+// A wait that asks once without sleeping first: in the softmax's loop most have ended
+// long before (a wait that may sleep costs 150 cycles even then, and a tile has three).
+__device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return ws_test(bar, parity) || ws_wait(bar, parity, abort);
+}
+
 // Eight rotation pairs (elements of lo with those of hi) of a bf16 row at `pos`.
 __device__ __noinline__ void tr_rotate8(uint4& lo, uint4& hi, long long pos, const unsigned long long* turns) {
     uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -343,6 +352,17 @@ __global__ void __launch_bounds__(256) tree_stage_kernel(const __grid_constant__
         *reinterpret_cast<uint4*>(dst) = x;
         *reinterpret_cast<uint4*>(dst + D / 2) = y;
     }
+}
+
+// O[128 x D] (+)= P[128 x 64] V[64 x D]: P in tensor memory (bf16 pairs), vd: the descriptor of V's
+// rows 0 .. 15 in a stage; `more`: accumulate onto O.
+template <int D>
+__device__ __forceinline__ void tr_issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t vd, uint32_t more) {
+    constexpr uint32_t idesc = ws_idesc(kWsRows, D, 1);
+#pragma unroll
+    for (int ks = 0; ks < kWsKeys / 16; ++ks)
+        ws_mma_ts(d_tmem, p_tmem + (uint32_t)(ks * 8), vd + (uint64_t)((ks * 2 * TrShape<D>::Group) >> 4), idesc,
+                  ks > 0 ? 1u : more);
 }
 
 template <int D>
@@ -410,7 +430,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         bool ok = true;
         const bool paged = p.layout == kPaged;
         const int bs = p.bs;
-        const int box = !paged || bs > kWsKeys ? kWsKeys : bs;  // rows of one copy
+        const int box = p.box;                                  // rows of one copy
         const int per = kWsKeys / box;                          // copies of a tile
         auto take_stage = [&](int s) -> bool {
             if (idx < NST || ws_wait(&bars->empty[s], ((idx / NST) - 1) & 1, abort)) return true;
@@ -456,21 +476,11 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     const int j = lane - k * per;
                     if (j >= 0 && j < per && row >= 0) {
                         mbar_expect_tx(&bars->full[s], (uint32_t)(box * D * 4));
-                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes + j * box * 128;
-                        if (paged) {
-#pragma unroll
-                            for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                                for (int kv = 0; kv < 2; ++kv)
-                                    tma_load_4d(dst + cb * S::KVBlock + kv * kWsKeys * 128, &maps.cache, cb * 64, row, kv,
-                                                p.layer, &bars->full[s]);
-                        } else if (p.slot_whole) {
-                            tma_load_5d(dst, &maps.cache, 0, row, 0, p.layer, 0, &bars->full[s]);
-                        } else {
-#pragma unroll
-                            for (int cb = 0; cb < CB; ++cb)
-                                tma_load_4d(dst + cb * S::KVBlock, &maps.cache, cb * 64, row, 0, p.layer, &bars->full[s]);
-                        }
+                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes + j * (box / 8) * S::Group;
+                        if (p.grouped)
+                            tma_load_5d(dst, &maps.cache, 0, 0, 0, 0, row >> 3, &bars->full[s]);
+                        else
+                            tma_load_4d(dst, &maps.cache, 0, row, 0, 0, &bars->full[s]);
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -502,15 +512,14 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 const unsigned r0 = __ballot_sync(0xffffffffu, d.see[0] != 0ull), r1 = __ballot_sync(0xffffffffu, d.see[1] != 0ull);
                 const int s = idx % NST;
                 if (take_stage(s)) {
+                    // (8 tokens a copy: a lane for K and one for V)
+                    if (lane < kWsKeys / 4) {
+                        mbar_expect_tx(&bars->full[s], (uint32_t)S::VOff);
+                        tma_load_4d(sm + S::OffStage + s * S::StageBytes + (lane >> 1) * S::Group + (lane & 1) * S::VOff,
+                                    (lane & 1) ? &maps.v : &maps.k, 0, sg.b * p.T + 8 * (lane >> 1), 0, sg.h, &bars->full[s]);
+                    }
+                    __syncwarp();
                     if (lane == 0) {
-                        mbar_expect_tx(&bars->full[s], (uint32_t)S::StageBytes);
-                        unsigned char* dst = sm + S::OffStage + s * S::StageBytes;
-#pragma unroll
-                        for (int cb = 0; cb < CB; ++cb) {
-                            tma_load_3d(dst + cb * S::KVBlock, &maps.k, cb * 64, sg.h, sg.b * p.T, &bars->full[s]);
-                            tma_load_3d(dst + cb * S::KVBlock + kWsKeys * 128, &maps.v, cb * 64, sg.h, sg.b * p.T,
-                                        &bars->full[s]);
-                        }
                         meta[s].present = (unsigned long long)r0 | ((unsigned long long)r1 << 32);
                         meta[s].kind = kTileDraft;
                         meta[s].slot0 = 0;
@@ -544,12 +553,12 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
 #pragma unroll 1
                     for (int r = lane; r < kWsKeys; r += 32) {
                         if ((present >> r) & 1ull) continue;
-                        unsigned char* st = sm + S::OffStage + s * S::StageBytes + kWsKeys * 128 + r * 128;
+                        unsigned char* st = sm + S::OffStage + s * S::StageBytes + (r >> 3) * S::Group + S::VOff + (r & 7) * 128;
 #pragma unroll
                         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
                             for (int ch = 0; ch < 8; ++ch)
-                                *reinterpret_cast<uint4*>(st + cb * S::KVBlock + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<uint4*>(st + cb * 1024 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
@@ -565,8 +574,8 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         bool ok = true;
         int idx0 = 0, base = 0, loads = 0;             // tiles of the segments before; of this Q tile; its loads
         const uint64_t qd = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
-        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, 1024);
-        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + kWsKeys * 128, S::KVBlock, 1024);
+        const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, S::Group);
+        const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + S::VOff, 1024, S::Group);
         const uint32_t s0 = tmem + S::SCol0 + (uint32_t)(i * 2 * kWsKeys), o_t = tmem + (uint32_t)(i * D);
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     if (ws_test(&bars->ready[s], (t / NST) & 1)) {
                         ws_fence_after();
                         if (lane == 0) {
-                            ws_issue_s<D, kWsRows * 128, S::KVBlock>(s0 + (uint32_t)(((base + ns) & 1) * kWsKeys), qd,
+                            ws_issue_s<D, kWsRows * 128, 1024>(s0 + (uint32_t)(((base + ns) & 1) * kWsKeys), qd,
                                                                      kd0 + (uint64_t)((s * S::StageBytes) >> 4));
                             ws_commit(&bars->s_full[i][(base + ns) & 1]);
                         }
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     const int t = idx0 + (sg.alt ? 2 * npv + i : npv), s = t % NST;
                     if (lane == 0) {
                         // P_i in the S buffer it came from (bf16 pairs)
-                        ws_issue_pv<D>(o_t, s0 + (uint32_t)(((base + npv) & 1) * kWsKeys),
+                        tr_issue_pv<D>(o_t, s0 + (uint32_t)(((base + npv) & 1) * kWsKeys),
                                        vd0 + (uint64_t)((s * S::StageBytes) >> 4), npv > 0);
                         ws_commit(&bars->o_done[i]);
                         ws_commit(&bars->empty[s]);        // this Q tile is done with the tile's K and V
@@ -707,7 +716,14 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             float m_run = -INFINITY, l_run = 0.f;          // m in base-2 units of the scaled scores
             for (int lt = 0; lt < nt; ++lt) {
                 const int j = base + lt;
-                if (!ws_wait(&bars->s_full[qi][j & 1], (j >> 1) & 1, abort)) {
+                // the stage's meta, on the way to the scores
+                const int gt = idx0 + (sg.alt ? 2 * lt + qi : lt);
+                if (!tr_wait(&bars->ready[gt % NST], (gt / NST) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                const TrStageMeta mt = meta[gt % NST];
+                if (!tr_wait(&bars->s_full[qi][j & 1], (j >> 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
@@ -717,18 +733,12 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 ws_ld32(lane_base + scol, sv);
                 ws_ld32(lane_base + scol + 32, sv + 32);
                 ws_wait_ld();
-                const int gt = idx0 + (sg.alt ? 2 * lt + qi : lt);
-                if (!ws_wait(&bars->ready[gt % NST], (gt / NST) & 1, abort)) {    // the stage's meta
-                    ok = false;
-                    break;
-                }
-                const TrStageMeta mt = meta[gt % NST];
-                unsigned long long vis = mt.present;
-                if (mt.kind == kTileDraft)
-                    vis &= see;
-                else if (mt.kind == kTileWindow)
-                    vis &= tr_window(p, sg.pos, mt.slot0, depth);
-                if (__any_sync(0xffffffffu, vis != ~0ull)) {
+                if (mt.kind != kTileOpen || mt.present != ~0ull) {           // (uniform)
+                    unsigned long long vis = mt.present;
+                    if (mt.kind == kTileDraft)
+                        vis &= see;
+                    else if (mt.kind == kTileWindow)
+                        vis &= tr_window(p, sg.pos, mt.slot0, depth);
                     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
                     for (int k = 0; k < kWsKeys; ++k)
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 // rescaled, that is asked for after this tile's weights have been handed over
                 const bool rescale = lt > 0 && __any_sync(0xffffffffu, alpha != 1.f);
                 if (rescale) {
-                    if (!ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                    if (!tr_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
                         ok = false;
                         break;
                     }
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 ws_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_full[qi]);
-                if (lt > 0 && !rescale && !ws_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                if (lt > 0 && !rescale && !tr_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
                     ok = false;
                     break;
                 }

@@ -54,7 +54,7 @@ struct TreeParams {
     int col_units;              // units a tile of all columns of a kv head
     int last_units;             // units a tile of the last column: its Q tiles
     int rows;                   // partial rows of a slot
-    int slot_whole;             // window layouts: the map brings every column block in one copy
+    int box, grouped;           // cached rows of a copy; whether the map counts groups of 8 rows
     int ctas;
     int comb_rows;              // rows of a combine CTA
     int rope;
@@ -62,8 +62,12 @@ struct TreeParams {
     unsigned long long theta[kMaxHalfDim];
 };
 
-// cache: window layouts 64 slots of K and V (five or four dimensions), paged a
-// block; k, v: the draft's rows.
+// One copy brings rows of K and V, every column block, in the order that the products
+// take: [8 rows][K|V][column block][8 x 128 bytes].
+//  cache   the layer's rows; where kv heads and blocks begin at multiples of 8 rows
+//          (grouped) {64 columns, row of 8, column block, K|V, group of 8 rows}, boxes of a
+//          block or of 64 rows; else {64 columns, row, column block, K|V}, boxes of 8 rows.
+//  k, v    the draft's rows {64 columns, token, column block, kv head}, boxes of 8 tokens.
 struct TreeMaps {
     CUtensorMap cache, k, v;
 };
