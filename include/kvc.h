@@ -356,7 +356,8 @@ KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, in
  * keys, channel by channel; a decode step asks them which blocks can hold large
  * scores, and attends those alone.  Every element type and rope NONE or BAKED
  * (the keys as the cache stores them); kvc_decode_attention_selected bf16 and
- * INT8 caches.
+ * INT8 caches.  Tables of at most 2^30 blocks a sequence, here, in
+ * kvc_decode_attention_weighed and in kvc_block_evict (else KVC_ERR_UNSUPPORTED).
  *
  * Bounds of the blocks, caller-owned memory of kvc_bounds_bytes(d) bytes (0 if
  * `d` is refused), 16-byte aligned: int8 codes [layers, num_blocks, kv_heads, 2,
@@ -372,8 +373,9 @@ KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, in
  * n_new), from the block's first row to position pos[b] + n - 1: call it after
  * the append of those tokens, and after a block was copied (kvc_block_prepare)
  * or brought in.  Positions below 0 are padding.  A block that several
- * sequences map is written by each of them.  Keys are finite.  Device errors as
- * in kvc_append.  Workspace: kvc_workspace_bytes(d). */
+ * sequences map is written by each of them: they have to reach the same row of
+ * it, or its codes and step may come from different ones.  Keys are finite.
+ * Device errors as in kvc_append.  Workspace: kvc_workspace_bytes(d). */
 KVC_API size_t kvc_bounds_bytes(const kvc_desc* d);
 KVC_API int kvc_block_bounds(const kvc_desc* d, const void* cache, int32_t layer, void* bounds, const int32_t* pos,
                              int32_t n_new, const int32_t* n_tok, const int32_t* block_table, void* workspace,

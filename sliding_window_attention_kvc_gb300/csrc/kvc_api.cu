@@ -1134,6 +1134,13 @@ KVC_API int kvc_block_release(const kvc_desc* d, int32_t* block_table, uint32_t*
     return launch_block_release(p, n, (cudaStream_t)stream) == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
+// What the calls on parts of a cache take of a descriptor: a paged cache, and tables whose indices stay in 32 bits a
+// whole CTA's stride past their end.
+static int part_desc(const kvc_desc* d) {
+    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    return d->max_blocks_per_seq > (1 << 30) ? KVC_ERR_UNSUPPORTED : KVC_OK;
+}
+
 // The bounds of a paged cache's blocks: codes, then steps (kvc_block_bounds).
 static size_t bounds_code_bytes(const kvc_desc* d) {
     return (size_t)d->layers * d->num_blocks * d->kv_heads * 2 * d->head_dim;
@@ -1141,7 +1148,7 @@ static size_t bounds_code_bytes(const kvc_desc* d) {
 
 KVC_API size_t kvc_bounds_bytes(const kvc_desc* d) {
     Geo g;
-    if (check_desc(d, &g) != KVC_OK || d->layout != KVC_LAYOUT_PAGED) return 0;
+    if (check_desc(d, &g) != KVC_OK || part_desc(d) != KVC_OK) return 0;
     return bounds_code_bytes(d) + (size_t)d->layers * d->num_blocks * d->kv_heads * 4;
 }
 
@@ -1151,7 +1158,7 @@ KVC_API int kvc_block_bounds(const kvc_desc* d, const void* cache, int32_t layer
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
-    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if ((rc = part_desc(d))) return rc;
     if (!cache || !bounds || !pos || !block_table || !workspace) return KVC_ERR_NULL;
     if (!aligned16(cache) || !aligned16(bounds) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(n_tok) & 3u))
         return KVC_ERR_ALIGN;
@@ -1188,7 +1195,8 @@ KVC_API int kvc_block_bounds(const kvc_desc* d, const void* cache, int32_t layer
 
 // What kvc_select_blocks and kvc_decode_attention_selected take of a descriptor and k.
 static int select_desc(const kvc_desc* d, const Geo& g, int32_t k) {
-    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    const int rc = part_desc(d);
+    if (rc) return rc;
     if (g.G > 128) return KVC_ERR_UNSUPPORTED;
     if (k < 1 || k > (1 << 24)) return KVC_ERR_ARG;
     return KVC_OK;
@@ -1265,7 +1273,7 @@ KVC_API int kvc_decode_attention_selected(const kvc_desc* d, const void* cache, 
 
 KVC_API size_t kvc_weighed_workspace_bytes(const kvc_desc* d) {
     Geo g;
-    if (check_desc(d, &g) != KVC_OK || d->layout != KVC_LAYOUT_PAGED || d->dtype == KVC_F32) return 0;
+    if (check_desc(d, &g) != KVC_OK || part_desc(d) != KVC_OK || d->dtype == KVC_F32) return 0;
     return weigh_layout(d, g).total;
 }
 
@@ -1276,7 +1284,7 @@ KVC_API int kvc_decode_attention_weighed(const kvc_desc* d, const void* cache, i
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
-    if (d->layout != KVC_LAYOUT_PAGED) return KVC_ERR_DESC;
+    if ((rc = part_desc(d))) return rc;
     if (d->dtype == KVC_F32) return KVC_ERR_UNSUPPORTED;
     if (!weights) return KVC_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(weights) & 3u) return KVC_ERR_ALIGN;
@@ -1296,6 +1304,7 @@ KVC_API int kvc_block_evict(const kvc_desc* d, float* weights, const int32_t* po
     Geo g;
     int rc = check_desc(d, &g);
     if (rc) return rc;
+    if ((rc = part_desc(d))) return rc;
     if (!weights || !pos || !block_table || !refcount || !free_list || !free_count) return KVC_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(weights) & 3u) return KVC_ERR_ALIGN;
     if (first < 0 || recent < 1 || (long long)first + recent > keep) return KVC_ERR_ARG;

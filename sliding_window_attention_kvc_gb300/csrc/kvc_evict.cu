@@ -35,13 +35,13 @@ __global__ void __launch_bounds__(kWeighThreads, 6) weigh_kernel(const __grid_co
     // (positions, table and valid bits were final before the decode could start the kernels
     // behind it: they are read while it runs)
     ev_pdl_launch();
-    const int t = clamp_paged_t(p.pos[b], p.maxb, p.bs);
+    const int t = clamp_paged_t(__ldcg(p.pos + b), p.maxb, p.bs);
     const float* sc = p.scores + (long long)b * p.Hq * p.stride;
     const float2* ml = p.ml + (long long)b * p.Hq;
     float* wrow = p.weights + (long long)b * p.maxb;
     auto attended = [&](int lb) {
-        const int phys = __ldg(trow + lb);
-        return phys >= 0 && phys < p.num_blocks && (!p.valid || ((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u));
+        const int phys = __ldcg(trow + lb);
+        return phys >= 0 && phys < p.num_blocks && (!p.valid || ((__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u));
     };
     auto store = [&](int lb, float sum) { wrow[lb] = p.decay == 0.f ? sum : fmaf(p.decay, wrow[lb], sum); };
     // weights of positions pos .. pos + 3 (pos a multiple of 4, within the row) over heads h0 .. h1 - 1; what lies
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kWeighThreads, 6) weigh_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // eviction
 // ---------------------------------------------------------------------------
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 1024;             // at most; at least 256
 constexpr int kEvictWarps = kEvictThreads / 32;
 
 // Order of weights as unsigned integers: -0 counts as 0, NaN as the heaviest.
@@ -152,7 +152,7 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
     if (lane == 31) s_w[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = s_w[lane];
+        int w = lane < (int)(blockDim.x >> 5) ? s_w[lane] : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int a = __shfl_up_sync(0xffffffffu, w, off);
@@ -162,7 +162,7 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
     }
     __syncthreads();
     const int ex = x - v + (warp > 0 ? s_w[warp - 1] : 0);
-    *tot = s_w[kEvictWarps - 1];
+    *tot = s_w[(blockDim.x >> 5) - 1];
     __syncthreads();
     return ex;
 }
@@ -185,19 +185,20 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    __shared__ int s_hist[4][256];
+    __shared__ int s_hist[4][256];              // this CTA's counts of each pass
+    __shared__ __align__(16) int s_part[256 * 8];   // a pass's counts, a column for every eighth lane
     __shared__ int s_w[kEvictWarps];
     __shared__ int s_count[2];                  // mapped, and those that may go
     __shared__ int s_digit, s_beyond, s_in, s_last;
     __shared__ uint32_t s_key[kEvictKeys];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x / CL;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x / CL;
     auto sync_all = [&]() {
         if (CL > 1)
             cluster.sync();
         else
             __syncthreads();
     };
-    for (int i = tid; i < 4 * 256; i += kEvictThreads) s_hist[0][i] = 0;
+    for (int i = tid; i < 256 * 8; i += nt) s_part[i] = 0;
     if (tid < 2) s_count[tid] = 0;
     __syncthreads();
     ev_pdl_wait();
@@ -211,18 +212,18 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     const bool kept = hi_i - lo_i <= kEvictKeys;
     int live = 0, loose = 0;
 #pragma unroll 1
-    for (int base = lo_i; base < hi_i; base += 4 * kEvictThreads) {
+    for (int base = lo_i; base < hi_i; base += 4 * nt) {
         int e[4];
         float w[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int i = base + u * kEvictThreads + tid;
+            const int i = base + u * nt + tid;
             e[u] = i < hi_i ? trow[i] : -1;
             w[u] = i < hi_i ? wrow[i] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int i = base + u * kEvictThreads + tid;
+            const int i = base + u * nt + tid;
             const bool may = e[u] >= 0 && i >= p.first && i < hi;
             live += e[u] >= 0;
             loose += may;
@@ -236,12 +237,21 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         atomicAdd(&s_count[1], loose);
     }
     sync_all();
+    // a value of each CTA of the cluster (at most eight: all on their way together)
+    auto of_all = [&](int* mine, int (&v)[8]) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = c < CL ? *cluster.map_shared_rank(mine, c) : 0;
+    };
     int nlive = 0, nloose = 0;
-#pragma unroll 1
-    for (int c = 0; c < CL; ++c) {
-        const int* o = cluster.map_shared_rank(s_count, c);
-        nlive += o[0];
-        nloose += o[1];
+    {
+        int v[8], w[8];
+        of_all(&s_count[0], v);
+        of_all(&s_count[1], w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            nlive += v[c];
+            nloose += w[c];
+        }
     }
     // this thread's key of index i (a long table's keys are worked out again)
     auto key_of = [&](int i) -> uint32_t {
@@ -257,25 +267,27 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         for (;; ++pass) {
             const int shift = 24 - 8 * pass;
 #pragma unroll 1
-            for (int base = lo_i; base < hi_i; base += kEvictThreads) {
+            for (int base = lo_i; base < hi_i; base += nt) {
                 const uint32_t key = key_of(base + tid);
                 const bool in = key != kKeyStays && (key & mask) == prefix;
-                const uint32_t d = (key >> shift) & 255u;
-                const unsigned act = __ballot_sync(0xffffffffu, in);
-                const int lead = __ffs(act) - 1;
-                const uint32_t d0 = __shfl_sync(0xffffffffu, d, max(lead, 0));
-                if (__all_sync(0xffffffffu, !in || d == d0)) {      // one addition where all have the same
-                    if (lane == lead) atomicAdd(&s_hist[pass][d0], __popc(act));
-                } else if (in) {
-                    atomicAdd(&s_hist[pass][d], 1);
-                }
+                // (most weights share a few digits: eight lanes that add to one of them meet four at a time)
+                if (in) atomicAdd(&s_part[((key >> shift) & 255u) * 8 + (lane & 7)], 1);
+            }
+            __syncthreads();
+            if (tid < 256) {
+                int4* c = reinterpret_cast<int4*>(s_part + tid * 8);
+                const int4 x = c[0], y = c[1];
+                s_hist[pass][tid] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+                c[0] = c[1] = make_int4(0, 0, 0, 0);
             }
             sync_all();
             // a thread a digit: its keys in the cluster, and those of smaller digits
             int mine = 0, incl = 0;
             if (tid < 256) {
-#pragma unroll 1
-                for (int o = 0; o < CL; ++o) mine += *cluster.map_shared_rank(&s_hist[pass][tid], o);
+                int v[8];
+                of_all(&s_hist[pass][tid], v);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) mine += v[c];
                 incl = mine;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -304,18 +316,22 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         // keys whose digits lie below `prefix` go, and the first `want` of those that begin with it: so many of
         // them lie in the CTAs before
         int before = 0;
-#pragma unroll 1
-        for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&s_hist[pass][digit], c);
+        {
+            int v[8];
+            of_all(&s_hist[pass][digit], v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) before += c < rank ? v[c] : 0;
+        }
         const int own = s_hist[pass][digit];
         const int take = before >= want ? 0 : min(own, want - before);      // of this CTA's
         int run = 0;                            // such keys before this pass
 #pragma unroll 1
-        for (int base = lo_i; base < hi_i; base += 4 * kEvictThreads) {
+        for (int base = lo_i; base < hi_i; base += 4 * nt) {
             int phys[4], old[4];
             unsigned goes = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = base + u * kEvictThreads + tid;
+                const int i = base + u * nt + tid;
                 const uint32_t key = key_of(i), top = key & mask;
                 bool g = key != kKeyStays && top < prefix;
                 const bool same = key != kKeyStays && top == prefix;
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if ((goes >> u) & 1u) {
-                    const int i = base + u * kEvictThreads + tid;
+                    const int i = base + u * nt + tid;
                     trow[i] = -1;
                     wrow[i] = 0.f;
                     old[u] = 0;
@@ -360,40 +376,49 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     const int words = (p.num_blocks + 31) / 32;
     const int w0 = (int)((long long)words * rank / CL), w1 = (int)((long long)words * (rank + 1) / CL);
     const int free0 = *p.free_count;
+    const bool short_ = w1 - w0 <= 256 * 8;     // the words stay in shared memory
     int mine = 0;
 #pragma unroll 1
-    for (int i = w0 + tid; i < w1; i += kEvictThreads) mine += __popc(__ldcg(p.back + i));
+    for (int i = w0 + tid; i < w1; i += nt) {
+        const uint32_t w = __ldcg(p.back + i);
+        if (short_) s_part[i - w0] = (int)w;
+        mine += __popc(w);
+    }
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (tid == 0) s_count[0] = 0;
     __syncthreads();
     if (lane == 0 && mine) atomicAdd(&s_count[0], mine);
     sync_all();
     int at = free0, all = free0;                // list entries before this CTA's, and in the end
-#pragma unroll 1
-    for (int c = 0; c < CL; ++c) {
-        const int n = cluster.map_shared_rank(s_count, c)[0];
-        at += c < rank ? n : 0;
-        all += n;
-    }
-    // a quarter of a word a thread: the marked blocks in order into shared memory, and out in whole lines
-    static_assert(kEvictKeys >= 8 * kEvictThreads, "every block of a pass may be marked");
-#pragma unroll 1
-    for (int base = w0; base < w1; base += kEvictThreads / 4) {
-        const int i = base + (tid >> 2), part = tid & 3;
-        const uint32_t w = i < w1 ? __ldcg(p.back + i) : 0u;
-        uint32_t byte = (w >> (8 * part)) & 255u;
-        int tot;
-        int k = evict_scan(__popc(byte), s_w, &tot);
-        while (byte) {
-            s_key[k++] = (uint32_t)(i * 32 + 8 * part + __ffs(byte) - 1);
-            byte &= byte - 1u;
+    {
+        int v[8];
+        of_all(&s_count[0], v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            at += c < rank ? v[c] : 0;
+            all += v[c];
         }
-        __syncthreads();                        // (and the word has been read by its four threads)
+    }
+    // the marked blocks of 256 words in order into shared memory, and out in whole lines
+    static_assert(kEvictKeys >= 32 * 256, "every block of a pass may be marked");
+    const int per = nt / 256, bits = 32 / per;  // threads of a word, marks of a thread
+#pragma unroll 1
+    for (int base = w0; base < w1; base += 256) {
+        const int i = base + tid / per, part = tid % per;
+        const uint32_t w = i < w1 ? (short_ ? (uint32_t)s_part[i - w0] : __ldcg(p.back + i)) : 0u;
+        uint32_t mark = per == 1 ? w : (w >> (bits * part)) & ((1u << bits) - 1u);
+        int tot;
+        int k = evict_scan(__popc(mark), s_w, &tot);
+        while (mark) {
+            s_key[k++] = (uint32_t)(i * 32 + bits * part + __ffs(mark) - 1);
+            mark &= mark - 1u;
+        }
+        __syncthreads();                        // (and the word has been read by all of its threads)
         if (w && part == 0) {
             p.back[i] = 0u;
             if (p.valid) p.valid[i] &= ~w;
         }
-        for (int j = tid; j < tot; j += kEvictThreads) {
+        for (int j = tid; j < tot; j += nt) {
             if (at + j >= 0 && at + j < p.num_blocks)
                 p.free_list[at + j] = (int)s_key[j];
             else
@@ -433,11 +458,13 @@ cudaError_t launch_weigh(const WeighParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_block_evict(const EvictParams& p, cudaStream_t s) {
-    // up to four keys a thread, as far as eight CTAs go (a cluster of eight runs on every GPU)
-    int cl = 1;
-    while (cl < 8 && (long long)cl * 4 * kEvictThreads < p.maxb) cl *= 2;
+    // up to four keys a thread, as far as eight CTAs go (a cluster of eight runs on every GPU); no more
+    // threads than keys: their barriers are what a short table waits for
+    int cl = 1, threads = 256;
+    while (threads < kEvictThreads && threads < p.maxb) threads *= 2;
+    while (cl < 8 && (long long)cl * 4 * threads < p.maxb) cl *= 2;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = ev_config(dim3((unsigned)(p.B * cl)), kEvictThreads, s, attr);
+    cudaLaunchConfig_t cfg = ev_config(dim3((unsigned)(p.B * cl)), threads, s, attr);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cl;
     attr[1].val.clusterDim.y = 1;

@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kPathThreads) append_path_kernel(const __grid_
             const int h = u / UPH, c = (u - h * UPH) * CH;
             const Elt* kr = ks + (long long)h * D + c;
             const Elt* vr = vs + (long long)h * D + c;
-            uint4 a = __ldg(reinterpret_cast<const uint4*>(kr)), e = __ldg(reinterpret_cast<const uint4*>(kr + D / 2));
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(vr)), y = __ldg(reinterpret_cast<const uint4*>(vr + D / 2));
+            uint4 a = __ldcg(reinterpret_cast<const uint4*>(kr)), e = __ldcg(reinterpret_cast<const uint4*>(kr + D / 2));
+            const uint4 x = __ldcg(reinterpret_cast<const uint4*>(vr)), y = __ldcg(reinterpret_cast<const uint4*>(vr + D / 2));
             if (p.rope == kRopeBaked) {
                 float f[CH], g[CH];
                 TR::unpack(a, f);

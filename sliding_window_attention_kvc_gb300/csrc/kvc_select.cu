@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const __gr
                 const int r = min(base + u * RPW, rows - 1);  // (a row twice changes nothing)
 #pragma unroll
                 for (int k = 0; k < NCH; ++k)
-                    w[u][k] = __ldg(reinterpret_cast<const uint4*>(src + (long long)r * D + (k * LPR + c) * VPL));
-                s[u] = sizeof(Elt) == 1 ? __ldg(sc + r) : 1.f;
+                    w[u][k] = __ldcg(reinterpret_cast<const uint4*>(src + (long long)r * D + (k * LPR + c) * VPL));
+                s[u] = sizeof(Elt) == 1 ? __ldcg(sc + r) : 1.f;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     sl_pdl_wait();
     sl_pdl_launch();
     const int lb0 = (blockIdx.x * W + warp) * 32;                     // this warp's blocks
-    int phys = lb0 + lane < p.maxb ? __ldg(p.table + (long long)b * p.maxb + lb0 + lane) : -1;
+    int phys = lb0 + lane < p.maxb ? __ldcg(p.table + (long long)b * p.maxb + lb0 + lane) : -1;
     const int traw = p.pos[b];
     const int t = clamp_paged_t(traw, p.maxb, p.bs);
     if ((traw < 0 || traw != t) && blockIdx.x == 0 && h == 0 && tid == 0) set_error(p.err, 0x4u /* KVC_DEV_BAD_POSITION */);
@@ -315,19 +315,19 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
         phys = -1;
     }
-    if (phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
+    if (phys >= 0 && p.valid && !((__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
     const unsigned have = __ballot_sync(0xffffffffu, phys >= 0);
     const int ln = lane % LPB, sub = lane / LPB;
     const uint32_t unit = (uint32_t)max(phys, 0) * (uint32_t)p.Hkv + (uint32_t)h;      // (fits: the steps are an array of them)
-    const float step = have ? __ldg(p.steps + unit) : 0.f;
+    const float step = have ? __ldcg(p.steps + unit) : 0.f;
     const uint4* src = reinterpret_cast<const uint4*>(p.codes) + ln;
     uint4 hi[2][U], lo[2][U];
     auto load = [&](int it) {                                         // the ends of U BPW blocks
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint4* at = src + (size_t)__shfl_sync(0xffffffffu, unit, (it * U + u) * BPW + sub) * (2 * LPB);
-            hi[it & 1][u] = __ldg(at);
-            lo[it & 1][u] = __ldg(at + LPB);
+            hi[it & 1][u] = __ldcg(at);
+            lo[it & 1][u] = __ldcg(at + LPB);
         }
     };
     if (have) load(0);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                EltTraits<Act>::unpack(__ldg(reinterpret_cast<const uint4*>(qr + e * (D / 2)) + c), x[e] + c * V);
+                EltTraits<Act>::unpack(__ldcg(reinterpret_cast<const uint4*>(qr + e * (D / 2)) + c), x[e] + c * V);
         if (p.rope != kRopeNone) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -663,12 +663,12 @@ __global__ void __launch_bounds__(kListThreads) select_list_kernel(const __grid_
         if (lb >= 0 && lb <= before) {
             set_error(p.err, 0x10u);
         } else if (lb >= 0 && lb <= last) {
-            phys = __ldg(trow + lb);
+            phys = __ldcg(trow + lb);
             if (phys >= p.num_blocks) {
                 set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
                 phys = -1;
             }
-            if (phys >= 0 && p.valid && !((__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
+            if (phys >= 0 && p.valid && !((__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u)) phys = -1;
         }
         const unsigned have = __ballot_sync(0xffffffffu, phys >= 0);
         if (lane == 0) s_cnt[warp] = __popc(have);

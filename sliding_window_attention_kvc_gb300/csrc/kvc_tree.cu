@@ -91,7 +91,9 @@ __device__ __forceinline__ int tr_cached(const TreeParams& p, int pos) {
     const long long lim = (long long)p.maxb * p.bs;
     return pos < lim ? pos : (int)lim;
 }
-__device__ __forceinline__ int tr_tiles(const TreeParams& p, int pos) { return (tr_cached(p, pos) + kWsKeys - 1) / kWsKeys + 1; }
+__device__ __forceinline__ int tr_tiles(const TreeParams& p, int pos) {
+    return (int)(((unsigned)tr_cached(p, pos) + kWsKeys - 1) / kWsKeys) + 1;      // (2^31 and more on the way)
+}
 __device__ __forceinline__ long long tr_seq_units(const TreeParams& p, int pos) {
     return (long long)tr_tiles(p, pos) * p.col_units * p.Hkv;
 }
@@ -121,7 +123,7 @@ __device__ __noinline__ TrParts tr_partition(const TreeParams& p) {
     for (int base = 0; base < p.B; base += 32) {
         const int o = base + lane;
         if (o < p.B) {
-            const int kt = tr_tiles(p, __ldg(p.pos + o));
+            const int kt = tr_tiles(p, p.pos[o]);
             tot += (long long)kt * p.col_units * p.Hkv;
             lo = min(lo, kt);
             hi = max(hi, kt);
@@ -149,7 +151,7 @@ __device__ __noinline__ TrWalk tr_find(const TreeParams& p, long long u) {
     long long run = 0;
     for (int base = 0; base < p.B; base += 32) {
         const int o = base + lane;
-        const long long n = o < p.B ? tr_seq_units(p, __ldg(p.pos + o)) : 0;
+        const long long n = o < p.B ? tr_seq_units(p, p.pos[o]) : 0;
         long long incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -185,10 +187,10 @@ struct TrSegment {
 template <int D>
 __device__ __noinline__ TrSegment tr_segment(const TreeParams& p, TrWalk& w, long long u, long long hi) {
     TrSegment s;
-    s.pos = __ldg(p.pos + w.b);
+    s.pos = p.pos[w.b];
     for (long long n = tr_seq_units(p, s.pos); u >= w.before + n && w.b < p.B - 1;) {
         w.before += n;
-        s.pos = __ldg(p.pos + ++w.b);
+        s.pos = p.pos[++w.b];
         n = tr_seq_units(p, s.pos);
     }
     s.b = w.b;
@@ -237,7 +239,7 @@ __device__ __noinline__ TrDraft tr_draft(const TreeParams& p, int b, int pos, bo
         const int i = lane + 32 * e;
         int par = -2;
         if (i < p.T && pos >= 0) {
-            par = __ldg(p.parent + (long long)b * p.T + i);
+            par = __ldcg(p.parent + (long long)b * p.T + i);
             if (par >= i) {
                 if (report) set_error(p.err, 0x10u /* KVC_DEV_BAD_ENTRY */);
                 par = -2;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(256) tree_stage_kernel(const __grid_constant__
     tr_pdl_wait();
     tr_pdl_launch();
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    const int pos = __ldg(p.pos + b);
+    const int pos = p.pos[b];
     if (tid < 32) {
         const TrDraft d = tr_draft(p, b, pos, false);
         s_depth[lane] = __popcll(d.see[0]) - 1;
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(256) tree_stage_kernel(const __grid_constant__
         if (s_depth[t] < 0) continue;
         const long long at = ((long long)b * p.T * p.Hkv + row) * D + c;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k_new) + at;
-        uint4 x = __ldg(reinterpret_cast<const uint4*>(src)), y = __ldg(reinterpret_cast<const uint4*>(src + D / 2));
+        uint4 x = __ldcg(reinterpret_cast<const uint4*>(src)), y = __ldcg(reinterpret_cast<const uint4*>(src + D / 2));
         tr_rotate8(x, y, (long long)pos + s_depth[t], p.theta + c);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.stage) + at;
         *reinterpret_cast<uint4*>(dst) = x;
@@ -456,13 +458,13 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                     const int r0 = cp * box;
                     if (paged) {
                         const int lb = r0 / bs;
-                        const int phys = __ldg(trow + lb);
+                        const int phys = __ldcg(trow + lb);
                         bool att = phys >= 0;
                         if (phys >= p.num_blocks) {
                             set_error(p.err, 0x1u /* KVC_DEV_BAD_BLOCK */);
                             att = false;
                         }
-                        if (att && p.valid) att = (__ldg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u;
+                        if (att && p.valid) att = (__ldcg(p.valid + (phys >> 5)) >> (phys & 31)) & 1u;
                         if (att) row = (int)(((long long)phys * p.Hkv + sg.h) * bs + (r0 - lb * bs));
                     } else {
                         row = (int)(((long long)sg.b * p.Hkv + sg.h) * p.capacity + r0);
@@ -655,15 +657,16 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         TrDraft draft{};
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
-            if (sg.b != at_b) {
+            // (the draft's ancestors: before the q rows where those are rotated, else while the
+            // first product runs)
+            auto know_draft = [&]() {
+                if (sg.b == at_b) return;
                 draft = tr_draft(p, sg.b, sg.pos, false);
                 at_b = sg.b;
-            }
+            };
+            if (p.rope != kRopeNone) know_draft();
             const int c0 = sg.alt ? 0 : qi * p.tq;         // the Q tile's first token in the column
             const bool row_ok = tl < p.tq && c0 + tl < sg.tokens;
-            const unsigned long long see = draft.of(row_ok ? sg.n0 + c0 + tl : 0);
-            const bool real = row_ok && see != 0ull;
-            const int depth = __popcll(see) - 1;
             const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
             // Q rows, rotated at their positions when BAKED, unscaled bf16
             if (nt > 0) {
@@ -682,8 +685,8 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                             const __nv_bfloat16* qrow =
                                 static_cast<const __nv_bfloat16*>(p.q) +
                                 (((long long)sg.b * p.T + sg.n0 + c0 + rtl) * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
-                            a[it] = __ldg(reinterpret_cast<const uint4*>(qrow + 8 * c));
-                            e[it] = __ldg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
+                            a[it] = __ldcg(reinterpret_cast<const uint4*>(qrow + 8 * c));
+                            e[it] = __ldcg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
                         }
                     }
 #pragma unroll
@@ -713,6 +716,10 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->q_ready[qi]);
             }
+            know_draft();
+            const unsigned long long see = draft.of(row_ok ? sg.n0 + c0 + tl : 0);
+            const bool real = row_ok && see != 0ull;
+            const int depth = __popcll(see) - 1;
             float m_run = -INFINITY, l_run = 0.f;          // m in base-2 units of the scaled scores
             for (int lt = 0; lt < nt; ++lt) {
                 const int j = base + lt;

@@ -96,6 +96,8 @@ class Draft:
         c = self.c
         G = c.H // c.KV
         freq = plain.frequencies(c.D)[0]
+        kept = {}
+        table = self.table if c.layout == "paged" else None
         for b, n in enumerate(c.lens):
             if b in skip:
                 continue
@@ -107,15 +109,18 @@ class Draft:
                 t = n + len(line) - 1
                 ps = [p for p in plain.attended(c.layout, t, c.window, c.sinks) if p < n]
                 if c.layout == "paged":
-                    ps = [p for p in ps if 0 <= int(self.table[b][p // c.bs]) < c.d.num_blocks
-                          and int(self.table[b][p // c.bs]) not in dead]
+                    ps = [p for p in ps if 0 <= table[b][p // c.bs] < c.d.num_blocks and table[b][p // c.bs] not in dead]
                 kd, vd = self.k[b, line].double(), self.v[b, line].double()
                 q = self.q[b, i].double()
                 if self.rope == "baked":
                     kd = plain.rotate(kd, torch.arange(n, n + len(line), device="cuda"), freq, 1.0, "half")
                     q = plain.rotate(q, torch.tensor(t, device="cuda"), freq, 1.0, "half")
                 if ps:
-                    k, v = c.rows(b, ps)
+                    if (b, ps[0], len(ps)) not in kept:          # (positions of one sequence: whole runs but for sinks)
+                        kept[b, ps[0], len(ps)] = (ps, c.rows(b, ps))
+                    same, (k, v) = kept[b, ps[0], len(ps)]
+                    if same != ps:
+                        k, v = c.rows(b, ps)
                     kd, vd = torch.cat([k, kd]), torch.cat([v, vd])
                 see = torch.ones(1, kd.shape[0], dtype=torch.bool, device="cuda")
                 want, w = plain.attend(q[None], kd, vd, see, see, c.scale)

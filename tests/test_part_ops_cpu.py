@@ -195,3 +195,22 @@ def test_tree_refusals(kvc):
     with pytest.raises(ValueError, match="CUDA"):
         kvc.tree_attention(d, kv, 0, q, kv, kv, torch.zeros(3, dtype=torch.int32), torch.zeros(3, 5, dtype=torch.int32),
                            torch.zeros(64, dtype=torch.uint8))
+
+
+def test_longest_tables(kvc):
+    """Tables of more than 2^30 blocks a sequence are refused by every call that walks them: their indices are 32
+    bits, a whole CTA's stride past the end."""
+    L = kvc.lib()
+
+    def calls(maxb):
+        d = kvc.make_desc(**dict(PAGED, batch=1, block_size=1, max_blocks_per_seq=maxb))
+        r = ctypes.byref(d)
+        return (L.kvc_block_bounds(r, A, 0, A, A, 4, None, A, A, 0, None),
+                L.kvc_select_blocks(r, A, 0, A, A, 4, 1, 1, A, None, A, A, 0, None),
+                L.kvc_decode_attention_selected(r, A, 0, A, A, A, 4, A, None, A, A, 0, None),
+                L.kvc_decode_attention_weighed(r, A, 0, A, A, A, None, 1.0, A, A, A, 0, None),
+                L.kvc_block_evict(r, A, A, 3, 1, 1, A, None, A, A, A, A, 0, None)), (
+            kvc.bounds_bytes(d) > 0, kvc.select_workspace_bytes(d, 4) > 0, kvc.weighed_workspace_bytes(d) > 0)
+
+    assert calls((1 << 30) + 1) == ((kvc.KVC_ERR_UNSUPPORTED,) * 5, (False,) * 3)
+    assert calls(1 << 30) == ((kvc.KVC_ERR_WORKSPACE,) * 5, (True,) * 3)
