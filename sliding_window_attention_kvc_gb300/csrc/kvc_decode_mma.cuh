@@ -582,7 +582,11 @@ __device__ __noinline__ void append_token_warp(const DecodeParams& p, long long 
 // wholly below the sequence's start are not copied.  Paged bf16 batch of 64, 1008 MB of
 // attended rows, distance bias and starts: 166 us, 0.89 of the measured bandwidth;
 // 8 rings of 4096, cap: 27 us, 0.73 (31 replayed from a graph).
-// EXT: one of DecodeExt's additions to a paged decode.
+// EXT: one of DecodeExt's additions to a paged decode.  Batch of 64, 32 / 8 heads of 128,
+// bf16: lists of 128 blocks of 16 a kv head (537 MB) 93 us with the lists' kernel and the
+// combine, 0.85 of the measured bandwidth; every row's score kept (1.13 GB attended) 204 us
+// with plan, combine and weights, where the plain decode takes 180: the scores are 36 MB
+// more, written and read again (they stay in L2), and one more launch.
 template <int D, int GH, bool PAGED, bool READ, bool Q8, bool SCORE, int EXT = kExtNone>
 // Two CTAs (ten warps) per SM: three warps share a sub-partition's 16K
 // registers, so a thread may hold at most 168.

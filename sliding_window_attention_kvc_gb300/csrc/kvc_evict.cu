@@ -23,7 +23,9 @@ constexpr int kWeighParts = kWeighThreads / (kWeighRows / 4);   // head groups t
 // 2^(s - M) / L of four positions (one 16-byte load a head) over a quarter of the q
 // heads, in head order; the quarters, then the rows of each block, are added in
 // order: the same sums whatever the decode's shares were.  What bounds it: 4 bytes a
-// row and head, which the decode has just left in L2, and an exponential for each.
+// row and head, which the decode has just left in L2, and an exponential for each
+// (64 sequences, 32 heads, 277,000 rows: 13 us launched alone on cold caches; its way to
+// position and table passes while the combine runs).
 __global__ void __launch_bounds__(kWeighThreads, 6) weigh_kernel(const __grid_constant__ WeighParams p) {
     __shared__ float4 s_part[kWeighThreads];
     __shared__ float s_row[kWeighRows];
@@ -175,9 +177,10 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
 // last cluster to finish (an atomic ticket, no waiting) puts the marked ones on the
 // free list in ascending order and clears their resident bits.
 // What bounds it: a dozen dependent trips to L2, barriers and a cold instruction
-// cache, whatever the length (a single CTA a sequence took 309 us for two of up to
-// 62,500 blocks; the free list written a word of 32 marks a thread, 32 lines a store,
-// held it at 83).
+// cache, whatever the length: 16 us for 64 sequences of up to 512 blocks, 37 for two of
+// up to 62,500 (309 with a single CTA a sequence; 83 with the free list written a word
+// of 32 marks a thread, 32 lines a store; 42 with one counter a digit, its additions in
+// turn, and 1024 threads whatever the table).
 constexpr int kEvictKeys = 8192;                // keys a CTA keeps
 constexpr uint32_t kKeyStays = 0xffffffffu;     // not among the blocks that may go
 

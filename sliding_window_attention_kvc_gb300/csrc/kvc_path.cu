@@ -13,7 +13,8 @@ constexpr int kPathThreads = 128;
 // of the second half of a row, which are rotated with each other when BAKED (as
 // kvc_append rotates them), of K and of V: four loads in flight, whole sectors
 // written.  INT8: a warp a kv head.  A handful of rows: the latency of one
-// dependent chain (count, index, row) is what it costs.
+// dependent chain (count, index, row) is what it costs: 2.1 us for up to 8 of 32
+// tokens of 64 sequences, 8 kv heads of 128, bf16, replayed from a graph.
 template <typename Elt, int D>
 __global__ void __launch_bounds__(kPathThreads) append_path_kernel(const __grid_constant__ PathParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
