@@ -76,7 +76,11 @@ struct alignas(16) TrStageMeta {
 
 struct TrBars {
     uint64_t full[6], ready[6], empty[6];
-    uint64_t s_full[2][2], p_full[2], o_done[2], q_ready[2], fin[2];
+    // (of two tiles in turn: a warp hands over P of a tile before it asks for O of the tile before, and the
+    // issuer may ask for a P once the next has been handed over; on one barrier each, a warp or an issuer held
+    // up for a product's time would find the phase after the one it asks for, and wait for good)
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
+    uint64_t q_ready[2], fin[2];
     uint64_t both[2];               // alternate tiles: both warpgroups' sums are there; both have read them
     uint32_t tmem;
     int abort;
@@ -393,9 +397,11 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             mbar_init(&bars->empty[s], NQ);
         }
         for (int i = 0; i < 2; ++i) {
-            for (int u = 0; u < 2; ++u) mbar_init(&bars->s_full[i][u], 1);
-            mbar_init(&bars->p_full[i], 4);
-            mbar_init(&bars->o_done[i], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&bars->s_full[i][u], 1);
+                mbar_init(&bars->p_full[i][u], 4);
+                mbar_init(&bars->o_done[i][u], 1);
+            }
             mbar_init(&bars->q_ready[i], 4);
             mbar_init(&bars->fin[i], 1);
             mbar_init(&bars->both[i], 4 * NQ);
@@ -610,14 +616,14 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                         continue;
                     }
                 }
-                if (npv < ns && ws_test(&bars->p_full[i], (base + npv) & 1)) {
+                if (npv < ns && ws_test(&bars->p_full[i][(base + npv) & 1], ((base + npv) >> 1) & 1)) {
                     ws_fence_after();
                     const int t = idx0 + (sg.alt ? 2 * npv + i : npv), s = t % NST;
                     if (lane == 0) {
                         // P_i in the S buffer it came from (bf16 pairs)
                         tr_issue_pv<D>(o_t, s0 + (uint32_t)(((base + npv) & 1) * kWsKeys),
                                        vd0 + (uint64_t)((s * S::StageBytes) >> 4), npv > 0);
-                        ws_commit(&bars->o_done[i]);
+                        ws_commit(&bars->o_done[i][(base + npv) & 1]);
                         ws_commit(&bars->empty[s]);        // this Q tile is done with the tile's K and V
                     }
                     __syncwarp();
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 // rescaled, that is asked for after this tile's weights have been handed over
                 const bool rescale = lt > 0 && __any_sync(0xffffffffu, alpha != 1.f);
                 if (rescale) {
-                    if (!tr_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                    if (!tr_wait(&bars->o_done[qi][(j - 1) & 1], ((j - 1) >> 1) & 1, abort)) {
                         ok = false;
                         break;
                     }
@@ -795,8 +801,8 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 ws_wait_st();
                 ws_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[qi]);
-                if (lt > 0 && !rescale && !tr_wait(&bars->o_done[qi], (j - 1) & 1, abort)) {
+                if (lane == 0) mbar_arrive(&bars->p_full[qi][j & 1]);
+                if (lt > 0 && !rescale && !tr_wait(&bars->o_done[qi][(j - 1) & 1], ((j - 1) >> 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             }
             // the last P V, then the partial (m, l, o) of each row
             if (nt > 0) {
-                if (!ws_wait(&bars->o_done[qi], (base + nt - 1) & 1, abort)) {
+                if (!ws_wait(&bars->o_done[qi][(base + nt - 1) & 1], ((base + nt - 1) >> 1) & 1, abort)) {
                     give_up();
                     break;
                 }

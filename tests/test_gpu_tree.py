@@ -372,3 +372,20 @@ def test_calls_at_once_on_two_streams(kvc):
     torch.cuda.synchronize()
     for r, w, o in zip(runs, want, outs):
         assert torch.equal(o, w) and kvc.get_error(r.ws) == 0
+
+
+@pytest.mark.parametrize("layout,D,T,lens", [("paged", 128, 64, [60001]), ("paged", 64, 64, [30000, 9000]),
+                                             ("paged", 256, 40, [20000]), ("ring", 128, 32, [5000] * 8)])
+def test_many_launches(kvc, layout, D, T, lens):
+    """No wait of a role is ever overtaken by the phase after the one it asks for: thousands of launches, each with the
+    first one's bits and without an error (one in some hundred long drafts would wait for good)."""
+    kw = dict(bs=16) if layout == "paged" else dict(window=4096)
+    s = Draft(kvc, layout, lens, T, [_tree(T, "random", b) for b in range(len(lens))], H=32 if layout == "ring" else 8,
+              KV=8 if layout == "ring" else 2, D=D, **kw)
+    first = s.run(kvc, calls=1).view(torch.int16).clone()
+    c, out = s.c, torch.empty_like(s.q)
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(4000):
+        kvc.tree_attention(c.d, c.cache, c.layer, s.q, s.k, s.v, s.pos0, s.parent, s.ws, c.table, out=out)
+        same &= (out.view(torch.int16) == first).all()
+    assert kvc.get_error(s.ws) == 0 and bool(same)
