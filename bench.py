@@ -381,10 +381,10 @@ class ClockSampler:
 # capture per workload, and the digest of the kernel's sources
 # (KERNEL_TRAFFIC_FILES) they were taken on: reported only while those
 # sources are unchanged.
-KERNEL_TRAFFIC = {"ring_bf16": 137129472, "sink_window_bf16": 542839552,
-                  "paged_shared_prefix_bf16": 842615808, "long_context_pool_bf16": 155723264,
-                  "ring_int8": 69640192}
-KERNEL_TRAFFIC_SOURCES = "493a159d06b4594331754d9e513fb8dd2901f99221b2fbc74c74f70b726fed74"
+KERNEL_TRAFFIC = {"ring_bf16": 137132288, "sink_window_bf16": 542906112,
+                  "paged_shared_prefix_bf16": 840988416, "long_context_pool_bf16": 155747840,
+                  "ring_int8": 69635328}
+KERNEL_TRAFFIC_SOURCES = "46a13812ab0c0b9dba27ddf63945a8c190b78d2e3d22c865b10c16f82599802f"
 
 
 # the sources decode_mma_kernel and its launch are built from
