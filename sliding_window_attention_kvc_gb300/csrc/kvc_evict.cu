@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     __shared__ __align__(16) int s_part[256 * 8];   // a pass's counts, a column for every eighth lane
     __shared__ int s_w[kEvictWarps];
     __shared__ int s_count[2];                  // mapped, and those that may go
-    __shared__ int s_digit, s_beyond, s_in, s_last;
+    __shared__ int s_digit, s_beyond, s_in, s_cut, s_last;
     __shared__ uint32_t s_key[kEvictKeys];
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x / CL;
     auto sync_all = [&]() {
@@ -327,7 +327,25 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         }
         const int own = s_hist[pass][digit];
         const int take = before >= want ? 0 : min(own, want - before);      // of this CTA's
-        int run = 0;                            // such keys before this pass
+        int cut = take > 0 ? hi_i : lo_i;       // those in front of it
+        if (take > 0 && take < own) {           // (uniform) a contiguous run of keys a thread: one scan
+            const int run = (hi_i - lo_i + nt - 1) / nt, a0 = lo_i + tid * run, a1 = min(a0 + run, hi_i);
+            auto same = [&](int i) {
+                const uint32_t key = key_of(i);
+                return key != kKeyStays && (key & mask) == prefix;
+            };
+            int n = 0, tot;
+            for (int i = a0; i < a1; ++i) n += same(i);
+            int k = evict_scan(n, s_w, &tot);
+            if (k < take && k + n >= take) {
+                int i = a0;
+                for (;; ++i)
+                    if (same(i) && ++k == take) break;
+                s_cut = i + 1;
+            }
+            __syncthreads();
+            cut = s_cut;
+        }
 #pragma unroll 1
         for (int base = lo_i; base < hi_i; base += 4 * nt) {
             int phys[4], old[4];
@@ -336,16 +354,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
             for (int u = 0; u < 4; ++u) {
                 const int i = base + u * nt + tid;
                 const uint32_t key = key_of(i), top = key & mask;
-                bool g = key != kKeyStays && top < prefix;
-                const bool same = key != kKeyStays && top == prefix;
-                if (take == own) {
-                    g = g || same;
-                } else if (take > 0) {          // (uniform)
-                    int tot;
-                    const int ex = evict_scan(same, s_w, &tot);
-                    g = g || (same && run + ex < take);
-                    run += tot;
-                }
+                const bool g = key != kKeyStays && (top < prefix || (top == prefix && i < cut));
                 goes |= (unsigned)g << u;
                 phys[u] = g ? trow[i] : 0;
             }
@@ -402,31 +411,44 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
             all += v[c];
         }
     }
-    // the marked blocks of 256 words in order into shared memory, and out in whole lines
-    static_assert(kEvictKeys >= 32 * 256, "every block of a pass may be marked");
-    const int per = nt / 256, bits = 32 / per;  // threads of a word, marks of a thread
+    // 2048 words at a time: a scan places them, then a warp a word writes its marked blocks side by side
+    static_assert(kEvictKeys >= 256 * 8, "a place for each word");
 #pragma unroll 1
-    for (int base = w0; base < w1; base += 256) {
-        const int i = base + tid / per, part = tid % per;
-        const uint32_t w = i < w1 ? (short_ ? (uint32_t)s_part[i - w0] : __ldcg(p.back + i)) : 0u;
-        uint32_t mark = per == 1 ? w : (w >> (bits * part)) & ((1u << bits) - 1u);
-        int tot;
-        int k = evict_scan(__popc(mark), s_w, &tot);
-        while (mark) {
-            s_key[k++] = (uint32_t)(i * 32 + bits * part + __ffs(mark) - 1);
-            mark &= mark - 1u;
+    for (int base = w0; base < w1; base += 256 * 8) {
+        const int n = min(w1 - base, 256 * 8);
+        if (!short_) {
+            for (int k = tid; k < n; k += nt) s_part[k] = (int)__ldcg(p.back + base + k);
+            __syncthreads();
         }
-        __syncthreads();                        // (and the word has been read by all of its threads)
-        if (w && part == 0) {
-            p.back[i] = 0u;
-            if (p.valid) p.valid[i] &= ~w;
+        const int run = (n + nt - 1) / nt, a0 = min(tid * run, n), a1 = min(a0 + run, n);
+        int c = 0, tot;
+        for (int k = a0; k < a1; ++k) c += __popc(s_part[k]);
+        int k0 = at + evict_scan(c, s_w, &tot);
+        for (int k = a0; k < a1; ++k) {
+            s_key[k] = (uint32_t)k0;
+            k0 += __popc(s_part[k]);
         }
-        for (int j = tid; j < tot; j += nt) {
-            if (at + j >= 0 && at + j < p.num_blocks)
-                p.free_list[at + j] = (int)s_key[j];
-            else
-                index_fault(p.err, 41, at + j);
+        for (int k = tid; k < n; k += nt) {
+            const uint32_t w = (uint32_t)s_part[k];
+            if (w) {
+                p.back[base + k] = 0u;
+                if (p.valid) atomicAnd(&p.valid[base + k], ~w);
+            }
         }
+        __syncthreads();
+        const uint32_t below = (1u << lane) - 1u;
+        for (int k = 32 * warp; k < n; k += nt) {
+            const uint32_t word = k + lane < n ? (uint32_t)s_part[k + lane] : 0u, place = k + lane < n ? s_key[k + lane] : 0u;
+            if (!__any_sync(0xffffffffu, word != 0u)) continue;
+            const int id = 32 * (base + k) + lane;
+#pragma unroll 8
+            for (int x = 0; x < 32; ++x) {
+                const uint32_t w = __shfl_sync(0xffffffffu, word, x);
+                const uint32_t j = __shfl_sync(0xffffffffu, place, x) + __popc(w & below);
+                if (((w >> lane) & 1u) && j < (uint32_t)p.num_blocks) p.free_list[j] = id + 32 * x;
+            }
+        }
+        if (tid == 0 && (at < 0 || at + tot > p.num_blocks)) index_fault(p.err, 41, at + tot);
         at += tot;
         __syncthreads();
     }
