@@ -177,17 +177,24 @@ __device__ __forceinline__ int evict_scan(int v, int* s_w, int* tot) {
 // last cluster to finish (an atomic ticket, no waiting) puts the marked ones on the
 // free list in ascending order and clears their resident bits.
 // What bounds it: a dozen dependent trips to L2, barriers and a cold instruction
-// cache, whatever the length: 16 us for 64 sequences of up to 512 blocks, 37 for two of
-// up to 62,500 (309 with a single CTA a sequence; 83 with the free list written a word
-// of 32 marks a thread, 32 lines a store; 42 with one counter a digit, its additions in
-// turn, and 1024 threads whatever the table).
+// cache, for long tables the atomics too: 12.5 us for 64 sequences of up to 512 blocks,
+// 32 for two of up to 62,500 (309 with a single CTA a sequence; 83 with the free list
+// written a word of 32 marks a thread, 32 lines a store; 42 with one counter a digit, its
+// additions in turn, and 1024 threads whatever the table; 37 with the free list staged in
+// shared memory, 256 words at a time).
 constexpr int kEvictKeys = 8192;                // keys a CTA keeps
 constexpr uint32_t kKeyStays = 0xffffffffu;     // not among the blocks that may go
 
+// CTAs of a sequence at most (16 brought two of up to 62,500 blocks from 34 to 32 us, and a call that gives
+// nothing back from 10 to 13).
+constexpr int kEvictCluster = 8;
+
+// CLM: the most CTAs of a cluster (1: no cluster, nothing is gathered).
+template <int CLM>
 __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid_constant__ EvictParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int CL = CLM > 1 ? (int)cluster.num_blocks() : 1, rank = CLM > 1 ? (int)cluster.block_rank() : 0;
     __shared__ int s_hist[4][256];              // this CTA's counts of each pass
     __shared__ __align__(16) int s_part[256 * 8];   // a pass's counts, a column for every eighth lane
     __shared__ int s_w[kEvictWarps];
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     __shared__ uint32_t s_key[kEvictKeys];
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x / CL;
     auto sync_all = [&]() {
-        if (CL > 1)
+        if (CLM > 1)
             cluster.sync();
         else
             __syncthreads();
@@ -240,18 +247,18 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         atomicAdd(&s_count[1], loose);
     }
     sync_all();
-    // a value of each CTA of the cluster (at most eight: all on their way together)
-    auto of_all = [&](int* mine, int (&v)[8]) {
+    // a value of each CTA of the cluster (all on their way together)
+    auto of_all = [&](int* mine, int (&v)[CLM]) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = c < CL ? *cluster.map_shared_rank(mine, c) : 0;
+        for (int c = 0; c < CLM; ++c) v[c] = CLM == 1 ? *mine : (c < CL ? *cluster.map_shared_rank(mine, c) : 0);
     };
     int nlive = 0, nloose = 0;
     {
-        int v[8], w[8];
+        int v[CLM], w[CLM];
         of_all(&s_count[0], v);
         of_all(&s_count[1], w);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < CLM; ++c) {
             nlive += v[c];
             nloose += w[c];
         }
@@ -287,10 +294,10 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
             // a thread a digit: its keys in the cluster, and those of smaller digits
             int mine = 0, incl = 0;
             if (tid < 256) {
-                int v[8];
+                int v[CLM];
                 of_all(&s_hist[pass][tid], v);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) mine += v[c];
+                for (int c = 0; c < CLM; ++c) mine += v[c];
                 incl = mine;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -320,10 +327,10 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
         // them lie in the CTAs before
         int before = 0;
         {
-            int v[8];
+            int v[CLM];
             of_all(&s_hist[pass][digit], v);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) before += c < rank ? v[c] : 0;
+            for (int c = 0; c < CLM; ++c) before += c < rank ? v[c] : 0;
         }
         const int own = s_hist[pass][digit];
         const int take = before >= want ? 0 : min(own, want - before);      // of this CTA's
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     sync_all();                                 // the cluster's marks are made, its counts read
     if (rank == 0 && tid == 0) s_last = atomicAdd(p.ticket, 1u) == (unsigned)(gridDim.x / CL) - 1u;
     sync_all();
-    if (!*cluster.map_shared_rank(&s_last, 0)) {
+    if (!(CLM > 1 ? *cluster.map_shared_rank(&s_last, 0) : s_last)) {
         sync_all();                             // (no CTA leaves while it is read)
         return;
     }
@@ -403,10 +410,10 @@ __global__ void __launch_bounds__(kEvictThreads) block_evict_kernel(const __grid
     sync_all();
     int at = free0, all = free0;                // list entries before this CTA's, and in the end
     {
-        int v[8];
+        int v[CLM];
         of_all(&s_count[0], v);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < CLM; ++c) {
             at += c < rank ? v[c] : 0;
             all += v[c];
         }
@@ -483,19 +490,20 @@ cudaError_t launch_weigh(const WeighParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_block_evict(const EvictParams& p, cudaStream_t s) {
-    // up to four keys a thread, as far as eight CTAs go (a cluster of eight runs on every GPU); no more
-    // threads than keys: their barriers are what a short table waits for
+    // up to four keys a thread, as far as a cluster goes; no more threads than keys: their barriers are
+    // what a short table waits for
     int cl = 1, threads = 256;
     while (threads < kEvictThreads && threads < p.maxb) threads *= 2;
-    while (cl < 8 && (long long)cl * 4 * threads < p.maxb) cl *= 2;
+    while (cl < kEvictCluster && (long long)cl * 4 * threads < p.maxb) cl *= 2;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = ev_config(dim3((unsigned)(p.B * cl)), threads, s, attr);
+    if (cl == 1) return cudaLaunchKernelEx(&cfg, block_evict_kernel<1>, p);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cl;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, block_evict_kernel, p);
+    return cudaLaunchKernelEx(&cfg, block_evict_kernel<kEvictCluster>, p);
 }
 
 }  // namespace kvc
