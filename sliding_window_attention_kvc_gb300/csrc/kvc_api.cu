@@ -1411,6 +1411,7 @@ KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t lay
     p.Hq = d->q_heads;
     p.Hkv = d->kv_heads;
     p.G = g.G;
+    p.inv_g = (65536 + g.G - 1) / g.G;
     p.layer = layer;
     p.layout = d->layout;
     p.window = d->window;

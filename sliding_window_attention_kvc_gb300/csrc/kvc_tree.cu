@@ -93,6 +93,10 @@ constexpr int tr_smem_bytes() {
     return S::OffMeta + S::STAGES * (int)sizeof(TrStageMeta) + (int)sizeof(TrBars) + 1024;
 }
 
+// The token of a row of a column: row / G (exact for rows below 256; a division by a value that is not known at
+// compile time is thirty instructions, and a cold one each).
+__device__ __forceinline__ int tr_token(const TreeParams& p, int row) { return (row * p.inv_g) >> 16; }
+
 // Cached rows of sequence b: live slots of a window layout, positions of a paged one.
 __device__ __forceinline__ int tr_cached(const TreeParams& p, int pos) {
     if (pos <= 0) return 0;
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         const int r = tid - (kTrSoftmax0 + 4 * qi) * 32;   // row = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
-        const int tl = r / p.G;
+        const int tl = tr_token(p, r);
         bool ok = true;
         int idx0 = 0, base = 0, at_b = -1, joins = 0;
         TrDraft draft{};
@@ -681,40 +685,39 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
             // Q rows, rotated at their positions when BAKED, unscaled bf16
             if (nt > 0) {
-                // (D / 16 lanes share a row: a load covers whole lines; a batch is in flight at once)
+                // (D / 16 lanes share a row: a load covers whole lines; a batch is in flight at once.  Rows
+                // behind the last token are its again: nothing is taken from them.)
                 constexpr int LPR = D / 16, RPW = 32 / LPR, NB = 32 / RPW < 8 ? 32 / RPW : 8;
                 const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
+                const int q_r0 = (warp & 3) * 32 + lane / LPR, last_t = max(min(p.tq, sg.tokens - c0) - 1, 0);
+                const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) +
+                                          (((long long)sg.b * p.T + sg.n0 + c0) * p.Hq + sg.h * p.G) * D + 8 * c;
+                // Q tile: [column block][128 rows][128 B], 128-byte swizzle; RPW rows on, bits 4 .. 6 change by a constant
+                auto place = [&](int ch) { return (ch >> 3) * (kWsRows * 128) + q_r0 * 128 + (((ch ^ q_r0) & 7) << 4); };
+                const int p1 = place(c), p2 = place(c + D / 16);
 #pragma unroll 1
                 for (int it0 = 0; it0 < 32 / RPW; it0 += NB) {
                     uint4 a[NB], e[NB];
 #pragma unroll
                     for (int it = 0; it < NB; ++it) {
-                        const int rr = (warp & 3) * 32 + (it0 + it) * RPW + lane / LPR;
-                        const int rtl = rr / p.G;
-                        a[it] = e[it] = make_uint4(0u, 0u, 0u, 0u);
-                        if (rtl < p.tq && c0 + rtl < sg.tokens) {
-                            const __nv_bfloat16* qrow =
-                                static_cast<const __nv_bfloat16*>(p.q) +
-                                (((long long)sg.b * p.T + sg.n0 + c0 + rtl) * p.Hq + sg.h * p.G + (rr - rtl * p.G)) * D;
-                            a[it] = __ldcg(reinterpret_cast<const uint4*>(qrow + 8 * c));
-                            e[it] = __ldcg(reinterpret_cast<const uint4*>(qrow + D / 2 + 8 * c));
-                        }
+                        const int rr = q_r0 + (it0 + it) * RPW, rtl = tr_token(p, rr);
+                        const __nv_bfloat16* qrow = q0 + (long long)(min(rtl, last_t) * p.Hq + rr - rtl * p.G) * D;
+                        a[it] = __ldcg(reinterpret_cast<const uint4*>(qrow));
+                        e[it] = __ldcg(reinterpret_cast<const uint4*>(qrow + D / 2));
                     }
 #pragma unroll
                     for (int it = 0; it < NB; ++it) {
-                        // Q tile: [column block][128 rows][128 B], 128-byte swizzle
-                        const int rr = (warp & 3) * 32 + (it0 + it) * RPW + lane / LPR;
-                        const int c1 = c, c2 = c + D / 16;
-                        *reinterpret_cast<uint4*>(Qs + (c1 >> 3) * (kWsRows * 128) + rr * 128 + (((c1 ^ rr) & 7) << 4)) = a[it];
-                        *reinterpret_cast<uint4*>(Qs + (c2 >> 3) * (kWsRows * 128) + rr * 128 + (((c2 ^ rr) & 7) << 4)) = e[it];
+                        const int on = (it0 + it) * RPW * 128, turn = ((it * RPW) & 7) << 4;
+                        *reinterpret_cast<uint4*>(Qs + ((p1 + on) ^ turn)) = a[it];
+                        *reinterpret_cast<uint4*>(Qs + ((p2 + on) ^ turn)) = e[it];
                     }
                 }
                 if (p.rope != kRopeNone) {
                     // each lane's own chunks, in place
 #pragma unroll 1
                     for (int it = 0; it < 32 / RPW; ++it) {
-                        const int rr = (warp & 3) * 32 + it * RPW + lane / LPR;
-                        const int rtl = rr / p.G;
+                        const int rr = q_r0 + it * RPW;
+                        const int rtl = tr_token(p, rr);
                         const bool rok = rtl < p.tq && c0 + rtl < sg.tokens;
                         const unsigned long long mine = draft.of(rok ? sg.n0 + c0 + rtl : 0);
                         const int c1 = c, c2 = c + D / 16;
@@ -891,7 +894,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
 #pragma unroll 4
                     for (int it = 0; it < CPL; ++it) {
                         const int rr = (warp & 3) * 32 + (32 / CPL) * it + lane / CPL, ch = lane % CPL;
-                        const int rtl = rr / p.G;
+                        const int rtl = tr_token(p, rr);
                         if (rtl < p.tq && c0 + rtl < sg.tokens) {
                             const float4 w = *stg(rr, ch);
                             if (whole) {
@@ -1004,7 +1007,7 @@ __global__ void __launch_bounds__(kTrCombineThreads) tree_combine_kernel(const _
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int t = row / p.G;
+        const int t = tr_token(p, row);
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                              (((long long)b * p.T + m * p.mq + t) * p.Hq + h * p.G + (row - t * p.G)) * D;
 #pragma unroll
@@ -1045,12 +1048,13 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
     cudaLaunchConfig_t cfg = tr_config(dim3(p.ctas), TrShape<D>::Threads, kSmem, stream, &attr);
     e = cudaLaunchKernelEx(&cfg, tree_kernel<D>, p, maps);
     if (e != cudaSuccess) return e;
-    // few columns, each of many shares: a row a warp; many: four, so that a CTA's way to its
-    // parts is paid once for them
+    // a row a warp, or several where the CTAs would not be on the GPU together (four an SM): a second
+    // wave of them cost the drafts over 8 rings 4 us
     TreeParams c = p;
     const long long cols = (long long)p.B * p.Hkv * p.ncol;
     const int rows = (p.T < p.mq ? p.T : p.mq) * p.G, pass = kTrCombineThreads / (D / 4 < 32 ? D / 4 : 32);
-    c.comb_rows = cols * rows <= 152LL * 8 * pass ? pass : 4 * pass;
+    const long long most = cols * ((rows + pass - 1) / pass), turns = (most + kTreeCtas * 4 - 1) / (kTreeCtas * 4);
+    c.comb_rows = pass * (int)(turns < (rows + pass - 1) / pass ? turns : (rows + pass - 1) / pass);
     cfg = tr_config(dim3((unsigned)cols, (rows + c.comb_rows - 1) / c.comb_rows), kTrCombineThreads, 0, stream, &attr);
     return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, c);
 }

@@ -49,6 +49,7 @@ struct TreeParams {
     float* part_o;
     int2* col_shares;           // [columns]: the first and the last share of each
     int B, T, Hq, Hkv, G, layer;
+    int inv_g;                  // 65536 / G, rounded up
     int layout, window, sinks, capacity, bs, num_blocks, maxb;
     int tq, mq, ncol;           // tokens of a Q tile, of a column; columns of a (sequence, kv head)
     int col_units;              // units a tile of all columns of a kv head
