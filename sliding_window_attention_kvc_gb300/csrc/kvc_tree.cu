@@ -24,10 +24,10 @@
 // What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for
 // 4 x 64 x 128 x D flops a Q tile: bytes up to one Q tile, the tensor pipe's turns
 // beyond (a tile's S waits behind the P V before it).  Drafts of 32 tokens over 8 rings
-// of 4096, 32 / 8 heads of 128 (139 MB): 45 us, the tiles at 0.91 of the measured
-// bandwidth for half of it, then what comes once: the way to the first product, the
-// rows' write, the combine.  64 tokens over 100,003 (411 MB, 105 GFLOP): 103 us,
-// 0.59 of the bandwidth and 0.53 of the bf16 rate at once.
+// of 4096, 32 / 8 heads of 128 (139 MB): 41 us, half of it tiles at the rate of DRAM, then
+// what comes once: the way to the first product, the rows' write, the combine.  64 tokens
+// over 100,003 (411 MB, 105 GFLOP): 102 us, 0.59 of the bandwidth and 0.53 of the bf16 rate
+// at once.
 #include <atomic>
 
 #include "kvc_decode.cuh"
@@ -39,6 +39,7 @@ namespace kvc {
 namespace {
 
 constexpr int kTrSoftmax0 = 4;              // first softmax warp
+constexpr int kTrMaxStages = 10;
 constexpr float kTrLazy = 8.f;              // the reference maximum moves when a tile's exceeds it by more
 
 __device__ __forceinline__ void tr_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -47,7 +48,9 @@ __device__ __forceinline__ void tr_pdl_launch() { asm volatile("griddepcontrol.l
 template <int D>
 struct TrShape {
     static constexpr int NQ = tree_q_tiles(D);
-    static constexpr int STAGES = D == 64 ? 6 : (D == 128 ? 4 : 2);
+    // as many as there is room for (bytes on their way are what few rows are bound by: drafts of 8 over 64 rings
+    // of 4096 took 219 us with four stages of 128, 203 with five)
+    static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 2);
     static constexpr int CB = D / 64;                          // 64-column blocks of a row
     static constexpr int QBytes = kWsRows * D * 2;             // one Q tile
     // a stage: [8 rows of the tile][K|V][column block][8 rows x 128 bytes], so that one copy brings any
@@ -75,7 +78,7 @@ struct alignas(16) TrStageMeta {
 };
 
 struct TrBars {
-    uint64_t full[6], ready[6], empty[6];
+    uint64_t full[kTrMaxStages], ready[kTrMaxStages], empty[kTrMaxStages];
     // (of two tiles in turn: a warp hands over P of a tile before it asks for O of the tile before, and the
     // issuer may ask for a P once the next has been handed over; on one barrier each, a warp or an issuer held
     // up for a product's time would find the phase after the one it asks for, and wait for good)
@@ -90,7 +93,8 @@ struct TrBars {
 template <int D>
 constexpr int tr_smem_bytes() {
     using S = TrShape<D>;
-    return S::OffMeta + S::STAGES * (int)sizeof(TrStageMeta) + (int)sizeof(TrBars) + 1024;
+    static_assert(S::STAGES <= kTrMaxStages, "barriers of every stage");
+    return S::OffMeta + S::STAGES * (int)sizeof(TrStageMeta) + (int)sizeof(TrBars);
 }
 
 // The token of a row of a column: row / G (exact for rows below 256; a division by a value that is not known at
@@ -385,9 +389,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using S = TrShape<D>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
-    extern __shared__ unsigned char tr_raw[];
-    const uint32_t raw_u = smem_u32(tr_raw);
-    unsigned char* sm = tr_raw + (((raw_u + 1023u) & ~1023u) - raw_u);
+    extern __shared__ __align__(1024) unsigned char sm[];          // (swizzled tiles: their blocks are 1024 bytes)
     const uint32_t sm_u = smem_u32(sm);
     TrStageMeta* meta = reinterpret_cast<TrStageMeta*>(sm + S::OffMeta);
     TrBars* bars = reinterpret_cast<TrBars*>(sm + S::OffMeta + NST * sizeof(TrStageMeta));
@@ -418,6 +420,10 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
     }
     tr_pdl_wait();
     tr_pdl_launch();
+    if (sm_u & 1023u) {                              // (uniform; never seen: nothing else lies in shared memory)
+        if (tid == 0) index_fault(p.err, 42, sm_u);
+        return;
+    }
     const TrParts parts = tr_partition(p);
     const long long units = parts.units;
     const int shares = parts.shares, x = blockIdx.x;
