@@ -381,10 +381,10 @@ class ClockSampler:
 # capture per workload, and the digest of the kernel's sources
 # (KERNEL_TRAFFIC_FILES) they were taken on: reported only while those
 # sources are unchanged.
-KERNEL_TRAFFIC = {"ring_bf16": 137132288, "sink_window_bf16": 542906112,
-                  "paged_shared_prefix_bf16": 840988416, "long_context_pool_bf16": 155747840,
-                  "ring_int8": 69635328}
-KERNEL_TRAFFIC_SOURCES = "46a13812ab0c0b9dba27ddf63945a8c190b78d2e3d22c865b10c16f82599802f"
+KERNEL_TRAFFIC = {"ring_bf16": 137052672, "sink_window_bf16": 542770688,
+                  "paged_shared_prefix_bf16": 841697280, "long_context_pool_bf16": 155712768,
+                  "ring_int8": 69626880}
+KERNEL_TRAFFIC_SOURCES = "32253c009e4f04176d62ae91b776c1b1166ea74348e3f6384cb1b7d0617ba407"
 
 
 # the sources decode_mma_kernel and its launch are built from

@@ -24,7 +24,7 @@
 // What bounds it: a tile is 64 rows of K and V (32 KB at head_dim 128) for
 // 4 x 64 x 128 x D flops a Q tile: bytes up to one Q tile, the tensor pipe's turns
 // beyond (a tile's S waits behind the P V before it).  Drafts of 32 tokens over 8 rings
-// of 4096, 32 / 8 heads of 128 (139 MB): 41 us, half of it tiles at the rate of DRAM, then
+// of 4096, 32 / 8 heads of 128 (139 MB): 40 us, half of it tiles at the rate of DRAM, then
 // what comes once: the way to the first product, the rows' write, the combine.  64 tokens
 // over 100,003 (411 MB, 105 GFLOP): 102 us, 0.59 of the bandwidth and 0.53 of the bf16 rate
 // at once.
@@ -45,12 +45,15 @@ constexpr float kTrLazy = 8.f;              // the reference maximum moves when 
 __device__ __forceinline__ void tr_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void tr_pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-template <int D>
+// FEW: drafts of one Q tile at head_dim 128: both warpgroups' products read one copy of it, which leaves room for a
+// stage more.
+template <int D, bool FEW = false>
 struct TrShape {
     static constexpr int NQ = tree_q_tiles(D);
+    static constexpr int QTiles = FEW ? 1 : NQ;
     // as many as there is room for (bytes on their way are what few rows are bound by: drafts of 8 over 64 rings
-    // of 4096 took 219 us with four stages of 128, 203 with five)
-    static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 2);
+    // of 4096 took 219 us with four stages at head_dim 128, 203 with five, 196 with FEW's six)
+    static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? (FEW ? 6 : 5) : 2);
     static constexpr int CB = D / 64;                          // 64-column blocks of a row
     static constexpr int QBytes = kWsRows * D * 2;             // one Q tile
     // a stage: [8 rows of the tile][K|V][column block][8 rows x 128 bytes], so that one copy brings any
@@ -59,7 +62,7 @@ struct TrShape {
     static constexpr int Group = 2 * VOff;
     static constexpr int StageBytes = (kWsKeys / 8) * Group;
     static constexpr int OffQ = 0;
-    static constexpr int OffStage = OffQ + NQ * QBytes;
+    static constexpr int OffStage = OffQ + QTiles * QBytes;
     static constexpr int OffMeta = OffStage + STAGES * StageBytes;
     static constexpr int TmemCols = 512;
     static constexpr int SCol0 = NQ * D;                       // S buffers after the O tiles
@@ -90,9 +93,9 @@ struct TrBars {
     float2 ml[2][kWsRows];          // ... and their (m, l)
 };
 
-template <int D>
+template <int D, bool FEW>
 constexpr int tr_smem_bytes() {
-    using S = TrShape<D>;
+    using S = TrShape<D, FEW>;
     static_assert(S::STAGES <= kTrMaxStages, "barriers of every stage");
     return S::OffMeta + S::STAGES * (int)sizeof(TrStageMeta) + (int)sizeof(TrBars);
 }
@@ -384,10 +387,10 @@ __device__ __forceinline__ void tr_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
                   ks > 0 ? 1u : more);
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
-    using S = TrShape<D>;
+    using S = TrShape<D, FEW>;
     constexpr int NQ = S::NQ, NST = S::STAGES, CB = S::CB;
     extern __shared__ __align__(1024) unsigned char sm[];          // (swizzled tiles: their blocks are 1024 bytes)
     const uint32_t sm_u = smem_u32(sm);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 mbar_init(&bars->p_full[i][u], 4);
                 mbar_init(&bars->o_done[i][u], 1);
             }
-            mbar_init(&bars->q_ready[i], 4);
+            mbar_init(&bars->q_ready[i], FEW ? 8 : 4);
             mbar_init(&bars->fin[i], 1);
             mbar_init(&bars->both[i], 4 * NQ);
         }
@@ -596,17 +599,15 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         const int i = warp >> 1;
         bool ok = true;
         int idx0 = 0, base = 0, loads = 0;             // tiles of the segments before; of this Q tile; its loads
-        const uint64_t qd = ws_sdesc(sm_u + S::OffQ + i * S::QBytes, 16, 1024);
+        const uint64_t qd = ws_sdesc(sm_u + S::OffQ + (FEW ? 0 : i * S::QBytes), 16, 1024);
         const uint64_t kd0 = ws_sdesc(sm_u + S::OffStage, 16, S::Group);
         const uint64_t vd0 = ws_sdesc(sm_u + S::OffStage + S::VOff, 1024, S::Group);
         const uint32_t s0 = tmem + S::SCol0 + (uint32_t)(i * 2 * kWsKeys), o_t = tmem + (uint32_t)(i * D);
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
             const int own = sg.tiles(i), others = sg.nt - own;
-            if (own > 0) {
-                ok = ws_wait(&bars->q_ready[i], loads & 1, abort);
-                ++loads;
-            }
+            if (own > 0) ok = ws_wait(&bars->q_ready[FEW ? 0 : i], loads & 1, abort);
+            loads += FEW || own > 0;
             int ns = 0, npv = 0, nother = 0;           // S issued, P V issued, the other Q tile's tiles passed
             long long t0 = clock64();
             while (ok && (npv < own || nother < others)) {
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         const int qi = (warp - kTrSoftmax0) >> 2;          // Q tile
         const int r = tid - (kTrSoftmax0 + 4 * qi) * 32;   // row = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        unsigned char* Qs = sm + S::OffQ + qi * S::QBytes;
+        unsigned char* Qs = sm + S::OffQ + (FEW ? 0 : qi * S::QBytes);
         const int tl = tr_token(p, r);
         bool ok = true;
         int idx0 = 0, base = 0, at_b = -1, joins = 0;
@@ -690,19 +691,20 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             const bool row_ok = tl < p.tq && c0 + tl < sg.tokens;
             const int nt = sg.tiles(qi);                   // 0: the other warpgroup has the segment's one tile
             // Q rows, rotated at their positions when BAKED, unscaled bf16
-            if (nt > 0) {
+            if (FEW || nt > 0) {
                 // (D / 16 lanes share a row: a load covers whole lines; a batch is in flight at once.  Rows
                 // behind the last token are its again: nothing is taken from them.)
-                constexpr int LPR = D / 16, RPW = 32 / LPR, NB = 32 / RPW < 8 ? 32 / RPW : 8;
+                constexpr int ROWS = FEW ? 16 : 32;        // of a warp (FEW: a tile's among both warpgroups')
+                constexpr int LPR = D / 16, RPW = 32 / LPR, NB = ROWS / RPW < 8 ? ROWS / RPW : 8;
                 const int c = lane % LPR;                  // 8-column chunk, paired with c + D / 16
-                const int q_r0 = (warp & 3) * 32 + lane / LPR, last_t = max(min(p.tq, sg.tokens - c0) - 1, 0);
+                const int q_r0 = (FEW ? warp - kTrSoftmax0 : warp & 3) * ROWS + lane / LPR, last_t = max(min(p.tq, sg.tokens - c0) - 1, 0);
                 const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) +
                                           (((long long)sg.b * p.T + sg.n0 + c0) * p.Hq + sg.h * p.G) * D + 8 * c;
                 // Q tile: [column block][128 rows][128 B], 128-byte swizzle; RPW rows on, bits 4 .. 6 change by a constant
                 auto place = [&](int ch) { return (ch >> 3) * (kWsRows * 128) + q_r0 * 128 + (((ch ^ q_r0) & 7) << 4); };
                 const int p1 = place(c), p2 = place(c + D / 16);
 #pragma unroll 1
-                for (int it0 = 0; it0 < 32 / RPW; it0 += NB) {
+                for (int it0 = 0; it0 < ROWS / RPW; it0 += NB) {
                     uint4 a[NB], e[NB];
 #pragma unroll
                     for (int it = 0; it < NB; ++it) {
@@ -721,7 +723,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 if (p.rope != kRopeNone) {
                     // each lane's own chunks, in place
 #pragma unroll 1
-                    for (int it = 0; it < 32 / RPW; ++it) {
+                    for (int it = 0; it < ROWS / RPW; ++it) {
                         const int rr = q_r0 + it * RPW;
                         const int rtl = tr_token(p, rr);
                         const bool rok = rtl < p.tq && c0 + rtl < sg.tokens;
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->q_ready[qi]);
+                if (lane == 0) mbar_arrive(&bars->q_ready[FEW ? 0 : qi]);
             }
             know_draft();
             const unsigned long long see = draft.of(row_ok ? sg.n0 + c0 + tl : 0);
@@ -864,11 +866,12 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
             if (!whole && row_ok && (!sg.alt || qi == 0)) p.part_ml[row_a + r] = make_float2(m_run, l_run);
             if (nt > 0 || sg.alt) {
                 // through the Q tile's shared memory (its products are done), each row in the
-                // place of its own q (which this warp alone writes), CP columns at a time, so
-                // that whole lines go out
-                constexpr int CP = D == 64 ? 32 : 64, CPL = CP / 4;            // 16-byte chunks of a staged row
+                // place of its own q (which this warp alone writes; FEW: a column block for each
+                // warpgroup, and no q before both are done), CP columns at a time, so that whole
+                // lines go out
+                constexpr int CP = D == 64 || FEW ? 32 : 64, CPL = CP / 4;            // 16-byte chunks of a staged row
                 auto stg = [&](int row, int ch) {
-                    return reinterpret_cast<float4*>(Qs + (ch >> 3) * (kWsRows * 128) + row * 128 + (((ch ^ row) & 7) << 4));
+                    return reinterpret_cast<float4*>(Qs + (FEW ? qi : ch >> 3) * (kWsRows * 128) + row * 128 + (((ch ^ row) & 7) << 4));
                 };
 #pragma unroll 1
                 for (int c6 = 0; c6 < cols; c6 += CP) {
@@ -1036,9 +1039,9 @@ cudaLaunchConfig_t tr_config(dim3 grid, int threads, int smem, cudaStream_t stre
     return cfg;
 }
 
-template <int D>
+template <int D, bool FEW = false>
 cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_t stream) {
-    constexpr int kSmem = tr_smem_bytes<D>();
+    constexpr int kSmem = tr_smem_bytes<D, FEW>();
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
     static std::atomic<unsigned long long> configured{0};
     int dev = 0;
@@ -1046,13 +1049,13 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(tree_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = tr_config(dim3(p.ctas), TrShape<D>::Threads, kSmem, stream, &attr);
-    e = cudaLaunchKernelEx(&cfg, tree_kernel<D>, p, maps);
+    cudaLaunchConfig_t cfg = tr_config(dim3(p.ctas), TrShape<D, FEW>::Threads, kSmem, stream, &attr);
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<D, FEW>, p, maps);
     if (e != cudaSuccess) return e;
     // a row a warp, or several where the CTAs would not be on the GPU together (four an SM): a second
     // wave of them cost the drafts over 8 rings 4 us
@@ -1068,7 +1071,10 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
 }  // namespace
 
 cudaError_t launch_tree(int D, const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
-    return D == 64 ? launch_tree_t<64>(p, maps, s) : (D == 128 ? launch_tree_t<128>(p, maps, s) : launch_tree_t<256>(p, maps, s));
+    if (D == 64) return launch_tree_t<64>(p, maps, s);
+    if (D == 256) return launch_tree_t<256>(p, maps, s);
+    // (one unit a tile: drafts of up to 128 rows)
+    return p.col_units == 1 ? launch_tree_t<128, true>(p, maps, s) : launch_tree_t<128>(p, maps, s);
 }
 
 cudaError_t launch_tree_stage(int D, const TreeParams& p, cudaStream_t s) {
