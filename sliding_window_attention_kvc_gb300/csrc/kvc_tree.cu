@@ -86,6 +86,9 @@ struct TrBars {
     // issuer may ask for a P once the next has been handed over; on one barrier each, a warp or an issuer held
     // up for a product's time would find the phase after the one it asks for, and wait for good)
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
+    // (an issuer's own: it counts the segments that bring it a tile.  On one barrier for both, a segment of one
+    // tile, which only the first issuer asks for, left the second a phase behind: it began the next segment's
+    // products on the q before; and asking for every phase it could find the one after, and wait for good)
     uint64_t q_ready[2], fin[2];
     uint64_t both[2];               // alternate tiles: both warpgroups' sums are there; both have read them
     uint32_t tmem;
@@ -606,8 +609,7 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
         for (long long u = lo; u < hi && ok;) {
             const TrSegment sg = tr_segment<D>(p, walk, u, hi);
             const int own = sg.tiles(i), others = sg.nt - own;
-            if (own > 0) ok = ws_wait(&bars->q_ready[FEW ? 0 : i], loads & 1, abort);
-            loads += FEW || own > 0;
+            if (own > 0) ok = ws_wait(&bars->q_ready[i], loads++ & 1, abort);
             int ns = 0, npv = 0, nother = 0;           // S issued, P V issued, the other Q tile's tiles passed
             long long t0 = clock64();
             while (ok && (npv < own || nother < others)) {
@@ -736,7 +738,10 @@ __global__ void __launch_bounds__(TrShape<D>::Threads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->q_ready[FEW ? 0 : qi]);
+                if (lane == 0) {
+                    mbar_arrive(&bars->q_ready[FEW ? 0 : qi]);
+                    if (FEW && sg.nt > 1) mbar_arrive(&bars->q_ready[1]);      // (the second issuer has a tile)
+                }
             }
             know_draft();
             const unsigned long long see = draft.of(row_ok ? sg.n0 + c0 + tl : 0);
