@@ -969,6 +969,10 @@ __global__ void __launch_bounds__(kTrCombineThreads) tree_combine_kernel(const _
     const int tokens = min(p.mq, p.T - m * p.mq);
     tr_pdl_wait();
     const int2 sh = __ldcg(p.col_shares + col);
+    if (!tree_shares_held(sh.x, sh.y, p.ctas)) {
+        if (tid == 0) index_fault(p.err, 43, sh.x);
+        return;
+    }
     const int np = sh.y - sh.x + 1;
     if (np <= 1) return;                                                  // one share: written whole
     const long long slot = (long long)sh.x + col;

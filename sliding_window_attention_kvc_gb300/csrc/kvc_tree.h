@@ -32,6 +32,12 @@ constexpr int kTreeMinTiles = 2;
 // Q tiles of 128 rows of one column: head_dim 256 leaves tensor memory for one.
 __host__ __device__ constexpr int tree_q_tiles(int D) { return D == 256 ? 1 : 2; }
 
+// Whether shares first .. last of a column can be joined.  tree_kernel stores the two as it
+// walks the columns; where one of its waits gave up, they are whatever the workspace held.
+__host__ __device__ constexpr bool tree_shares_held(int first, int last, int ctas) {
+    return first >= 0 && first <= last && last < ctas;
+}
+
 // Attention of a tree of drafted tokens (kvc_tree_attention).  A column is
 // (sequence, kv head, up to mq tokens); its keys are tiles of 64: the cached rows
 // (slots, or positions of a paged sequence), then the draft itself.
