@@ -478,7 +478,10 @@ KVC_API int kvc_tree_attention(const kvc_desc* d, const void* cache, int32_t lay
  *   n_path        [batch] int32 (NULL: P for all); above P counts as P
  *                 (KVC_DEV_BAD_ENTRY), below 0 as 0.
  * Sequences with pos0[b] < 0 append nothing.  Other device errors as in
- * kvc_append.  Workspace: kvc_workspace_bytes(d). */
+ * kvc_append: PAGED, every block that the path reaches is mapped, and private to
+ * the sequence, before the call (kvc_block_prepare at pos0[b] and at the first
+ * row of each further block; it readies one position's block a call).
+ * Workspace: kvc_workspace_bytes(d). */
 KVC_API int kvc_append_path(const kvc_desc* d, void* cache, int32_t layer, const void* k_new, const void* v_new,
                             int32_t T, const int32_t* pos0, const int32_t* path, int32_t P, const int32_t* n_path,
                             const int32_t* block_table, void* workspace, size_t workspace_bytes, void* stream);
