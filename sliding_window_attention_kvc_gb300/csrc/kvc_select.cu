@@ -490,16 +490,14 @@ __device__ __forceinline__ void pick_count(int* hist, bool in, uint32_t digit) {
     }
 }
 
-// The digit that holds the want-th key (1-based) from the top (DOWN) or the
-// bottom; how many keys lie beyond it on that side goes to *beyond.  By warp 0.
-template <bool DOWN>
+// The digit that holds the want-th key (1-based) from the top; how many keys lie
+// above it goes to *beyond.  By warp 0.
 __device__ __forceinline__ void pick_digit(const int* hist, int want, int* digit, int* beyond) {
     const int lane = threadIdx.x & 31;
     int c[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int d = lane * 8 + i;
-        c[i] = hist[DOWN ? 255 - d : d];
+        c[i] = hist[255 - (lane * 8 + i)];
         sum += c[i];
     }
     int incl = sum;
@@ -513,7 +511,7 @@ __device__ __forceinline__ void pick_digit(const int* hist, int want, int* digit
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (run < want && run + c[i] >= want) {
-                *digit = DOWN ? 255 - (lane * 8 + i) : lane * 8 + i;
+                *digit = 255 - (lane * 8 + i);
                 *beyond = run;
             }
             run += c[i];
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const __grid_c
             for (int u = 0; u < 4; ++u) pick_count(s_hist[pass], k[u] != 0u && (k[u] & mask) == prefix, (k[u] >> shift) & 255u);
         }
         __syncthreads();
-        if (tid < 32) pick_digit<true>(s_hist[pass], want, &s_digit[pass], &s_beyond[pass]);
+        if (tid < 32) pick_digit(s_hist[pass], want, &s_digit[pass], &s_beyond[pass]);
         __syncthreads();
         const int digit = s_digit[pass];
         if (digit < 0) {                       // fewer candidates than k (seen in the first pass): all of them
