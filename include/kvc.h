@@ -365,8 +365,10 @@ KVC_API int kvc_decode_attention_shared(const kvc_desc* d, const void* cache, in
  * smallest, then fp32 steps [layers, num_blocks, kv_heads]:
  *     step = max over channels of max(|largest|, |smallest|) / 127,
  *     codes ceil(largest / step) and floor(smallest / step), clamped to +-127
- * (IEEE fp32 quotients; a step of 0 has codes 0), so that code * step bounds the
- * keys from outside.
+ * (IEEE fp32 quotients; a step of 0 has codes 0).  A code * step lies outside of
+ * its keys, or inside by no more than the fp32 roundings of step and quotient:
+ * 2^-23 of the block's largest |key| of that head, where that is 127 * 2^-126
+ * or more (smaller keys have a step that is no normal number, or 0).
  *
  * kvc_block_bounds works them out for every logical block that holds one of the
  * positions pos[b] .. pos[b] + n - 1 (n = n_tok[b], cut to 0 .. n_new; NULL:

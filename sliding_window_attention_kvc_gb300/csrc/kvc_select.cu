@@ -7,7 +7,8 @@
 //     q . k = sum q_d k_d <= sum max(q_d hi_d, q_d lo_d) = U,
 // so a block whose U is small holds no key that the query attends much.  hi and
 // lo are kept as 8-bit codes of one step s = max(|hi|, |lo|) / 127, hi rounded
-// up and lo down, so that the codes' bound is a bound still; q enters as codes
+// up and lo down, so that the codes' bound is a bound still, but for the fp32
+// roundings of s and of the quotients (2^-23 of 127 s at most); q enters as codes
 // too (step max|q| / 127).  U is then s s_q u, u an integer below 127 127 256 <
 // 2^24: its products run four to an instruction (dp4a), and no order of the
 // sums, here or in any other program, gives another score.
