@@ -427,7 +427,8 @@ KVC_API int kvc_decode_attention_selected(const kvc_desc* d, const void* cache, 
  *               attended),
  * in an order of sums that depends on nothing but the shapes.  decay 0 .. 1 (else
  * KVC_ERR_ARG); with 0 the old values are not read.  One array can take several
- * layers' calls, the decay given to the step's first.
+ * layers' calls, the decay given to the step's first.  The caller zeroes a
+ * sequence's row when another sequence takes its place.
  *   workspace  kvc_weighed_workspace_bytes(d) bytes (0 if `d` is refused): the
  *              decode workspace, which it serves as too, and a score for every q
  *              head and position. */
