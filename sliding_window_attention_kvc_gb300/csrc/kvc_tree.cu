@@ -27,7 +27,9 @@
 // of 4096, 32 / 8 heads of 128 (139 MB): 40 us, half of it tiles at the rate of DRAM, then
 // what comes once: the way to the first product, the rows' write, the combine.  64 tokens
 // over 100,003 (411 MB, 105 GFLOP): 102 us, 0.59 of the bandwidth and 0.53 of the bf16 rate
-// at once.
+// at once.  With baked keys the q rows are rotated one after the other before a CTA's first
+// product, and the draft's keys by a launch of their own: 63 and 140 us.  At head_dim 64 31
+// and 86 us, at 256 (two stages) 76 and 286.
 #include <atomic>
 
 #include "kvc_decode.cuh"
@@ -134,7 +136,12 @@ struct TrWalk {
 // Units of all sequences, and the shares they are cut into (a whole warp's call): one a
 // CTA; fewer where the columns are alike and fewer than the CTAs: then each is cut into
 // the same whole number of shares, and no CTA begins a second segment (its way to the
-// first product, and a partial, cost 6 us; bandwidth is reached with 100 CTAs and more).
+// first product, and a partial, cost 6 us).  Whole shares / all 152 CTAs, drafts of 32 over
+// rings of 4096, 8 kv heads: 8 rings 41 / 46 us, 9 43 / 49, 10 54 / 53, 12 55 / 58, 14 56 / 63,
+// 18 60 / 77.  From 77 columns on a column is one share: 10 and 11 rings leave 72 and 64 CTAs
+// idle, which drafts of 8 (10 rings 55 / 46, 12 55 / 51) and of 64 (10 rings 78 / 71) and long
+// rings (10 of 16384 170 / 126, 12 172 / 145, 18 191 / 206) are slower for; short ones are
+// not (10 of 1024 24 / 33).
 struct TrParts {
     long long units;
     int shares;
